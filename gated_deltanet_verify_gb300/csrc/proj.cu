@@ -15,8 +15,9 @@
 //   * Warp 0 is the TMA producer: each stage holds kKBlk columns of K of the
 //     W tile and of X as 64-column (128-byte) TMA boxes in the 128-byte
 //     swizzled K-major layout the tensor core reads directly.
-//     Two threads issue the MMAs (8 per stage), warp 1 the even stages into
-//     one tensor-memory accumulator and warp 2 the odd ones into a second, and
+//     Two threads issue the MMAs (8 per stage), warp 1 those of the ring's even
+//     stages into one tensor-memory accumulator and warp 2 those of the odd
+//     ones into a second, and
 //     free each stage through tcgen05.commit on its "empty" barrier: one
 //     thread's MMAs follow each other ~150 cycles apart whatever their size
 //     (measured from M = 64, N = 16 to M = 128, N = 256), and two issuing
@@ -223,13 +224,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 tma_box(st + wbytes + b * xbox, &a.x_map, (kb0 + i) * kKBlk + 64 * b, m0, full(s));
         }
     } else if (tid == 32 || tid == 64) {
-        // ---- MMA issuers: stages e, e + 2, ... into accumulator e (8 MMAs of K = 16 per stage); each stage is
-        // freed when its MMAs complete
+        // ---- MMA issuers: the even or the odd stages of the ring into accumulator e (8 MMAs of K = 16 per stage);
+        // each stage is freed when its MMAs complete.  A stage always has the same issuer, which has then seen
+        // every earlier use of it complete: with the K blocks dealt out by their own parity, a ring of an odd
+        // number of stages would hand a stage from one issuer to the other and back, and a wait for its use u + 2
+        // could take the phase of use u (the same parity) for it while the load of use u + 1 is still in flight
         const int e = wid - 1;
         const uint32_t acc = tmem + (uint32_t)(e * a.Mt);
         const uint32_t id = idesc_bf16(a.Mt);
-        for (int i = e; i < kb1 - kb0 && ok; i += 2) {
+        for (int i = e; i < kb1 - kb0 && ok; ++i) {
             const int s = i % S;
+            if ((s & 1) != e) continue;
             ok = mbar_wait(full(s), (i / S) & 1);
             fence_after_sync();
             const uint32_t st = sbase + (uint32_t)s * stage_bytes;
@@ -341,7 +346,7 @@ bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, l
     // with 100 KB each, the K splits spread over every SM, measured slower: 26 us)
     a.stages = (int)((216u * 1024u) / stage);
     if (a.stages > kMaxStages) a.stages = kMaxStages;
-    if (a.stages < 1) {
+    if (a.stages < 2) {                                           // one for each MMA issuer
         why = "pipeline stage larger than shared memory";
         return false;
     }
