@@ -28,10 +28,13 @@ GDN_ERR_TIMEOUT = 8
 GDN_ERR_WORKSPACE = 9
 GDN_ERR_TREE = 10
 GDN_ERR_BOUNDS = 11
+GDN_ERR_SAMPLE = 12
+GDN_ERR_LENGTH = 13
+GDN_ERR_ADAPTER = 14
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_ALIGN", 4: "GDN_ERR_DTYPE",
                 5: "GDN_ERR_TRIM_RANGE", 6: "GDN_ERR_NO_CAPTURE", 7: "GDN_ERR_LAUNCH", 8: "GDN_ERR_TIMEOUT",
                 9: "GDN_ERR_WORKSPACE", 10: "GDN_ERR_TREE",
-                11: "GDN_ERR_BOUNDS"}
+                11: "GDN_ERR_BOUNDS", 12: "GDN_ERR_SAMPLE", 13: "GDN_ERR_LENGTH", 14: "GDN_ERR_ADAPTER"}
 
 GDN_F32 = 0
 GDN_BF16 = 1
@@ -39,7 +42,10 @@ GDN_BF16 = 1
 EXPORTED_SYMBOLS = ("gdn_verify_forward", "gdn_verify_tree", "gdn_rollback", "gdn_rollback_tree",
                     "gdn_rollback_layers", "gdn_rollback_tree_layers", "gdn_verify_after_rollback", "gdn_verify_lazy", "gdn_commit_lazy", "gdn_step_io_layout",
                     "gdn_verify_step_host", "gdn_proj_in_ld", "gdn_layer_workspace_bytes",
-                    "gdn_project_in", "gdn_project_out", "gdn_layer_verify", "gdn_prefill_workspace_bytes",
+                    "gdn_project_in", "gdn_project_out", "gdn_layer_verify", "gdn_lora_workspace_bytes",
+                    "gdn_project_in_lora", "gdn_project_out_lora", "gdn_layer_lora_workspace_bytes",
+                    "gdn_layer_verify_lora", "gdn_sample", "gdn_accept", "gdn_accept_tree",
+                    "gdn_prefill_workspace_bytes",
                     "gdn_prefill_chunked", "gdn_prefill_chunked_static", "gdn_prefill_static_scratch_bytes",
                     "gdn_last_error", "gdn_version")
 
@@ -70,6 +76,21 @@ class StepIO(ctypes.Structure):
 
 class ProjWeights(ctypes.Structure):
     _fields_ = [("n_embd", ctypes.c_int), ("w_in", ctypes.c_void_p), ("w_out", ctypes.c_void_p)]
+
+
+class Lora(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int), ("rank", ctypes.c_int), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+class SampleDims(ctypes.Structure):
+    _fields_ = [("n_slots", ctypes.c_int), ("n_tokens", ctypes.c_int), ("vocab", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("ld", ctypes.c_longlong)]
+
+
+class SampleParams(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p)]
 
 
 def make_dims(n_slots: int, n_qk_heads: int, n_v_heads: int, d_k: int, d_v: int, n_tokens: int,
@@ -124,6 +145,24 @@ def lib() -> ctypes.CDLL:
         L.gdn_layer_verify.argtypes = ([ctypes.POINTER(Dims), ctypes.POINTER(LayerParams),
                                         ctypes.POINTER(ProjWeights)] + [vp] * 7 + [ctypes.c_size_t, vp, vp])
         L.gdn_layer_verify.restype = ip
+        L.gdn_lora_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ip]
+        L.gdn_lora_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_layer_lora_workspace_bytes.argtypes = [ctypes.POINTER(Dims), ip, ip]
+        L.gdn_layer_lora_workspace_bytes.restype = ctypes.c_size_t
+        for fn in (L.gdn_project_in_lora, L.gdn_project_out_lora):
+            fn.argtypes = [ctypes.POINTER(Dims), ctypes.POINTER(ProjWeights), ctypes.POINTER(Lora), vp, vp, vp, vp,
+                           ctypes.c_size_t, vp, vp]
+            fn.restype = ip
+        L.gdn_layer_verify_lora.argtypes = ([ctypes.POINTER(Dims), ctypes.POINTER(LayerParams),
+                                             ctypes.POINTER(ProjWeights), ctypes.POINTER(Lora), ctypes.POINTER(Lora)] +
+                                            [vp] * 8 + [ctypes.c_size_t, vp, vp])
+        L.gdn_layer_verify_lora.restype = ip
+        L.gdn_sample.argtypes = [ctypes.POINTER(SampleDims), ctypes.POINTER(SampleParams)] + [vp] * 6
+        L.gdn_sample.restype = ip
+        L.gdn_accept.argtypes = [ctypes.POINTER(Dims)] + [vp] * 8
+        L.gdn_accept.restype = ip
+        L.gdn_accept_tree.argtypes = [ctypes.POINTER(Dims)] + [vp] * 10
+        L.gdn_accept_tree.restype = ip
         L.gdn_prefill_workspace_bytes.argtypes = [ctypes.POINTER(Dims)]
         L.gdn_prefill_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_prefill_chunked.argtypes = ([ctypes.POINTER(Dims), ctypes.POINTER(LayerParams)] + [vp] * 8 +
@@ -294,6 +333,84 @@ def gdn_layer_verify(dims: Dims, params: LayerParams, w: "ProjWeights", x, state
     _check(lib().gdn_layer_verify(ctypes.byref(dims), ctypes.byref(params), ctypes.byref(w), _ptr(x), _ptr(state),
                                   _ptr(conv_state), _ptr(cap_state), _ptr(cap_conv), _ptr(y), _ptr(workspace),
                                   int(ws_bytes), _ptr(d_status), _stream(stream)))
+
+
+def lora(n_adapters: int, rank: int, a, b, scale=None) -> Lora:
+    """The low-rank adapters beside one projection of K input and N output columns (device tensors or pointers): a
+    [n_adapters][rank][K] and b [n_adapters][N][rank] bf16, scale [n_adapters] f32 (None: 1)."""
+    v = Lora(int(n_adapters), int(rank), _ptr(a), _ptr(b), _ptr(scale))
+    v.tensors = (a, b, scale)            # the struct holds addresses: keep what they point to
+    return v
+
+
+def gdn_lora_workspace_bytes(dims: Dims, rank: int) -> int:
+    return int(lib().gdn_lora_workspace_bytes(ctypes.byref(dims), int(rank)))
+
+
+def gdn_project_in_lora(dims: Dims, w: "ProjWeights", lora: Lora, d_adapter, x, act, workspace, ws_bytes: int,
+                        d_status=None, stream=None) -> None:
+    """gdn_project_in, each slot's rows with the adapter d_adapter (device int32[B]) names beside it (-1: none)."""
+    _check(lib().gdn_project_in_lora(ctypes.byref(dims), ctypes.byref(w), ctypes.byref(lora), _ptr(d_adapter), _ptr(x),
+                                     _ptr(act), _ptr(workspace), int(ws_bytes), _ptr(d_status), _stream(stream)))
+
+
+def gdn_project_out_lora(dims: Dims, w: "ProjWeights", lora: Lora, d_adapter, out, y, workspace, ws_bytes: int,
+                         d_status=None, stream=None) -> None:
+    """gdn_project_out with adapters, as gdn_project_in_lora."""
+    _check(lib().gdn_project_out_lora(ctypes.byref(dims), ctypes.byref(w), ctypes.byref(lora), _ptr(d_adapter),
+                                      _ptr(out), _ptr(y), _ptr(workspace), int(ws_bytes), _ptr(d_status),
+                                      _stream(stream)))
+
+
+def gdn_layer_lora_workspace_bytes(dims: Dims, n_embd: int, rank: int) -> int:
+    return int(lib().gdn_layer_lora_workspace_bytes(ctypes.byref(dims), int(n_embd), int(rank)))
+
+
+def gdn_layer_verify_lora(dims: Dims, params: LayerParams, w: "ProjWeights", lora_in: Optional[Lora],
+                          lora_out: Optional[Lora], d_adapter, x, state, conv_state, cap_state, cap_conv, y, workspace,
+                          ws_bytes: int, d_status=None, stream=None) -> None:
+    """gdn_layer_verify with adapters beside its input projection, its output projection, or both."""
+    ref = lambda v: None if v is None else ctypes.byref(v)  # noqa: E731
+    _check(lib().gdn_layer_verify_lora(ctypes.byref(dims), ctypes.byref(params), ctypes.byref(w), ref(lora_in),
+                                       ref(lora_out), _ptr(d_adapter), _ptr(x), _ptr(state), _ptr(conv_state),
+                                       _ptr(cap_state), _ptr(cap_conv), _ptr(y), _ptr(workspace), int(ws_bytes),
+                                       _ptr(d_status), _stream(stream)))
+
+
+def make_sample_dims(n_slots: int, n_tokens: int, vocab: int, ld: Optional[int] = None,
+                     dtype: int = GDN_F32) -> SampleDims:
+    """Logits [n_slots * n_tokens][ld], the first vocab columns of each row used (ld None: vocab)."""
+    return SampleDims(n_slots, n_tokens, vocab, dtype, vocab if ld is None else ld)
+
+
+def sample_params(temperature=None, top_k=None, top_p=None, min_p=None) -> SampleParams:
+    """Per-slot sampling parameters: device f32[B] (top_k: int32[B]); None: temperature 1, filter off."""
+    v = SampleParams(_ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p))
+    v.tensors = (temperature, top_k, top_p, min_p)
+    return v
+
+
+def gdn_sample(dims: SampleDims, params: SampleParams, logits, u, tokens, logprob=None, d_status=None,
+               stream=None) -> None:
+    """One token per row of logits from the uniforms u [B][T]; tokens [B][T] int32, logprob [B][T] f32 or None."""
+    _check(lib().gdn_sample(ctypes.byref(dims), ctypes.byref(params), _ptr(logits), _ptr(u), _ptr(tokens),
+                            _ptr(logprob), _ptr(d_status), _stream(stream)))
+
+
+def gdn_accept(dims: Dims, draft, tokens, d_length, d_trim, d_next=None, d_emit=None, d_status=None,
+               stream=None) -> None:
+    """How much of its draft each slot keeps: d_trim [B] for the rollbacks, d_next [B], d_emit [B][T]."""
+    _check(lib().gdn_accept(ctypes.byref(dims), _ptr(draft), _ptr(tokens), _ptr(d_length), _ptr(d_trim), _ptr(d_next),
+                            _ptr(d_emit), _ptr(d_status), _stream(stream)))
+
+
+def gdn_accept_tree(dims: Dims, d_parent, draft, tokens, d_length, d_accept, d_next=None, d_emit=None, d_path=None,
+                    d_status=None, stream=None) -> None:
+    """The accepted path of each slot's draft tree: d_accept [B] for gdn_rollback_tree, d_next [B], d_emit and
+    d_path [B][T]."""
+    _check(lib().gdn_accept_tree(ctypes.byref(dims), _ptr(d_parent), _ptr(draft), _ptr(tokens), _ptr(d_length),
+                                 _ptr(d_accept), _ptr(d_next), _ptr(d_emit), _ptr(d_path), _ptr(d_status),
+                                 _stream(stream)))
 
 
 def gdn_prefill_workspace_bytes(dims: Dims) -> int:

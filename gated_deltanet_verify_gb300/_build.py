@@ -23,7 +23,7 @@ LIB = os.path.join(PKG, "libgdn_verify.so")
 CHECKED_BUILD = os.path.join(PKG, "_build_checked")
 CHECKED_LIB = os.path.join(PKG, "libgdn_verify_checked.so")
 
-SOURCES = ["gdn_api.cu", "verify.cu", "rollback.cu", "prefill.cu", "proj.cu"]
+SOURCES = ["gdn_api.cu", "verify.cu", "rollback.cu", "prefill.cu", "proj.cu", "lora.cu", "sample.cu", "accept.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

@@ -568,32 +568,63 @@ size_t gdn_layer_workspace_bytes(const gdn_dims *dims, int n_embd) {
     return align256(M * size_t(gdn_proj_in_ld(dims)) * 2) + align256(M * size_t(dims->n_v_heads) * dims->d_v * 2);
 }
 
+// checks of one projection's adapters
+static int check_lora(const gdn_lora *l, const int32_t *d_adapter) {
+    if (!l || !d_adapter) return fail(GDN_ERR_ARG, "adapters or adapter ids are NULL");
+    if (l->n_adapters < 1) return fail(GDN_ERR_SHAPE, "n_adapters must be positive (got %d)", l->n_adapters);
+    if (l->rank < 8 || l->rank > 128 || l->rank % 8)
+        return fail(GDN_ERR_SHAPE, "the adapter rank must be a multiple of 8 up to 128 (got %d)", l->rank);
+    if (!l->a || !l->b) return fail(GDN_ERR_ARG, "an adapter weight pointer is NULL");
+    if (!aligned16(l->a) || !aligned16(l->b) || !aligned16(l->scale) || !aligned16(d_adapter))
+        return fail(GDN_ERR_ALIGN, "adapter weights, scales and ids must be 16-byte aligned");
+    return GDN_OK;
+}
+
+static int check_workspace(const void *workspace, size_t ws_bytes, size_t need) {
+    if (!workspace || ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(GDN_ERR_ALIGN, "workspace must be 256-byte aligned");
+    return GDN_OK;
+}
+
+// X [M][K] -> Y [M][N] (row stride ldc) with W, and with the slots' adapters where `lora` is given
+static int project(const char *what, const gdn_dims *dims, const void *W, const void *X, void *Y, int N, int K,
+                   long long ldc, const gdn_lora *lora, const int32_t *d_adapter, void *scratch, int *d_status,
+                   void *stream) {
+    std::string why;
+    const int M = dims->n_slots * dims->n_tokens;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    bool ok;
+    if (lora) {
+        const gdn::LoraArgs a{lora->n_adapters, lora->rank, dims->n_tokens, lora->a, lora->b, lora->scale, d_adapter,
+                              static_cast<float *>(scratch)};
+        ok = gdn::gemm_xwt_lora_bf16(W, X, Y, M, N, K, ldc, a, d_status, st, why);
+    } else {
+        ok = gdn::gemm_xwt_bf16(W, X, Y, M, N, K, ldc, d_status, st, why);
+    }
+    return ok ? GDN_OK : fail(GDN_ERR_LAUNCH, "%s projection: %s", what, why.c_str());
+}
+
 static int project_in(const gdn_dims *dims, const gdn_proj_weights *w, const void *x, void *act, int *d_status,
-                      void *stream) {
+                      void *stream, const gdn_lora *lora = nullptr, const int32_t *d_adapter = nullptr,
+                      void *scratch = nullptr) {
     int rc = check_proj(dims, w);
     if (rc) return rc;
     if (!x || !act) return fail(GDN_ERR_ARG, "x or act is NULL");
     if (!aligned16(x) || !aligned16(act)) return fail(GDN_ERR_ALIGN, "x and act must be 16-byte aligned");
-    std::string why;
-    const int M = dims->n_slots * dims->n_tokens;
-    if (!gdn::gemm_xwt_bf16(w->w_in, x, act, M, int(proj_in_cols(*dims)), w->n_embd, gdn_proj_in_ld(dims), d_status,
-                            static_cast<cudaStream_t>(stream), why))
-        return fail(GDN_ERR_LAUNCH, "input projection: %s", why.c_str());
-    return GDN_OK;
+    return project("input", dims, w->w_in, x, act, int(proj_in_cols(*dims)), w->n_embd, gdn_proj_in_ld(dims), lora,
+                   d_adapter, scratch, d_status, stream);
 }
 
 static int project_out(const gdn_dims *dims, const gdn_proj_weights *w, const void *out, void *y, int *d_status,
-                       void *stream) {
+                       void *stream, const gdn_lora *lora = nullptr, const int32_t *d_adapter = nullptr,
+                       void *scratch = nullptr) {
     int rc = check_proj(dims, w);
     if (rc) return rc;
     if (!out || !y) return fail(GDN_ERR_ARG, "out or y is NULL");
     if (!aligned16(out) || !aligned16(y)) return fail(GDN_ERR_ALIGN, "out and y must be 16-byte aligned");
-    std::string why;
-    const int M = dims->n_slots * dims->n_tokens;
-    if (!gdn::gemm_xwt_bf16(w->w_out, out, y, M, w->n_embd, dims->n_v_heads * dims->d_v, w->n_embd, d_status,
-                            static_cast<cudaStream_t>(stream), why))
-        return fail(GDN_ERR_LAUNCH, "output projection: %s", why.c_str());
-    return GDN_OK;
+    return project("output", dims, w->w_out, out, y, w->n_embd, dims->n_v_heads * dims->d_v, w->n_embd, lora, d_adapter,
+                   scratch, d_status, stream);
 }
 
 int gdn_project_in(const gdn_dims *dims, const gdn_proj_weights *w, const void *x, void *act, void *workspace,
@@ -610,22 +641,18 @@ int gdn_project_out(const gdn_dims *dims, const gdn_proj_weights *w, const void 
     return project_out(dims, w, out, y, nullptr, stream);
 }
 
-int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w,
-                     const void *x, float *state, float *conv_state, float *cap_state, float *cap_conv, void *y,
-                     void *workspace, size_t ws_bytes, int *d_status, void *stream) {
-    g_err.clear();
-    int rc = check_proj(dims, w);
-    if (rc) return rc;
-    const size_t need = gdn_layer_workspace_bytes(dims, w->n_embd);
-    if (!workspace || ws_bytes < need)
-        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(GDN_ERR_ALIGN, "workspace must be 256-byte aligned");
+// the layer step in `workspace` (checked by the caller); lora_scratch: the adapters' part of it
+static int layer_impl(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w, const void *x,
+                      float *state, float *conv_state, float *cap_state, float *cap_conv, void *y, void *workspace,
+                      int *d_status, void *stream, const gdn_lora *lora_in = nullptr, const gdn_lora *lora_out = nullptr,
+                      const int32_t *d_adapter = nullptr, void *lora_scratch = nullptr) {
+    int rc;
     const gdn_dims &d = *dims;
     const size_t M = size_t(d.n_slots) * d.n_tokens;
     const long long ld = gdn_proj_in_ld(dims);
     unsigned char *act = static_cast<unsigned char *>(workspace);
     unsigned char *out = act + align256(M * size_t(ld) * 2);
-    if ((rc = project_in(dims, w, x, act, d_status, stream))) return rc;
+    if ((rc = project_in(dims, w, x, act, d_status, stream, lora_in, d_adapter, lora_scratch))) return rc;
     // the verify reads q|k|v, z, alpha and beta_raw as column blocks of the activation matrix
     const long long C = conv_channels(dims), V = (long long)d.n_v_heads * d.d_v;
     unsigned char *z = act + C * 2, *alpha = act + (C + V) * 2, *beta = alpha + size_t(d.n_v_heads) * 2;
@@ -635,7 +662,121 @@ int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const
                           d_status, stream, gdn::kChain, nullptr, nullptr, nullptr, nullptr, ld, w->w_out,
                           reinterpret_cast<uintptr_t>(w->w_out) % 16 ? 0 : w_out_bytes & ~size_t(15))))
         return rc;
-    return project_out(dims, w, out, y, d_status, stream);
+    return project_out(dims, w, out, y, d_status, stream, lora_out, d_adapter, lora_scratch);
+}
+
+int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w,
+                     const void *x, float *state, float *conv_state, float *cap_state, float *cap_conv, void *y,
+                     void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+    g_err.clear();
+    int rc = check_proj(dims, w);
+    if (rc) return rc;
+    if ((rc = check_workspace(workspace, ws_bytes, gdn_layer_workspace_bytes(dims, w->n_embd)))) return rc;
+    return layer_impl(dims, params, w, x, state, conv_state, cap_state, cap_conv, y, workspace, d_status, stream);
+}
+
+// ---- low-rank adapters beside the projections ------------------------------
+
+size_t gdn_lora_workspace_bytes(const gdn_dims *dims, int rank) {
+    if (!dims || dims->n_slots < 1 || dims->n_tokens < 1 || rank < 8 || rank > 128 || rank % 8) return 0;
+    return align256(gdn::lora_scratch_bytes((long long)dims->n_slots * dims->n_tokens, rank));
+}
+
+int gdn_project_in_lora(const gdn_dims *dims, const gdn_proj_weights *w, const gdn_lora *lora, const int32_t *d_adapter,
+                        const void *x, void *act, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+    g_err.clear();
+    int rc = check_proj(dims, w);
+    if (rc || (rc = check_lora(lora, d_adapter))) return rc;
+    if ((rc = check_workspace(workspace, ws_bytes, gdn_lora_workspace_bytes(dims, lora->rank)))) return rc;
+    return project_in(dims, w, x, act, d_status, stream, lora, d_adapter, workspace);
+}
+
+int gdn_project_out_lora(const gdn_dims *dims, const gdn_proj_weights *w, const gdn_lora *lora, const int32_t *d_adapter,
+                         const void *out, void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+    g_err.clear();
+    int rc = check_proj(dims, w);
+    if (rc || (rc = check_lora(lora, d_adapter))) return rc;
+    if ((rc = check_workspace(workspace, ws_bytes, gdn_lora_workspace_bytes(dims, lora->rank)))) return rc;
+    return project_out(dims, w, out, y, d_status, stream, lora, d_adapter, workspace);
+}
+
+size_t gdn_layer_lora_workspace_bytes(const gdn_dims *dims, int n_embd, int rank) {
+    const size_t own = gdn_lora_workspace_bytes(dims, rank), layer = gdn_layer_workspace_bytes(dims, n_embd);
+    return own && layer ? layer + own : 0;
+}
+
+int gdn_layer_verify_lora(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w,
+                          const gdn_lora *lora_in, const gdn_lora *lora_out, const int32_t *d_adapter,
+                          const void *x, float *state, float *conv_state, float *cap_state, float *cap_conv,
+                          void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+    g_err.clear();
+    int rc = check_proj(dims, w);
+    if (rc) return rc;
+    if (!lora_in && !lora_out) return fail(GDN_ERR_ARG, "both projections are without adapters");
+    if (lora_in && (rc = check_lora(lora_in, d_adapter))) return rc;
+    if (lora_out && (rc = check_lora(lora_out, d_adapter))) return rc;
+    int rank = lora_in ? lora_in->rank : 0;
+    if (lora_out && lora_out->rank > rank) rank = lora_out->rank;
+    if ((rc = check_workspace(workspace, ws_bytes, gdn_layer_lora_workspace_bytes(dims, w->n_embd, rank)))) return rc;
+    // the adapters' scratch serves the input projection, then the output projection, in stream order
+    void *scratch = static_cast<unsigned char *>(workspace) + gdn_layer_workspace_bytes(dims, w->n_embd);
+    return layer_impl(dims, params, w, x, state, conv_state, cap_state, cap_conv, y, workspace, d_status, stream, lora_in,
+                      lora_out, d_adapter, scratch);
+}
+
+// ---- sampling and acceptance ------------------------------------------------
+
+int gdn_sample(const gdn_sample_dims *dims, const gdn_sample_params *params, const void *logits, const float *u,
+               int32_t *tokens, float *logprob, int *d_status, void *stream) {
+    g_err.clear();
+    if (!dims || !params) return fail(GDN_ERR_ARG, "dims or params is NULL");
+    const gdn_sample_dims &d = *dims;
+    if (d.n_slots < 1 || d.n_tokens < 1 || (long long)d.n_slots * d.n_tokens > (1LL << 27))
+        return fail(GDN_ERR_SHAPE, "slots x tokens must be in [1, 2^27] (got %d x %d)", d.n_slots, d.n_tokens);
+    if (d.vocab < 1 || d.vocab > 524288 || d.ld < d.vocab)
+        return fail(GDN_ERR_SHAPE, "vocab must be in [1, 524288] and ld at least vocab (got %d, %lld)", d.vocab, d.ld);
+    if (d.dtype != GDN_F32 && d.dtype != GDN_BF16)
+        return fail(GDN_ERR_DTYPE, "dtype %d is neither GDN_F32 nor GDN_BF16", int(d.dtype));
+    if (!logits || !u || !tokens) return fail(GDN_ERR_ARG, "logits, u or tokens is NULL");
+    const void *ptrs[] = {params->temperature, params->top_k, params->top_p, params->min_p, logits, u, tokens, logprob};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return fail(GDN_ERR_ALIGN, "buffer %p is not 16-byte aligned", p);
+    const gdn::SampleArgs a{d.n_slots, d.n_tokens, d.vocab, d.ld, logits, u, params->temperature, params->top_p,
+                            params->min_p, params->top_k, tokens, logprob, d_status};
+    const cudaError_t e = gdn::launch_sample(a, d.dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "sample launch failed: %s", cudaGetErrorString(e));
+    return GDN_OK;
+}
+
+static int accept_impl(const gdn_dims *dims, const int32_t *d_parent, const int32_t *draft, const int32_t *tokens,
+                       const int32_t *d_length, int32_t *d_place, int32_t *d_next, int32_t *d_emit, int32_t *d_path,
+                       int *d_status, void *stream) {
+    int rc = check_common(dims);
+    if (rc) return rc;
+    if (dims->n_tokens > 64) return fail(GDN_ERR_SHAPE, "n_tokens must be <= 64 (got %d)", dims->n_tokens);
+    if (!draft || !tokens || !d_place) return fail(GDN_ERR_ARG, "draft, tokens or the result is NULL");
+    const void *ptrs[] = {d_parent, draft, tokens, d_length, d_place, d_next, d_emit, d_path};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return fail(GDN_ERR_ALIGN, "buffer %p is not 16-byte aligned", p);
+    const gdn::AcceptArgs a{dims->n_slots, dims->n_tokens, d_parent, draft, tokens, d_length, d_place, d_next, d_emit,
+                            d_path, d_status};
+    const cudaError_t e = gdn::launch_accept(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "accept launch failed: %s", cudaGetErrorString(e));
+    return GDN_OK;
+}
+
+int gdn_accept(const gdn_dims *dims, const int32_t *draft, const int32_t *tokens, const int32_t *d_length,
+               int32_t *d_trim, int32_t *d_next, int32_t *d_emit, int *d_status, void *stream) {
+    g_err.clear();
+    return accept_impl(dims, nullptr, draft, tokens, d_length, d_trim, d_next, d_emit, nullptr, d_status, stream);
+}
+
+int gdn_accept_tree(const gdn_dims *dims, const int32_t *d_parent, const int32_t *draft, const int32_t *tokens,
+                    const int32_t *d_length, int32_t *d_accept, int32_t *d_next, int32_t *d_emit, int32_t *d_path,
+                    int *d_status, void *stream) {
+    g_err.clear();
+    if (!d_parent) return fail(GDN_ERR_ARG, "parent ids are NULL");
+    return accept_impl(dims, d_parent, draft, tokens, d_length, d_accept, d_next, d_emit, d_path, d_status, stream);
 }
 
 }  // extern "C"

@@ -66,6 +66,16 @@ struct GemmArgs {
     int *d_status;
 };
 
+// A low-rank term beside the product, by the slot (T rows of X) a row belongs to: row m gets
+// h[m][0 .. r) . B[adapter[m / T]][n][0 .. r) more, added to the fp32 sum before its one rounding.
+struct LoraTerm {
+    const __nv_bfloat16 *B;             // [n_adapters][N][r]
+    const float *h;                     // [M][r], the adapter's scale in it
+    const int32_t *adapter;             // [slots]; outside [0, n_adapters): no term
+    int n_adapters, r, T;
+};
+struct NoTerm {};
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
@@ -164,7 +174,26 @@ __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence
 __host__ __device__ constexpr uint32_t w_stage_bytes() { return kTileN * kKBlk * 2; }
 __host__ __device__ inline uint32_t x_stage_bytes(int Mt) { return (uint32_t)Mt * kKBlk * 2; }
 
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a) {
+// v[q] += the low-rank term of rows m .. m + 15 at column n
+__device__ __forceinline__ void add_term(const LoraTerm &t, int m, int M, int n, int N, float *v) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");      // h, by the kernel before
+    if (n >= N) return;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        if (m + q >= M) break;
+        const int id = t.adapter[(m + q) / t.T];
+        if (id < 0 || id >= t.n_adapters) continue;
+        const __nv_bfloat16 *b = t.B + ((size_t)id * N + n) * t.r;
+        const float *h = t.h + (size_t)(m + q) * t.r;
+        float acc = 0.f;
+        for (int j = 0; j < t.r; ++j) acc = fmaf(h[j], __bfloat162float(b[j]), acc);
+        v[q] += acc;
+    }
+}
+__device__ __forceinline__ void add_term(const NoTerm &, int, int, int, int, float *) {}
+
+template <typename Term>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a, const Term term) {
     extern __shared__ __align__(1024) unsigned char sm[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];   // full[stages], empty[stages], done (2 arrivals)
     __shared__ uint32_t tslot;
@@ -264,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int c0 = 0; c0 < a.Mt; c0 += 16) {
                 float v[16];
                 tmem_ld16_sum(taddr + c0, n_acc, a.Mt, v);
+                add_term(term, m0 + c0, a.M, n, a.N, v);
                 if (n < a.N)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
@@ -289,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int c0 = 0; c0 < a.Mt; c0 += 16) {
                 float v[16];
                 tmem_ld16_sum(taddr + c0, n_acc, a.Mt, v);
+                add_term(term, m0 + c0, a.M, n, a.N, v);
                 if (n < a.N)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
@@ -317,8 +348,9 @@ static int gemm_splits(int n_tiles, int m_blocks, int n_kb, int Mt, size_t smem,
     return splits < 1 ? 1 : splits;
 }
 
-bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, int *d_status,
-                   cudaStream_t stream, std::string &why) {
+template <typename Term>
+static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, const Term &term,
+                        int *d_status, cudaStream_t stream, std::string &why) {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) {
         why = "the driver's tensor-map encoder is unavailable";
@@ -380,7 +412,7 @@ bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, l
             return false;
         }
     }
-    cudaError_t e = cudaFuncSetAttribute(gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(gemm_kernel<Term>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n_tiles, m_blocks, a.splits);
@@ -396,13 +428,29 @@ bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, l
         attr[1].val.clusterDim.z = a.splits;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, gemm_kernel, a);
+        e = cudaLaunchKernelEx(&cfg, gemm_kernel<Term>, a, term);
     }
     if (e != cudaSuccess) {
         why = std::string("projection GEMM launch: ") + cudaGetErrorString(e);
         return false;
     }
     return true;
+}
+
+bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, int *d_status,
+                   cudaStream_t stream, std::string &why) {
+    return gemm_launch(W, X, C, M, N, K, ldc, NoTerm{}, d_status, stream, why);
+}
+
+bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, const LoraArgs &lora,
+                        int *d_status, cudaStream_t stream, std::string &why) {
+    const cudaError_t e = launch_lora_shrink(X, M, K, lora, d_status, stream);
+    if (e != cudaSuccess) {
+        why = std::string("adapter launch: ") + cudaGetErrorString(e);
+        return false;
+    }
+    const LoraTerm term{static_cast<const __nv_bfloat16 *>(lora.b), lora.h, lora.adapter, lora.n_adapters, lora.rank, lora.T};
+    return gemm_launch(W, X, C, M, N, K, ldc, term, d_status, stream, why);
 }
 
 }  // namespace gdn

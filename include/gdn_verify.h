@@ -74,7 +74,10 @@ typedef enum {
     GDN_ERR_TIMEOUT = 8,     /* (device) a bounded wait gave up */
     GDN_ERR_WORKSPACE = 9,   /* workspace missing or smaller than the query returned */
     GDN_ERR_TREE = 10,       /* (device) a parent id is outside [-1, t-1]; that token ran from the root */
-    GDN_ERR_BOUNDS = 11      /* (device, checked builds only) an access fell outside its buffer and was skipped */
+    GDN_ERR_BOUNDS = 11,     /* (device, checked builds only) an access fell outside its buffer and was skipped */
+    GDN_ERR_SAMPLE = 12,     /* (device) a row that cannot be sampled (see gdn_sample); its token is -1 */
+    GDN_ERR_LENGTH = 13,     /* (device) a slot's draft length is out of range; nothing of it is accepted */
+    GDN_ERR_ADAPTER = 14     /* (device) an adapter id names none; the slot ran without one */
 } gdn_status;
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -321,6 +324,141 @@ int gdn_project_out(const gdn_dims *dims, const gdn_proj_weights *w, const void 
 int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w,
                      const void *x, float *state, float *conv_state, float *cap_state, float *cap_conv,
                      void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream);
+
+/*
+ * Low-rank adapters beside the shared projections: every slot of a batch may
+ * run with an adapter of its own.  For row m of slot s, with a = d_adapter[s],
+ *   act[m] = w_in x[m] + scale[a] * B[a] (A[a] x[m])
+ * (and the same for the output projection), in fp32 and rounded to bf16 once;
+ * A[a] x is held in fp32 too.  d_adapter is a DEVICE int32[n_slots]: -1 runs
+ * the slot without an adapter (its rows are then bit-identical to
+ * gdn_project_in / gdn_project_out); another id outside [0, n_adapters) does
+ * the same and writes GDN_ERR_ADAPTER to *d_status.  Several slots may name the
+ * same adapter.  Adapters of a lower rank are padded with zero rows of A and
+ * zero columns of B.  The pages have no adapters; the projections they stand
+ * beside are those of internal.h, TargetLayer.
+ *
+ * Limits: those of gdn_project_in; rank a multiple of 8, 8..128 (GDN_ERR_SHAPE).
+ * workspace: gdn_lora_workspace_bytes (0 on bad arguments), 256-byte aligned;
+ * it needs no initialisation, and calls that share it must be ordered.
+ */
+typedef struct {
+    int n_adapters;        /* >= 1 */
+    int rank;
+    const void *a;         /* [n_adapters][rank][K] bf16, K: the projection's input columns */
+    const void *b;         /* [n_adapters][N][rank] bf16, N: its output columns */
+    const float *scale;    /* [n_adapters] f32, or NULL: 1 */
+} gdn_lora;
+
+size_t gdn_lora_workspace_bytes(const gdn_dims *dims, int rank);
+
+/* gdn_project_in with adapters: K = n_embd, N = C + H_v*d_v + 2*H_v. */
+int gdn_project_in_lora(const gdn_dims *dims, const gdn_proj_weights *w, const gdn_lora *lora, const int32_t *d_adapter,
+                        const void *x, void *act, void *workspace, size_t ws_bytes, int *d_status, void *stream);
+
+/* gdn_project_out with adapters: K = H_v*d_v, N = n_embd. */
+int gdn_project_out_lora(const gdn_dims *dims, const gdn_proj_weights *w, const gdn_lora *lora, const int32_t *d_adapter,
+                         const void *out, void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream);
+
+/*
+ * gdn_layer_verify with adapters beside its input projection (lora_in), its
+ * output projection (lora_out) or both (either may be NULL, not both); the same
+ * d_adapter for the two.  workspace: gdn_layer_lora_workspace_bytes with the
+ * larger of the two ranks, 256-byte aligned; the activation matrix and the
+ * block's output sit where gdn_layer_verify puts them.
+ */
+size_t gdn_layer_lora_workspace_bytes(const gdn_dims *dims, int n_embd, int rank);
+int gdn_layer_verify_lora(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w,
+                          const gdn_lora *lora_in, const gdn_lora *lora_out, const int32_t *d_adapter,
+                          const void *x, float *state, float *conv_state, float *cap_state, float *cap_conv,
+                          void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream);
+
+/*
+ * Sampling the positions of a verify step: one token per row of logits, from
+ * uniforms that the caller gives (the target side's decision, which hf2q
+ * qwen35_target.rs, forward_decode_verify_batched, takes as a host argmax over
+ * the vocabulary).  Row (s, t) has the logits l[0 .. vocab); with T the slot's
+ * temperature, x_i = (l_i - max l) / T and w_i = exp(x_i):
+ *   - tokens are ordered by logit, highest first, the lower index first among
+ *     equals; a logit that is -inf or NaN is masked: its token is never drawn;
+ *   - top_k > 0 keeps the first top_k tokens of that order; top_p < 1 keeps, of
+ *     those, the shortest prefix whose mass is at least top_p of theirs;
+ *     min_p > 0 keeps tokens with w_i >= min_p (the top token has w = 1);
+ *   - the row's token is the smallest i with sum_{j <= i, kept} w_j > u * sum_{kept} w_j;
+ *     logprob (optional) is ln(w_token / sum_{kept} w_j).
+ * temperature 0 takes the top token (logprob 0).  The sums are exact (64-bit
+ * integers in units of 2^-44 of the top weight), so the result does not depend
+ * on the launch shape and a repeated call gives the same tokens; of +inf logits
+ * all are equally likely.
+ *
+ * The parameters are DEVICE arrays per slot (NULL: temperature 1, filters off).
+ * A row gets token -1 and logprob -inf, and GDN_ERR_SAMPLE goes to *d_status,
+ * if all its tokens are masked, its u is outside [0, 1), or its slot's
+ * parameters are outside: temperature 0 or 2^-20 .. 2^20, top_p > 0, min_p <= 1
+ * (top_k <= 0 and min_p <= 0 are off; NaN is outside).
+ *
+ * logits [B*T][ld] f32 or bf16 (columns past vocab are not used), u, tokens and
+ * logprob [B][T].  Limits: 1 <= vocab <= 524288, vocab <= ld, B*T <= 2^27.  No workspace.
+ */
+typedef struct {
+    int n_slots;           /* B */
+    int n_tokens;          /* T: positions per slot, which share its parameters */
+    int vocab;
+    gdn_dtype dtype;       /* of the logits */
+    long long ld;          /* row stride of the logits, in elements */
+} gdn_sample_dims;
+
+typedef struct {
+    const float *temperature;   /* [B] */
+    const int32_t *top_k;       /* [B] */
+    const float *top_p;         /* [B] */
+    const float *min_p;         /* [B] */
+} gdn_sample_params;
+
+int gdn_sample(const gdn_sample_dims *dims, const gdn_sample_params *params, const void *logits, const float *u,
+               int32_t *tokens, float *logprob, int *d_status, void *stream);
+
+/*
+ * How much of its draft each slot keeps (what a rollback then takes; hf2q
+ * qwen35_target.rs, rollback_kv: accepted_idx = n_tokens_max - 1 - trim).
+ * draft [B][T] are the T input tokens of the verify: the last committed token,
+ * then the guesses; tokens [B][T] what the target sampled after each input
+ * (gdn_sample).  With n the number of leading t with draft[t+1] == tokens[t]
+ * (t + 1 < length), the slot keeps inputs 0 .. n:
+ *   d_trim[s] = T-1-n, for gdn_rollback, gdn_rollback_layers,
+ *               gdn_verify_after_rollback, gdn_verify_lazy and gdn_commit_lazy;
+ *   d_next[s] = tokens[n], the next step's first input;
+ *   d_emit[s] = tokens[0 .. n], then -1: the step's output tokens.
+ * Every emitted token is the target's own sample, so the output follows the
+ * target's distribution whatever drafted it.  d_length (optional, DEVICE
+ * int32[B]): inputs of the slot that are real, 1 .. T (the others are padding);
+ * outside that the slot gets trim -1 and next -1, emits nothing, and writes
+ * GDN_ERR_LENGTH to *d_status (a rollback then leaves the slot untouched and
+ * reports it).  A negative token matches nothing.  Only n_slots and n_tokens of
+ * dims are used beyond the checks every call makes; T <= 64.  d_next and d_emit
+ * may be NULL.
+ */
+int gdn_accept(const gdn_dims *dims, const int32_t *draft, const int32_t *tokens, const int32_t *d_length,
+               int32_t *d_trim, int32_t *d_next, int32_t *d_emit, int *d_status, void *stream);
+
+/*
+ * The same for a draft tree (gdn_verify_tree's d_parent).  Node 0 is the last
+ * committed token (its parent is -1; further roots are never reached).  From
+ * node 0 the slot moves to the lowest child whose draft token is the one
+ * sampled at the node, until there is none:
+ *   d_accept[s] the last node reached, for gdn_rollback_tree(_layers);
+ *   d_next[s]   the token sampled there;
+ *   d_emit[s]   the tokens sampled along the path, then -1;
+ *   d_path[s]   the path's nodes, then -1 (the rows a caller keeps of its own
+ *               per-node caches).
+ * d_length: real nodes, 0 .. T; a slot of length 0 accepts nothing (accept -1,
+ * a no-op for the rollback).  A parent id that is not in [-1, t-1] (for node 0:
+ * not -1) writes GDN_ERR_TREE and its node is never reached.  d_next, d_emit and
+ * d_path may be NULL.
+ */
+int gdn_accept_tree(const gdn_dims *dims, const int32_t *d_parent, const int32_t *draft, const int32_t *tokens,
+                    const int32_t *d_length, int32_t *d_accept, int32_t *d_next, int32_t *d_emit, int32_t *d_path,
+                    int *d_status, void *stream);
 
 /*
  * One verify step from host memory: the inputs of the step arrive as one
