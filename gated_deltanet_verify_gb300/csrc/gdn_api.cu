@@ -743,7 +743,7 @@ int gdn_sample(const gdn_sample_dims *dims, const gdn_sample_params *params, con
         if (!aligned16(p)) return fail(GDN_ERR_ALIGN, "buffer %p is not 16-byte aligned", p);
     const gdn::SampleArgs a{d.n_slots, d.n_tokens, d.vocab, d.ld, logits, u, params->temperature, params->top_p,
                             params->min_p, params->top_k, tokens, logprob, d_status};
-    const cudaError_t e = gdn::launch_sample(a, d.dtype, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = gdn::launch_sample(a, d.dtype, dev_info().sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "sample launch failed: %s", cudaGetErrorString(e));
     return GDN_OK;
 }

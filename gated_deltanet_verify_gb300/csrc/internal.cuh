@@ -125,7 +125,7 @@ struct LoraArgs {
 };
 
 // Returns a cudaError_t of the launch (cudaSuccess when enqueued).
-cudaError_t launch_sample(const SampleArgs &a, gdn_dtype dtype, cudaStream_t stream);
+cudaError_t launch_sample(const SampleArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptArgs &a, cudaStream_t stream);
 // h = scale * X A^T per slot; reports an adapter id that names none.
 cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &lora, int *d_status, cudaStream_t stream);
