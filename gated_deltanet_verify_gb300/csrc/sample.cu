@@ -64,6 +64,7 @@ struct Shared {
     u64 red[kWarps];
     u64 warp_sum[kWarps];
     u64 word[4];                         // broadcast within the cluster (bc) or the CTA
+    double t_log_min_p;
     uint32_t cell_count[kCells];
     uint32_t hist[kBins];                // this CTA's counts
     uint32_t count[kBins];               // the cluster's, then summed up to and with each bin
@@ -149,7 +150,8 @@ struct Sampler {
     int I;
 
     __device__ __forceinline__ bool kept(uint32_t key, int i) const { return key > K || (key == K && i <= I); }
-    __device__ __forceinline__ u64 weigh(float l) const { return weight(l, top, sc, s.table); }
+    __device__ __forceinline__ Weight weigh(float l) const { return weight(l, top, sc, s.table); }
+    __device__ __forceinline__ u64 units(float l) const { return weigh(l).units(); }
     // monotone in l; 0 for the top logit (inf - inf gives NaN, which converts to 0)
     __device__ __forceinline__ int bin(float l) const {
         const int b = __float2int_rz((top - l) * bin_scale);
@@ -198,11 +200,25 @@ struct Sampler {
         sync_cluster();
         return s.xch[round];
     }
-    // one value of every CTA, summed: the same in all threads of the cluster
+    // the same of one sum or maximum (0 is neutral to op) over each CTA: by rank in s.xch[round][rank][0]
+    template <typename Op> __device__ __forceinline__ const u64 (*exchange_of(u64 v, Op op))[kExchange] {
+        v = warp_all(v, op);
+        __syncthreads();
+        if (lane == 0) s.red[wid] = v;
+        __syncthreads();
+        round ^= 1;
+        if (tid < n_cta) {
+            v = s.red[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) v = op(v, s.red[w]);
+            st_cluster64(map_cluster(&s.xch[round][rank][0], tid), v);
+        }
+        sync_cluster();
+        return s.xch[round];
+    }
+    // one value of every thread, summed over the cluster: the same in all its threads
     __device__ __forceinline__ u64 cluster_sum(u64 v) {
-        v = block_first(v, [](u64 a, u64 b) { return a + b; });
-        if (tid == 0) s.out[0] = v;
-        const auto x = exchange(1);
+        const auto x = exchange_of(v, [](u64 a, u64 b) { return a + b; });
         u64 t = 0;
         for (int r = 0; r < n_cta; ++r) t += x[r][0];
         return t;
@@ -318,61 +334,70 @@ struct Sampler {
 
     // K and I where the stat of the kept tokens, of bin b from `before` on, reaches target
     template <typename S> __device__ __forceinline__ void resolve(int b, u64 before, u64 target, S stat) {
-        // cells over the keys of the bin, its edges widened by their own rounding; keys beyond fall into the end cells
-        const float hi_l = fminf(top - b / bin_scale, 3.4028234e38f), lo_l = fmaxf(top - (b + 1) / bin_scale, -3.4028234e38f);
-        const uint32_t hi = key_of(hi_l + 0.0f) + 512, lo = b == kBins - 1 ? kNone : key_of(lo_l + 0.0f) - 512;
-        const int shift = max(0, 24 - __clz(max(1u, hi - lo)));
+        // a bin of few tokens goes to the list whole; else cells over its keys, its edges widened by their own rounding,
+        // keys beyond in the end cells
+        uint32_t n = s.count[b] - (b ? s.count[b - 1] : 0), lo = 0;
+        int shift = 32, at = kCells - 1;              // one cell
         auto cell = [&](uint32_t key) {
-            const uint32_t c = key < lo ? 0u : min((key - lo) >> shift, uint32_t(kCells - 1));
+            const uint32_t c = key < lo || shift > 31 ? 0u : min((key - lo) >> shift, uint32_t(kCells - 1));
             return kCells - 1 - int(c);
         };
-        for (int i = tid; i < kCells; i += kThreads) s.cell_stat[i] = s.cell_count[i] = 0;
         if (tid == 0) s.n_list = 0;
-        sync_cluster();
-        const uint32_t stat_at = map_cluster(s.cell_stat, 0), count_at = map_cluster(s.cell_count, 0);
-        each([&](float l, int i) {
-            if (!(l > -INFINITY) || bin(l) != b) return;
-            const uint32_t key = key_of(l);
-            if (!kept(key, i)) return;
-            const int c = cell(key);
-            add_cluster64(stat_at + c * 8, stat(l));
-            add_cluster32(count_at + c * 4, 1);
-        });
-        sync_cluster();
-        if (rank == 0 && wid == 0) {
-            u64 c[kCells / 32], t = 0;
+        if (n > kList) {
+            const float hi_l = fminf(top - b / bin_scale, 3.4028234e38f), lo_l = fmaxf(top - (b + 1) / bin_scale, -3.4028234e38f);
+            const uint32_t hi = key_of(hi_l + 0.0f) + 512;
+            lo = b == kBins - 1 ? kNone : key_of(lo_l + 0.0f) - 512;
+            shift = max(0, 24 - __clz(max(1u, hi - lo)));
+            for (int i = tid; i < kCells; i += kThreads) s.cell_stat[i] = s.cell_count[i] = 0;
+            sync_cluster();
+            const uint32_t stat_at = map_cluster(s.cell_stat, 0), count_at = map_cluster(s.cell_count, 0);
+            each([&](float l, int i) {
+                if (!(l > -INFINITY) || bin(l) != b) return;
+                const uint32_t key = key_of(l);
+                if (!kept(key, i)) return;
+                const int c = cell(key);
+                add_cluster64(stat_at + c * 8, stat(l));
+                add_cluster32(count_at + c * 4, 1);
+            });
+            sync_cluster();
+            if (rank == 0 && wid == 0) {
+                u64 c[kCells / 32], t = 0;
 #pragma unroll
-            for (int j = 0; j < kCells / 32; ++j) t += c[j] = s.cell_stat[lane * (kCells / 32) + j];
-            u64 run = t;
+                for (int j = 0; j < kCells / 32; ++j) t += c[j] = s.cell_stat[lane * (kCells / 32) + j];
+                u64 run = t;
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const u64 o = __shfl_up_sync(kFull, run, m);
-                if (lane >= m) run += o;
-            }
-            run += before - t;
-#pragma unroll
-            for (int j = 0; j < kCells / 32; ++j) {
-                if (run < target && target <= run + c[j]) {
-                    const int at = lane * (kCells / 32) + j;
-                    const u64 head = (u64(at) << 32) | s.cell_count[at];
-                    for (int r = 0; r < n_cta; ++r) {
-                        st_cluster64(map_cluster(&s.word[0], r), head);
-                        st_cluster64(map_cluster(&s.word[1], r), run);
-                    }
+                for (int m = 1; m < 32; m <<= 1) {
+                    const u64 o = __shfl_up_sync(kFull, run, m);
+                    if (lane >= m) run += o;
                 }
-                run += c[j];
+                run += before - t;
+#pragma unroll
+                for (int j = 0; j < kCells / 32; ++j) {
+                    if (run < target && target <= run + c[j]) {
+                        const int to = lane * (kCells / 32) + j;
+                        const u64 head = (u64(to) << 32) | s.cell_count[to];
+                        for (int r = 0; r < n_cta; ++r) {
+                            st_cluster64(map_cluster(&s.word[0], r), head);
+                            st_cluster64(map_cluster(&s.word[1], r), run);
+                        }
+                    }
+                    run += c[j];
+                }
             }
+            sync_cluster();
+            at = int(s.word[0] >> 32);
+            n = uint32_t(s.word[0]);
+            before = s.word[1];
+        } else {
+            sync_cluster();
         }
-        sync_cluster();
-        const int at = int(s.word[0] >> 32);
-        const uint32_t n = uint32_t(s.word[0]);
-        before = s.word[1];
         auto here = [&](float l, uint32_t key, int i) {
             return l > -INFINITY && bin(l) == b && cell(key) == at && kept(key, i);
         };
         if (n <= kList) {
             gather(here, stat);
             sync_cluster();
+            n = s.n_list;                             // without the tokens of the bin that top-k left out
             if (rank == 0 && tid < int(n)) {
                 const Item me = s.list[tid];
                 u64 run = before;
@@ -500,7 +525,7 @@ struct Sampler {
 };
 
 template <typename L>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
     constexpr int E = Vec<L>::N;
@@ -533,6 +558,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
     const int k = a.top_k ? a.top_k[slot] : 0;
     const float p = a.top_p ? a.top_p[slot] : 1.0f, mp = a.min_p ? a.min_p[slot] : 0.0f;
     const bool fine = sample_params_ok(temp, p, mp) && u >= 0.0f && u < 1.0f;
+    if (tid == 0 && mp > 0.0f) s.t_log_min_p = double(temp) * log(double(mp));       // while the copies are in flight
     asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;\n" ::: "memory");
 
     // 1. the top logit; each thread cleans the vectors that it copied itself
@@ -558,12 +584,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
         x.data[v] = Vec<L>::put(l);
     }
     auto most = [](u64 p, u64 q) { return p > q ? p : q; };
-    u64 first = x.block_first((u64(key_of(best)) << 32) | uint32_t(~best_i), most);
-    if (tid == 0) s.out[0] = first;
+    u64 first = (u64(key_of(best)) << 32) | uint32_t(~best_i);
     __syncwarp();
     if (n_cta > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
     {
-        const auto got = x.exchange(1);
+        const auto got = x.exchange_of(first, most);
         first = 0;
         for (int r = 0; r < n_cta; ++r) first = most(first, got[r][0]);
     }
@@ -585,7 +610,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
     x.bin_scale = 16.0f * x.sc.hi;
     x.K = kNone + 1;
     x.I = V;
-    const uint32_t k_min_p = mp > 0.0f ? min_p_key(mp, temp, x.top) : 0u;
+    const uint32_t k_min_p = mp > 0.0f ? min_p_key(s.t_log_min_p, x.top) : 0u;
     bool by_k = k > 0 && k < V;
     const bool by_p = p < 1.0f;
     u64 all_mass = 0;                      // of what top-k left, where top-p needs it
@@ -606,17 +631,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
             for (;;) {
                 for (int i = tid; i < kWindow; i += kThreads) s.win[i] = 0;
                 __syncthreads();
-                u64 m_all = 0, m_before = 0;
+                Weight m_all{0, 0}, m_before{0, 0};
                 x.each([&](float l, int i) {
                     if (!x.kept(key_of(l), i)) return;
-                    const u64 w = x.weigh(l);
+                    const Weight w = x.weigh(l);
                     const int b = x.bin(l) - b0;
                     m_all += w;
                     if (b < 0) m_before += w;
-                    else if (b < kWindow && w) atomicAdd(&s.win[b], w);
+                    else if (b < kWindow) atomicAdd(&s.win[b], w.units());
                 });
                 auto add = [](u64 p, u64 q) { return p + q; };
-                const u64 b_all = x.block_first(m_all, add), b_before = x.block_first(m_before, add);
+                const u64 b_all = x.block_first(m_all.units(), add), b_before = x.block_first(m_before.units(), add);
                 if (tid == 0) {
                     s.out[0] = b_all;
                     s.out[1] = b_before;
@@ -649,14 +674,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
                     if (!by_k && s.count[b] <= kList) {
                         list_to = b;
                     } else {
-                        x.resolve(b, before, target, [&](float l) { return x.weigh(l); });
+                        x.resolve(b, before, target, [&](float l) { return x.units(l); });
                         know_mass = true;
                         // the kept tokens of this CTA in the bin itself
-                        u64 m = 0;
+                        Weight in_bin{0, 0};
                         x.each([&](float l, int i) {
-                            if (l > -INFINITY && x.bin(l) == b && x.kept(key_of(l), i)) m += x.weigh(l);
+                            if (l > -INFINITY && x.bin(l) == b && x.kept(key_of(l), i)) in_bin += x.weigh(l);
                         });
-                        m = x.block_first(m, add);
+                        const u64 m = x.block_first(in_bin.units(), add);
                         if (tid == 0) s.word[3] = my_mass + m;
                     }
                     break;
@@ -672,7 +697,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
         if (tid == 0) s.n_list = 0;
         x.sync_cluster();
         x.gather([&](float l, uint32_t, int) { return l > -INFINITY && x.bin(l) <= list_to; },
-                 [&](float l) { return x.weigh(l); });
+                 [&](float l) { return x.units(l); });
         x.sync_cluster();
         if (x.rank != 0) return;
         const int n = s.n_list;
@@ -724,11 +749,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleArgs a, in
         x.I = V;
         know_mass = false;
     }
-    auto stat = [&](float l, int i) -> u64 { return x.kept(key_of(l), i) ? x.weigh(l) : 0; };
+    auto stat = [&](float l, int i) -> u64 { return x.kept(key_of(l), i) ? x.units(l) : 0; };
     auto sums = [&]() {
-        u64 m = 0;
-        x.each([&](float l, int i) { m += stat(l, i); });
-        x.warp_sums(m);
+        Weight m{0, 0};
+        x.each([&](float l, int i) {
+            if (x.kept(key_of(l), i)) m += x.weigh(l);
+        });
+        x.warp_sums(m.units());
     };
     if (!know_mass) {
         sums();

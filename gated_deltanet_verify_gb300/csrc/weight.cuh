@@ -11,8 +11,9 @@
 // fp32 would lose the small differences (its 2^-24 times a vocabulary of
 // borders is a wrong token every few dozen rows) and fp64 runs at 1/64 of the
 // fp32 rate here, so the products carry their rounding errors in a second fp32
-// (Dekker's and Knuth's error-free sums and products): about 35 fp32 and integer
-// instructions per weight, its error below 2^-44.
+// (Dekker's and Knuth's error-free sums and products): about 50 fp32 and integer
+// instructions per weight, its error below 2^-44.  fp64 is kept out of what every
+// thread does: one fp64 logarithm in all threads of a CTA costs microseconds.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,9 +41,8 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// 2^(j/1024): x, y = low and high word of the integer nearest to it times 2^46, z, w = its fp32 head and tail
+// 2^(j/1024) as an fp32 head and tail
 struct WeightRow {
-    uint32_t lo, hi;
     float head, tail;
 };
 
@@ -60,9 +60,8 @@ constexpr WeightRows make_weight_rows() {
             term *= x / n;
             v += term;
         }
-        const uint64_t i = uint64_t(v * 70368744177664.0 + 0.5);       // 2^46
         const float h = float(v);
-        t.r[j] = {uint32_t(i), uint32_t(i >> 32), h, float(v - double(h))};
+        t.r[j] = {h, float(v - double(h))};
     }
     return t;
 }
@@ -70,76 +69,86 @@ constexpr WeightRows make_weight_rows() {
 __device__ constexpr WeightRows kWeightRows = make_weight_rows();
 
 struct __align__(16) WeightTable {
-    uint4 r[1024];
+    float2 r[1024];
     // by all threads of a block; a barrier follows before the first use
     __device__ __forceinline__ void fill(int tid, int n) {
-        for (int i = tid; i < 1024; i += n) r[i] = reinterpret_cast<const uint4 *>(kWeightRows.r)[i];
+        for (int i = tid; i < 512; i += n)
+            reinterpret_cast<uint4 *>(r)[i] = reinterpret_cast<const uint4 *>(kWeightRows.r)[i];
     }
 };
 
-// log2(e) / T as an fp32 head and tail
+// log2(e) / T as an fp32 head and tail: the quotient, and the rest of the division over T
 struct Scale {
     float hi, lo;
 };
 __device__ __forceinline__ Scale scale_of(float temp) {
-    const double c = 1.4426950408889634074 / double(temp);
-    const float h = float(c);
-    return {h, float(c - double(h))};
+    constexpr float L = 1.44269502162933349609375f, Ll = 1.92596303350001e-8f;      // log2(e) = L + Ll
+    const float h = __fdiv_rn(L, temp);
+    return {h, __fdiv_rn(fmaf(-h, temp, L) + Ll, temp)};
 }
 
-__device__ __forceinline__ unsigned long long weight(float l, float top, Scale c, const WeightTable &tab) {
-    if (l == top) return 1ull << 44;
+// hi * 2^22 + lo units of 2^-44, lo signed: up to 256 of them add up word by word
+struct Weight {
+    int hi, lo;
+    __device__ __forceinline__ Weight &operator+=(const Weight &o) {
+        hi += o.hi;
+        lo += o.lo;
+        return *this;
+    }
+    __device__ __forceinline__ unsigned long long units() const {
+        return (unsigned long long)((long long)hi * 4194304 + lo);
+    }
+};
+
+__device__ __forceinline__ Weight weight(float l, float top, Scale c, const WeightTable &tab) {
     // l - top = s + e exactly
     const float s = l - top, b = s - l, e = (l - (s - b)) - (top + b);
     const float y = s * c.hi;
-    if (!(y > -45.5f)) return 0;                             // below half a unit
     const float ye = fmaf(e, c.hi, fmaf(s, c.lo, fmaf(s, c.hi, -y)));
     // y = q + g, q a multiple of 1/1024 (1.5 * 2^13 has a last place of 2^-10); then g + ye as gh + gl
     const float t = y + 12288.0f, g = y - (t - 12288.0f);
-    const int m = __float_as_int(t) - __float_as_int(12288.0f);
+    const int m = __float_as_int(t);               // 1024 y in its low bits: those of 12288 end in 22 zeros
     const float gh = g + ye, gl = (g - gh) + ye;
     constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
     const float a = gh * L, ae = fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -a)));
-    const float tail = fmaf(a * a, fmaf(a, 0.16666667f, 0.5f), ae);
-    const uint4 r = tab.r[m & 1023];
-    const float th = __uint_as_float(r.z), tl = __uint_as_float(r.w);
-    // th (1 + a + tail) - th = p + q
-    const float p = th * a, q = fmaf(th, tail, fmaf(tl, a, fmaf(th, a, -p)));
-    // p (below 2^-10) in units of 2^-32, the rest (below 2^-22) in units of 2^-44: the last places of 1.5 * 2^-9
-    // and 1.5 * 2^-21
-    constexpr float M1 = 0x1.8p-9f, M2 = 0x1.8p-21f;
-    const float t1 = p + M1, t2 = ((p - (t1 - M1)) + q) + M2;
-    const int i1 = __float_as_int(t1) - __float_as_int(M1), i2 = __float_as_int(t2) - __float_as_int(M2);
-    const long long v = ((long long)(((unsigned long long)r.y << 32) | r.x)) + ((long long)i1 << 14) + ((long long)i2 << 2);
-    // 2^46 -> units of 2^-44, times 2^n (n <= 0), to nearest
-    const int sh = 2 - (m >> 10);
-    return (unsigned long long)((v + (1ll << (sh - 1))) >> sh);
+    const float rest = fmaf(a * a, fmaf(a, 0.16666667f, 0.5f), ae);
+    const float2 r = tab.r[m & 1023];
+    // (head + tail) (1 + a + rest) = h + lw
+    const float p = r.x * a, q = fmaf(r.x, rest, fmaf(r.y, a, fmaf(r.x, a, -p))) + r.y;
+    const float h = r.x + p, lw = (p - (h - r.x)) + q;
+    // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
+    const float f = __int_as_float(((m & ~1023) << 13) + 0x3f800000);
+    const float hs = h * f, ls = lw * f;
+    constexpr float M1 = 3.0f, M2 = 0x1.8p-21f;
+    const float t1 = hs + M1, t2 = ((hs - (t1 - M1)) + ls) + M2;
+    const bool some = y > -45.5f;                  // else below half a unit (or masked: y is -inf)
+    Weight w{some ? __float_as_int(t1) - __float_as_int(M1) : 0, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
+    if (l == top) w = {1 << 22, 0};                // inf - inf above
+    return w;
 }
 
-// ln(exp((l - top) / T) / (total 2^-44)), l - top and the logarithm in fp64: once per row
+// ln(exp((l - top) / T) / (total 2^-44)), in fp32: both terms are at most 0, so they do not cancel; the quotient (of a
+// rounded difference), log1pf (at most 1 ulp, of a rounded argument) and their sum are off by at most 2^-22 of it
 __device__ __forceinline__ float log_prob(float l, float top, float temp, unsigned long long total) {
-    const double x = l == top ? 0.0 : (double(l) - double(top)) / double(temp);
-    return float(x - (log(double(total)) - 44 * 0.693147180559945309417));
+    const float x = l == top ? 0.0f : __fdiv_rn(l - top, temp);
+    const long long over = (long long)(total - (1ull << 44));
+    return x - log1pf(float(over) * 0x1p-44f);
 }
 
-// the smallest integer mass that is at least p of total (at least one unit)
+// ceil(p total), at least one unit: the mass at which top-p ends (p < 1)
 __device__ __forceinline__ unsigned long long mass_target(float p, unsigned long long total) {
-    const double t = ceil(double(p) * double(total));
-    const unsigned long long v = t < 1.0 ? 1ull : (unsigned long long)t;
-    return v < total ? v : total;
+    const unsigned long long f = (unsigned long long)(p * 18446744073709551616.0f);
+    const unsigned long long v = __umul64hi(f, total) + (f * total != 0);
+    return v > 1 ? v : 1;
 }
 // floor(u total): the token is the first whose running mass is above it
 __device__ __forceinline__ unsigned long long draw_target(float u, unsigned long long total) {
-    const unsigned long long v = __umul64hi((unsigned long long)(double(u) * 18446744073709551616.0), total);
-    return v < total ? v : total - 1;
+    return __umul64hi((unsigned long long)(u * 18446744073709551616.0f), total);
 }
-// the lowest key of a logit with exp((l - top) / T) >= min_p
-__device__ __forceinline__ uint32_t min_p_key(float min_p, float temp, float top) {
-    if (min_p >= 1.0f) return key_of(top);
-    const double border = double(top) + double(temp) * log(double(min_p));
-    float f = __double2float_ru(border);
-    const uint32_t k = key_of(f + 0.0f), kt = key_of(top);
-    return k < kt ? k : kt;
+// the lowest key of a logit with exp((l - top) / T) >= min_p, given T ln(min_p) (at most 0) in fp64
+__device__ __forceinline__ uint32_t min_p_key(double t_log_min_p, float top) {
+    const uint32_t k = key_of(__double2float_ru(double(top) + t_log_min_p) + 0.0f), k_top = key_of(top);
+    return k < k_top ? k : k_top;
 }
 // temperature 0 (greedy) or in [2^-20, 2^20], top_p above 0, min_p at most 1; NaN is refused
 __device__ __forceinline__ bool sample_params_ok(float temp, float p, float mp) {

@@ -48,8 +48,10 @@ def check(logits, u, temp=None, top_k=None, top_p=None, min_p=None, T=1, vocab=N
         if ref[0] < 0:
             assert lph[i] == -np.inf
         else:
-            # fp64 up to its own rounding (the sum is within 2^-44 of the top weight a token), then one fp32 rounding
-            assert abs(lph[i] - ref[1]) <= 2.0 ** -24 * abs(ref[1]) + V * 2.0 ** -44 + 1e-12, (i, lph[i], ref)
+            # x - ln(sum), both terms <= 0: x is a rounded quotient of a rounded difference (2 units of 2^-24 of it), the
+            # logarithm is within 1 ulp (2 units) of a rounded argument (1 unit), their difference is rounded (1 unit): 4
+            # units of the whole at most; the sum itself is within 2^-44 of the top weight a token
+            assert abs(lph[i] - ref[1]) <= 4 * 2.0 ** -24 * abs(ref[1]) + V * 2.0 ** -44 + 1e-12, (i, lph[i], ref)
 
 
 def logits_of(rows, V, dtype=torch.float32, seed=0, std=3.0):
