@@ -14,20 +14,26 @@
 // unless u lies within ~1e-11 of a border.  For the same reason the atomics
 // below (integer counts and masses) leave no trace of their order.
 //
-// A thread-block cluster holds a row in its CTAs' shared memory, so the logits
-// are read from HBM once; what follows are passes over shared memory, joined by
-// exchanges of a few words between the CTAs:
-//   1. the top logit (and its lowest index: all that temperature 0 needs);
-//   2. with top-k or top-p, a histogram of the tokens over bins of 1/16 octave
-//      of weight (monotone in the logit), merged over the cluster: it gives the
-//      bin in which top-k ends, and an estimate of the one in which top-p ends;
-//   3. with top-p, the exact masses: of all, of the bins before a window of 32
-//      around the estimate, and of each bin in it;
-//   4. the border inside its bin: a finer histogram over the keys there, then the
-//      few tokens of one of its cells by counting in the first CTA.  Where the
-//      kept tokens are few from the start (up to kList), the first CTA takes them
-//      all and ends the row alone;
-//   5. the kept mass of every CTA, the CTA that holds the drawn place, the token.
+// A thread-block cluster of 1 to 16 CTAs takes a row and goes over it two or
+// three times; the first pass reads HBM, the others find it in L1 or L2:
+//   1. the top logit and its lowest index (all that temperature 0 needs);
+//   2. top-k: the tokens from a bound on, to the first CTA's list.  The bound is
+//      the k-th largest of the threads' own tops, so it lies just below the k-th
+//      token wherever threads rarely hold two of the first k.  If the list stays
+//      short (kFew), the first CTA ranks it by counting and ends the row alone;
+//   3. top-p (or a long top-k): a histogram of the tokens over bins of 1/64
+//      octave of weight, merged over the cluster, gives about where the border
+//      lies;
+//   4. the exact masses of all tokens and of those before the border's bin; the
+//      tokens of that bin (or two) go to the list, where a radix selection over
+//      (key, index) finds the border.  If they are too many, once more with cells
+//      of 1/1024 bin; if they are equal, they are counted off by index.  Without
+//      top-k and top-p this pass only sums;
+//   5. the warp that holds the drawn place goes over its stretch once more.
+//
+// What bounds it: with many rows the exact weights, about 60 instructions a
+// token, and the passes' traffic; with few rows latency -- a cluster barrier
+// costs ~0.7 us, a block-wide sum ~0.5 us.
 #include "internal.cuh"
 
 #include <cuda_bf16.h>
@@ -37,15 +43,17 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kBins = 768;               // 1/16 octave each: 45.5 octaves, where weights end, lie in bin 728
-constexpr int kWindow = 32;
-constexpr int kCells = 256;
-constexpr int kList = 512;
+constexpr int kBins = 3072;              // 1/64 octave each: 45.5 octaves, where weights end, lie in bin 2912
+constexpr float kBinOctaves = 1.0f / 64;
+constexpr int kHead = 512;               // bins whose tokens' places inside them are summed too
+constexpr int kFine = 1024;              // cells a bin, where a bin is too full
+constexpr int kList = 2048;
+constexpr int kFew = 512;
+constexpr int kSmall = 256;              // items that are ranked by counting in a selection
+constexpr int kCells = 512;
 constexpr int kMaxCluster = 16;
-constexpr int kExchange = 2 + kWindow;
+constexpr int kExchange = 5;
 using u64 = unsigned long long;
 
 struct Item {
@@ -56,27 +64,24 @@ struct Item {
 struct Shared {
     WeightTable table;
     Item list[kList];
+    Item small[kSmall];
+    u64 cell_stat[kCells];
     u64 xch[2][kMaxCluster][kExchange];  // what each CTA of the cluster sent, two rounds
     u64 out[kExchange];                  // what this CTA sends
-    u64 sum[kExchange];                  // summed over the cluster
-    u64 cell_stat[kCells];
-    u64 win[kWindow];
-    u64 red[kWarps];
-    u64 warp_sum[kWarps];
-    u64 word[4];                         // broadcast within the cluster (bc) or the CTA
+    u64 red[32];
+    u64 warp_sum[32];                    // each warp's kept mass
+    u64 warp_ties[32];
+    u64 word, word2;                     // broadcast by the first CTA, or within a CTA
     double t_log_min_p;
-    uint32_t cell_count[kCells];
     uint32_t hist[kBins];                // this CTA's counts
-    uint32_t count[kBins];               // the cluster's, then summed up to and with each bin
-    float fred[kWarps];
-    uint32_t ured[kWarps];
-    int n_list;
+    uint32_t count[kBins];               // the cluster's, summed up to and with each bin
+    uint32_t hist_in[kHead], in[kHead];  // the sums of places inside the first bins, in 1/256 bin: this CTA's, all
+    float fred[32], fraction;
+    uint32_t ured[32];
+    uint32_t n_list, n_small;
     int found;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ uint32_t map_cluster(const void *p, uint32_t rank) {
     uint32_t r;
@@ -104,58 +109,62 @@ __device__ __forceinline__ uint32_t add_cluster32(uint32_t addr, uint32_t v) {
 }
 
 // the logits of one 16-byte vector
-template <typename L> struct Vec;
-template <> struct Vec<float> {
-    static constexpr int N = 4;
-    __device__ __forceinline__ static void get(const uint4 &v, float *f) {
-        f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[4], float) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y); f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8], __nv_bfloat16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    __device__ __forceinline__ static uint4 put(const float *f) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    }
+}
+
+struct Add {
+    __device__ __forceinline__ u64 operator()(u64 a, u64 b) const { return a + b; }
 };
-template <> struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    __device__ __forceinline__ static void get(const uint4 &v, float *f) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-    // the values came from bf16: their upper halves hold all of them
-    __device__ __forceinline__ static uint4 put(const float *f) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = (__float_as_uint(f[2 * i]) >> 16) | (__float_as_uint(f[2 * i + 1]) & 0xffff0000u);
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
+struct Most {
+    __device__ __forceinline__ u64 operator()(u64 a, u64 b) const { return a > b ? a : b; }
 };
 
-template <typename L>
+enum Border { kFound, kBefore, kBehind, kCrowded };
+
+template <typename L, int NT>
 struct Sampler {
-    static constexpr int E = Vec<L>::N;
+    static constexpr int E = 16 / sizeof(L);
+    static constexpr int kWarps = NT / 32;
+    static constexpr int kPer = kBins / NT;
     Shared &s;
-    uint4 *data;                         // this CTA's vectors
-    int nv, seg;                         // vectors of this CTA; of a warp
-    int base;                            // index of element 0 of vector 0 (negative before a row's first token)
+    const L *row;                        // the row's first logit
+    const uint4 *vecs;                   // the row as 16-byte vectors from the last boundary before it
+    int V, head;                         // head: elements of vector 0 before the row
+    int row_vecs, cta_vecs;
+    int v0, nv, seg;                     // this CTA's vectors: v0 .. v0 + nv; seg of them a warp
     int n_cta, rank, round;
     int tid, lane, wid;
     float top;
     Scale sc;
     float bin_scale;                     // bins per unit of logit
-    uint32_t K;                          // kept: key > K, or key == K and index <= I
+    float low;                           // kept: logit > low, or logit == low and index <= I (a masked one never is)
     int I;
 
-    __device__ __forceinline__ bool kept(uint32_t key, int i) const { return key > K || (key == K && i <= I); }
+    __device__ __forceinline__ bool kept(float l, int i) const { return l > low || (l == low && i <= I); }
     __device__ __forceinline__ Weight weigh(float l) const { return weight(l, top, sc, s.table); }
     __device__ __forceinline__ u64 units(float l) const { return weigh(l).units(); }
-    // monotone in l; 0 for the top logit (inf - inf gives NaN, which converts to 0)
-    __device__ __forceinline__ int bin(float l) const {
-        const int b = __float2int_rz((top - l) * bin_scale);
-        return b < kBins - 1 ? b : kBins - 1;
+    // the logit at which bin b (or cell b of bins of 1/kFine) begins, going down
+    __device__ __forceinline__ float edge_of(float b, float scale) const {
+        return b <= 0.f ? INFINITY : top - __fdiv_rn(b, scale);
+    }
+
+    __device__ __forceinline__ void start_row(const SampleArgs &a, int r) {
+        row = static_cast<const L *>(a.logits) + size_t(r) * size_t(a.ld);
+        head = int((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(L));
+        vecs = reinterpret_cast<const uint4 *>(row - head);
+        row_vecs = (head + V + E - 1) / E;
+        v0 = min(row_vecs, rank * cta_vecs);
+        nv = min(row_vecs, v0 + cta_vecs) - v0;
+        seg = (nv + kWarps - 1) / kWarps;
     }
 
     __device__ __forceinline__ void sync_cluster() const {
@@ -164,15 +173,30 @@ struct Sampler {
         else asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     }
 
-    // f(logit, index) for every element of this CTA, warps over stretches of their own, in index order within a lane
-    // and between the lanes of one step; masked elements (and those beside the row) come as -inf
-    template <typename F> __device__ __forceinline__ void each(F f) const {
-        const int end = min(nv, (wid + 1) * seg);
-        for (int v = wid * seg + lane; v < end; v += 32) {
-            float l[E];
-            Vec<L>::get(data[v], l);
+    // vector v of the row; what lies beside the row is masked (the last vector may end behind the buffer)
+    __device__ __forceinline__ void load(int v, float (&l)[E]) const {
+        const int i0 = v * E - head;
+        if (i0 >= 0 && i0 + E <= V) {
+            unpack(vecs[v], l, L());
+        } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) f(l[e], base + v * E + e);
+            for (int e = 0; e < E; ++e) l[e] = i0 + e >= 0 && i0 + e < V ? to_float(row[i0 + e]) : -INFINITY;
+        }
+    }
+    // f(logit, index) for every element of this CTA, warps over stretches of their own; two vectors in flight a thread
+    template <typename F> __device__ __forceinline__ void each(F f) const {
+        const int end = v0 + min(nv, (wid + 1) * seg);
+        for (int v = v0 + wid * seg + lane; v < end; v += 64) {
+            float l[E], m[E];
+            const bool two = v + 32 < end;
+            load(v, l);
+            if (two) load(v + 32, m);
+#pragma unroll
+            for (int e = 0; e < E; ++e) f(l[e], v * E - head + e);
+            if (two) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) f(m[e], (v + 32) * E - head + e);
+            }
         }
     }
 
@@ -181,416 +205,519 @@ struct Sampler {
         for (int m = 16; m; m >>= 1) v = op(v, u64(__shfl_xor_sync(kFull, v, m)));
         return v;
     }
-    // a sum or maximum (0 is neutral to op) over the block; threads 0 .. 31 hold the result
-    template <typename Op> __device__ __forceinline__ u64 block_first(u64 v, Op op) const {
+    // a sum or maximum (0 is neutral to op) over the block, the same in all its threads
+    template <typename Op> __device__ __forceinline__ u64 block_all(u64 v, Op op) const {
         v = warp_all(v, op);
         __syncthreads();
         if (lane == 0) s.red[wid] = v;
         __syncthreads();
-        return wid == 0 ? warp_all(lane < kWarps ? s.red[lane] : 0ull, op) : 0;
+        return warp_all(lane < kWarps ? s.red[lane] : 0ull, op);
     }
     // s.out[0 .. n) of every CTA to all: afterwards s.xch[round] holds them by rank
     __device__ __forceinline__ const u64 (*exchange(int n))[kExchange] {
         __syncthreads();
         round ^= 1;
-        for (int t = tid; t < n * n_cta; t += kThreads) {
+        for (int t = tid; t < n * n_cta; t += NT) {
             const int to = t / n, j = t - to * n;
             st_cluster64(map_cluster(&s.xch[round][rank][j], to), s.out[j]);
         }
         sync_cluster();
         return s.xch[round];
     }
-    // the same of one sum or maximum (0 is neutral to op) over each CTA: by rank in s.xch[round][rank][0]
-    template <typename Op> __device__ __forceinline__ const u64 (*exchange_of(u64 v, Op op))[kExchange] {
-        v = warp_all(v, op);
-        __syncthreads();
-        if (lane == 0) s.red[wid] = v;
-        __syncthreads();
-        round ^= 1;
-        if (tid < n_cta) {
-            v = s.red[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) v = op(v, s.red[w]);
-            st_cluster64(map_cluster(&s.xch[round][rank][0], tid), v);
-        }
-        sync_cluster();
-        return s.xch[round];
+    // one value of every thread over the cluster: the same in all its threads
+    template <typename Op> __device__ __forceinline__ u64 cluster_all(u64 v, Op op) {
+        v = block_all(v, op);
+        if (n_cta == 1) return v;
+        if (tid == 0) s.out[0] = v;
+        const auto x = exchange(1);
+        v = 0;
+        for (int r = 0; r < n_cta; ++r) v = op(v, x[r][0]);
+        return v;
     }
-    // one value of every thread, summed over the cluster: the same in all its threads
-    __device__ __forceinline__ u64 cluster_sum(u64 v) {
-        const auto x = exchange_of(v, [](u64 a, u64 b) { return a + b; });
-        u64 t = 0;
-        for (int r = 0; r < n_cta; ++r) t += x[r][0];
-        return t;
-    }
-
-    // the merged histogram of the tokens' bins, summed up to and with each bin, in s.count
-    __device__ __forceinline__ void histogram() {
-        for (int i = tid; i < kBins; i += kThreads) s.hist[i] = 0;
-        __syncthreads();
-        each([&](float l, int) {
-            if (l > -INFINITY) atomicAdd(&s.hist[bin(l)], 1u);
-        });
-        sync_cluster();
-        if (n_cta == 1) {
-            for (int i = tid; i < kBins; i += kThreads) s.count[i] = s.hist[i];
-        } else {
-            // lane r of a group of n_cta reads CTA r's count of a bin and, with their sum, writes CTA r's copy
-            const int slice = kBins / n_cta;
-            for (int t = tid; t < kBins; t += kThreads) {
-                const int r = t & (n_cta - 1), b = rank * slice + t / n_cta;
-                uint32_t c = ld_cluster32(map_cluster(&s.hist[b], r));
-                for (int m = n_cta >> 1; m; m >>= 1) c += __shfl_xor_sync(kFull, c, m);     // whole warps: 768 bins
-                st_cluster32(map_cluster(&s.count[b], r), c);
-            }
-        }
-        sync_cluster();
-        // 256 threads take three bins each
-        uint32_t c[3] = {0, 0, 0};
-        if (tid < 256) {
-#pragma unroll
-            for (int j = 0; j < 3; ++j) c[j] = s.count[3 * tid + j];
-        }
-        uint32_t t = c[0] + c[1] + c[2], run = t;
+    template <typename T> __device__ __forceinline__ T warp_scan(T v) const {        // inclusive
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
-            const uint32_t o = __shfl_up_sync(kFull, run, m);
-            if (lane >= m) run += o;
+            const T o = __shfl_up_sync(kFull, v, m);
+            if (lane >= m) v += o;
         }
+        return v;
+    }
+
+    // the merged histogram of the kept tokens' places (top - l) scale - from, the last bin taking what lies beyond if
+    // `open`, summed up to and with each bin, in s.count; with `open` also the sums of the places inside the first bins,
+    // in s.in (a few heavy tokens taken at their bins' middles would spoil an estimate).  The list is empty afterwards.
+    __device__ __forceinline__ void histogram(float scale, int first, bool open) {
+        for (int i = tid; i < kBins; i += NT) s.hist[i] = 0;
+        for (int i = tid; i < kHead; i += NT) s.hist_in[i] = 0;
+        if (tid == 0) s.n_list = 0;
+        __syncthreads();
+        each([&](float l, int i) {
+            if (!kept(l, i)) return;
+            // monotone in l; 0 for the top logit (inf - inf gives NaN, which converts to 0)
+            const float x = (top - l) * scale;
+            int b = __float2int_rz(x) - first;
+            if (open) {
+                if (b < kHead) atomicAdd(&s.hist_in[b], uint32_t(__float2int_rz((x - b) * 256.f)));
+                b = min(b, kBins - 1);
+            }
+            if (unsigned(b) < unsigned(kBins)) atomicAdd(&s.hist[b], 1u);
+        });
+        sync_cluster();
+        const uint32_t *from = s.hist;
+        if (n_cta > 1) {
+            // lane r of a group of n_cta reads CTA r's count of a bin and, with their sum, writes CTA r's copy
+            const int slice = kBins / n_cta;
+            for (int t = tid; t < kBins; t += NT) {                 // whole warps: 3072 is a multiple of NT
+                const int r = t & (n_cta - 1), b = rank * slice + t / n_cta;
+                uint32_t c = ld_cluster32(map_cluster(&s.hist[b], r));
+                for (int m = n_cta >> 1; m; m >>= 1) c += __shfl_xor_sync(kFull, c, m);
+                st_cluster32(map_cluster(&s.count[b], r), c);
+            }
+            for (int t = tid; open && t < kHead; t += NT) {
+                const int r = t & (n_cta - 1), b = rank * (kHead / n_cta) + t / n_cta;
+                uint32_t c = ld_cluster32(map_cluster(&s.hist_in[b], r));
+                for (int m = n_cta >> 1; m; m >>= 1) c += __shfl_xor_sync(kFull, c, m);
+                st_cluster32(map_cluster(&s.in[b], r), c);
+            }
+            sync_cluster();
+            from = s.count;
+        } else {
+            for (int t = tid; t < kHead; t += NT) s.in[t] = s.hist_in[t];
+        }
+        uint32_t c[kPer], t = 0;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) t += c[j] = from[kPer * tid + j];
+        uint32_t run = warp_scan(t);
         if (lane == 31) s.ured[wid] = run;
         __syncthreads();
-        for (int w = 0; w < wid; ++w) run += s.ured[w];
-        run -= t;
-        if (tid < 256) {
+        const uint32_t w = warp_scan(lane < kWarps ? s.ured[lane] : 0u);
+        run += (wid ? __shfl_sync(kFull, w, wid - 1) : 0u) - t;
 #pragma unroll
-            for (int j = 0; j < 3; ++j) s.count[3 * tid + j] = run += c[j];
-        }
+        for (int j = 0; j < kPer; ++j) s.count[kPer * tid + j] = run += c[j];
         __syncthreads();
     }
-    // the first bin up to which at least n tokens lie (n of them at least)
+    // the first bin up to which at least n tokens lie
     __device__ __forceinline__ int bin_of_count(uint32_t n) {
-        for (int b = tid; b < kBins; b += kThreads)
+        for (int b = tid; b < kBins; b += NT)
             if (s.count[b] >= n && (b == 0 || s.count[b - 1] < n)) s.found = b;
         __syncthreads();
         const int b = s.found;
         __syncthreads();
         return b;
     }
-    // about where the mass reaches p of that of the bins up to `last`, each bin's tokens taken at its middle
-    __device__ __forceinline__ int bin_of_mass(float p, int last) {
-        float c[3] = {0.f, 0.f, 0.f};
-        if (tid < 256) {
+    // about where the mass reaches `need` (or, need < 0, -need of that of the bins up to `last`), in units of the weight
+    // at the start, bins `octaves` wide, each one's tokens taken at its middle (with `open`, in the first bins, at their
+    // mean place): the bin and the fraction of it; past kBins if it is not reached
+    __device__ __forceinline__ float place_of_mass(float need, int last, float octaves, bool open) {
+        float c[kPer], t = 0.f;
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int b = 3 * tid + j;
-                const uint32_t n = s.count[b] - (b ? s.count[b - 1] : 0);
-                c[j] = b > last ? 0.f : float(n) * exp2f(-(b + 0.5f) * 0.0625f);
-            }
+        for (int j = 0; j < kPer; ++j) {
+            const int b = kPer * tid + j;
+            const uint32_t n = s.count[b] - (b ? s.count[b - 1] : 0);
+            const float in = open && b < kHead && n ? (s.in[b] + 0.5f * n) * (1.f / 256) / float(n) : 0.5f;
+            t += c[j] = b > last ? 0.f : float(n) * exp2f(-(b + in) * octaves);
         }
-        const float t = c[0] + c[1] + c[2];
-        float run = t;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const float o = __shfl_up_sync(kFull, run, m);
-            if (lane >= m) run += o;
-        }
+        float run = warp_scan(t);
         if (lane == 31) s.fred[wid] = run;
-        if (tid == 0) s.found = last;
-        __syncthreads();
-        float all = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < wid) run += s.fred[w];
-            all += s.fred[w];
-        }
-        run -= t;
-        const float need = p * all;
-        if (tid < 256) {
-#pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const float to = run + c[j];
-                if (to >= need && (run < need || (tid == 0 && j == 0)) && 3 * tid + j < last) atomicMin(&s.found, 3 * tid + j);
-                run = to;
-            }
-        }
-        __syncthreads();
-        const int b = s.found;
-        __syncthreads();
-        return b;
-    }
-
-    // tokens of the CTAs for which take(logit, key, index) holds, into the first CTA's list with their stat
-    template <typename T, typename S> __device__ __forceinline__ void gather(T take, S stat) {
-        const uint32_t n_at = map_cluster(&s.n_list, 0), list_at = map_cluster(s.list, 0);
-        each([&](float l, int i) {
-            const uint32_t key = key_of(l);
-            if (!take(l, key, i)) return;
-            const uint32_t at = add_cluster32(n_at, 1);
-            if (at < kList) {
-                st_cluster64(list_at + at * 16, (u64(key) << 32) | uint32_t(~i));
-                st_cluster64(list_at + at * 16 + 8, stat(l));
-            }
-        });
-    }
-
-    // K and I where the stat of the kept tokens, of bin b from `before` on, reaches target
-    template <typename S> __device__ __forceinline__ void resolve(int b, u64 before, u64 target, S stat) {
-        // a bin of few tokens goes to the list whole; else cells over its keys, its edges widened by their own rounding,
-        // keys beyond in the end cells
-        uint32_t n = s.count[b] - (b ? s.count[b - 1] : 0), lo = 0;
-        int shift = 32, at = kCells - 1;              // one cell
-        auto cell = [&](uint32_t key) {
-            const uint32_t c = key < lo || shift > 31 ? 0u : min((key - lo) >> shift, uint32_t(kCells - 1));
-            return kCells - 1 - int(c);
-        };
-        if (tid == 0) s.n_list = 0;
-        if (n > kList) {
-            const float hi_l = fminf(top - b / bin_scale, 3.4028234e38f), lo_l = fmaxf(top - (b + 1) / bin_scale, -3.4028234e38f);
-            const uint32_t hi = key_of(hi_l + 0.0f) + 512;
-            lo = b == kBins - 1 ? kNone : key_of(lo_l + 0.0f) - 512;
-            shift = max(0, 24 - __clz(max(1u, hi - lo)));
-            for (int i = tid; i < kCells; i += kThreads) s.cell_stat[i] = s.cell_count[i] = 0;
-            sync_cluster();
-            const uint32_t stat_at = map_cluster(s.cell_stat, 0), count_at = map_cluster(s.cell_count, 0);
-            each([&](float l, int i) {
-                if (!(l > -INFINITY) || bin(l) != b) return;
-                const uint32_t key = key_of(l);
-                if (!kept(key, i)) return;
-                const int c = cell(key);
-                add_cluster64(stat_at + c * 8, stat(l));
-                add_cluster32(count_at + c * 4, 1);
-            });
-            sync_cluster();
-            if (rank == 0 && wid == 0) {
-                u64 c[kCells / 32], t = 0;
-#pragma unroll
-                for (int j = 0; j < kCells / 32; ++j) t += c[j] = s.cell_stat[lane * (kCells / 32) + j];
-                u64 run = t;
-#pragma unroll
-                for (int m = 1; m < 32; m <<= 1) {
-                    const u64 o = __shfl_up_sync(kFull, run, m);
-                    if (lane >= m) run += o;
-                }
-                run += before - t;
-#pragma unroll
-                for (int j = 0; j < kCells / 32; ++j) {
-                    if (run < target && target <= run + c[j]) {
-                        const int to = lane * (kCells / 32) + j;
-                        const u64 head = (u64(to) << 32) | s.cell_count[to];
-                        for (int r = 0; r < n_cta; ++r) {
-                            st_cluster64(map_cluster(&s.word[0], r), head);
-                            st_cluster64(map_cluster(&s.word[1], r), run);
-                        }
-                    }
-                    run += c[j];
-                }
-            }
-            sync_cluster();
-            at = int(s.word[0] >> 32);
-            n = uint32_t(s.word[0]);
-            before = s.word[1];
-        } else {
-            sync_cluster();
-        }
-        auto here = [&](float l, uint32_t key, int i) {
-            return l > -INFINITY && bin(l) == b && cell(key) == at && kept(key, i);
-        };
-        if (n <= kList) {
-            gather(here, stat);
-            sync_cluster();
-            n = s.n_list;                             // without the tokens of the bin that top-k left out
-            if (rank == 0 && tid < int(n)) {
-                const Item me = s.list[tid];
-                u64 run = before;
-                for (int j = 0; j < int(n); ++j) {
-                    const Item o = s.list[j];
-                    if (o.order > me.order) run += o.stat;
-                }
-                if (run < target && target <= run + me.stat)
-                    for (int r = 0; r < n_cta; ++r) st_cluster64(map_cluster(&s.word[2], r), me.order);
-            }
-            sync_cluster();
-            K = uint32_t(s.word[2] >> 32);
-            I = int(~uint32_t(s.word[2]));
-            return;
-        }
-        // many tokens in one cell, most often equal ones: bisection over its keys, then the ties by index
-        uint32_t k_lo = 0xffffffffu, k_hi = 0;
-        each([&](float l, int i) {
-            const uint32_t key = key_of(l);
-            if (here(l, key, i)) {
-                k_lo = min(k_lo, key);
-                k_hi = max(k_hi, key);
-            }
-        });
-        auto most = [](u64 x, u64 y) { return x > y ? x : y; };
-        const u64 a = block_first(u64(~k_lo), most), z = block_first(u64(k_hi), most);
         if (tid == 0) {
-            s.out[0] = a;
-            s.out[1] = z;
+            s.found = kBins;
+            s.fraction = 0.5f;
         }
-        const auto x = exchange(2);
-        uint32_t lo_key = 0, hi_key = 0;
-        for (int r = 0; r < n_cta; ++r) {
-            lo_key = max(lo_key, uint32_t(x[r][0]));
-            hi_key = max(hi_key, uint32_t(x[r][1]));
+        __syncthreads();
+        const float w = warp_scan(lane < kWarps ? s.fred[lane] : 0.f);
+        run += (wid ? __shfl_sync(kFull, w, wid - 1) : 0.f) - t;
+        if (need < 0.f) need *= -__shfl_sync(kFull, w, 31);
+        int mine = kBins;
+        float fraction = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (mine == kBins && run + c[j] >= need && c[j] > 0.f) {
+                mine = kPer * tid + j;
+                fraction = fminf(fmaxf(__fdividef(need - run, c[j]), 0.f), 1.f);
+            }
+            run += c[j];
         }
-        lo_key = ~lo_key;
-        auto above = [&](uint32_t from) {           // the stat of the cell's tokens of that key and above, and `before`
-            u64 m = 0;
-            each([&](float l, int i) {
-                const uint32_t key = key_of(l);
-                if (key >= from && here(l, key, i)) m += stat(l);
-            });
-            return before + cluster_sum(m);
-        };
-        while (lo_key < hi_key) {
-            const uint32_t mid = lo_key + (hi_key - lo_key + 1) / 2;
-            if (above(mid) >= target) lo_key = mid;
-            else hi_key = mid - 1;
-        }
-        const u64 run = above(lo_key + 1), one = stat(value_of(lo_key)), need = (target - run + one - 1) / one;
-        // the need-th token of that key in index order
-        u64 m = 0;
-        each([&](float l, int i) {
-            const uint32_t key = key_of(l);
-            m += key == lo_key && kept(key, i);
-        });
-        auto tie = [&](float l, int i) -> u64 {
-            const uint32_t key = key_of(l);
-            return key == lo_key && kept(key, i);
-        };
-        warp_sums(m);
-        pick(need - 1, tie, [&](float, int i) {
-            for (int r = 0; r < n_cta; ++r) st_cluster64(map_cluster(&s.word[3], r), u64(uint32_t(i)));
-        });
-        sync_cluster();
-        K = lo_key;
-        I = int(uint32_t(s.word[3]));
+        if (mine < kBins) atomicMin(&s.found, mine);
+        __syncthreads();
+        if (mine < kBins && s.found == mine) s.fraction = fraction;
+        __syncthreads();
+        const float at = s.found + s.fraction;
+        __syncthreads();
+        return at;
     }
 
-    // each warp's sum of `mine` in s.warp_sum
-    __device__ __forceinline__ void warp_sums(u64 mine) {
-        mine = warp_all(mine, [](u64 a, u64 b) { return a + b; });
-        __syncthreads();
-        if (lane == 0) s.warp_sum[wid] = mine;
-        __syncthreads();
+    // a token to the first CTA's list, if there is room; one atomic for the lanes that come here together
+    __device__ __forceinline__ void push(uint32_t key, int i, u64 stat) const {
+        const unsigned here = __activemask();
+        const int first = __ffs(here) - 1;
+        uint32_t at = 0;
+        if (lane == first) at = add_cluster32(map_cluster(&s.n_list, 0), __popc(here));
+        at = __shfl_sync(here, at, first) + __popc(here & ((1u << lane) - 1));
+        if (at < kList) {
+            const uint32_t to = map_cluster(s.list, 0) + at * 16;
+            st_cluster64(to, (u64(key) << 32) | uint32_t(~i));
+            st_cluster64(to + 8, stat);
+        }
     }
-    // with the warps' sums of stat in s.warp_sum: at(logit, index), by one thread of the cluster, of the first token in
-    // index order up to which the stats sum to more than `place`
-    template <typename S, typename A> __device__ __forceinline__ void pick(u64 place, S stat, A at) {
-        u64 all = 0;
-        for (int w = 0; w < kWarps; ++w) all += s.warp_sum[w];
+
+    // with low: I, for this CTA, so that of the tokens of that logit (kept so far) the first `need` in index order are
+    // kept; each warp's kept ones, times `one`, are added to s.warp_sum
+    __device__ __forceinline__ void tie(float value, u64 need, u64 one) {
+        auto same = [&](float l, int i) -> u64 { return l == value && kept(l, i); };
+        u64 mine = 0;
+        each([&](float l, int i) { mine += same(l, i); });
+        mine = warp_all(mine, Add());
+        __syncthreads();
+        if (lane == 0) s.warp_ties[wid] = mine;
+        __syncthreads();
+        const u64 all = warp_all(lane < kWarps ? s.warp_ties[lane] : 0ull, Add());
         if (tid == 0) s.out[0] = all;
         const auto x = exchange(1);
         u64 run = 0;
         for (int r = 0; r < rank; ++r) run += x[r][0];
-        find(place, run, stat, at);
+        if (tid == 0) {
+            u64 to = run;
+            for (int w = 0; w < kWarps; ++w) {
+                const u64 n = s.warp_ties[w];
+                s.warp_sum[w] += (need <= to ? 0 : min(need - to, n)) * one;
+                to += n;
+            }
+        }
+        int limit = run < need ? 0x7fffffff : -1;
+        if (run < need && need < run + all) {
+            find(need - 1, run, s.warp_ties, same, [&](float, int i) { s.found = i; });
+            __syncthreads();
+            limit = s.found;
+        }
+        __syncthreads();
+        I = value == low ? min(I, limit) : limit;
+        low = value;
     }
-    // the same within this CTA, the sum before it being `run`
-    template <typename S, typename A> __device__ __forceinline__ void find(u64 place, u64 run, S stat, A at) {
-        for (int w = 0; w < wid; ++w) run += s.warp_sum[w];
-        if (!(run <= place && place < run + s.warp_sum[wid])) return;
-        const int end = min(nv, (wid + 1) * seg);
-        for (int v0 = wid * seg; v0 < end; v0 += 32) {
-            const int v = v0 + lane;
+
+    // low and I where the stat of the kept tokens reaches target, by bisection over the keys
+    template <typename S> __device__ __forceinline__ void slow_border(u64 target, S stat) {
+        auto from = [&](uint32_t key) {
+            const float least = value_of(key);
+            u64 m = 0;
+            each([&](float l, int i) {
+                if (l >= least && kept(l, i)) m += stat(l);
+            });
+            return cluster_all(m, Add());
+        };
+        const uint32_t top_key = key_of(top);
+        uint32_t lo = key_of(low), hi = top_key;
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            if (from(mid) >= target) lo = mid;
+            else hi = mid - 1;
+        }
+        const float value = value_of(lo) + 0.0f;
+        const u64 above = lo == top_key ? 0 : from(lo + 1), one = stat(value);
+        tie(value, (target - above + one - 1) / one, 0);
+    }
+
+    // by the first CTA: the order of the list's item at which the stats, `before` and on, reach target, or 0
+    __device__ __forceinline__ u64 select(int n, u64 before, u64 target) {
+        u64 lo = 0, hi = 0;
+        for (int t = tid; t < n; t += NT) {
+            const u64 o = s.list[t].order;
+            hi = max(hi, o);
+            lo = max(lo, ~o);
+        }
+        hi = block_all(hi, Most());
+        lo = ~block_all(lo, Most());
+        int live = n;
+        while (live > kSmall) {
+            // cells of equal width from hi down
+            const int shift = max(0, 55 - __clzll((long long)(hi - lo)));
+            for (int t = tid; t < kCells; t += NT) {
+                s.cell_stat[t] = 0;
+                s.hist[t] = 0;
+            }
+            if (tid == 0) s.n_small = kCells;
+            __syncthreads();
+            for (int t = tid; t < n; t += NT) {
+                const Item o = s.list[t];
+                if (o.order < lo || o.order > hi) continue;
+                const int c = int((hi - o.order) >> shift);
+                atomicAdd(&s.cell_stat[c], o.stat);
+                atomicAdd(&s.hist[c], 1u);
+            }
+            __syncthreads();
+            if (wid == 0) {
+                constexpr int kEach = kCells / 32;
+                u64 t = 0;
+                for (int j = 0; j < kEach; ++j) t += s.cell_stat[lane * kEach + j];
+                u64 run = before + warp_scan(t) - t;
+                for (int j = 0; j < kEach; ++j) {
+                    const u64 c = s.cell_stat[lane * kEach + j];
+                    if (run < target && target <= run + c) {
+                        s.n_small = lane * kEach + j;
+                        s.word2 = run;
+                    }
+                    run += c;
+                }
+            }
+            __syncthreads();
+            const u64 c = s.n_small;
+            if (c == kCells) return 0;
+            before = s.word2;
+            live = int(s.hist[c]);
+            if (c < ((hi - lo) >> shift)) lo = hi - ((c + 1) << shift) + 1;       // not the last cell
+            hi -= c << shift;
+            __syncthreads();
+        }
+        if (tid == 0) {
+            s.n_small = 0;
+            s.word2 = 0;
+        }
+        __syncthreads();
+        for (int t = tid; t < n; t += NT) {
+            const Item o = s.list[t];
+            if (o.order >= lo && o.order <= hi) s.small[atomicAdd(&s.n_small, 1u)] = o;
+        }
+        __syncthreads();
+        if (tid < live) {
+            const Item me = s.small[tid];
+            for (int j = 0; j < live; ++j) {
+                const Item o = s.small[j];
+                if (o.order > me.order) before += o.stat;
+            }
+            if (before < target && target <= before + me.stat) s.word2 = me.order;
+        }
+        __syncthreads();
+        return s.word2;
+    }
+
+    // low and I where the stat of the kept tokens (MASS: their weights, else 1) reaches its target, among the tokens of
+    // at most `from` and above `to`; target_of(all) gives it, from the stat of all kept tokens, which is returned, as is
+    // that of the tokens above `from`.  With kFound s.warp_sum holds each warp's kept stat.  The list is empty before
+    // and afterwards.
+    template <bool MASS, typename T>
+    __device__ __forceinline__ Border border(float from, float to, T target_of, u64 &all, u64 &before) {
+        Weight w_all{0, 0}, w_before{0, 0};
+        uint32_t n_all = 0, n_before = 0, n = 0, k_lo = 0xffffffffu, k_hi = 0;
+        each([&](float l, int i) {
+            if (!kept(l, i)) return;
+            Weight w{0, 0};
+            if (MASS) {
+                w = weigh(l);
+                w_all += w;
+                if (l > from) w_before += w;
+            } else {
+                ++n_all;
+                if (l > from) ++n_before;
+            }
+            if (l <= from && l > to) {
+                const uint32_t key = key_of(l + 0.0f);
+                ++n;
+                k_lo = min(k_lo, key);
+                k_hi = max(k_hi, key);
+                push(key, i, MASS ? w.units() : 1);
+            }
+        });
+        const u64 mine = warp_all(MASS ? w_before.units() : u64(n_before), Add());
+        all = block_all(MASS ? w_all.units() : u64(n_all), Add());
+        if (lane == 0) s.warp_sum[wid] = mine;
+        const u64 c_n = block_all(n, Add());
+        const u64 c_lo = block_all(u64(~k_lo), Most()), c_hi = block_all(u64(k_hi), Most());
+        const u64 c_before = warp_all(lane < kWarps ? s.warp_sum[lane] : 0ull, Add());
+        if (tid == 0) {
+            s.out[0] = all;
+            s.out[1] = c_before;
+            s.out[2] = c_n;
+            s.out[3] = c_lo;
+            s.out[4] = c_hi;
+        }
+        const auto x = exchange(5);
+        before = all = n = k_lo = k_hi = 0;
+        for (int r = 0; r < n_cta; ++r) {
+            all += x[r][0];
+            before += x[r][1];
+            n += uint32_t(x[r][2]);
+            k_lo = max(k_lo, uint32_t(x[r][3]));
+            k_hi = max(k_hi, uint32_t(x[r][4]));
+        }
+        k_lo = ~k_lo;
+        const u64 target = target_of(all);
+        const u64 one = n > kList && MASS ? units(value_of(k_lo)) : 1;
+        const u64 need = one ? (target - before + one - 1) / one : u64(n) + 1;     // of equal tokens
+        const Border got = before >= target ? kBefore : n == 0 ? kBehind : n <= kList ? kFound
+                         : k_lo != k_hi ? kCrowded : need > n ? kBehind : kFound;
+        if (got != kFound || n > kList) {
+            if (tid == 0) s.n_list = 0;
+            if (got == kFound) tie(value_of(k_lo), need, one);
+            else sync_cluster();
+            return got;
+        }
+        if (rank == 0) {
+            const u64 at = select(int(n), before, target);
+            if (at)
+                for (int t = tid; t < int(n); t += NT) {
+                    const Item o = s.list[t];
+                    if (o.order < at) continue;
+                    // a kept token: its mass to the warp in whose stretch it lies
+                    const int v = (int(~uint32_t(o.order)) + head) / E, r = v / cta_vecs, first = r * cta_vecs;
+                    const int its = (min(row_vecs, first + cta_vecs) - first + kWarps - 1) / kWarps;
+                    add_cluster64(map_cluster(&s.warp_sum[(v - first) / its], r), o.stat);
+                }
+            if (tid < n_cta) st_cluster64(map_cluster(&s.word, tid), at);
+            if (tid == 0) s.n_list = 0;
+        }
+        sync_cluster();
+        const u64 at = s.word;
+        if (at == 0) return kBehind;
+        low = value_of(uint32_t(at >> 32));
+        I = int(~uint32_t(at));
+        return kFound;
+    }
+
+    // the same, the border being looked for: near `place` (in bins) first; whether s.warp_sum holds the kept stats
+    template <bool MASS, typename T> __device__ __forceinline__ bool look_for(float place, T target_of) {
+        u64 all, before;
+        // the estimate is good to a fraction of a bin
+        float b0 = floorf(place - 0.45f), b1 = floorf(place + 0.45f) + 1.f;
+        if (!MASS) b0 = floorf(place), b1 = b0 + 1.f;
+        for (int turn = 0; turn < 6; ++turn) {
+            Border got = border<MASS>(edge_of(b0, bin_scale), edge_of(b1, bin_scale), target_of, all, before);
+            if (got == kFound) return true;
+            if (got == kCrowded) {
+                // cells of 1/kFine bin over three bins from b0 on
+                const int first = int(fmaxf(b0, 0.f)) * kFine;
+                const float scale = bin_scale * kFine;
+                histogram(scale, first, false);
+                const u64 need = target_of(all) - before;
+                float c0, c1;
+                if (MASS) {
+                    const float at = place_of_mass(float(need) * 0x1p-44f * exp2f(fmaxf(b0, 0.f) * kBinOctaves), kBins - 1,
+                                                   kBinOctaves / kFine, false);
+                    c0 = floorf(at) - 1.f;
+                    c1 = floorf(at) + 2.f;
+                } else {
+                    c0 = bin_of_count(uint32_t(min(need, u64(s.count[kBins - 1]))));
+                    c1 = c0 + 1.f;
+                }
+                if (border<MASS>(edge_of(first + c0, scale), edge_of(first + c1, scale), target_of, all, before) == kFound) return true;
+                break;
+            }
+            // off by a bin or more
+            const float by = b1 - b0 + turn;
+            if (got == kBefore) {
+                b1 = b0 + 1.f;
+                b0 = fmaxf(0.f, b0 - by);
+            } else {
+                b0 = b1 - 1.f;
+                b1 += by;
+            }
+        }
+        slow_border(target_of(all), [&](float l) { return MASS ? units(l) : u64(1); });
+        return false;
+    }
+
+    // by the whole CTA, the sum of stat before it being `run` and its warps' sums `warp`: at(logit, index), by one
+    // thread, of the first token in index order up to which the stats sum to more than `place`
+    template <typename S, typename A> __device__ __forceinline__ void find(u64 place, u64 run, const u64 *warp, S stat, A at) {
+        int w = 0;
+        while (w < kWarps && place >= run + warp[w]) run += warp[w++];
+        if (w == kWarps) return;
+        // the stretch of warp w, one vector a thread and round
+        const int end = v0 + min(nv, (w + 1) * seg);
+        for (int u = v0 + w * seg; u < end && run <= place; u += NT) {
+            const int v = u + tid;
             float l[E];
             u64 c[E], t = 0;
-            if (v < end) Vec<L>::get(data[v], l);
+            if (v < end) load(v, l);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                c[e] = v < end ? stat(l[e], base + v * E + e) : 0;
+                c[e] = v < end ? stat(l[e], v * E - head + e) : 0;
                 t += c[e];
             }
-            u64 to = t;
+            const u64 to = warp_scan(t);
+            __syncthreads();
+            if (lane == 31) s.red[wid] = to;
+            __syncthreads();
+            const u64 ws = warp_scan(lane < kWarps ? s.red[lane] : 0ull);
+            u64 before = run + (wid ? __shfl_sync(kFull, ws, wid - 1) : 0ull) + to - t;
+            run += __shfl_sync(kFull, ws, 31);
 #pragma unroll
-            for (int m = 1; m < 32; m <<= 1) {
-                const u64 o = __shfl_up_sync(kFull, to, m);
-                if (lane >= m) to += o;
+            for (int e = 0; e < E; ++e) {
+                if (before <= place && place < before + c[e]) at(l[e], v * E - head + e);
+                before += c[e];
             }
-            const unsigned hit = __ballot_sync(kFull, run + to > place);
-            if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    u64 r = run + to - t;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        if (r <= place && place < r + c[e]) at(l[e], base + v * E + e);
-                        r += c[e];
-                    }
-                }
-                return;
-            }
-            run += __shfl_sync(kFull, to, 31);
         }
     }
 };
 
-template <typename L>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
+template <typename L, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    constexpr int E = Vec<L>::N;
-    Sampler<L> x{s};
-    x.data = reinterpret_cast<uint4 *>(smem + (sizeof(Shared) + 15) / 16 * 16);
+    Sampler<L, NT> x{s};
+    constexpr int kWarps = NT / 32;
     x.tid = threadIdx.x; x.lane = x.tid & 31; x.wid = x.tid >> 5;
     x.n_cta = n_cta; x.rank = int(blockIdx.x) & (n_cta - 1); x.round = 0;
-    const int row = int(blockIdx.x) / n_cta, slot = row / a.T, V = a.V, tid = x.tid;
+    x.V = a.V; x.cta_vecs = cta_vecs;
+    const int tid = x.tid, row = int(blockIdx.x) / n_cta, slot = row / a.T;
 
     // a CTA's shared memory may be written by its peers once it has started: the wait for all to have done so comes
     // before the first exchange
     if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
-    s.table.fill(tid, kThreads);
+    s.table.fill(tid, NT);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    // the row as 16-byte vectors from the last 16-byte boundary before it
-    const L *logits = static_cast<const L *>(a.logits) + size_t(row) * size_t(a.ld);
-    const int head = int((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(L));
-    const int row_vecs = (head + V + E - 1) / E;
-    const int v0 = min(row_vecs, x.rank * cta_vecs);
-    x.nv = min(row_vecs, v0 + cta_vecs) - v0;
-    x.seg = (x.nv + kWarps - 1) / kWarps;
-    x.base = v0 * E - head;
-    const uint4 *src = reinterpret_cast<const uint4 *>(logits - head) + v0;
-    const int seg_end = min(x.nv, (x.wid + 1) * x.seg);
-    auto whole = [&](int v) { return x.base + v * E + E <= V; };      // ends inside the row
-    for (int v = x.wid * x.seg + x.lane; v < seg_end; v += 32)
-        if (whole(v)) cp_async16(smem_u32(x.data + v), src + v);
     const float temp = a.temperature ? a.temperature[slot] : 1.0f;
     const float u = a.u[row];
     const int k = a.top_k ? a.top_k[slot] : 0;
     const float p = a.top_p ? a.top_p[slot] : 1.0f, mp = a.min_p ? a.min_p[slot] : 0.0f;
     const bool fine = sample_params_ok(temp, p, mp) && u >= 0.0f && u < 1.0f;
-    if (tid == 0 && mp > 0.0f) s.t_log_min_p = double(temp) * log(double(mp));       // while the copies are in flight
-    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;\n" ::: "memory");
+    x.start_row(a, row);
 
-    // 1. the top logit; each thread cleans the vectors that it copied itself
+    bool by_k = k > 0 && k < a.V;
+    const bool by_p = p < 1.0f;
+
+    // 1. the top logit
     float best = -INFINITY;
     int best_i = 0;
-    for (int v = x.wid * x.seg + x.lane; v < seg_end; v += 32) {
-        float l[E];
-        const int i0 = x.base + v * E;
-        if (whole(v)) {
-            Vec<L>::get(x.data[v], l);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) l[e] = i0 + e >= 0 && i0 + e < V ? to_float(logits[i0 + e]) : -INFINITY;
+    x.each([&](float l, int i) {
+        if (l > best) {
+            best = l;
+            best_i = i;
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            l[e] = i0 + e < 0 ? -INFINITY : clean(l[e]);
-            if (l[e] > best) {
-                best = l[e];
-                best_i = i0 + e;
-            }
-        }
-        x.data[v] = Vec<L>::put(l);
+    });
+    const uint32_t k_best = key_of(best + 0.0f);
+    if (tid == 0) {
+        if (mp > 0.0f) s.t_log_min_p = double(temp) * log(double(mp));
+        s.n_list = 0;
     }
-    auto most = [](u64 p, u64 q) { return p > q ? p : q; };
-    u64 first = (u64(key_of(best)) << 32) | uint32_t(~best_i);
+    // top-k's bound: some key that at least k / n_cta of this CTA's threads reach (if that many hold a token at all);
+    // the least of the CTAs' bounds is reached by k tokens
+    const int share = (k + n_cta - 1) / n_cta;
+    uint32_t bound = kNone + 1;
+    const bool bounded = by_k && fine && temp != 0.0f && share <= NT / 4;
+    if (bounded) {
+        uint32_t lo = kNone + 1, hi = 0xff800000u;             // the key of +inf
+        while (lo < hi) {
+            const uint32_t mid = lo + (hi - lo + 1) / 2;
+            const int n = __syncthreads_count(k_best >= mid);
+            if (n >= share) lo = mid;
+            else hi = mid - 1;
+            if (n >= share && n <= share + share / 4) break;
+        }
+        bound = lo;
+    }
+    const u64 c_best = x.block_all((u64(k_best) << 32) | uint32_t(~best_i), Most());
+    if (tid == 0) {
+        s.out[0] = c_best;
+        s.out[1] = bound;
+    }
     __syncwarp();
     if (n_cta > 1) asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
+    u64 first = 0;
     {
-        const auto got = x.exchange_of(first, most);
-        first = 0;
-        for (int r = 0; r < n_cta; ++r) first = most(first, got[r][0]);
+        const auto got = x.exchange(2);
+        for (int r = 0; r < n_cta; ++r) {
+            first = max(first, got[r][0]);
+            bound = min(bound, uint32_t(got[r][1]));
+        }
     }
     const uint32_t k_top = uint32_t(first >> 32);
     auto finish = [&](int token, float logprob) {
@@ -607,100 +734,39 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
     }
     x.top = value_of(k_top);
     x.sc = scale_of(temp);
-    x.bin_scale = 16.0f * x.sc.hi;
-    x.K = kNone + 1;
-    x.I = V;
+    x.bin_scale = x.sc.hi / kBinOctaves;
+    x.low = -3.4028234e38f;
+    x.I = a.V;
     const uint32_t k_min_p = mp > 0.0f ? min_p_key(s.t_log_min_p, x.top) : 0u;
-    bool by_k = k > 0 && k < V;
-    const bool by_p = p < 1.0f;
-    u64 all_mass = 0;                      // of what top-k left, where top-p needs it
-    u64 my_mass = 0;                       // this CTA's kept mass, where it is known before the last pass
-    bool know_mass = false;
-    int list_to = -1;                      // >= 0: the kept tokens lie in the bins up to this one and fit the list
-    if (by_k || by_p) {
-        x.histogram();
+    bool short_list = false;
+    if (bounded) {
+        const float least = value_of(bound);
+        x.each([&](float l, int i) {
+            if (l >= least) x.push(key_of(l + 0.0f), i, x.units(l));
+        });
+        x.sync_cluster();
+        const uint32_t n = ld_cluster32(map_cluster(&s.n_list, 0));
+        short_list = n <= kFew;
+        // the first CTA stays until its peers have read n: it waits for them when it is done
+        if (!short_list || x.rank != 0) x.sync_cluster();
+        else if (n_cta > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+    }
+    bool know_mass = false;                // s.warp_sum holds the kept masses
+    if (!short_list && (by_k || by_p)) {
+        x.histogram(x.bin_scale, 0, true);
         int last = kBins - 1;
-        if (by_k && s.count[kBins - 1] <= uint32_t(k)) by_k = false;
-        if (by_k) {
-            last = x.bin_of_count(k);
-            if (s.count[last] <= kList) list_to = last;
-            else x.resolve(last, last ? s.count[last - 1] : 0, u64(k), [](float) { return u64(1); });
-        }
-        if (by_p && list_to < 0) {
-            int b0 = max(0, min(x.bin_of_mass(p, last) - kWindow / 2, kBins - kWindow));
-            for (;;) {
-                for (int i = tid; i < kWindow; i += kThreads) s.win[i] = 0;
-                __syncthreads();
-                Weight m_all{0, 0}, m_before{0, 0};
-                x.each([&](float l, int i) {
-                    if (!x.kept(key_of(l), i)) return;
-                    const Weight w = x.weigh(l);
-                    const int b = x.bin(l) - b0;
-                    m_all += w;
-                    if (b < 0) m_before += w;
-                    else if (b < kWindow) atomicAdd(&s.win[b], w.units());
-                });
-                auto add = [](u64 p, u64 q) { return p + q; };
-                const u64 b_all = x.block_first(m_all.units(), add), b_before = x.block_first(m_before.units(), add);
-                if (tid == 0) {
-                    s.out[0] = b_all;
-                    s.out[1] = b_before;
-                }
-                for (int i = tid; i < kWindow; i += kThreads) s.out[2 + i] = s.win[i];
-                const auto got = x.exchange(kExchange);
-                if (tid < kExchange) {
-                    u64 t = 0;
-                    for (int r = 0; r < n_cta; ++r) t += got[r][tid];
-                    s.sum[tid] = t;
-                }
-                __syncthreads();
-                all_mass = s.sum[0];
-                const u64 target = mass_target(p, all_mass);
-                u64 run = s.sum[1];
-                int b = -1;
-                u64 before = 0;
-                my_mass = s.out[1];
-                if (run < target)
-                    for (int i = 0; i < kWindow; ++i) {
-                        if (run < target && target <= run + s.sum[2 + i]) {
-                            b = i;
-                            before = run;
-                        }
-                        if (b < 0) my_mass += s.out[2 + i];
-                        run += s.sum[2 + i];
-                    }
-                if (b >= 0) {
-                    b += b0;
-                    if (!by_k && s.count[b] <= kList) {
-                        list_to = b;
-                    } else {
-                        x.resolve(b, before, target, [&](float l) { return x.units(l); });
-                        know_mass = true;
-                        // the kept tokens of this CTA in the bin itself
-                        Weight in_bin{0, 0};
-                        x.each([&](float l, int i) {
-                            if (l > -INFINITY && x.bin(l) == b && x.kept(key_of(l), i)) in_bin += x.weigh(l);
-                        });
-                        const u64 m = x.block_first(in_bin.units(), add);
-                        if (tid == 0) s.word[3] = my_mass + m;
-                    }
-                    break;
-                }
-                // the estimate was off: the window before or behind
-                b0 = s.sum[1] >= target ? max(0, b0 - kWindow) : min(b0 + kWindow, kBins - kWindow);
-                __syncthreads();
-            }
+        by_k = by_k && s.count[kBins - 1] > uint32_t(k);
+        if (by_k) last = x.bin_of_count(k);
+        const float place = by_p ? x.place_of_mass(-p, last, kBinOctaves, true) : 0.f;
+        if (by_k) x.template look_for<false>(float(last), [&](u64) { return u64(k); });
+        if (by_p) {
+            know_mass = x.template look_for<true>(fminf(place, float(last)), [&](u64 all) { return mass_target(p, all); });
         }
     }
-    if (list_to >= 0) {
-        // few tokens: the first CTA ranks them all by counting, and ends the row
-        if (tid == 0) s.n_list = 0;
-        x.sync_cluster();
-        x.gather([&](float l, uint32_t, int) { return l > -INFINITY && x.bin(l) <= list_to; },
-                 [&](float l) { return x.units(l); });
-        x.sync_cluster();
+    if (short_list) {
+        // the first CTA ranks them all by counting, and ends the row
         if (x.rank != 0) return;
-        const int n = s.n_list;
+        const int n = int(s.n_list);
         Item me{0, 0};
         u64 before = 0;
         int place = 0;
@@ -714,24 +780,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
                 }
             }
         }
-        auto add = [](u64 p, u64 q) { return p + q; };
-        bool keep = tid < n && (!by_k || place < k);
+        bool keep = tid < n && place < k;
         if (by_p) {
-            if (by_k) {
-                const u64 t = x.block_first(keep ? me.stat : 0, add);
-                if (tid == 0) s.word[0] = t;
-                __syncthreads();
-                all_mass = s.word[0];
-            }
-            keep = keep && before < mass_target(p, all_mass);
+            const u64 all = x.block_all(keep ? me.stat : 0, Add());
+            keep = keep && before < mass_target(p, all);
         }
         keep = keep && uint32_t(me.order >> 32) >= k_min_p;
-        const u64 total_first = x.block_first(keep ? me.stat : 0, add);
-        if (tid == 0) s.word[0] = total_first;
-        __syncthreads();
+        const u64 total = x.block_all(keep ? me.stat : 0, Add()), target = draw_target(u, total);
         if (tid < n) s.list[tid].stat = keep ? me.stat : 0;
         __syncthreads();
-        const u64 total = s.word[0], target = draw_target(u, total);
         if (keep) {
             u64 run = 0;
             for (int j = 0; j < n; ++j) {
@@ -742,87 +799,71 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a,
             if (run <= target && target < run + me.stat)
                 finish(int(~uint32_t(me.order)), log_prob(value_of(uint32_t(me.order >> 32)), x.top, temp, total));
         }
+        __syncwarp();
+        if (n_cta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         return;
     }
-    if (k_min_p > x.K) {
-        x.K = k_min_p;
-        x.I = V;
+    if (k_min_p > key_of(x.low)) {
+        x.low = value_of(k_min_p);
+        x.I = a.V;
         know_mass = false;
     }
-    auto stat = [&](float l, int i) -> u64 { return x.kept(key_of(l), i) ? x.units(l) : 0; };
-    auto sums = [&]() {
+    if (!know_mass) {
         Weight m{0, 0};
         x.each([&](float l, int i) {
-            if (x.kept(key_of(l), i)) m += x.weigh(l);
+            if (x.kept(l, i)) m += x.weigh(l);
         });
-        x.warp_sums(m.units());
-    };
-    if (!know_mass) {
-        sums();
-        if (tid == 0) {
-            u64 t = 0;
-            for (int w = 0; w < kWarps; ++w) t += s.warp_sum[w];
-            s.out[0] = t;
-        }
-    } else if (tid == 0) {
-        s.out[0] = s.word[3];
+        const u64 mine = x.warp_all(m.units(), Add());
+        __syncthreads();
+        if (x.lane == 0) s.warp_sum[x.wid] = mine;
+        __syncthreads();
     }
-    const auto got = x.exchange(1);
-    u64 run = 0, total = 0;
-    for (int r = 0; r < n_cta; ++r) {
-        if (r < x.rank) run += got[r][0];
-        total += got[r][0];
+    const u64 mine = x.warp_all(x.lane < kWarps ? s.warp_sum[x.lane] : 0ull, Add());
+    u64 run = 0, total = mine;
+    if (n_cta > 1) {
+        if (tid == 0) s.out[0] = mine;
+        const auto got = x.exchange(1);
+        total = 0;
+        for (int r = 0; r < n_cta; ++r) {
+            if (r < x.rank) run += got[r][0];
+            total += got[r][0];
+        }
     }
     const u64 target = draw_target(u, total);
-    if (!(run <= target && target < run + got[x.rank][0])) return;
-    if (know_mass) sums();
-    x.find(target, run, stat, [&](float l, int i) { finish(i, log_prob(l, x.top, temp, total)); });
+    if (run <= target && target < run + mine)
+        x.find(target, run, s.warp_sum, [&](float l, int i) -> u64 { return x.kept(l, i) ? x.units(l) : 0; },
+               [&](float l, int i) { finish(i, log_prob(l, x.top, temp, total)); });
 }
 
-// CTAs per row, a power of two up to 16
-int row_ctas(int rows, int vocab, int elem, int sms) {
-    const size_t bytes = size_t(vocab) * elem + 16;
+// CTAs per row, a power of two up to 16, and threads per CTA
+struct Plan {
+    int n_cta, threads;
+};
+Plan plan_of(int rows, int vocab, int sms) {
     int n = 1;
-    while (n < kMaxCluster && bytes / n > 64 * 1024) n *= 2;
-    // few rows: more CTAs each, while they are not more than two per SM and have a few vectors a thread
-    while (n < kMaxCluster && rows * n * 2 <= 2 * sms && bytes / (2 * n) >= 8 * 1024) n *= 2;
-    return n;
+    while (n < kMaxCluster && (long long)rows * n * 2 <= sms && vocab / (2 * n) >= 4096) n *= 2;
+    return {n, n == 1 && vocab > 8192 ? 1024 : 512};
 }
 
-template <typename L> cudaError_t launch_t(const SampleArgs &a, int sms, cudaStream_t stream) {
-    const int n = row_ctas(a.B * a.T, a.V, sizeof(L), sms);
-    constexpr int E = Vec<L>::N;
+template <typename L, int NT> cudaError_t launch_t(const SampleArgs &a, int n, cudaStream_t stream) {
+    constexpr int E = 16 / sizeof(L);
     const int row_vecs = (a.V + 2 * E - 2) / E;              // whatever its first vector's alignment
     const int vecs = (row_vecs + n - 1) / n;
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + size_t(vecs) * 16;
-    auto kern = sample_kernel<L>;
-    // function attributes belong to the context: the limits raised so far, by context id
-    struct Attrs {
-        int smem = 0;
-        bool nonportable = false;
-    };
-    static PerContext<Attrs> attrs;
+    auto kern = sample_kernel<L, NT>;
+    // function attributes belong to the context: set once in each
+    static PerContext<int> attrs;
     unsigned long long ctx = 0;
-    Attrs have;
-    const bool known = current_context_id(&ctx) && attrs.get(ctx, &have);
-    if (!known || int(smem) > have.smem || (n > 8 && !have.nonportable)) {
-        cudaError_t e = cudaSuccess;
-        if (int(smem) > have.smem) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-            if (e != cudaSuccess) return e;
-            have.smem = int(smem);
-        }
-        if (n > 8 && !have.nonportable) {
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            have.nonportable = true;
-        }
-        if (current_context_id(&ctx)) attrs.put(ctx, have);
+    int set = 0;
+    if (!(current_context_id(&ctx) && attrs.get(ctx, &set))) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (current_context_id(&ctx)) attrs.put(ctx, 1);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.B) * unsigned(a.T) * unsigned(n), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(NT, 1, 1);
+    cfg.dynamicSmemBytes = sizeof(Shared);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -839,7 +880,12 @@ template <typename L> cudaError_t launch_t(const SampleArgs &a, int sms, cudaStr
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream) {
-    return dtype == GDN_BF16 ? launch_t<__nv_bfloat16>(a, sm_count, stream) : launch_t<float>(a, sm_count, stream);
+    const Plan plan = plan_of(a.B * a.T, a.V, sm_count);
+    if (plan.threads == 1024)
+        return dtype == GDN_BF16 ? launch_t<__nv_bfloat16, 1024>(a, plan.n_cta, stream)
+                                 : launch_t<float, 1024>(a, plan.n_cta, stream);
+    return dtype == GDN_BF16 ? launch_t<__nv_bfloat16, 512>(a, plan.n_cta, stream)
+                             : launch_t<float, 512>(a, plan.n_cta, stream);
 }
 
 }  // namespace gdn

@@ -26,13 +26,7 @@ constexpr uint32_t kNone = 0x007fffffu;       // the key of -inf: a token that c
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// NaN counts as masked, -0 as 0
-template <typename L>
-__device__ __forceinline__ float clean(L x) {
-    const float f = to_float(x);
-    return f != f ? -INFINITY : f + 0.0f;
-}
-// order-preserving 32-bit key of a float that is not NaN, and back
+// order-preserving 32-bit key of a float that is neither NaN nor -0, and back
 __device__ __forceinline__ uint32_t key_of(float f) {
     const uint32_t b = __float_as_uint(f);
     return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
@@ -87,16 +81,17 @@ __device__ __forceinline__ Scale scale_of(float temp) {
     return {h, __fdiv_rn(fmaf(-h, temp, L) + Ll, temp)};
 }
 
-// hi * 2^22 + lo units of 2^-44, lo signed: up to 256 of them add up word by word
+// hi * 2^22 + lo units of 2^-44, |lo| at most 2^21: up to 1000 of them add up word by word
 struct Weight {
-    int hi, lo;
+    uint32_t hi;
+    int lo;
     __device__ __forceinline__ Weight &operator+=(const Weight &o) {
         hi += o.hi;
         lo += o.lo;
         return *this;
     }
     __device__ __forceinline__ unsigned long long units() const {
-        return (unsigned long long)((long long)hi * 4194304 + lo);
+        return ((unsigned long long)hi << 22) + (long long)lo;
     }
 };
 
@@ -122,8 +117,8 @@ __device__ __forceinline__ Weight weight(float l, float top, Scale c, const Weig
     constexpr float M1 = 3.0f, M2 = 0x1.8p-21f;
     const float t1 = hs + M1, t2 = ((hs - (t1 - M1)) + ls) + M2;
     const bool some = y > -45.5f;                  // else below half a unit (or masked: y is -inf)
-    Weight w{some ? __float_as_int(t1) - __float_as_int(M1) : 0, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
-    if (l == top) w = {1 << 22, 0};                // inf - inf above
+    Weight w{some ? __float_as_uint(t1) - __float_as_uint(M1) : 0u, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
+    if (l == top) w = {1u << 22, 0};                // inf - inf above
     return w;
 }
 

@@ -91,6 +91,25 @@ def test_large_vocabularies(V, dtype):
           top_p=[1.0, 0.95, 0.9, 1.0], min_p=[0.0, 0.0, 0.0, 0.03])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("std,temp", [(1.0, 1.3), (0.05, 1.0), (4.0, 900.0), (2.0, 2.0 ** 20), (6.0, 0.02)])
+def test_borders_among_many_tokens(std, temp, dtype):
+    # nearly flat rows: thousands of tokens around the border, equal ones (bf16) or different ones
+    l = logits_of(6, 150001, dtype, seed=40, std=std)
+    check(l, uniforms(6, seed=41), temp=[temp] * 6, top_p=[0.3, 0.7, 0.95, 0.999, 1.0, 0.9],
+          top_k=[0, 0, 0, 0, 40000, 100000])
+    check(l, uniforms(6, seed=42), temp=[temp] * 6, top_k=[600, 3000, 20000, 75000, 150000, 1023])
+
+
+@pytest.mark.parametrize("rows", [1, 3, 40, 80, 200])
+def test_launch_shapes(rows):
+    # from many CTAs a row to one; the first k tokens in one place, so that few threads hold them
+    l = logits_of(rows, 30011, seed=50 + rows)
+    l[:, 4000:4400] += 20.0
+    check(l, uniforms(rows, seed=3), temp=[0.9] * rows, top_k=[(7 * i) % 390 + 1 for i in range(rows)],
+          top_p=[1.0 if i % 2 else 0.9 for i in range(rows)])
+
+
 @pytest.mark.parametrize("pad", [1, 3, 8, 61])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_row_strides_and_what_lies_between_rows(pad, dtype):
