@@ -597,8 +597,11 @@ static int project(const char *what, const gdn_dims *dims, const void *W, const 
     bool ok;
     if (lora) {
         const gdn::LoraArgs a{lora->n_adapters, lora->rank, dims->n_tokens, lora->a, lora->b, lora->scale, d_adapter,
-                              static_cast<float *>(scratch)};
-        ok = gdn::gemm_xwt_lora_bf16(W, X, Y, M, N, K, ldc, a, d_status, st, why);
+                              scratch};
+        if ((long long)lora->n_adapters * N > 0x7fffff00LL || (long long)M * 64 > 0x7fffff00LL)
+            return fail(GDN_ERR_SHAPE, "%s projection: %d adapters of %d columns, or %d rows, are too many", what,
+                        lora->n_adapters, N, M);
+        ok = gdn::gemm_xwt_lora_bf16(W, X, Y, M, N, K, ldc, a, dev_info().sms, d_status, st, why);
     } else {
         ok = gdn::gemm_xwt_bf16(W, X, Y, M, N, K, ldc, d_status, st, why);
     }
@@ -679,7 +682,7 @@ int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const
 
 size_t gdn_lora_workspace_bytes(const gdn_dims *dims, int rank) {
     if (!dims || dims->n_slots < 1 || dims->n_tokens < 1 || rank < 8 || rank > 128 || rank % 8) return 0;
-    return align256(gdn::lora_scratch_bytes((long long)dims->n_slots * dims->n_tokens, rank));
+    return align256(gdn::lora_scratch_bytes(dims->n_slots, dims->n_tokens, rank));
 }
 
 int gdn_project_in_lora(const gdn_dims *dims, const gdn_proj_weights *w, const gdn_lora *lora, const int32_t *d_adapter,

@@ -121,15 +121,17 @@ struct LoraArgs {
     const void *a, *b;                // [n_adapters][rank][K], [n_adapters][N][rank] bf16
     const float *scale;               // [n_adapters] or NULL (1)
     const int32_t *adapter;           // [slots]
-    float *h;                         // scratch: lora_scratch_bytes
+    void *h;                          // scratch: lora_scratch_bytes
 };
 
 // Returns a cudaError_t of the launch (cudaSuccess when enqueued).
 cudaError_t launch_sample(const SampleArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptArgs &a, cudaStream_t stream);
-// h = scale * X A^T per slot; reports an adapter id that names none.
-cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &lora, int *d_status, cudaStream_t stream);
-size_t lora_scratch_bytes(long long M, int rank);
+// h = scale * X A^T per slot and group of 16 rows; reports an adapter id that names none.
+cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &lora, int sms, int *d_status, cudaStream_t stream);
+size_t lora_scratch_bytes(long long slots, int T, int rank);
+// Aligned groups of 16 rows that the T rows of one slot may touch.
+int lora_groups_per_slot(int T);
 cudaError_t launch_verify(const VerifyArgs &a, gdn_dtype act, int sm_count, cudaStream_t stream);
 cudaError_t launch_rollback(const RollbackArgs &a, cudaStream_t stream);
 
@@ -149,7 +151,7 @@ bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, l
 
 // The same with the low-rank term of each slot's adapter added to the fp32 sums.
 bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, const LoraArgs &lora,
-                        int *d_status, cudaStream_t stream, std::string &why);
+                        int sms, int *d_status, cudaStream_t stream, std::string &why);
 
 // cuTensorMapEncodeTiled from the driver, looked up once (NULL if unavailable).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

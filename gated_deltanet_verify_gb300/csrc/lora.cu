@@ -1,7 +1,23 @@
 // lora.cu -- the first half of a low-rank adapter: h = scale_a X A_a^T, each
-// slot's rows with the slot's own adapter.  The second half, h B_a^T, is added
-// to the shared projection's fp32 sums in the GEMM's epilogue (proj.cu), so a
-// projection with adapters rounds once, like one without.  h stays in fp32.
+// slot's rows with the slot's own adapter.  The second half, h B_a^T, goes
+// through the tensor cores into the accumulators of the shared projection
+// (proj.cu), so a projection with adapters rounds its output once, like one
+// without.
+//
+// Unit of work: a pair of a slot and one of the aligned groups of 16 rows of X
+// that its rows touch (rows of other slots count as zero), because the second
+// half is a product over such groups.  h is summed in fp32 and stored as two
+// bf16 numbers, head and tail, 2^-17 of it being lost at most: the two products
+// that this costs the tensor cores are cheaper than fp32 arithmetic, and one
+// bf16 alone would lose as much as the output's own rounding.
+//
+// X and A are read once each per pair, straight from global memory into the
+// fragments of mma.sync (m16n8k16, bf16, fp32 sums): with K permuted alike on
+// both sides a lane's fragments of two k steps are 16 contiguous bytes of a
+// row.  The work is a stream of A at best (r K elements a slot), and a chain of
+// a few loads at one slot; so K is split over a cluster of up to 8 CTAs and
+// their 8 warps, and the sums are joined through distributed shared memory in a
+// fixed order.
 #include "internal.cuh"
 
 #include <cuda_bf16.h>
@@ -9,48 +25,160 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxSplit = 8;
 
-// one warp per (row, rank column)
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const __nv_bfloat16 *X, int M, int K, const LoraArgs a,
-                                                               int *d_status) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+struct ShrinkArgs {
+    const __nv_bfloat16 *X, *A;
+    int M, K, T, r, P, n_adapters;
+    const int32_t *adapter;
+    const float *scale;
+    __nv_bfloat16 *h;                // [pair][head, tail][16][r]
+    int *d_status;
+};
+
+__device__ __forceinline__ uint32_t map_cluster(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld16(const __nv_bfloat16 *p, bool ok) {
+    return ok ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// R8: rank / 8 at most, the tiles of eight rank columns held in registers
+template <int R8>
+__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs a) {
+    extern __shared__ float part[];              // [warp][16][r]; the first [16][r] holds the CTA's sum afterwards
+    // the projection may start on its own weights; it waits for this grid's results itself
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const long long i = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (i >= (long long)M * a.rank) return;
-    const int m = int(i / a.rank), j = int(i % a.rank);
-    const int id = a.adapter[m / a.T];
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int pair = blockIdx.x, s = pair / a.P, j = pair % a.P;
+    const int group = s * a.T / 16 + j;
+    if (group * 16 >= (s + 1) * a.T) return;     // the slot's rows end before: uniform over the cluster
+    const int id = a.adapter[s];
     if (id < 0 || id >= a.n_adapters) {
-        if ((id < -1 || id >= a.n_adapters) && lane == 0 && d_status)
-            atomicCAS(d_status, int(GDN_OK), int(GDN_ERR_ADAPTER));
+        if (id != -1 && threadIdx.x == 0 && a.d_status) atomicCAS(a.d_status, int(GDN_OK), int(GDN_ERR_ADAPTER));
         return;
     }
-    const __nv_bfloat16 *x = X + (size_t)m * K;
-    const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(a.a) + ((size_t)id * a.rank + j) * K;
-    float acc = 0.f;
-    for (int k = lane; k < K; k += 32) acc = fmaf(__bfloat162float(x[k]), __bfloat162float(w[k]), acc);
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int r = a.r, n8 = r / 8, S = gridDim.y, split = blockIdx.y;
+    const int m0 = group * 16 + g, m1 = m0 + 8, lo = s * a.T, hi = min(a.M, lo + a.T);
+    const bool in0 = m0 >= lo && m0 < hi, in1 = m1 >= lo && m1 < hi;
+    const __nv_bfloat16 *x0 = a.X + (size_t)m0 * a.K, *x1 = a.X + (size_t)m1 * a.K;
+    const __nv_bfloat16 *w = a.A + ((size_t)id * r + g) * a.K;
+    float acc[R8][4];
 #pragma unroll
-    for (int s = 16; s; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-    if (lane == 0) a.h[i] = a.scale ? a.scale[id] * acc : acc;
+    for (int n = 0; n < R8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+    for (int k0 = (split * kWarps + wid) * 32; k0 < a.K; k0 += S * kWarps * 32) {
+        const int k = k0 + 8 * t;
+        const bool ok = k < a.K;                 // K is a multiple of 8
+        const uint4 p = ld16(x0 + k, ok && in0), q = ld16(x1 + k, ok && in1);
+        uint4 b[R8];
+#pragma unroll
+        for (int n = 0; n < R8; ++n) b[n] = ld16(w + (size_t)n * 8 * a.K + k, ok && n < n8);
+#pragma unroll
+        for (int n = 0; n < R8; ++n) {
+            mma16816(acc[n], p.x, q.x, p.y, q.y, b[n].x, b[n].y);
+            mma16816(acc[n], p.z, q.z, p.w, q.w, b[n].z, b[n].w);
+        }
+    }
+    float *mine = part + wid * 16 * r;
+#pragma unroll
+    for (int n = 0; n < R8; ++n)
+        if (n < n8) {
+            *reinterpret_cast<float2 *>(mine + g * r + n * 8 + 2 * t) = make_float2(acc[n][0], acc[n][1]);
+            *reinterpret_cast<float2 *>(mine + (g + 8) * r + n * 8 + 2 * t) = make_float2(acc[n][2], acc[n][3]);
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * r; i += kThreads) {
+        float v = part[i];
+#pragma unroll
+        for (int q = 1; q < kWarps; ++q) v += part[q * 16 * r + i];
+        part[i] = v;                             // only this thread reads or writes element i of any warp
+    }
+    const float scale = a.scale ? a.scale[id] : 1.0f;
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    // the CTAs of the cluster share out the elements
+    for (int i = split * kThreads + threadIdx.x; i < 16 * r; i += S * kThreads) {
+        float v = 0.f;
+        if (S == 1) v = part[i];
+        else
+            for (int q = 0; q < S; ++q) v += ld_cluster(map_cluster(part + i, q));
+        // rows of other slots are zero whatever the adapter holds
+        const int m = group * 16 + i / r;
+        v = m >= lo && m < hi ? v * scale : 0.f;
+        const __nv_bfloat16 head = __float2bfloat16_rn(v);
+        const float rest = v - __bfloat162float(head);
+        // an infinite or NaN h stays what it is
+        const __nv_bfloat16 tail = __float2bfloat16_rn(rest - rest == 0.f ? rest : 0.f);
+        __nv_bfloat16 *to = a.h + (size_t)pair * 32 * r + i;
+        to[0] = head;
+        to[16 * r] = tail;
+    }
+    if (S > 1) cluster_sync();                   // the peers have read this CTA's sums
+}
+
+template <int R8> cudaError_t launch_t(const ShrinkArgs &a, int pairs, int sms, cudaStream_t stream) {
+    // CTAs a pair: while they fit the SMs twice over, and every warp has a k step
+    int S = 1;
+    while (S < kMaxSplit && (long long)pairs * S * 2 <= 2LL * sms && a.K >= 2 * S * kWarps * 32) S *= 2;
+    const size_t smem = size_t(kWarps) * 16 * a.r * 4;
+    auto kern = lora_shrink_kernel<R8>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(pairs), unsigned(S), 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = S;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 }  // namespace
 
-size_t lora_scratch_bytes(long long M, int rank) { return size_t(M) * rank * 4; }
+int lora_groups_per_slot(int T) { return T % 16 == 0 ? T / 16 : (T + 14) / 16 + 1; }
 
-cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &lora, int *d_status, cudaStream_t stream) {
-    const long long warps = (long long)M * lora.rank;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((warps + kThreads / 32 - 1) / (kThreads / 32)), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, lora_shrink_kernel, static_cast<const __nv_bfloat16 *>(X), M, K, lora, d_status);
+size_t lora_scratch_bytes(long long slots, int T, int rank) {
+    return size_t(slots) * lora_groups_per_slot(T) * 32 * rank * 2;
+}
+
+cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &l, int sms, int *d_status, cudaStream_t stream) {
+    const int P = lora_groups_per_slot(l.T);
+    const ShrinkArgs a{static_cast<const __nv_bfloat16 *>(X), static_cast<const __nv_bfloat16 *>(l.a), M, K, l.T, l.rank, P,
+                       l.n_adapters, l.adapter, l.scale, static_cast<__nv_bfloat16 *>(l.h), d_status};
+    const int pairs = M / l.T * P;
+    if (l.rank <= 16) return launch_t<2>(a, pairs, sms, stream);
+    if (l.rank <= 32) return launch_t<4>(a, pairs, sms, stream);
+    if (l.rank <= 64) return launch_t<8>(a, pairs, sms, stream);
+    return launch_t<16>(a, pairs, sms, stream);
 }
 
 }  // namespace gdn

@@ -36,11 +36,16 @@
 //     split's shared memory (distributed shared memory), and after a second
 //     barrier the first split adds them to its own in split order and writes
 //     bf16.  No global scratch, and the sum's order is fixed.
+//   * With low-rank adapters (LoraTerm) the ring goes on after the K blocks with
+//     the adapters' B tiles and the matching rows of h: the same MMAs with N = 16,
+//     each into the columns of its 16 activation rows.  Warp 3 lists them while
+//     the K blocks stream.
 //   * Every wait is bounded; a wait that gives up reports GDN_ERR_TIMEOUT on
 //     the caller's status word (when one is given) and the tile is skipped.
 #include "internal.cuh"
 
 #include <cuda_bf16.h>
+#include <type_traits>
 
 namespace gdn {
 namespace {
@@ -66,15 +71,26 @@ struct GemmArgs {
     int *d_status;
 };
 
-// A low-rank term beside the product, by the slot (T rows of X) a row belongs to: row m gets
-// h[m][0 .. r) . B[adapter[m / T]][n][0 .. r) more, added to the fp32 sum before its one rounding.
+// A low-rank term beside the product, by the slot (T rows of X) a row belongs to (h by lora.cu): units of an aligned
+// group of 16 rows, one slot's part of it and 64 rank columns, D[:, group] += B_tile (h_head + h_tail)^T.  They follow
+// the K blocks through the same ring of stages; a stage holds `per_stage` units of kUnit bytes (the B tile's 64-column
+// box, then the 32 rows of head and tail).
 struct LoraTerm {
-    const __nv_bfloat16 *B;             // [n_adapters][N][r]
-    const float *h;                     // [M][r], the adapter's scale in it
+    CUtensorMap b_map, h_map;           // [n_adapters * N][r]; [pairs * 32][r]
     const int32_t *adapter;             // [slots]; outside [0, n_adapters): no term
-    int n_adapters, r, T;
+    int n_adapters, r, T, P;            // P: groups a slot's rows may touch
+    int per_stage;
 };
 struct NoTerm {};
+constexpr uint32_t kUnit = 16384 + 4096;
+struct Unit {
+    int h_row, b_row, column, box;      // column: of D
+};
+// the most units a block of Mt rows can have: its slots (T rows each) and the groups they cut, by 64 rank columns
+__host__ __device__ constexpr int max_units(int Mt, int T, int r) {
+    const int slots = (Mt + T - 1) / T + 1;
+    return ((slots < Mt ? slots : Mt) + Mt / 16) * ((r + 63) / 64);
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -174,41 +190,31 @@ __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence
 __host__ __device__ constexpr uint32_t w_stage_bytes() { return kTileN * kKBlk * 2; }
 __host__ __device__ inline uint32_t x_stage_bytes(int Mt) { return (uint32_t)Mt * kKBlk * 2; }
 
-// v[q] += the low-rank term of rows m .. m + 15 at column n
-__device__ __forceinline__ void add_term(const LoraTerm &t, int m, int M, int n, int N, float *v) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");      // h, by the kernel before
-    if (n >= N) return;
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-        if (m + q >= M) break;
-        const int id = t.adapter[(m + q) / t.T];
-        if (id < 0 || id >= t.n_adapters) continue;
-        const __nv_bfloat16 *b = t.B + ((size_t)id * N + n) * t.r;
-        const float *h = t.h + (size_t)(m + q) * t.r;
-        float acc = 0.f;
-        for (int j = 0; j < t.r; ++j) acc = fmaf(h[j], __bfloat162float(b[j]), acc);
-        v[q] += acc;
-    }
-}
-__device__ __forceinline__ void add_term(const NoTerm &, int, int, int, int, float *) {}
-
 template <typename Term>
-__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a, const Term term) {
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a,
+                                                        const __grid_constant__ Term term) {
     extern __shared__ __align__(1024) unsigned char sm[];
-    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];   // full[stages], empty[stages], done (2 arrivals)
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];   // full[stages], empty[stages], done (2 arrivals), units
     __shared__ uint32_t tslot;
+    __shared__ int n_units;
+    constexpr bool kLora = std::is_same<Term, LoraTerm>::value;
     const int tid = threadIdx.x, wid = tid >> 5;
     const int nt = blockIdx.x, mb = blockIdx.y, split = blockIdx.z;   // the splits of a tile: one cluster
     const int n0 = nt * kTileN, m0 = mb * a.Mt;
     const int kb0 = split * a.kb_per_split;
     const int kb1 = min(a.n_kb, kb0 + a.kb_per_split);
+    // K blocks of this CTA; with a term both issuers' accumulators are in use, so both get one: past the split's own
+    // it is one past the end of K, which reads zeros
+    const int nb = kLora ? max(kb1 - kb0, 2) : kb1 - kb0;
+    auto k_of = [&](int i) { return (kLora && kb0 + i >= kb1 ? a.n_kb : kb0 + i) * kKBlk; };
     const int S = a.stages;
     const uint32_t wbytes = w_stage_bytes(), xbytes = x_stage_bytes(a.Mt);
     const uint32_t stage_bytes = wbytes + xbytes;
     const uint32_t sbase = (smem_u32(sm) + 1023u) & ~1023u;   // swizzled tiles start on 1024 bytes
     auto full = [&](int s) { return smem_u32(&bars[s]); };
     auto empty = [&](int s) { return smem_u32(&bars[kMaxStages + s]); };
-    const uint32_t done = smem_u32(&bars[2 * kMaxStages]);
+    const uint32_t done = smem_u32(&bars[2 * kMaxStages]), listed = smem_u32(&bars[2 * kMaxStages + 1]);
+    Unit *units = reinterpret_cast<Unit *>(sm + (sbase - smem_u32(sm)) + (size_t)S * stage_bytes);
 
     if (wid == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&tslot)),
@@ -221,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             mbar_init(empty(s), 1);
         }
         mbar_init(done, 2);
+        mbar_init(listed, 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     fence_before_sync();
@@ -231,26 +238,41 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     if (tid == 0) {
         // ---- producer: the weight boxes of the first stages go out before the dependency wait
-        const int pre = min(S, kb1 - kb0);
+        const int pre = min(S, nb);
         const uint32_t xbox = (uint32_t)a.Mt * 128;            // bytes of one X box
         for (int i = 0; i < pre; ++i) {
             const uint32_t st = sbase + (uint32_t)i * stage_bytes;
             mbar_expect_tx(full(i), stage_bytes);
-            for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, (kb0 + i) * kKBlk + 64 * b, n0, full(i));
+            for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(i));
         }
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         for (int i = 0; i < pre; ++i)
             for (int b = 0; b < kBoxes; ++b)
-                tma_box(sbase + (uint32_t)i * stage_bytes + wbytes + b * xbox, &a.x_map, (kb0 + i) * kKBlk + 64 * b, m0,
+                tma_box(sbase + (uint32_t)i * stage_bytes + wbytes + b * xbox, &a.x_map, k_of(i) + 64 * b, m0,
                         full(i));
-        for (int i = pre; i < kb1 - kb0 && ok; ++i) {
+        for (int i = pre; i < nb && ok; ++i) {
             const int s = i % S;
             ok = mbar_wait(empty(s), ((i / S) - 1) & 1);       // the MMAs of stage use i - S are done
             const uint32_t st = sbase + (uint32_t)s * stage_bytes;
             mbar_expect_tx(full(s), stage_bytes);
-            for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, (kb0 + i) * kKBlk + 64 * b, n0, full(s));
+            for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(s));
             for (int b = 0; b < kBoxes; ++b)
-                tma_box(st + wbytes + b * xbox, &a.x_map, (kb0 + i) * kKBlk + 64 * b, m0, full(s));
+                tma_box(st + wbytes + b * xbox, &a.x_map, k_of(i) + 64 * b, m0, full(s));
+        }
+        if constexpr (kLora) {
+            ok = ok && mbar_wait(listed, 0);
+            const int n = ok ? n_units : 0;
+            for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += term.per_stage) {
+                const int s = i % S, un = min(term.per_stage, n - u0);
+                if (i >= S) ok = mbar_wait(empty(s), ((i / S) - 1) & 1);
+                const uint32_t st = sbase + (uint32_t)s * stage_bytes;
+                mbar_expect_tx(full(s), (uint32_t)un * kUnit);
+                for (int u = 0; u < un; ++u) {
+                    const Unit q = units[u0 + u];
+                    tma_box(st + (uint32_t)u * kUnit, &term.b_map, 64 * q.box, q.b_row, full(s));
+                    tma_box(st + (uint32_t)u * kUnit + 16384u, &term.h_map, 64 * q.box, q.h_row, full(s));
+                }
+            }
         }
     } else if (tid == 32 || tid == 64) {
         // ---- MMA issuers: the even or the odd stages of the ring into accumulator e (8 MMAs of K = 16 per stage);
@@ -261,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const int e = wid - 1;
         const uint32_t acc = tmem + (uint32_t)(e * a.Mt);
         const uint32_t id = idesc_bf16(a.Mt);
-        for (int i = e; i < kb1 - kb0 && ok; ++i) {
+        for (int i = e; i < nb && ok; ++i) {
             const int s = i % S;
             if ((s & 1) != e) continue;
             ok = mbar_wait(full(s), (i / S) & 1);
@@ -275,7 +297,57 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             }
             mma_commit(empty(s));
         }
+        if constexpr (kLora) {
+            ok = ok && mbar_wait(listed, 0);
+            const int n = ok ? n_units : 0;
+            for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += term.per_stage) {
+                const int s = i % S, un = min(term.per_stage, n - u0);
+                if ((s & 1) != e) continue;
+                ok = mbar_wait(full(s), (i / S) & 1);
+                fence_after_sync();
+                for (int u = 0; u < un; ++u) {
+                    const Unit q = units[u0 + u];
+                    const uint32_t b = sbase + (uint32_t)s * stage_bytes + (uint32_t)u * kUnit, h = b + 16384u;
+                    const int steps = (min(64, term.r - 64 * q.box) + 15) / 16;
+                    for (int j = 0; j < steps; ++j) {
+                        mma_bf16(acc + q.column, make_desc_sw128(b + 32u * j), make_desc_sw128(h + 32u * j), idesc_bf16(16), 1u);
+                        mma_bf16(acc + q.column, make_desc_sw128(b + 32u * j), make_desc_sw128(h + 2048u + 32u * j),
+                                 idesc_bf16(16), 1u);
+                    }
+                }
+                mma_commit(empty(s));
+            }
+        }
         mma_commit(done);
+    } else if (kLora && wid == 3) {
+        // ---- the units of this block and split, in slot order
+        if constexpr (kLora) {
+            asm volatile("griddepcontrol.wait;\n" ::: "memory");
+            const int lane = tid & 31, rows = min(a.M, m0 + a.Mt), s0 = m0 / term.T, s1 = (rows - 1) / term.T;
+            const int boxes = (term.r + 63) / 64;
+            int n = 0;                                   // of all splits
+            for (int sb = s0; sb <= s1; sb += 32) {
+                const int s = sb + lane, id = s <= s1 ? term.adapter[s] : -1;
+                const int first = s * term.T / 16;       // the slot's first group
+                const int g0 = max(first, m0 / 16), g1 = min(((s + 1) * term.T - 1) / 16, (rows - 1) / 16);
+                const int mine = id >= 0 && id < term.n_adapters ? (g1 - g0 + 1) * boxes : 0;
+                int to = mine;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int o = __shfl_up_sync(0xffffffffu, to, d);
+                    if (lane >= d) to += o;
+                }
+                for (int q = 0; q < mine; ++q) {
+                    const int at = n + to - mine + q, g = g0 + q / boxes;
+                    if (at % a.splits == split)
+                        units[at / a.splits] = {(s * term.P + g - first) * 32, id * a.N + n0, g * 16 - m0, q % boxes};
+                }
+                n += __shfl_sync(0xffffffffu, to, 31);
+            }
+            if (lane == 0) n_units = (n - split + a.splits - 1) / a.splits;
+            __syncwarp();
+            if (lane == 0) asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.release.cta.shared::cta.b64 st, [%0];\n\t}\n" ::"r"(listed) : "memory");
+        }
     }
     __syncwarp();
     // ---- epilogue: the accumulator of weight row n0 + tid, every activation row of the block
@@ -284,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     // one verdict for the whole CTA (the collective TMEM loads below need every lane of a warp)
     const bool good = __syncthreads_and(got && ok) != 0;
     if (!good && tid == 0 && a.d_status) atomicCAS(a.d_status, int(GDN_OK), int(GDN_ERR_TIMEOUT));
-    const int n_acc = kb1 - kb0 > 1 ? 2 : 1;                 // the odd stages' accumulator holds a sum only if used
+    const int n_acc = nb > 1 ? 2 : 1;                 // the odd stages' accumulator holds a sum only if used
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int n = n0 + tid;
     const uint32_t taddr = tmem + ((uint32_t)(32 * wid) << 16);
@@ -293,7 +365,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int c0 = 0; c0 < a.Mt; c0 += 16) {
                 float v[16];
                 tmem_ld16_sum(taddr + c0, n_acc, a.Mt, v);
-                add_term(term, m0 + c0, a.M, n, a.N, v);
                 if (n < a.N)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
@@ -319,7 +390,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int c0 = 0; c0 < a.Mt; c0 += 16) {
                 float v[16];
                 tmem_ld16_sum(taddr + c0, n_acc, a.Mt, v);
-                add_term(term, m0 + c0, a.M, n, a.N, v);
                 if (n < a.N)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
@@ -349,8 +419,9 @@ static int gemm_splits(int n_tiles, int m_blocks, int n_kb, int Mt, size_t smem,
 }
 
 template <typename Term>
-static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, const Term &term,
+static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, Term &term,
                         int *d_status, cudaStream_t stream, std::string &why) {
+    constexpr bool kLora = std::is_same<Term, LoraTerm>::value;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) {
         why = "the driver's tensor-map encoder is unavailable";
@@ -382,8 +453,12 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
         why = "pipeline stage larger than shared memory";
         return false;
     }
-    const size_t smem = (size_t)a.stages * stage + 1024;          // + room to align the tiles to 1024 bytes
+    size_t smem = (size_t)a.stages * stage + 1024;                // + room to align the tiles to 1024 bytes
     const int splits = gemm_splits(n_tiles, m_blocks, a.n_kb, a.Mt, smem - 1024, sms);
+    if constexpr (kLora) {
+        smem += (size_t)max_units(a.Mt, term.T, term.r) * sizeof(Unit);
+        term.per_stage = (int)(stage / kUnit);
+    }
     a.kb_per_split = (a.n_kb + splits - 1) / splits;
     a.splits = (a.n_kb + a.kb_per_split - 1) / a.kb_per_split;
     a.C = static_cast<__nv_bfloat16 *>(C);
@@ -439,17 +514,41 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
 
 bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, int *d_status,
                    cudaStream_t stream, std::string &why) {
-    return gemm_launch(W, X, C, M, N, K, ldc, NoTerm{}, d_status, stream, why);
+    NoTerm none;
+    return gemm_launch(W, X, C, M, N, K, ldc, none, d_status, stream, why);
 }
 
 bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, const LoraArgs &lora,
-                        int *d_status, cudaStream_t stream, std::string &why) {
-    const cudaError_t e = launch_lora_shrink(X, M, K, lora, d_status, stream);
+                        int sms, int *d_status, cudaStream_t stream, std::string &why) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) {
+        why = "the driver's tensor-map encoder is unavailable";
+        return false;
+    }
+    LoraTerm term{};
+    term.adapter = lora.adapter;
+    term.n_adapters = lora.n_adapters; term.r = lora.rank; term.T = lora.T;
+    term.P = lora_groups_per_slot(lora.T);
+    // 64-column boxes in the 128-byte swizzle: 128 rows of B, the 16 + 16 rows of a pair's head and tail
+    const cuuint32_t estr[2] = {1, 1};
+    auto map = [&](CUtensorMap *m, const void *p, cuuint64_t rows, cuuint32_t box_rows) {
+        const cuuint64_t dims[2] = {(cuuint64_t)lora.rank, rows};
+        const cuuint64_t strides[1] = {(cuuint64_t)lora.rank * 2};
+        const cuuint32_t box[2] = {64u, box_rows};
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!map(&term.b_map, lora.b, (cuuint64_t)lora.n_adapters * N, kTileN) ||
+        !map(&term.h_map, lora.h, (cuuint64_t)(M / lora.T) * term.P * 32, 32)) {
+        why = "adapter tensor map";
+        return false;
+    }
+    const cudaError_t e = launch_lora_shrink(X, M, K, lora, sms, d_status, stream);
     if (e != cudaSuccess) {
         why = std::string("adapter launch: ") + cudaGetErrorString(e);
         return false;
     }
-    const LoraTerm term{static_cast<const __nv_bfloat16 *>(lora.b), lora.h, lora.adapter, lora.n_adapters, lora.rank, lora.T};
     return gemm_launch(W, X, C, M, N, K, ldc, term, d_status, stream, why);
 }
 

@@ -329,14 +329,16 @@ int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const
  * Low-rank adapters beside the shared projections: every slot of a batch may
  * run with an adapter of its own.  For row m of slot s, with a = d_adapter[s],
  *   act[m] = w_in x[m] + scale[a] * B[a] (A[a] x[m])
- * (and the same for the output projection), in fp32 and rounded to bf16 once;
- * A[a] x is held in fp32 too.  d_adapter is a DEVICE int32[n_slots]: -1 runs
- * the slot without an adapter (its rows are then bit-identical to
- * gdn_project_in / gdn_project_out); another id outside [0, n_adapters) does
- * the same and writes GDN_ERR_ADAPTER to *d_status.  Several slots may name the
- * same adapter.  Adapters of a lower rank are padded with zero rows of A and
- * zero columns of B.  The pages have no adapters; the projections they stand
- * beside are those of internal.h, TargetLayer.
+ * (and the same for the output projection), with fp32 sums and one rounding to
+ * bf16; scale[a] * A[a] x is summed in fp32 and carried to 2^-17 of itself (as
+ * two bf16 numbers).  d_adapter is a DEVICE int32[n_slots]: -1 runs the slot
+ * without an adapter (its rows then equal gdn_project_in's / gdn_project_out's);
+ * another id outside [0, n_adapters) does the same and writes GDN_ERR_ADAPTER
+ * to *d_status.  Several slots may name the same adapter.  Adapters of a lower
+ * rank are padded with zero rows of A and zero columns of B.  B must be finite
+ * (slots that share an aligned group of 16 rows share a product in which the
+ * others' rows of h are zero).  The pages have no adapters; the projections they
+ * stand beside are those of internal.h, TargetLayer.
  *
  * Limits: those of gdn_project_in; rank a multiple of 8, 8..128 (GDN_ERR_SHAPE).
  * workspace: gdn_lora_workspace_bytes (0 on bad arguments), 256-byte aligned;

@@ -67,7 +67,8 @@ def accept_tree_row(parent, draft, tokens, length, T):
 def lora(x, w, a, b, scale, ids, T):
     """(y, bound) for x [M][K], w [N][K], a [n][r][K], b [n][N][r] in fp64: the product with each slot's adapter,
     and how far a kernel with fp32 sums and one bf16 rounding may be off.  A sum of n fp32 products is off by at most
-    n 2^-24 of the sum of their magnitudes (taken twice); h = A x enters B h with its own error."""
+    n 2^-24 of the sum of their magnitudes (taken twice); h = A x enters B h with its own error and is carried as two
+    bf16 numbers: the tail's half step is 2^-8 of at most 2^-8 of it."""
     y = x @ w.T
     mag = np.abs(x) @ np.abs(w).T
     K, r = x.shape[1], a.shape[1]
@@ -78,5 +79,5 @@ def lora(x, w, a, b, scale, ids, T):
             h = scale[i] * (x[rows] @ a[i].T)
             hm = abs(scale[i]) * (np.abs(x[rows]) @ np.abs(a[i]).T)
             y[rows] += h @ b[i].T
-            err[rows] += (K + r + 8) * 2.0 ** -23 * (hm @ np.abs(b[i]).T)
+            err[rows] += ((K + 2 * r + 8) * 2.0 ** -23 * hm + 2.0 ** -16 * np.abs(h)) @ np.abs(b[i]).T
     return y, 2.0 ** -8 * (np.abs(y) + err) + err

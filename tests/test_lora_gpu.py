@@ -111,6 +111,20 @@ def test_a_slot_without_an_adapter_is_the_shared_projection_bit_for_bit(side, kw
     assert torch.equal(c.run(), base)          # a term of zeros
 
 
+def test_a_slot_does_not_see_its_neighbours():
+    # slots that share groups of 16 rows: an infinite input, scale or A of one leaves the others' rows as they were
+    s = shape_of(n_slots=6, n_tokens=5)
+    c = Case(s, "in", 3, 16, [0, 1, 2, -1, 1, 0])
+    want = c.run().clone()
+    c.x[5:10] = float("inf")
+    c.scale[2] = float("inf")
+    c.a[2, 3] = float("nan")
+    got = c.run()
+    for slot in (0, 3, 4, 5):
+        assert torch.equal(got[5 * slot:5 * slot + 5], want[5 * slot:5 * slot + 5]), slot
+    assert not torch.isfinite(got[5:15].float()).any()
+
+
 @pytest.mark.parametrize("bad", [-2, 3, 2 ** 31 - 1])
 def test_an_unknown_adapter_is_reported_and_runs_without(bad):
     c = Case(shape_of(), "in", 3, 16, [0, bad, 2])
