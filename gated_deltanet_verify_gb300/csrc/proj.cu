@@ -30,12 +30,12 @@
 //     while the previous kernel finishes.
 //   * Epilogue: thread t of the 128 reads TMEM lane t (weight row n0 + t)
 //     and writes column n0 + t of every output row.  With K split S ways the
-//     S CTAs of a tile form a thread-block cluster: after a cluster barrier
-//     (every split's MMAs are done, so the first split's pipeline buffers are
-//     free) the other splits write their fp32 partial tiles into the first
-//     split's shared memory (distributed shared memory), and after a second
-//     barrier the first split adds them to its own in split order and writes
-//     bf16.  No global scratch, and the sum's order is fixed.
+//     S CTAs of a tile form a thread-block cluster and share out its columns:
+//     after a cluster barrier (every split's MMAs are done, so the pipeline
+//     buffers are free) each writes the others' columns of its fp32 partial tile
+//     into their shared memory (distributed shared memory), and after a second
+//     barrier each adds up its own columns in split order and writes bf16.  No
+//     global scratch, and the sum's order is fixed.
 //   * With low-rank adapters (LoraTerm) the ring goes on after the K blocks with
 //     the adapters' B tiles and the matching rows of h: the same MMAs with N = 16,
 //     each into the columns of its 16 activation rows.  Warp 3 lists them while
@@ -177,8 +177,8 @@ __device__ __forceinline__ uint32_t map_cluster(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(local), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -373,33 +373,51 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     }
             }
     } else {
-        // partial tiles of splits 1 .. S-1 -> the first split's shared memory, [split-1][column][row]
-        cluster_sync();                            // every split's MMAs are done: split 0's buffers are free
-        if (split > 0) {
-            const uint32_t dst = map_cluster(sbase, 0) + (uint32_t)((split - 1) * a.Mt * kTileN + tid) * 4u;
-            for (int c0 = 0; c0 < a.Mt; c0 += 16) {
-                float v[16];
-                tmem_ld16_sum(taddr + c0, n_acc, a.Mt, v);
+        // The splits share out the 16-column chunks (chunk c is split c % splits's): each sends the others' chunks of its
+        // partial tile to their owners, as [sender][four columns][row][4], and adds up its own in split order.
+        // (One owner for all and scalar stores took 0.17 us a column: 36 us for 128 rows of the output projection.)
+        constexpr uint32_t kChunk = 16 * kTileN * 4;
+        cluster_sync();                            // every split's MMAs are done: the pipeline buffers are free
+        for (int c = 0; 16 * c < a.Mt; ++c) {
+            const int owner = c % a.splits;
+            if (owner == split) continue;
+            float v[16];
+            tmem_ld16_sum(taddr + 16 * c, n_acc, a.Mt, v);
+            const int from = split < owner ? split : split - 1;
+            const uint32_t dst = map_cluster(sbase, owner) + (uint32_t)((c / a.splits) * (a.splits - 1) + from) * kChunk + tid * 16u;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) st_cluster_f32(dst + (uint32_t)((c0 + q) * kTileN) * 4u, good ? v[q] : 0.f);
+            for (int q = 0; q < 4; ++q) {
+                const float *p = v + 4 * q;
+                st_cluster_f32x4(dst + (uint32_t)q * kTileN * 16u, good ? p[0] : 0.f, good ? p[1] : 0.f, good ? p[2] : 0.f,
+                                 good ? p[3] : 0.f);
             }
         }
         cluster_sync();                            // every partial has landed
-        if (split == 0 && good) {
-            const float *red = reinterpret_cast<const float *>(sm + (sbase - smem_u32(sm)));
-            for (int c0 = 0; c0 < a.Mt; c0 += 16) {
-                float v[16];
-                tmem_ld16_sum(taddr + c0, n_acc, a.Mt, v);
+        if (good)
+            for (int c = split; 16 * c < a.Mt; c += a.splits) {
+                float v[16], acc[16];
+                tmem_ld16_sum(taddr + 16 * c, n_acc, a.Mt, v);
+                const float4 *red = reinterpret_cast<const float4 *>(sm + (sbase - smem_u32(sm)) +
+                                                                     (size_t)(c / a.splits) * (a.splits - 1) * kChunk) + tid;
+                for (int sp = 0; sp < a.splits; ++sp) {
+                    const int from = sp < split ? sp : sp - 1;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float4 w = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                        if (sp != split) w = red[(size_t)from * (kChunk / 16) + q * kTileN];
+                        acc[4 * q] = sp ? acc[4 * q] + w.x : w.x;
+                        acc[4 * q + 1] = sp ? acc[4 * q + 1] + w.y : w.y;
+                        acc[4 * q + 2] = sp ? acc[4 * q + 2] + w.z : w.z;
+                        acc[4 * q + 3] = sp ? acc[4 * q + 3] + w.w : w.w;
+                    }
+                }
                 if (n < a.N)
 #pragma unroll
                     for (int q = 0; q < 16; ++q) {
-                        const int m = m0 + c0 + q;
-                        float acc = v[q];
-                        for (int sp = 1; sp < a.splits; ++sp) acc += red[((sp - 1) * a.Mt + c0 + q) * kTileN + tid];
-                        if (m < a.M) a.C[(size_t)m * a.ldc + n] = __float2bfloat16_rn(acc);
+                        const int m = m0 + 16 * c + q;
+                        if (m < a.M) a.C[(size_t)m * a.ldc + n] = __float2bfloat16_rn(acc[q]);
                     }
             }
-        }
     }
     fence_before_sync();
     __syncthreads();
