@@ -65,9 +65,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 template <int R8>
 __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs a) {
     extern __shared__ float part[];              // [warp][16][r]; the first [16][r] holds the CTA's sum afterwards
-    // the projection may start on its own weights; it waits for this grid's results itself
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    // The projection starts once every CTA here has seen the kernel before complete, so it may read X at once; it
+    // waits for this grid's results itself.
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int pair = blockIdx.x, s = pair / a.P, j = pair % a.P;
     const int group = s * a.T / 16 + j;
     if (group * 16 >= (s + 1) * a.T) return;     // the slot's rows end before: uniform over the cluster
@@ -85,18 +86,27 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
     float acc[R8][4];
 #pragma unroll
     for (int n = 0; n < R8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-    for (int k0 = (split * kWarps + wid) * 32; k0 < a.K; k0 += S * kWarps * 32) {
-        const int k = k0 + 8 * t;
-        const bool ok = k < a.K;                 // K is a multiple of 8
-        const uint4 p = ld16(x0 + k, ok && in0), q = ld16(x1 + k, ok && in1);
-        uint4 b[R8];
+    // the loads of kAhead steps are in flight at once
+    constexpr int kAhead = R8 <= 8 ? 4 : 2;
+    const int step = S * kWarps * 32;
+    for (int k0 = (split * kWarps + wid) * 32; k0 < a.K; k0 += kAhead * step) {
+        uint4 p[kAhead], q[kAhead], b[kAhead][R8];
 #pragma unroll
-        for (int n = 0; n < R8; ++n) b[n] = ld16(w + (size_t)n * 8 * a.K + k, ok && n < n8);
+        for (int h = 0; h < kAhead; ++h) {
+            const int k = k0 + h * step + 8 * t;
+            const bool ok = k < a.K;             // K is a multiple of 8
+            p[h] = ld16(x0 + k, ok && in0);
+            q[h] = ld16(x1 + k, ok && in1);
 #pragma unroll
-        for (int n = 0; n < R8; ++n) {
-            mma16816(acc[n], p.x, q.x, p.y, q.y, b[n].x, b[n].y);
-            mma16816(acc[n], p.z, q.z, p.w, q.w, b[n].z, b[n].w);
+            for (int n = 0; n < R8; ++n) b[h][n] = ld16(w + (size_t)n * 8 * a.K + k, ok && n < n8);
         }
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int n = 0; n < R8; ++n) {
+                mma16816(acc[n], p[h].x, q[h].x, p[h].y, q[h].y, b[h][n].x, b[h][n].y);
+                mma16816(acc[n], p[h].z, q[h].z, p[h].w, q[h].w, b[h][n].z, b[h][n].w);
+            }
     }
     float *mine = part + wid * 16 * r;
 #pragma unroll
@@ -117,10 +127,15 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
     else __syncthreads();
     // the CTAs of the cluster share out the elements
     for (int i = split * kThreads + threadIdx.x; i < 16 * r; i += S * kThreads) {
-        float v = 0.f;
-        if (S == 1) v = part[i];
-        else
-            for (int q = 0; q < S; ++q) v += ld_cluster(map_cluster(part + i, q));
+        float v = part[i];
+        if (S > 1) {
+            float w[kMaxSplit];                  // all in flight at once
+#pragma unroll
+            for (int q = 0; q < kMaxSplit; ++q) w[q] = q < S ? ld_cluster(map_cluster(part + i, q)) : 0.f;
+            v = w[0];
+#pragma unroll
+            for (int q = 1; q < kMaxSplit; ++q) v += w[q];
+        }
         // rows of other slots are zero whatever the adapter holds
         const int m = group * 16 + i / r;
         v = m >= lo && m < hi ? v * scale : 0.f;

@@ -72,17 +72,16 @@ struct GemmArgs {
 };
 
 // A low-rank term beside the product, by the slot (T rows of X) a row belongs to (h by lora.cu): units of an aligned
-// group of 16 rows, one slot's part of it and 64 rank columns, D[:, group] += B_tile (h_head + h_tail)^T.  They follow
-// the K blocks through the same ring of stages; a stage holds `per_stage` units of kUnit bytes (the B tile's 64-column
-// box, then the 32 rows of head and tail).
+// group of 16 rows, one slot's part of it and up to 64 rank columns, D[:, group] += B_tile (h_head + h_tail)^T.  They
+// follow the K blocks through the same ring of stages; a stage holds several units (the B tile's box, 128 rows of
+// `width` columns, then the 32 rows of head and tail), whose swizzle is as wide as their rows: 32, 64 or 128 bytes.
 struct LoraTerm {
     CUtensorMap b_map, h_map;           // [n_adapters * N][r]; [pairs * 32][r]
     const int32_t *adapter;             // [slots]; outside [0, n_adapters): no term
     int n_adapters, r, T, P;            // P: groups a slot's rows may touch
-    int per_stage;
+    int width;                          // rank columns a unit: 16, 32 or 64
 };
 struct NoTerm {};
-constexpr uint32_t kUnit = 16384 + 4096;
 struct Unit {
     int h_row, b_row, column, box;      // column: of D
 };
@@ -90,6 +89,15 @@ struct Unit {
 __host__ __device__ constexpr int max_units(int Mt, int T, int r) {
     const int slots = (Mt + T - 1) / T + 1;
     return ((slots < Mt ? slots : Mt) + Mt / 16) * ((r + 63) / 64);
+}
+// rank columns a unit, and its bytes
+__host__ __device__ constexpr int unit_width(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
+__host__ __device__ constexpr uint32_t unit_bytes(int width) { return (uint32_t)(kTileN + 32) * width * 2; }
+// n units in steps of the ring: a stage's fill each, but both issuers busy
+__device__ __forceinline__ int units_per_step(int n, uint32_t stage_bytes, int width) {
+    const int fill = (int)(stage_bytes / unit_bytes(width));
+    const int steps = max((n + fill - 1) / fill, min(n, 2));
+    return steps ? (n + steps - 1) / steps : 1;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
@@ -136,6 +144,11 @@ __device__ __forceinline__ uint64_t make_desc_sw128(uint32_t saddr) {
     d |= (uint64_t)1 << 46;                                    // descriptor version (sm_100 family)
     d |= (uint64_t)2 << 61;                                    // layout: 128-byte swizzle
     return d;
+}
+// the same for rows of `width` bf16 columns (16, 32 or 64) in the swizzle of that width
+__device__ __forceinline__ uint64_t make_desc_sw(uint32_t saddr, int width) {
+    const uint64_t layout = width == 16 ? 6 : width == 32 ? 4 : 2;
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(width) << 32 | (uint64_t)1 << 46 | layout << 61;
 }
 // instruction descriptor: kind::f16 with bf16 A and B, fp32 D, both K-major, M = 128
 __host__ __device__ constexpr uint32_t idesc_bf16(int N) {
@@ -245,7 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             mbar_expect_tx(full(i), stage_bytes);
             for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(i));
         }
-        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        // with adapters the kernel before is the one that computes h: it lets this one start only when X is there, and
+        // the wait for h is warp 3's
+        if constexpr (!kLora) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         for (int i = 0; i < pre; ++i)
             for (int b = 0; b < kBoxes; ++b)
                 tma_box(sbase + (uint32_t)i * stage_bytes + wbytes + b * xbox, &a.x_map, k_of(i) + 64 * b, m0,
@@ -262,15 +277,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         if constexpr (kLora) {
             ok = ok && mbar_wait(listed, 0);
             const int n = ok ? n_units : 0;
-            for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += term.per_stage) {
-                const int s = i % S, un = min(term.per_stage, n - u0);
+            const int per = units_per_step(n, stage_bytes, term.width);
+            const uint32_t ub = unit_bytes(term.width), hb = (uint32_t)kTileN * term.width * 2;
+            for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += per) {
+                const int s = i % S, un = min(per, n - u0);
                 if (i >= S) ok = mbar_wait(empty(s), ((i / S) - 1) & 1);
                 const uint32_t st = sbase + (uint32_t)s * stage_bytes;
-                mbar_expect_tx(full(s), (uint32_t)un * kUnit);
+                mbar_expect_tx(full(s), (uint32_t)un * ub);
                 for (int u = 0; u < un; ++u) {
                     const Unit q = units[u0 + u];
-                    tma_box(st + (uint32_t)u * kUnit, &term.b_map, 64 * q.box, q.b_row, full(s));
-                    tma_box(st + (uint32_t)u * kUnit + 16384u, &term.h_map, 64 * q.box, q.h_row, full(s));
+                    tma_box(st + (uint32_t)u * ub, &term.b_map, 64 * q.box, q.b_row, full(s));
+                    tma_box(st + (uint32_t)u * ub + hb, &term.h_map, 64 * q.box, q.h_row, full(s));
                 }
             }
         }
@@ -300,19 +317,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         if constexpr (kLora) {
             ok = ok && mbar_wait(listed, 0);
             const int n = ok ? n_units : 0;
-            for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += term.per_stage) {
-                const int s = i % S, un = min(term.per_stage, n - u0);
+            const int per = units_per_step(n, stage_bytes, term.width);
+            const uint32_t ub = unit_bytes(term.width), hb = (uint32_t)kTileN * term.width * 2, tail = 32u * term.width;
+            for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += per) {
+                const int s = i % S, un = min(per, n - u0);
                 if ((s & 1) != e) continue;
                 ok = mbar_wait(full(s), (i / S) & 1);
                 fence_after_sync();
                 for (int u = 0; u < un; ++u) {
                     const Unit q = units[u0 + u];
-                    const uint32_t b = sbase + (uint32_t)s * stage_bytes + (uint32_t)u * kUnit, h = b + 16384u;
+                    const uint32_t b = sbase + (uint32_t)s * stage_bytes + (uint32_t)u * ub, h = b + hb;
                     const int steps = (min(64, term.r - 64 * q.box) + 15) / 16;
                     for (int j = 0; j < steps; ++j) {
-                        mma_bf16(acc + q.column, make_desc_sw128(b + 32u * j), make_desc_sw128(h + 32u * j), idesc_bf16(16), 1u);
-                        mma_bf16(acc + q.column, make_desc_sw128(b + 32u * j), make_desc_sw128(h + 2048u + 32u * j),
-                                 idesc_bf16(16), 1u);
+                        const uint64_t bd = make_desc_sw(b + 32u * j, term.width);
+                        mma_bf16(acc + q.column, bd, make_desc_sw(h + 32u * j, term.width), idesc_bf16(16), 1u);
+                        mma_bf16(acc + q.column, bd, make_desc_sw(h + tail + 32u * j, term.width), idesc_bf16(16), 1u);
                     }
                 }
                 mma_commit(empty(s));
@@ -339,8 +358,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 }
                 for (int q = 0; q < mine; ++q) {
                     const int at = n + to - mine + q, g = g0 + q / boxes;
-                    if (at % a.splits == split)
-                        units[at / a.splits] = {(s * term.P + g - first) * 32, id * a.N + n0, g * 16 - m0, q % boxes};
+                    if (at % a.splits != split) continue;
+                    const Unit u{(s * term.P + g - first) * 32, id * a.N + n0, g * 16 - m0, q % boxes};
+                    units[at / a.splits] = u;
+                    // its B tile comes at the end of the ring: into L2 by then
+                    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(
+                                     reinterpret_cast<uint64_t>(&term.b_map)),
+                                 "r"(64 * u.box), "r"(u.b_row)
+                                 : "memory");
                 }
                 n += __shfl_sync(0xffffffffu, to, 31);
             }
@@ -475,7 +500,6 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
     const int splits = gemm_splits(n_tiles, m_blocks, a.n_kb, a.Mt, smem - 1024, sms);
     if constexpr (kLora) {
         smem += (size_t)max_units(a.Mt, term.T, term.r) * sizeof(Unit);
-        term.per_stage = (int)(stage / kUnit);
     }
     a.kb_per_split = (a.n_kb + splits - 1) / splits;
     a.splits = (a.n_kb + a.kb_per_split - 1) / a.kb_per_split;
@@ -547,14 +571,18 @@ bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int
     term.adapter = lora.adapter;
     term.n_adapters = lora.n_adapters; term.r = lora.rank; term.T = lora.T;
     term.P = lora_groups_per_slot(lora.T);
-    // 64-column boxes in the 128-byte swizzle: 128 rows of B, the 16 + 16 rows of a pair's head and tail
+    term.width = unit_width(lora.rank);
+    const CUtensorMapSwizzle swizzle = term.width == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                       : term.width == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                          : CU_TENSOR_MAP_SWIZZLE_128B;
+    // boxes of `width` columns: 128 rows of B, the 16 + 16 rows of a pair's head and tail
     const cuuint32_t estr[2] = {1, 1};
     auto map = [&](CUtensorMap *m, const void *p, cuuint64_t rows, cuuint32_t box_rows) {
         const cuuint64_t dims[2] = {(cuuint64_t)lora.rank, rows};
         const cuuint64_t strides[1] = {(cuuint64_t)lora.rank * 2};
-        const cuuint32_t box[2] = {64u, box_rows};
+        const cuuint32_t box[2] = {(cuuint32_t)term.width, box_rows};
         return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, estr,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     if (!map(&term.b_map, lora.b, (cuuint64_t)lora.n_adapters * N, kTileN) ||
