@@ -61,10 +61,10 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// R8: rank / 8 at most, the tiles of eight rank columns held in registers
+// R8: the tiles of eight rank columns held in registers, at most; more than 64 columns go to CTAs by 64
 template <int R8>
 __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs a) {
-    extern __shared__ float part[];              // [warp][16][r]; the first [16][r] holds the CTA's sum afterwards
+    extern __shared__ float part[];              // [warp][16][rl]; the first [16][rl] holds the CTA's sum afterwards
     // The projection starts once every CTA here has seen the kernel before complete, so it may read X at once; it
     // waits for this grid's results itself.
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -78,16 +78,16 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
         return;
     }
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int r = a.r, n8 = r / 8, S = gridDim.y, split = blockIdx.y;
+    const int r = a.r, j0 = blockIdx.z * 64, rl = min(64, r - j0), n8 = rl / 8, S = gridDim.y, split = blockIdx.y;
     const int m0 = group * 16 + g, m1 = m0 + 8, lo = s * a.T, hi = min(a.M, lo + a.T);
     const bool in0 = m0 >= lo && m0 < hi, in1 = m1 >= lo && m1 < hi;
     const __nv_bfloat16 *x0 = a.X + (size_t)m0 * a.K, *x1 = a.X + (size_t)m1 * a.K;
-    const __nv_bfloat16 *w = a.A + ((size_t)id * r + g) * a.K;
+    const __nv_bfloat16 *w = a.A + ((size_t)id * r + j0 + g) * a.K;
     float acc[R8][4];
 #pragma unroll
     for (int n = 0; n < R8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
     // the loads of kAhead steps are in flight at once
-    constexpr int kAhead = R8 <= 8 ? 4 : 2;
+    constexpr int kAhead = 4;
     const int step = S * kWarps * 32;
     for (int k0 = (split * kWarps + wid) * 32; k0 < a.K; k0 += kAhead * step) {
         uint4 p[kAhead], q[kAhead], b[kAhead][R8];
@@ -108,25 +108,25 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
                 mma16816(acc[n], p[h].z, q[h].z, p[h].w, q[h].w, b[h][n].z, b[h][n].w);
             }
     }
-    float *mine = part + wid * 16 * r;
+    float *mine = part + wid * 16 * rl;
 #pragma unroll
     for (int n = 0; n < R8; ++n)
         if (n < n8) {
-            *reinterpret_cast<float2 *>(mine + g * r + n * 8 + 2 * t) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2 *>(mine + (g + 8) * r + n * 8 + 2 * t) = make_float2(acc[n][2], acc[n][3]);
+            *reinterpret_cast<float2 *>(mine + g * rl + n * 8 + 2 * t) = make_float2(acc[n][0], acc[n][1]);
+            *reinterpret_cast<float2 *>(mine + (g + 8) * rl + n * 8 + 2 * t) = make_float2(acc[n][2], acc[n][3]);
         }
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * r; i += kThreads) {
+    for (int i = threadIdx.x; i < 16 * rl; i += kThreads) {
         float v = part[i];
 #pragma unroll
-        for (int q = 1; q < kWarps; ++q) v += part[q * 16 * r + i];
+        for (int q = 1; q < kWarps; ++q) v += part[q * 16 * rl + i];
         part[i] = v;                             // only this thread reads or writes element i of any warp
     }
     const float scale = a.scale ? a.scale[id] : 1.0f;
     if (S > 1) cluster_sync();
     else __syncthreads();
     // the CTAs of the cluster share out the elements
-    for (int i = split * kThreads + threadIdx.x; i < 16 * r; i += S * kThreads) {
+    for (int i = split * kThreads + threadIdx.x; i < 16 * rl; i += S * kThreads) {
         float v = part[i];
         if (S > 1) {
             float w[kMaxSplit];                  // all in flight at once
@@ -137,13 +137,13 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
             for (int q = 1; q < kMaxSplit; ++q) v += w[q];
         }
         // rows of other slots are zero whatever the adapter holds
-        const int m = group * 16 + i / r;
+        const int m = group * 16 + i / rl;
         v = m >= lo && m < hi ? v * scale : 0.f;
         const __nv_bfloat16 head = __float2bfloat16_rn(v);
         const float rest = v - __bfloat162float(head);
         // an infinite or NaN h stays what it is
         const __nv_bfloat16 tail = __float2bfloat16_rn(rest - rest == 0.f ? rest : 0.f);
-        __nv_bfloat16 *to = a.h + (size_t)pair * 32 * r + i;
+        __nv_bfloat16 *to = a.h + ((size_t)pair * 32 + i / rl) * r + j0 + i % rl;
         to[0] = head;
         to[16 * r] = tail;
     }
@@ -151,17 +151,14 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
 }
 
 template <int R8> cudaError_t launch_t(const ShrinkArgs &a, int pairs, int sms, cudaStream_t stream) {
-    // CTAs a pair: while they fit the SMs twice over, and every warp has a k step
+    // CTAs a pair and 64 rank columns: while all fit the SMs twice over, and every warp has a k step
+    const int parts = (a.r + 63) / 64;
     int S = 1;
-    while (S < kMaxSplit && (long long)pairs * S * 2 <= 2LL * sms && a.K >= 2 * S * kWarps * 32) S *= 2;
-    const size_t smem = size_t(kWarps) * 16 * a.r * 4;
+    while (S < kMaxSplit && (long long)pairs * parts * S * 2 <= 2LL * sms && a.K >= 2 * S * kWarps * 32) S *= 2;
+    const size_t smem = size_t(kWarps) * 16 * (a.r < 64 ? a.r : 64) * 4;
     auto kern = lora_shrink_kernel<R8>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(pairs), unsigned(S), 1);
+    cfg.gridDim = dim3(unsigned(pairs), unsigned(S), unsigned(parts));
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -192,8 +189,7 @@ cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &l, i
     const int pairs = M / l.T * P;
     if (l.rank <= 16) return launch_t<2>(a, pairs, sms, stream);
     if (l.rank <= 32) return launch_t<4>(a, pairs, sms, stream);
-    if (l.rank <= 64) return launch_t<8>(a, pairs, sms, stream);
-    return launch_t<16>(a, pairs, sms, stream);
+    return launch_t<8>(a, pairs, sms, stream);
 }
 
 }  // namespace gdn

@@ -203,11 +203,12 @@ __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence
 __host__ __device__ constexpr uint32_t w_stage_bytes() { return kTileN * kKBlk * 2; }
 __host__ __device__ inline uint32_t x_stage_bytes(int Mt) { return (uint32_t)Mt * kKBlk * 2; }
 
-template <typename Term>
+// H: the parts a stage is filled and freed in (its boxes of 64 K columns shared out), each with its own barriers
+template <typename Term, int H>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a,
                                                         const __grid_constant__ Term term) {
     extern __shared__ __align__(1024) unsigned char sm[];
-    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];   // full[stages], empty[stages], done (2 arrivals), units
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];   // full and empty by stage and half, done (2 arrivals), units
     __shared__ uint32_t tslot;
     __shared__ int n_units;
     constexpr bool kLora = std::is_same<Term, LoraTerm>::value;
@@ -224,8 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     const uint32_t wbytes = w_stage_bytes(), xbytes = x_stage_bytes(a.Mt);
     const uint32_t stage_bytes = wbytes + xbytes;
     const uint32_t sbase = (smem_u32(sm) + 1023u) & ~1023u;   // swizzled tiles start on 1024 bytes
-    auto full = [&](int s) { return smem_u32(&bars[s]); };
-    auto empty = [&](int s) { return smem_u32(&bars[kMaxStages + s]); };
+    constexpr int kPart = kBoxes / H;
+    static_assert(kBoxes % H == 0, "whole boxes");
+    auto full = [&](int s, int h = 0) { return smem_u32(&bars[s * H + h]); };
+    auto empty = [&](int s, int h = 0) { return smem_u32(&bars[kMaxStages + s * H + h]); };
     const uint32_t done = smem_u32(&bars[2 * kMaxStages]), listed = smem_u32(&bars[2 * kMaxStages + 1]);
     Unit *units = reinterpret_cast<Unit *>(sm + (sbase - smem_u32(sm)) + (size_t)S * stage_bytes);
 
@@ -235,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     }
     if (tid == 32) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+        for (int s = 0; s < S * H; ++s) {
+            mbar_init(smem_u32(&bars[s]), 1);
+            mbar_init(smem_u32(&bars[kMaxStages + s]), 1);
         }
         mbar_init(done, 2);
         mbar_init(listed, 1);
@@ -255,8 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const uint32_t xbox = (uint32_t)a.Mt * 128;            // bytes of one X box
         for (int i = 0; i < pre; ++i) {
             const uint32_t st = sbase + (uint32_t)i * stage_bytes;
-            mbar_expect_tx(full(i), stage_bytes);
-            for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(i));
+            for (int b = 0; b < kBoxes; ++b) {
+                if (b % kPart == 0) mbar_expect_tx(full(i, b / kPart), stage_bytes / H);
+                tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(i, b / kPart));
+            }
         }
         // with adapters the kernel before is the one that computes h: it lets this one start only when X is there, and
         // the wait for h is warp 3's
@@ -264,15 +269,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         for (int i = 0; i < pre; ++i)
             for (int b = 0; b < kBoxes; ++b)
                 tma_box(sbase + (uint32_t)i * stage_bytes + wbytes + b * xbox, &a.x_map, k_of(i) + 64 * b, m0,
-                        full(i));
+                        full(i, b / kPart));
         for (int i = pre; i < nb && ok; ++i) {
             const int s = i % S;
-            ok = mbar_wait(empty(s), ((i / S) - 1) & 1);       // the MMAs of stage use i - S are done
             const uint32_t st = sbase + (uint32_t)s * stage_bytes;
-            mbar_expect_tx(full(s), stage_bytes);
-            for (int b = 0; b < kBoxes; ++b) tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(s));
-            for (int b = 0; b < kBoxes; ++b)
-                tma_box(st + wbytes + b * xbox, &a.x_map, k_of(i) + 64 * b, m0, full(s));
+            for (int h = 0; h < H && ok; ++h) {
+                ok = mbar_wait(empty(s, h), ((i / S) - 1) & 1);       // the MMAs of stage use i - S are done
+                mbar_expect_tx(full(s, h), stage_bytes / H);
+                for (int b = h * kPart; b < (h + 1) * kPart; ++b)
+                    tma_box(st + b * 16384u, &a.w_map, k_of(i) + 64 * b, n0, full(s, h));
+                for (int b = h * kPart; b < (h + 1) * kPart; ++b)
+                    tma_box(st + wbytes + b * xbox, &a.x_map, k_of(i) + 64 * b, m0, full(s, h));
+            }
         }
         if constexpr (kLora) {
             ok = ok && mbar_wait(listed, 0);
@@ -281,8 +289,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const uint32_t ub = unit_bytes(term.width), hb = (uint32_t)kTileN * term.width * 2;
             for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += per) {
                 const int s = i % S, un = min(per, n - u0);
-                if (i >= S) ok = mbar_wait(empty(s), ((i / S) - 1) & 1);
+                for (int h = 0; h < H; ++h)                          // units take the stage whole
+                    if (i >= S) ok = ok && mbar_wait(empty(s, h), ((i / S) - 1) & 1);
                 const uint32_t st = sbase + (uint32_t)s * stage_bytes;
+                for (int h = 1; h < H; ++h) mbar_expect_tx(full(s, h), 0);
                 mbar_expect_tx(full(s), (uint32_t)un * ub);
                 for (int u = 0; u < un; ++u) {
                     const Unit q = units[u0 + u];
@@ -303,16 +313,19 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         for (int i = e; i < nb && ok; ++i) {
             const int s = i % S;
             if ((s & 1) != e) continue;
-            ok = mbar_wait(full(s), (i / S) & 1);
-            fence_after_sync();
             const uint32_t st = sbase + (uint32_t)s * stage_bytes;
+            for (int h = 0; h < H; ++h) {
+                ok = ok && mbar_wait(full(s, h), (i / S) & 1);
+                fence_after_sync();
 #pragma unroll
-            for (int j = 0; j < kKBlk / 16; ++j) {          // 16 columns (32 bytes of each row) per MMA
-                const uint32_t b = j >> 2, c = 32u * (j & 3);
-                mma_bf16(acc, make_desc_sw128(st + b * 16384u + c),
-                         make_desc_sw128(st + wbytes + b * (uint32_t)a.Mt * 128u + c), id, (i > e || j > 0) ? 1u : 0u);
+                for (int j = 0; j < kKBlk / 16; ++j) {          // 16 columns (32 bytes of each row) per MMA
+                    const uint32_t b = j >> 2, c = 32u * (j & 3);
+                    if ((int)b / kPart == h)
+                        mma_bf16(acc, make_desc_sw128(st + b * 16384u + c),
+                                 make_desc_sw128(st + wbytes + b * (uint32_t)a.Mt * 128u + c), id, (i > e || j > 0) ? 1u : 0u);
+                }
+                mma_commit(empty(s, h));
             }
-            mma_commit(empty(s));
         }
         if constexpr (kLora) {
             ok = ok && mbar_wait(listed, 0);
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += per) {
                 const int s = i % S, un = min(per, n - u0);
                 if ((s & 1) != e) continue;
-                ok = mbar_wait(full(s), (i / S) & 1);
+                for (int h = 0; h < H; ++h) ok = ok && mbar_wait(full(s, h), (i / S) & 1);
                 fence_after_sync();
                 for (int u = 0; u < un; ++u) {
                     const Unit q = units[u0 + u];
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         mma_bf16(acc + q.column, bd, make_desc_sw(h + tail + 32u * j, term.width), idesc_bf16(16), 1u);
                     }
                 }
-                mma_commit(empty(s));
+                for (int h = 0; h < H; ++h) mma_commit(empty(s, h));
             }
         }
         mma_commit(done);
@@ -496,6 +509,9 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
         why = "pipeline stage larger than shared memory";
         return false;
     }
+    // a ring of two stages (more than 160 activation rows) moves by halves, so that three of its four are in flight
+    // while one feeds the MMAs
+    auto kern = a.stages == 2 ? gemm_kernel<Term, kBoxes> : gemm_kernel<Term, 1>;
     size_t smem = (size_t)a.stages * stage + 1024;                // + room to align the tiles to 1024 bytes
     const int splits = gemm_splits(n_tiles, m_blocks, a.n_kb, a.Mt, smem - 1024, sms);
     if constexpr (kLora) {
@@ -529,7 +545,7 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
             return false;
         }
     }
-    cudaError_t e = cudaFuncSetAttribute(gemm_kernel<Term>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n_tiles, m_blocks, a.splits);
@@ -545,7 +561,7 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
         attr[1].val.clusterDim.z = a.splits;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, gemm_kernel<Term>, a, term);
+        e = cudaLaunchKernelEx(&cfg, kern, a, term);
     }
     if (e != cudaSuccess) {
         why = std::string("projection GEMM launch: ") + cudaGetErrorString(e);
