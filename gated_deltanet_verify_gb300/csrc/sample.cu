@@ -150,7 +150,7 @@ struct Sampler {
     int I;
 
     __device__ __forceinline__ bool kept(float l, int i) const { return l > low || (l == low && i <= I); }
-    __device__ __forceinline__ Weight weigh(float l) const { return weight(l, top, sc, s.table); }
+    __device__ __forceinline__ Weight weigh(float l) const { return weight<sizeof(L) == 4>(l, top, sc, s.table); }
     __device__ __forceinline__ u64 units(float l) const { return weigh(l).units(); }
     // the logit at which bin b (or cell b of bins of 1/kFine) begins, going down
     __device__ __forceinline__ float edge_of(float b, float scale) const {
@@ -809,10 +809,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         know_mass = false;
     }
     if (!know_mass) {
+        // I is set where top-k or top-p ended among equals: else the logit alone decides
         Weight m{0, 0};
-        x.each([&](float l, int i) {
-            if (x.kept(l, i)) m += x.weigh(l);
-        });
+        if (x.I == a.V)
+            x.each([&](float l, int) {
+                if (l >= x.low) m += x.weigh(l);
+            });
+        else
+            x.each([&](float l, int i) {
+                if (x.kept(l, i)) m += x.weigh(l);
+            });
         const u64 mine = x.warp_all(m.units(), Add());
         __syncthreads();
         if (x.lane == 0) s.warp_sum[x.wid] = mine;
@@ -840,9 +846,16 @@ struct Plan {
     int n_cta, threads;
 };
 Plan plan_of(int rows, int vocab, int sms) {
+    // few rows: one CTA of 512 threads per SM in all, 4096 tokens each at least (16 rows of 131072, top-p: 4, 8 and 16
+    // CTAs take 58, 50 and 75 us).  From a quarter to half as many rows as SMs, four CTAs, two per SM, even out rows of
+    // different cost (64 mixed rows: 45 us against 67 with two).
     int n = 1;
     while (n < kMaxCluster && (long long)rows * n * 2 <= sms && vocab / (2 * n) >= 4096) n *= 2;
-    return {n, n == 1 && vocab > 8192 ? 1024 : 512};
+    if (n == 2 && (long long)rows * 4 <= 2LL * sms && vocab / 4 >= 4096) n = 4;
+    // one CTA per row: 1024 threads while rows are fewer than two per SM (128 rows of 100003, top-p: 77 us against 98
+    // with 512; 512 rows of 50000: 177 against 148); a thread's weights add up in 32 bits for 1000 tokens
+    const bool wide = n == 1 && vocab > 8192 && (rows <= 2 * sms || vocab > 262144);
+    return {n, wide ? 1024 : 512};
 }
 
 template <typename L, int NT> cudaError_t launch_t(const SampleArgs &a, int n, cudaStream_t stream) {

@@ -95,22 +95,42 @@ struct Weight {
     }
 };
 
+// Below 2^kSmall of the top weight the products' own rounding errors, 2^-34 of the weight, are left out: what they lose
+// stays below 2^-41 of the top weight, and there are few tokens near that.
+constexpr float kSmall = -7.0f;
+
+// EXACT: l - top is taken with its rounding error (it has none for bf16 logits that are not tiny beside the top one)
+template <bool EXACT>
 __device__ __forceinline__ Weight weight(float l, float top, Scale c, const WeightTable &tab) {
     // l - top = s + e exactly
-    const float s = l - top, b = s - l, e = (l - (s - b)) - (top + b);
+    const float s = l - top;
+    float e = 0.f;
+    if (EXACT || fabsf(l) < fabsf(top) * 0x1p-15f) {
+        const float b = s - l;
+        e = (l - (s - b)) - (top + b);
+    }
     const float y = s * c.hi;
-    const float ye = fmaf(e, c.hi, fmaf(s, c.lo, fmaf(s, c.hi, -y)));
+    float ye = fmaf(s, c.lo, fmaf(s, c.hi, -y));
+    ye = fmaf(e, c.hi, ye);
     // y = q + g, q a multiple of 1/1024 (1.5 * 2^13 has a last place of 2^-10); then g + ye as gh + gl
     const float t = y + 12288.0f, g = y - (t - 12288.0f);
     const int m = __float_as_int(t);               // 1024 y in its low bits: those of 12288 end in 22 zeros
-    const float gh = g + ye, gl = (g - gh) + ye;
+    const float gh = g + ye;
     constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
-    const float a = gh * L, ae = fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -a)));
-    const float rest = fmaf(a * a, fmaf(a, 0.16666667f, 0.5f), ae);
+    const float a = gh * L;
     const float2 r = tab.r[m & 1023];
+    float rest = a * a * fmaf(a, 0.16666667f, 0.5f);
     // (head + tail) (1 + a + rest) = h + lw
-    const float p = r.x * a, q = fmaf(r.x, rest, fmaf(r.y, a, fmaf(r.x, a, -p))) + r.y;
-    const float h = r.x + p, lw = (p - (h - r.x)) + q;
+    const float p = r.x * a, h = r.x + p;
+    float q;
+    if (y > kSmall) {
+        const float gl = (g - gh) + ye;
+        rest += fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -a)));
+        q = fmaf(r.x, rest, fmaf(r.y, a, fmaf(r.x, a, -p))) + r.y;
+    } else {
+        q = fmaf(r.x, rest, r.y);
+    }
+    const float lw = (p - (h - r.x)) + q;
     // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
     const float f = __int_as_float(((m & ~1023) << 13) + 0x3f800000);
     const float hs = h * f, ls = lw * f;
@@ -118,7 +138,7 @@ __device__ __forceinline__ Weight weight(float l, float top, Scale c, const Weig
     const float t1 = hs + M1, t2 = ((hs - (t1 - M1)) + ls) + M2;
     const bool some = y > -45.5f;                  // else below half a unit (or masked: y is -inf)
     Weight w{some ? __float_as_uint(t1) - __float_as_uint(M1) : 0u, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
-    if (l == top) w = {1u << 22, 0};                // inf - inf above
+    if (l == top) w = {1u << 22, 0};               // inf - inf above
     return w;
 }
 
