@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     x.top = value_of(k_top);
     x.sc = scale_of(temp);
     x.bin_scale = x.sc.hi / kBinOctaves;
-    x.low = -3.4028234e38f;
+    x.low = x.top == INFINITY ? INFINITY : -3.4028234e38f;       // of infinite logits all are equally likely, others out
     x.I = a.V;
     const uint32_t k_min_p = mp > 0.0f ? min_p_key(s.t_log_min_p, x.top) : 0u;
     bool short_list = false;

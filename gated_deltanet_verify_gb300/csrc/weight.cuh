@@ -11,8 +11,8 @@
 // fp32 would lose the small differences (its 2^-24 times a vocabulary of
 // borders is a wrong token every few dozen rows) and fp64 runs at 1/64 of the
 // fp32 rate here, so the products carry their rounding errors in a second fp32
-// (Dekker's and Knuth's error-free sums and products): about 50 fp32 and integer
-// instructions per weight, its error below 2^-44.  fp64 is kept out of what every
+// (Dekker's and Knuth's error-free sums and products): about 40 fp32 and integer
+// instructions per weight, its error below 2^-44 (2^-41 for some small ones).  fp64 is kept out of what every
 // thread does: one fp64 logarithm in all threads of a CTA costs microseconds.
 #pragma once
 
@@ -95,51 +95,54 @@ struct Weight {
     }
 };
 
-// Below 2^kSmall of the top weight the products' own rounding errors, 2^-34 of the weight, are left out: what they lose
-// stays below 2^-41 of the top weight, and there are few tokens near that.
+// Below 2^kSmall of the top weight, rounding errors of 2^-35 of the weight are let be: they stay below 2^-41 of the top
+// weight, and there are few tokens near that.
 constexpr float kSmall = -7.0f;
 
-// EXACT: l - top is taken with its rounding error (it has none for bf16 logits that are not tiny beside the top one)
+// The weight of a logit that is not masked.  EXACT: l - top is taken with its rounding error (it has none for bf16
+// logits that are not tiny beside the top one).  A token's weight has to be the same wherever it is taken, so no product
+// and sum here is left to the compiler to contract or not.
 template <bool EXACT>
 __device__ __forceinline__ Weight weight(float l, float top, Scale c, const WeightTable &tab) {
+    constexpr float kMost = 3.4028234e38f, M = 12288.0f;
+    l = fminf(l, kMost);                           // of infinite logits: l - top is 0
+    top = fminf(top, kMost);
     // l - top = s + e exactly
-    const float s = l - top;
+    const float s = __fsub_rn(l, top);
     float e = 0.f;
     if (EXACT || fabsf(l) < fabsf(top) * 0x1p-15f) {
-        const float b = s - l;
-        e = (l - (s - b)) - (top + b);
+        const float b = __fsub_rn(s, l);
+        e = __fsub_rn(__fsub_rn(l, __fsub_rn(s, b)), __fadd_rn(top, b));
     }
-    const float y = s * c.hi;
-    float ye = fmaf(s, c.lo, fmaf(s, c.hi, -y));
-    ye = fmaf(e, c.hi, ye);
-    // y = q + g, q a multiple of 1/1024 (1.5 * 2^13 has a last place of 2^-10); then g + ye as gh + gl
-    const float t = y + 12288.0f, g = y - (t - 12288.0f);
-    const int m = __float_as_int(t);               // 1024 y in its low bits: those of 12288 end in 22 zeros
-    const float gh = g + ye;
-    constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
-    const float a = gh * L;
+    // y = (s + e) (c.hi + c.lo) = q + g, q a multiple of 1/1024 (1.5 * 2^13 has a last place of 2^-10), |g| <= 2^-11
+    const float t = fmaf(s, c.hi, M), q = __fsub_rn(t, M);
+    const int m = __float_as_int(t);               // 1024 q in its low bits: those of 12288 end in 22 zeros
     const float2 r = tab.r[m & 1023];
-    float rest = a * a * fmaf(a, 0.16666667f, 0.5f);
-    // (head + tail) (1 + a + rest) = h + lw
-    const float p = r.x * a, h = r.x + p;
-    float q;
-    if (y > kSmall) {
-        const float gl = (g - gh) + ye;
-        rest += fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -a)));
-        q = fmaf(r.x, rest, fmaf(r.y, a, fmaf(r.x, a, -p))) + r.y;
+    constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
+    // 2^g = 1 + a (1 + a / 2 + a^2 / 6) with a = g ln 2; head (1 + a') + tail = h + lw
+    float h, lw;
+    if (t > M + kSmall) {
+        const float y = __fmul_rn(s, c.hi), g = __fsub_rn(y, q);
+        const float ye = fmaf(e, c.hi, fmaf(s, c.lo, fmaf(s, c.hi, -y)));
+        const float gh = __fadd_rn(g, ye), gl = __fadd_rn(__fsub_rn(g, gh), ye);
+        const float a = __fmul_rn(gh, L);
+        const float rest = fmaf(__fmul_rn(a, a), fmaf(a, 0.16666667f, 0.5f),
+                                fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -a))));
+        h = fmaf(r.x, a, r.x);
+        lw = __fadd_rn(fmaf(r.x, a, __fsub_rn(r.x, h)), fmaf(r.x, rest, fmaf(r.y, a, r.y)));
     } else {
-        q = fmaf(r.x, rest, r.y);
+        const float g = __fadd_rn(fmaf(s, c.hi, -q), fmaf(e, c.hi, __fmul_rn(s, c.lo)));
+        const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
+        h = fmaf(r.x, b, r.x);
+        lw = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h)), r.y);
     }
-    const float lw = (p - (h - r.x)) + q;
     // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
     const float f = __int_as_float(((m & ~1023) << 13) + 0x3f800000);
-    const float hs = h * f, ls = lw * f;
     constexpr float M1 = 3.0f, M2 = 0x1.8p-21f;
-    const float t1 = hs + M1, t2 = ((hs - (t1 - M1)) + ls) + M2;
-    const bool some = y > -45.5f;                  // else below half a unit (or masked: y is -inf)
-    Weight w{some ? __float_as_uint(t1) - __float_as_uint(M1) : 0u, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
-    if (l == top) w = {1u << 22, 0};               // inf - inf above
-    return w;
+    const float hs = __fmul_rn(h, f), t1 = __fadd_rn(hs, M1);
+    const float t2 = __fadd_rn(fmaf(lw, f, __fsub_rn(hs, __fsub_rn(t1, M1))), M2);
+    const bool some = t > M - 45.5f;               // else below half a unit
+    return {some ? __float_as_uint(t1) - __float_as_uint(M1) : 0u, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
 }
 
 // ln(exp((l - top) / T) / (total 2^-44)), in fp32: both terms are at most 0, so they do not cancel; the quotient (of a
