@@ -120,21 +120,18 @@ __device__ __forceinline__ Weight weight(float l, float top, Scale c, const Weig
     const float2 r = tab.r[m & 1023];
     constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
     // 2^g = 1 + a (1 + a / 2 + a^2 / 6) with a = g ln 2; head (1 + a') + tail = h + lw
-    float h, lw;
+    const float g = __fadd_rn(fmaf(s, c.hi, -q), fmaf(e, c.hi, __fmul_rn(s, c.lo)));
+    const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
+    float h = fmaf(r.x, b, r.x), lw = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h)), r.y);
     if (t > M + kSmall) {
-        const float y = __fmul_rn(s, c.hi), g = __fsub_rn(y, q);
+        const float y = __fmul_rn(s, c.hi), g0 = __fsub_rn(y, q);
         const float ye = fmaf(e, c.hi, fmaf(s, c.lo, fmaf(s, c.hi, -y)));
-        const float gh = __fadd_rn(g, ye), gl = __fadd_rn(__fsub_rn(g, gh), ye);
-        const float a = __fmul_rn(gh, L);
-        const float rest = fmaf(__fmul_rn(a, a), fmaf(a, 0.16666667f, 0.5f),
-                                fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -a))));
-        h = fmaf(r.x, a, r.x);
-        lw = __fadd_rn(fmaf(r.x, a, __fsub_rn(r.x, h)), fmaf(r.x, rest, fmaf(r.y, a, r.y)));
-    } else {
-        const float g = __fadd_rn(fmaf(s, c.hi, -q), fmaf(e, c.hi, __fmul_rn(s, c.lo)));
-        const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
-        h = fmaf(r.x, b, r.x);
-        lw = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h)), r.y);
+        const float gh = __fadd_rn(g0, ye), gl = __fadd_rn(__fsub_rn(g0, gh), ye);
+        const float ah = __fmul_rn(gh, L);
+        const float rest = fmaf(__fmul_rn(ah, ah), fmaf(ah, 0.16666667f, 0.5f),
+                                fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -ah))));
+        h = fmaf(r.x, ah, r.x);
+        lw = __fadd_rn(fmaf(r.x, ah, __fsub_rn(r.x, h)), fmaf(r.x, rest, fmaf(r.y, ah, r.y)));
     }
     // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
     const float f = __int_as_float(((m & ~1023) << 13) + 0x3f800000);
