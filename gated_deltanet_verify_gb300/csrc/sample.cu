@@ -76,7 +76,8 @@ struct Shared {
     uint32_t hist[kBins];                // this CTA's counts
     uint32_t count[kBins];               // the cluster's, summed up to and with each bin
     uint32_t hist_in[kHead], in[kHead];  // the sums of places inside the first bins, in 1/256 bin: this CTA's, all
-    float fred[32], fraction;
+    float fred[32];
+    u64 place;                           // a bin, and as a float the fraction of it
     uint32_t ured[32];
     uint32_t n_list, n_small;
     int found;
@@ -273,12 +274,15 @@ struct Sampler {
         return v;
     }
 
+    __device__ __forceinline__ void clear() {
+        for (int i = tid; i < kBins; i += NT) s.hist[i] = 0;
+        for (int i = tid; i < kHead; i += NT) s.hist_in[i] = 0;
+    }
     // the merged histogram of the kept tokens' places (top - l) scale - from, the last bin taking what lies beyond if
     // `open`, summed up to and with each bin, in s.count; with `open` also the sums of the places inside the first bins,
     // in s.in (a few heavy tokens taken at their bins' middles would spoil an estimate).  The list is empty afterwards.
     __device__ __forceinline__ void histogram(float scale, int first, bool open) {
-        for (int i = tid; i < kBins; i += NT) s.hist[i] = 0;
-        for (int i = tid; i < kHead; i += NT) s.hist_in[i] = 0;
+        if (!open) clear();                      // at the start they are clear
         if (tid == 0) s.n_list = 0;
         __syncthreads();
         each([&](float l, int i) {
@@ -346,15 +350,20 @@ struct Sampler {
         for (int j = 0; j < kPer; ++j) {
             const int b = kPer * tid + j;
             const uint32_t n = s.count[b] - (b ? s.count[b - 1] : 0);
-            const float in = open && b < kHead && n ? (s.in[b] + 0.5f * n) * (1.f / 256) / float(n) : 0.5f;
+            float in = open && b < kHead && n ? __fdividef(s.in[b] + 0.5f * n, 256.f * n) : 0.5f;
+            if (sizeof(L) == 2 && open && b >= kHead) {
+                // bf16 logits are sparse: the highest one that begins below the bin's edge, if it is the only one in it
+                const uint32_t bits = __float_as_uint(top - __fdividef(float(b), bin_scale));
+                const uint32_t v = (bits & 0x80000000u ? bits + 0xffffu : bits) & 0xffff0000u;
+                const float at = (top - __uint_as_float(v)) * bin_scale - float(b);
+                const float next = (top - __uint_as_float(bits & 0x80000000u ? v + 0x10000u : v - 0x10000u)) * bin_scale - float(b);
+                if (at < 1.f && next >= 1.f) in = fmaxf(at, 0.f);
+            }
             t += c[j] = b > last ? 0.f : float(n) * exp2f(-(b + in) * octaves);
         }
         float run = warp_scan(t);
         if (lane == 31) s.fred[wid] = run;
-        if (tid == 0) {
-            s.found = kBins;
-            s.fraction = 0.5f;
-        }
+        if (tid == 0) s.place = u64(kBins) << 32;
         __syncthreads();
         const float w = warp_scan(lane < kWarps ? s.fred[lane] : 0.f);
         run += (wid ? __shfl_sync(kFull, w, wid - 1) : 0.f) - t;
@@ -369,13 +378,10 @@ struct Sampler {
             }
             run += c[j];
         }
-        if (mine < kBins) atomicMin(&s.found, mine);
+        if (mine < kBins) atomicMin(&s.place, (u64(mine) << 32) | __float_as_uint(fraction));
         __syncthreads();
-        if (mine < kBins && s.found == mine) s.fraction = fraction;
-        __syncthreads();
-        const float at = s.found + s.fraction;
-        __syncthreads();
-        return at;
+        const u64 at = s.place;
+        return float(at >> 32) + __uint_as_float(uint32_t(at));
     }
 
     // a token to the first CTA's list, if there is room; one atomic for the lanes that come here together
@@ -606,7 +612,7 @@ struct Sampler {
 
     // the same, the border being looked for: near `place` (in bins) first; whether s.warp_sum holds the kept stats
     template <bool MASS, typename T> __device__ __forceinline__ bool look_for(float place, T target_of) {
-        u64 all, before;
+        u64 all = 0, before;
         // the estimate is good to a fraction of a bin
         float b0 = floorf(place - 0.45f), b1 = floorf(place + 0.45f) + 1.f;
         if (!MASS) b0 = floorf(place), b1 = b0 + 1.f;
@@ -629,7 +635,8 @@ struct Sampler {
                     c0 = bin_of_count(uint32_t(min(need, u64(s.count[kBins - 1]))));
                     c1 = c0 + 1.f;
                 }
-                if (border<MASS>(edge_of(first + c0, scale), edge_of(first + c1, scale), target_of, all, before) == kFound) return true;
+                if (border<MASS>(edge_of(first + c0, scale), edge_of(first + c1, scale), target_of, all, before) == kFound)
+                    return true;
                 break;
             }
             // off by a bin or more
@@ -695,6 +702,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     // before the first exchange
     if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
     s.table.fill(tid, NT);
+    x.clear();
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const float temp = a.temperature ? a.temperature[slot] : 1.0f;
     const float u = a.u[row];
