@@ -8,7 +8,7 @@
 // sum_{j <= i, kept} w_j > u * sum_{kept} w_j, in index order.
 //
 // A border of that last sum decides the token, so every sum is exact: a weight
-// is a 64-bit integer in units of 2^-44 of the largest weight (weight.cuh), and
+// is a 64-bit integer in units of about 2^-44 of the largest one (weight.cuh), and
 // the integer sums do not depend on the order they are taken in -- the token is
 // the same whatever the launch shape, and equals the one of 64-bit arithmetic
 // unless u lies within ~1e-11 of a border.  For the same reason the atomics
@@ -44,7 +44,7 @@ namespace gdn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kBins = 3072;              // 1/64 octave each: 45.5 octaves, where weights end, lie in bin 2912
+constexpr int kBins = 2944;              // 1/64 octave each: 46 octaves; weights end at 45.5
 constexpr float kBinOctaves = 1.0f / 64;
 constexpr int kHead = 512;               // bins whose tokens' places inside them are summed too
 constexpr int kFine = 1024;              // cells a bin, where a bin is too full
@@ -135,7 +135,7 @@ template <typename L, int NT>
 struct Sampler {
     static constexpr int E = 16 / sizeof(L);
     static constexpr int kWarps = NT / 32;
-    static constexpr int kPer = kBins / NT;
+    static constexpr int kPer = (kBins + NT - 1) / NT;
     Shared &s;
     const L *row;                        // the row's first logit
     const uint4 *vecs;                   // the row as 16-byte vectors from the last boundary before it
@@ -151,7 +151,7 @@ struct Sampler {
     int I;
 
     __device__ __forceinline__ bool kept(float l, int i) const { return l > low || (l == low && i <= I); }
-    __device__ __forceinline__ Weight weigh(float l) const { return weight<sizeof(L) == 4>(l, top, sc, s.table); }
+    __device__ __forceinline__ Weight weigh(float l) const { return weight(l, sc, s.table); }
     __device__ __forceinline__ u64 units(float l) const { return weigh(l).units(); }
     // the logit at which bin b (or cell b of bins of 1/kFine) begins, going down
     __device__ __forceinline__ float edge_of(float b, float scale) const {
@@ -301,14 +301,16 @@ struct Sampler {
         if (n_cta > 1) {
             // lane r of a group of n_cta reads CTA r's count of a bin and, with their sum, writes CTA r's copy
             const int slice = kBins / n_cta, r = tid & (n_cta - 1);
-            uint32_t c[kPer];                                       // whole warps: 3072 is a multiple of NT
+            uint32_t c[kPer];                                       // whole warps: kBins is a multiple of 32
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) c[j] = ld_cluster32(map_cluster(&s.hist[rank * slice + (tid + j * NT) / n_cta], r));
+            for (int j = 0; j < kPer; ++j)
+                c[j] = tid + j * NT < kBins ? ld_cluster32(map_cluster(&s.hist[rank * slice + (tid + j * NT) / n_cta], r)) : 0;
             for (int m = n_cta >> 1; m; m >>= 1)
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) c[j] += __shfl_xor_sync(kFull, c[j], m);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) st_cluster32(map_cluster(&s.count[rank * slice + (tid + j * NT) / n_cta], r), c[j]);
+            for (int j = 0; j < kPer; ++j)
+                if (tid + j * NT < kBins) st_cluster32(map_cluster(&s.count[rank * slice + (tid + j * NT) / n_cta], r), c[j]);
             for (int t = tid; open && t < kHead; t += NT) {
                 const int b = rank * (kHead / n_cta) + t / n_cta;
                 uint32_t c = ld_cluster32(map_cluster(&s.hist_in[b], r));
@@ -322,14 +324,15 @@ struct Sampler {
         }
         uint32_t c[kPer], t = 0;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) t += c[j] = from[kPer * tid + j];
+        for (int j = 0; j < kPer; ++j) t += c[j] = kPer * tid + j < kBins ? from[kPer * tid + j] : 0;
         uint32_t run = warp_scan(t);
         if (lane == 31) s.ured[wid] = run;
         __syncthreads();
         const uint32_t w = warp_scan(lane < kWarps ? s.ured[lane] : 0u);
         run += (wid ? __shfl_sync(kFull, w, wid - 1) : 0u) - t;
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) s.count[kPer * tid + j] = run += c[j];
+        for (int j = 0; j < kPer; ++j)
+            if (kPer * tid + j < kBins) s.count[kPer * tid + j] = run += c[j];
         __syncthreads();
     }
     // the first bin up to which at least n tokens lie
@@ -349,7 +352,7 @@ struct Sampler {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int b = kPer * tid + j;
-            const uint32_t n = s.count[b] - (b ? s.count[b - 1] : 0);
+            const uint32_t n = b < kBins ? s.count[b] - (b ? s.count[b - 1] : 0) : 0;
             float in = open && b < kHead && n ? __fdividef(s.in[b] + 0.5f * n, 256.f * n) : 0.5f;
             if (sizeof(L) == 2 && open && b >= kHead) {
                 // bf16 logits are sparse: the highest one that begins below the bin's edge, if it is the only one in it
@@ -627,7 +630,7 @@ struct Sampler {
                 const u64 need = target_of(all) - before;
                 float c0, c1;
                 if (MASS) {
-                    const float at = place_of_mass(float(need) * 0x1p-44f * exp2f(fmaxf(b0, 0.f) * kBinOctaves), kBins - 1,
+                    const float at = place_of_mass(float(need) / float(units(top)) * exp2f(fmaxf(b0, 0.f) * kBinOctaves), kBins - 1,
                                                    kBinOctaves / kFine, false);
                     c0 = floorf(at) - 1.f;
                     c1 = floorf(at) + 2.f;
@@ -772,8 +775,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         return;
     }
     x.top = value_of(k_top);
-    x.sc = scale_of(temp);
-    x.bin_scale = x.sc.hi / kBinOctaves;
+    x.sc = scale_of(temp, x.top);
+    x.bin_scale = scale_of(temp, 0.0f).hi / kBinOctaves;
     x.low = x.top == INFINITY ? INFINITY : -3.4028234e38f;       // of infinite logits all are equally likely, others out
     x.I = a.V;
     const uint32_t k_min_p = mp > 0.0f ? min_p_key(s.t_log_min_p, x.top) : 0u;
@@ -781,7 +784,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     if (bounded) {
         const float least = value_of(bound);
         x.each([&](float l, int i) {
-            if (l >= least) x.push(key_of(l + 0.0f), i, x.units(l));
+            if (l >= least) x.push(key_of(l + 0.0f), i, l >= x.low ? x.units(l) : 0);
         });
         x.sync_cluster();
         const uint32_t n = ld_cluster32(map_cluster(&s.n_list, 0));
@@ -836,7 +839,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
                 if (uint32_t(o.order) > uint32_t(me.order)) run += o.stat;
             }
             if (run <= target && target < run + me.stat)
-                finish(int(~uint32_t(me.order)), log_prob(value_of(uint32_t(me.order >> 32)), x.top, temp, total));
+                finish(int(~uint32_t(me.order)), log_prob(value_of(uint32_t(me.order >> 32)), x.top, temp, x.units(x.top), total));
         }
         __syncwarp();
         if (n_cta > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -877,7 +880,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     const u64 target = draw_target(u, total);
     if (run <= target && target < run + mine)
         x.find(target, run, s.warp_sum, [&](float l, int i) -> u64 { return x.kept(l, i) ? x.units(l) : 0; },
-               [&](float l, int i) { finish(i, log_prob(l, x.top, temp, total)); });
+               [&](float l, int i) { finish(i, log_prob(l, x.top, temp, x.units(x.top), total)); });
 }
 
 // CTAs per row, a power of two up to 16, and threads per CTA

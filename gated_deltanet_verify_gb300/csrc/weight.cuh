@@ -1,17 +1,17 @@
 // weight.cuh -- softmax weights as 64-bit integers, and the order of logits.
 //
-// weight(l) = exp((l - top) / T) in units of 2^-44, rounded to nearest: at most
-// 2^44 for the top logit, so 2^19 tokens sum to at most 2^63.  Integer sums are
-// exact and do not depend on their order.
+// weight(l) = exp((l - ref) / T) in units of 2^-44, rounded to nearest, where ref is the top logit or a little above:
+// at most 2^44, so 2^19 tokens sum to at most 2^63.  Only ratios of weights count, so ref need not be exact.  Integer
+// sums are exact and do not depend on their order.
 //
 // The exponential is table-driven (P. T. P. Tang, "Table-driven implementation
 // of the exponential function in IEEE floating-point arithmetic", ACM TOMS 15,
-// 1989): y = (l - top) log2(e) / T is split into n + j/1024 + g with |g| <=
+// 1989): y = (l - ref) log2(e) / T is split into n + j/1024 + g with |g| near
 // 2^-11, and 2^y = 2^n 2^(j/1024) (1 + a + a^2/2 + a^3/6), a = g ln 2.  Plain
 // fp32 would lose the small differences (its 2^-24 times a vocabulary of
 // borders is a wrong token every few dozen rows) and fp64 runs at 1/64 of the
 // fp32 rate here, so the products carry their rounding errors in a second fp32
-// (Dekker's and Knuth's error-free sums and products): about 40 fp32 and integer
+// (Dekker's and Knuth's error-free sums and products): about 30 fp32 and integer
 // instructions per weight, its error below 2^-44 (2^-41 for some small ones).  fp64 is kept out of what every
 // thread does: one fp64 logarithm in all threads of a CTA costs microseconds.
 #pragma once
@@ -71,14 +71,28 @@ struct __align__(16) WeightTable {
     }
 };
 
-// log2(e) / T as an fp32 head and tail: the quotient, and the rest of the division over T
+// What the weights of a row share: y = x c - at with x = l - shift, c = hi + lo = log2(e) / T, and `at` (top - shift) c
+// rounded up to a multiple of 2^-10 (by one or two of them, so that y < 0).  With q a multiple of 2^-10 too, at + q is
+// exact, and one fused multiply-add takes y - q from l without a difference of logits first.  Where (top - shift) c
+// would be too large for that, the shift is the top logit; what counts there lies within 1/40 of it, so l - top is exact.
 struct Scale {
-    float hi, lo;
+    float hi, lo, shift, at, from;                 // from: 12288 - at, where y is rounded to q
 };
-__device__ __forceinline__ Scale scale_of(float temp) {
+__device__ __forceinline__ Scale scale_of(float temp, float top) {
     constexpr float L = 1.44269502162933349609375f, Ll = 1.92596303350001e-8f;      // log2(e) = L + Ll
-    const float h = __fdiv_rn(L, temp);
-    return {h, __fdiv_rn(fmaf(-h, temp, L) + Ll, temp)};
+    Scale c;
+    c.hi = __fdiv_rn(L, temp);                     // the quotient, and the rest of the division over T
+    c.lo = __fdiv_rn(fmaf(-c.hi, temp, L) + Ll, temp);
+    c.shift = c.at = 0.f;
+    if (top == INFINITY) {
+        c.hi = c.lo = 0.f;                         // only infinite logits are kept, all alike
+    } else {
+        const float p = __fmul_rn(top, c.hi);
+        if (fabsf(p) < 2048.f) c.at = (ceilf(p * 1024.f) + 1.f) * (1.f / 1024);
+        else c.shift = top;
+    }
+    c.from = __fsub_rn(12288.0f, c.at);
+    return c;
 }
 
 // hi * 2^22 + lo units of 2^-44, |lo| at most 2^21: up to 1000 of them add up word by word
@@ -95,43 +109,32 @@ struct Weight {
     }
 };
 
-// Below 2^kSmall of the top weight, rounding errors of 2^-35 of the weight are let be: they stay below 2^-41 of the top
+// Below 2^kSmall of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-41 of the top
 // weight, and there are few tokens near that.
 constexpr float kSmall = -7.0f;
 
-// The weight of a logit that is not masked.  EXACT: l - top is taken with its rounding error (it has none for bf16
-// logits that are not tiny beside the top one).  A token's weight has to be the same wherever it is taken, so no product
-// and sum here is left to the compiler to contract or not.
-template <bool EXACT>
-__device__ __forceinline__ Weight weight(float l, float top, Scale c, const WeightTable &tab) {
-    constexpr float kMost = 3.4028234e38f, M = 12288.0f;
-    l = fminf(l, kMost);                           // of infinite logits: l - top is 0
-    top = fminf(top, kMost);
-    // l - top = s + e exactly
-    const float s = __fsub_rn(l, top);
-    float e = 0.f;
-    if (EXACT || fabsf(l) < fabsf(top) * 0x1p-15f) {
-        const float b = __fsub_rn(s, l);
-        e = __fsub_rn(__fsub_rn(l, __fsub_rn(s, b)), __fadd_rn(top, b));
-    }
-    // y = (s + e) (c.hi + c.lo) = q + g, q a multiple of 1/1024 (1.5 * 2^13 has a last place of 2^-10), |g| <= 2^-11
-    const float t = fmaf(s, c.hi, M), q = __fsub_rn(t, M);
+// The weight of a logit that is kept.  A token's weight has to be the same wherever it is taken, so no product and sum
+// here is left to the compiler to contract or not.
+__device__ __forceinline__ Weight weight(float l, const Scale &c, const WeightTable &tab) {
+    constexpr float M = 12288.0f;                  // 1.5 * 2^13: its last place is 2^-10
+    const float x = __fsub_rn(fminf(l, 3.4028234e38f), c.shift);
+    const float t = fmaf(x, c.hi, c.from), q = __fsub_rn(t, M), at = __fadd_rn(c.at, q);
     const int m = __float_as_int(t);               // 1024 q in its low bits: those of 12288 end in 22 zeros
     const float2 r = tab.r[m & 1023];
     constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
-    // 2^g = 1 + a (1 + a / 2 + a^2 / 6) with a = g ln 2; head (1 + a') + tail = h + lw
-    const float g = __fadd_rn(fmaf(s, c.hi, -q), fmaf(e, c.hi, __fmul_rn(s, c.lo)));
+    // 2^g = 1 + b, b = a (1 + a / 2 + a^2 / 6) with g = y - q, a = g ln 2; (head + tail) 2^g = h + lw
+    const float g = fmaf(x, c.lo, fmaf(x, c.hi, -at));
     const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
     float h = fmaf(r.x, b, r.x), lw = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h)), r.y);
     if (t > M + kSmall) {
-        const float y = __fmul_rn(s, c.hi), g0 = __fsub_rn(y, q);
-        const float ye = fmaf(e, c.hi, fmaf(s, c.lo, fmaf(s, c.hi, -y)));
-        const float gh = __fadd_rn(g0, ye), gl = __fadd_rn(__fsub_rn(g0, gh), ye);
-        const float ah = __fmul_rn(gh, L);
-        const float rest = fmaf(__fmul_rn(ah, ah), fmaf(ah, 0.16666667f, 0.5f),
-                                fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -ah))));
-        h = fmaf(r.x, ah, r.x);
-        lw = __fadd_rn(fmaf(r.x, ah, __fsub_rn(r.x, h)), fmaf(r.x, rest, fmaf(r.y, ah, r.y)));
+        // g, a and b as sums of two
+        const float p = __fmul_rn(x, c.hi), g0 = __fsub_rn(p, at), ge = fmaf(x, c.lo, fmaf(x, c.hi, -p));
+        const float gh = __fadd_rn(g0, ge), gl = __fadd_rn(__fsub_rn(g0, gh), ge);
+        const float ah = __fmul_rn(gh, L), al = fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -ah)));
+        const float z = __fmul_rn(__fmul_rn(ah, ah), fmaf(ah, 0.16666667f, 0.5f));
+        const float bh = __fadd_rn(ah, z), bl = __fadd_rn(__fadd_rn(__fsub_rn(ah, bh), z), al);
+        h = fmaf(r.x, bh, r.x);
+        lw = __fadd_rn(fmaf(r.x, bh, __fsub_rn(r.x, h)), fmaf(r.x, bl, fmaf(r.y, bh, r.y)));
     }
     // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
     const float f = __int_as_float(((m & ~1023) << 13) + 0x3f800000);
@@ -142,12 +145,13 @@ __device__ __forceinline__ Weight weight(float l, float top, Scale c, const Weig
     return {some ? __float_as_uint(t1) - __float_as_uint(M1) : 0u, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
 }
 
-// ln(exp((l - top) / T) / (total 2^-44)), in fp32: both terms are at most 0, so they do not cancel; the quotient (of a
-// rounded difference), log1pf (at most 1 ulp, of a rounded argument) and their sum are off by at most 2^-22 of it
-__device__ __forceinline__ float log_prob(float l, float top, float temp, unsigned long long total) {
+// ln(w / total) for a token of logit l, given the top token's weight, in fp32: (l - top) / T less ln(total / w_top), both
+// at most 0, so they do not cancel; the quotient (of a rounded difference), log1pf (at most 1 ulp, of a rounded
+// quotient) and their sum are off by at most 2^-22 of it
+__device__ __forceinline__ float log_prob(float l, float top, float temp, unsigned long long w_top,
+                                          unsigned long long total) {
     const float x = l == top ? 0.0f : __fdiv_rn(l - top, temp);
-    const long long over = (long long)(total - (1ull << 44));
-    return x - log1pf(float(over) * 0x1p-44f);
+    return x - log1pf(__fdiv_rn(float(total - w_top), float(w_top)));
 }
 
 // ceil(p total), at least one unit: the mass at which top-p ends (p < 1)
