@@ -83,6 +83,8 @@ struct Shared {
     int found;
 };
 
+constexpr size_t kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
+
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return uint32_t(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ uint32_t map_cluster(const void *p, uint32_t rank) {
     uint32_t r;
@@ -135,8 +137,10 @@ template <typename L, int NT>
 struct Sampler {
     static constexpr int E = 16 / sizeof(L);
     static constexpr int kWarps = NT / 32;
+    static constexpr int kRing = NT == 1024 ? 4 : 2;     // vectors of a thread on their way, a power of two
     static constexpr int kPer = (kBins + NT - 1) / NT;
     Shared &s;
+    uint4 *ring;                         // [kRing][NT]
     const L *row;                        // the row's first logit
     const uint4 *vecs;                   // the row as 16-byte vectors from the last boundary before it
     int V, head;                         // head: elements of vector 0 before the row
@@ -151,8 +155,11 @@ struct Sampler {
     int I;
 
     __device__ __forceinline__ bool kept(float l, int i) const { return l > low || (l == low && i <= I); }
-    __device__ __forceinline__ Weight weigh(float l) const { return weight(l, sc, s.table); }
-    __device__ __forceinline__ u64 units(float l) const { return weigh(l).units(); }
+    __device__ __forceinline__ u64 units(float l) const {
+        Weight w;
+        weights<1>(&l, sc, s.table, &w);
+        return w.units();
+    }
     // the logit at which bin b (or cell b of bins of 1/kFine) begins, going down
     __device__ __forceinline__ float edge_of(float b, float scale) const {
         return b <= 0.f ? INFINITY : top - __fdiv_rn(b, scale);
@@ -184,34 +191,57 @@ struct Sampler {
             for (int e = 0; e < E; ++e) l[e] = i0 + e >= 0 && i0 + e < V ? to_float(row[i0 + e]) : -INFINITY;
         }
     }
-    // f(logit, index) for every element of this CTA, warps over stretches of their own; two vectors in flight a thread.
-    // BOTH: f is written out for both; else for one, for the largest f where each thread has few tokens and the loop
-    // costs little beside fetching its instructions (one row of 32768, top-p: 19.7 us against 21.7)
-    template <bool BOTH = true, typename F> __device__ __forceinline__ void each(F f) const {
-        const int end = v0 + min(nv, (wid + 1) * seg);
-        for (int v = v0 + wid * seg + lane; v < end; v += 64) {
-            float l[E], m[E];
-            const bool two = v + 32 < end;
-            load(v, l);
-            if (two) load(v + 32, m);
-            if (BOTH) {
+    // f(logits, v) for every vector of this CTA, warps over stretches of their own.  A thread's next vectors are on their
+    // way to a ring of its own in shared memory meanwhile (with two of them in registers instead, a pass took as long as
+    // the loads' latency allowed: 256 bf16 rows of 200000, the top logit alone, 36 us against 24)
+    template <typename F> __device__ __forceinline__ void each_vec(F f) const {
+        const int end = v0 + min(nv, (wid + 1) * seg), start = v0 + wid * seg + lane;
+        const int first = head ? 1 : 0, n_whole = (head + V) / E - first;          // vectors inside the row
+        const uint32_t slots = smem_u32(ring + tid);
+        uint32_t slot = 0;
+        const uint4 *src = vecs + start;
+        auto fetch = [&](int v, uint32_t at) {
+            if (v < end && unsigned(v - first) < unsigned(n_whole))
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(slots + at), "l"(src) : "memory");
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+            src += 32;
+        };
 #pragma unroll
-                for (int e = 0; e < E; ++e) f(l[e], v * E - head + e);
-                if (two) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) f(m[e], (v + 32) * E - head + e);
-                }
+        for (int j = 0; j < kRing - 1; ++j) fetch(start + 32 * j, uint32_t(j) * NT * 16);
+        for (int v = start; v < end; v += 32) {
+            fetch(v + 32 * (kRing - 1), (slot + (kRing - 1) * NT * 16) & (kRing * NT * 16 - 1));
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(kRing - 1) : "memory");
+            float l[E];
+            if (unsigned(v - first) < unsigned(n_whole)) {
+                uint4 u;
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slots + slot) : "memory");
+                unpack(u, l, L());
             } else {
-                const int i0 = v * E - head, i1 = two ? i0 + 32 * E : i0;
-#pragma unroll 1
-                for (int i = i0; i <= i1; i += 32 * E) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) f(l[e], i + e);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) l[e] = m[e];
-                }
+                load(v, l);
             }
+            slot = (slot + NT * 16) & (kRing * NT * 16 - 1);
+            f(l, v);
         }
+    }
+    // f(logit, index) for every element
+    template <typename F> __device__ __forceinline__ void each(F f) const {
+        each_vec([&](const float (&l)[E], int v) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) f(l[e], v * E - head + e);
+        });
+    }
+    // f(logit, weight, index in the vector, vector) for every element, four at a time, but those where all are below low
+    template <typename F> __device__ __forceinline__ void each_weight(F f) const {
+        each_vec([&](const float (&l)[E], int v) {
+#pragma unroll
+            for (int e = 0; e < E; e += 4) {
+                if (!(fmaxf(fmaxf(l[e], l[e + 1]), fmaxf(l[e + 2], l[e + 3])) >= low)) continue;      // none is kept
+                Weight w[4];
+                weights<4>(l + e, sc, s.table, w);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) f(l[e + j], w[j], e + j, v);
+            }
+        });
     }
 
     template <typename Op> __device__ __forceinline__ u64 warp_all(u64 v, Op op) const {
@@ -538,25 +568,29 @@ struct Sampler {
     __device__ __forceinline__ Border border(float from, float to, T target_of, u64 &all, u64 &before) {
         Weight w_all{0, 0}, w_before{0, 0};
         uint32_t n_all = 0, n_before = 0, n = 0, k_lo = 0xffffffffu, k_hi = 0;
-        each<NT == 1024>([&](float l, int i) {
-            if (!kept(l, i)) return;
-            Weight w{0, 0};
-            if (MASS) {
-                w = weigh(l);
+        auto hold = [&](float l, int i, u64 stat) {
+            const uint32_t key = key_of(l + 0.0f);
+            ++n;
+            k_lo = min(k_lo, key);
+            k_hi = max(k_hi, key);
+            push(key, i, stat);
+        };
+        if (MASS) {
+            each_weight([&](float l, const Weight &w, int e, int v) {
+                const int i = v * E - head + e;
+                if (!kept(l, i)) return;
                 w_all += w;
                 if (l > from) w_before += w;
-            } else {
+                else if (l > to) hold(l, i, w.units());
+            });
+        } else {
+            each([&](float l, int i) {
+                if (!kept(l, i)) return;
                 ++n_all;
                 if (l > from) ++n_before;
-            }
-            if (l <= from && l > to) {
-                const uint32_t key = key_of(l + 0.0f);
-                ++n;
-                k_lo = min(k_lo, key);
-                k_hi = max(k_hi, key);
-                push(key, i, MASS ? w.units() : 1);
-            }
-        });
+                else if (l > to) hold(l, i, 1);
+            });
+        }
         const u64 p_before = warp_all(MASS ? w_before.units() : u64(n_before), Add());
         const u64 p_all = warp_all(MASS ? w_all.units() : u64(n_all), Add());
         n = __reduce_add_sync(kFull, n);
@@ -694,8 +728,8 @@ template <typename L, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
-    Sampler<L, NT> x{s};
-    constexpr int kWarps = NT / 32;
+    Sampler<L, NT> x{s, reinterpret_cast<uint4 *>(smem + kSharedBytes)};
+    constexpr int kWarps = NT / 32, E = Sampler<L, NT>::E;
     x.tid = threadIdx.x; x.lane = x.tid & 31; x.wid = x.tid >> 5;
     x.n_cta = n_cta; x.rank = int(blockIdx.x) & (n_cta - 1); x.round = 0;
     x.V = a.V; x.cta_vecs = cta_vecs;
@@ -719,13 +753,23 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
 
     // 1. the top logit
     float best = -INFINITY;
-    int best_i = 0;
-    x.each([&](float l, int i) {
-        if (l > best) {
-            best = l;
-            best_i = i;
+    int best_v = 0, best_i = 0;
+    x.each_vec([&](const float (&l)[E], int v) {
+        float m = l[0];
+#pragma unroll
+        for (int e = 1; e < E; ++e) m = fmaxf(m, l[e]);         // of NaN and a number the number
+        if (m > best) {
+            best = m;
+            best_v = v;
         }
     });
+    if (best > -INFINITY) {
+        float l[E];
+        x.load(best_v, l);
+#pragma unroll
+        for (int e = E - 1; e >= 0; --e)
+            if (l[e] == best) best_i = best_v * E - x.head + e;
+    }
     const uint32_t k_best = key_of(best + 0.0f);
     if (tid == 0) {
         if (mp > 0.0f) s.t_log_min_p = double(temp) * log(double(mp));
@@ -854,12 +898,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         // I is set where top-k or top-p ended among equals: else the logit alone decides
         Weight m{0, 0};
         if (x.I == a.V)
-            x.each([&](float l, int) {
-                if (l >= x.low) m += x.weigh(l);
+            x.each_weight([&](float l, const Weight &w, int, int) {
+                if (l >= x.low) m += w;
             });
         else
-            x.each([&](float l, int i) {
-                if (x.kept(l, i)) m += x.weigh(l);
+            x.each_weight([&](float l, const Weight &w, int e, int v) {
+                if (x.kept(l, v * E - x.head + e)) m += w;
             });
         const u64 mine = x.warp_all(m.units(), Add());
         __syncthreads();
@@ -905,12 +949,13 @@ template <typename L, int NT> cudaError_t launch_t(const SampleArgs &a, int n, c
     const int row_vecs = (a.V + 2 * E - 2) / E;              // whatever its first vector's alignment
     const int vecs = (row_vecs + n - 1) / n;
     auto kern = sample_kernel<L, NT>;
+    const size_t smem = kSharedBytes + size_t(Sampler<L, NT>::kRing) * NT * 16;
     // function attributes belong to the context: set once in each
     static PerContext<int> attrs;
     unsigned long long ctx = 0;
     int set = 0;
     if (!(current_context_id(&ctx) && attrs.get(ctx, &set))) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Shared)));
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         if (current_context_id(&ctx)) attrs.put(ctx, 1);
@@ -918,7 +963,7 @@ template <typename L, int NT> cudaError_t launch_t(const SampleArgs &a, int n, c
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.B) * unsigned(a.T) * unsigned(n), 1, 1);
     cfg.blockDim = dim3(NT, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(Shared);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -12,7 +12,7 @@
 // borders is a wrong token every few dozen rows) and fp64 runs at 1/64 of the
 // fp32 rate here, so the products carry their rounding errors in a second fp32
 // (Dekker's and Knuth's error-free sums and products): about 30 fp32 and integer
-// instructions per weight, its error below 2^-44 (2^-41 for some small ones).  fp64 is kept out of what every
+// instructions per weight, its error below 2^-43 of the top weight (2^-38 for a few).  fp64 is kept out of what every
 // thread does: one fp64 logarithm in all threads of a CTA costs microseconds.
 #pragma once
 
@@ -77,6 +77,7 @@ struct __align__(16) WeightTable {
 // would be too large for that, the shift is the top logit; what counts there lies within 1/40 of it, so l - top is exact.
 struct Scale {
     float hi, lo, shift, at, from;                 // from: 12288 - at, where y is rounded to q
+    float least;                                   // an x whose weight rounds to 0; lower ones (and NaN) count as it
 };
 __device__ __forceinline__ Scale scale_of(float temp, float top) {
     constexpr float L = 1.44269502162933349609375f, Ll = 1.92596303350001e-8f;      // log2(e) = L + Ll
@@ -86,10 +87,12 @@ __device__ __forceinline__ Scale scale_of(float temp, float top) {
     c.shift = c.at = 0.f;
     if (top == INFINITY) {
         c.hi = c.lo = 0.f;                         // only infinite logits are kept, all alike
+        c.least = -3.4028234e38f;
     } else {
         const float p = __fmul_rn(top, c.hi);
         if (fabsf(p) < 2048.f) c.at = (ceilf(p * 1024.f) + 1.f) * (1.f / 1024);
         else c.shift = top;
+        c.least = (top - c.shift) - __fdiv_rn(46.5f, c.hi);
     }
     c.from = __fsub_rn(12288.0f, c.at);
     return c;
@@ -109,40 +112,59 @@ struct Weight {
     }
 };
 
-// Below 2^kSmall of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-41 of the top
-// weight, and there are few tokens near that.
-constexpr float kSmall = -7.0f;
+// Below 2^kSmall of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-38 of the top
+// weight, and few tokens are near that (all tokens' errors together are near 10^-12 of the sum).  At -7, 128 rows of
+// 100003 took 44.7 us, at -4 37.0: four tokens a thread share the branch, and seldom is none of 128 large.
+constexpr float kSmall = -4.0f;
 
-// The weight of a logit that is kept.  A token's weight has to be the same wherever it is taken, so no product and sum
-// here is left to the compiler to contract or not.
-__device__ __forceinline__ Weight weight(float l, const Scale &c, const WeightTable &tab) {
+// The weights of N logits (of a masked one: 0).  A token's weight has to be the same wherever it is taken, so no product
+// and sum here is left to the compiler to contract or not.  (Several at once, so that they share the branch around what
+// only large ones need.)
+template <int N>
+__device__ __forceinline__ void weights(const float *l, const Scale &c, const WeightTable &tab, Weight *w) {
     constexpr float M = 12288.0f;                  // 1.5 * 2^13: its last place is 2^-10
-    const float x = __fsub_rn(fminf(l, 3.4028234e38f), c.shift);
-    const float t = fmaf(x, c.hi, c.from), q = __fsub_rn(t, M), at = __fadd_rn(c.at, q);
-    const int m = __float_as_int(t);               // 1024 q in its low bits: those of 12288 end in 22 zeros
-    const float2 r = tab.r[m & 1023];
     constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
-    // 2^g = 1 + b, b = a (1 + a / 2 + a^2 / 6) with g = y - q, a = g ln 2; (head + tail) 2^g = h + lw
-    const float g = fmaf(x, c.lo, fmaf(x, c.hi, -at));
-    const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
-    float h = fmaf(r.x, b, r.x), lw = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h)), r.y);
-    if (t > M + kSmall) {
-        // g, a and b as sums of two
-        const float p = __fmul_rn(x, c.hi), g0 = __fsub_rn(p, at), ge = fmaf(x, c.lo, fmaf(x, c.hi, -p));
-        const float gh = __fadd_rn(g0, ge), gl = __fadd_rn(__fsub_rn(g0, gh), ge);
-        const float ah = __fmul_rn(gh, L), al = fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -ah)));
-        const float z = __fmul_rn(__fmul_rn(ah, ah), fmaf(ah, 0.16666667f, 0.5f));
-        const float bh = __fadd_rn(ah, z), bl = __fadd_rn(__fadd_rn(__fsub_rn(ah, bh), z), al);
-        h = fmaf(r.x, bh, r.x);
-        lw = __fadd_rn(fmaf(r.x, bh, __fsub_rn(r.x, h)), fmaf(r.x, bl, fmaf(r.y, bh, r.y)));
+    float x[N], t[N], h[N], lw[N];
+    bool large = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = fminf(fmaxf(__fsub_rn(l[i], c.shift), c.least), 3.4028234e38f);
+        t[i] = fmaf(x[i], c.hi, c.from);
+        const float at = __fadd_rn(c.at, __fsub_rn(t[i], M));
+        const float2 r = tab.r[__float_as_int(t[i]) & 1023];    // 1024 q is in the low bits: those of 12288 end in 22 zeros
+        // 2^g = 1 + b, b = a (1 + a / 2 + a^2 / 6) with g = y - q, a = g ln 2; (head + tail) 2^g = h + lw
+        const float g = fmaf(x[i], c.lo, fmaf(x[i], c.hi, -at));
+        const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
+        h[i] = fmaf(r.x, b, r.x);
+        lw[i] = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h[i])), r.y);
+        large |= t[i] > M + kSmall;
+    }
+    if (large) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // g, a and b as sums of two
+            const float at = __fadd_rn(c.at, __fsub_rn(t[i], M));
+            const float2 r = tab.r[__float_as_int(t[i]) & 1023];
+            const float p = __fmul_rn(x[i], c.hi), g0 = __fsub_rn(p, at), ge = fmaf(x[i], c.lo, fmaf(x[i], c.hi, -p));
+            const float gh = __fadd_rn(g0, ge), gl = __fadd_rn(__fsub_rn(g0, gh), ge);
+            const float ah = __fmul_rn(gh, L), al = fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -ah)));
+            const float z = __fmul_rn(__fmul_rn(ah, ah), fmaf(ah, 0.16666667f, 0.5f));
+            const float bh = __fadd_rn(ah, z), bl = __fadd_rn(__fadd_rn(__fsub_rn(ah, bh), z), al);
+            const float hl = fmaf(r.x, bh, r.x);
+            const float ll = __fadd_rn(fmaf(r.x, bh, __fsub_rn(r.x, hl)), fmaf(r.x, bl, fmaf(r.y, bh, r.y)));
+            h[i] = t[i] > M + kSmall ? hl : h[i];
+            lw[i] = t[i] > M + kSmall ? ll : lw[i];
+        }
     }
     // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
-    const float f = __int_as_float(((m & ~1023) << 13) + 0x3f800000);
     constexpr float M1 = 3.0f, M2 = 0x1.8p-21f;
-    const float hs = __fmul_rn(h, f), t1 = __fadd_rn(hs, M1);
-    const float t2 = __fadd_rn(fmaf(lw, f, __fsub_rn(hs, __fsub_rn(t1, M1))), M2);
-    const bool some = t > M - 45.5f;               // else below half a unit
-    return {some ? __float_as_uint(t1) - __float_as_uint(M1) : 0u, some ? __float_as_int(t2) - __float_as_int(M2) : 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float f = __int_as_float(((__float_as_int(t[i]) & ~1023) << 13) + 0x3f800000);
+        const float hs = __fmul_rn(h[i], f), t1 = __fadd_rn(hs, M1);
+        const float t2 = __fadd_rn(fmaf(lw[i], f, __fsub_rn(hs, __fsub_rn(t1, M1))), M2);
+        w[i] = {__float_as_uint(t1) - __float_as_uint(M1), __float_as_int(t2) - __float_as_int(M2)};
+    }
 }
 
 // ln(w / total) for a token of logit l, given the top token's weight, in fp32: (l - top) / T less ln(total / w_top), both
