@@ -15,7 +15,7 @@
 // below (integer counts and masses) leave no trace of their order.
 //
 // A thread-block cluster of 1 to 16 CTAs takes a row and goes over it two or
-// three times; the first pass reads HBM, the others find it in L1 or L2:
+// three times; the first pass reads HBM, the others find it in L2 (each_vec):
 //   1. the top logit and its lowest index (all that temperature 0 needs);
 //   2. top-k: the tokens from a bound on, to the first CTA's list.  The bound is
 //      the k-th largest of the threads' own tops, so it lies just below the k-th
@@ -31,9 +31,9 @@
 //      top-k and top-p this pass only sums;
 //   5. the warp that holds the drawn place goes over its stretch once more.
 //
-// What bounds it: with many rows the exact weights, about 60 instructions a
-// token, and the passes' traffic; with few rows latency -- a cluster barrier
-// costs ~0.7 us, a block-wide sum ~0.5 us.
+// What bounds it: with many rows the exact weights, about 25 instructions a
+// token, and top-p's histogram; with few rows
+// latency -- a cluster barrier costs ~0.7 us, a block-wide sum ~0.5 us.
 #include "internal.cuh"
 
 #include <cuda_bf16.h>
@@ -157,12 +157,13 @@ struct Sampler {
     __device__ __forceinline__ bool kept(float l, int i) const { return l > low || (l == low && i <= I); }
     __device__ __forceinline__ u64 units(float l) const {
         Weight w;
-        weights<1>(&l, sc, s.table, &w);
+        weights<1>(&l, l, sc, s.table, &w);
         return w.units();
     }
-    // the logit at which bin b (or cell b of bins of 1/kFine) begins, going down
+    // the logit at which bin b (or cell b of bins of 1/kFine) begins, going down; the top logit always lies in the first,
+    // though a logit as large as a mask's lowest value swallows a bin's width
     __device__ __forceinline__ float edge_of(float b, float scale) const {
-        return b <= 0.f ? INFINITY : top - __fdiv_rn(b, scale);
+        return b <= 0.f ? INFINITY : fminf(top - __fdiv_rn(b, scale), value_of(key_of(top) - 1));
     }
 
     __device__ __forceinline__ void start_row(const SampleArgs &a, int r) {
@@ -235,9 +236,10 @@ struct Sampler {
         each_vec([&](const float (&l)[E], int v) {
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
-                if (!(fmaxf(fmaxf(l[e], l[e + 1]), fmaxf(l[e + 2], l[e + 3])) >= low)) continue;      // none is kept
+                const float most = fmaxf(fmaxf(l[e], l[e + 1]), fmaxf(l[e + 2], l[e + 3]));
+                if (!(most >= low)) continue;      // none is kept
                 Weight w[4];
-                weights<4>(l + e, sc, s.table, w);
+                weights<4>(l + e, most, sc, s.table, w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) f(l[e + j], w[j], e + j, v);
             }

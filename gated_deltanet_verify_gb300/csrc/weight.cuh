@@ -11,9 +11,12 @@
 // fp32 would lose the small differences (its 2^-24 times a vocabulary of
 // borders is a wrong token every few dozen rows) and fp64 runs at 1/64 of the
 // fp32 rate here, so the products carry their rounding errors in a second fp32
-// (Dekker's and Knuth's error-free sums and products): about 30 fp32 and integer
-// instructions per weight, its error below 2^-43 of the top weight (2^-38 for a few).  fp64 is kept out of what every
-// thread does: one fp64 logarithm in all threads of a CTA costs microseconds.
+// (Dekker's and Knuth's error-free sums and products), all of them only for
+// weights above 2^-4 of the top one: about 22 instructions for the others, which
+// take no sum of two for g and end the series at g^2.  Errors: 2^-43 of the top
+// weight, 2^-38 for a few.  (Pairs of fp32 in one instruction, f32x2, took 4 %
+// longer: the moves cost more.)  fp64 is kept out of what every thread does: one
+// fp64 logarithm in all threads of a CTA costs microseconds.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,9 +38,11 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// 2^(j/1024) as an fp32 head and tail
+// 2^(j/1024) = head (1 + rest), the head an fp32 number, of which j 2^13 is taken off as an integer: with 1024 n + j times
+// 2^13 added again it is 2^n head (13 bits below the exponent's)
 struct WeightRow {
-    float head, tail;
+    int head;
+    float rest;
 };
 
 struct WeightRows {
@@ -54,8 +59,8 @@ constexpr WeightRows make_weight_rows() {
             term *= x / n;
             v += term;
         }
-        const float h = float(v);
-        t.r[j] = {h, float(v - double(h))};
+        const float h = float(v);                  // in [1, 2): its bits are those of 1 and 23 of (h - 1)
+        t.r[j] = {0x3f800000 + int((double(h) - 1) * 8388608) - (j << 13), float((v - double(h)) / double(h))};
     }
     return t;
 }
@@ -63,13 +68,18 @@ constexpr WeightRows make_weight_rows() {
 __device__ constexpr WeightRows kWeightRows = make_weight_rows();
 
 struct __align__(16) WeightTable {
-    float2 r[1024];
+    WeightRow r[1024];
     // by all threads of a block; a barrier follows before the first use
     __device__ __forceinline__ void fill(int tid, int n) {
         for (int i = tid; i < 512; i += n)
             reinterpret_cast<uint4 *>(r)[i] = reinterpret_cast<const uint4 *>(kWeightRows.r)[i];
     }
 };
+
+// Below 2^kSmall of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-38 of the top
+// weight, and few tokens are near that (all tokens' errors together are near 10^-12 of the sum).  At -7, 128 rows of
+// 100003 took 44.7 us, at -4 37.0: four tokens a thread share the branch, and seldom is none of 128 large.
+constexpr float kSmall = -4.0f;
 
 // What the weights of a row share: y = x c - at with x = l - shift, c = hi + lo = log2(e) / T, and `at` (top - shift) c
 // rounded up to a multiple of 2^-10 (by one or two of them, so that y < 0).  With q a multiple of 2^-10 too, at + q is
@@ -78,6 +88,7 @@ struct __align__(16) WeightTable {
 struct Scale {
     float hi, lo, shift, at, from;                 // from: 12288 - at, where y is rounded to q
     float least;                                   // an x whose weight rounds to 0; lower ones (and NaN) count as it
+    float large;                                   // a little below the logits whose y is above kSmall
 };
 __device__ __forceinline__ Scale scale_of(float temp, float top) {
     constexpr float L = 1.44269502162933349609375f, Ll = 1.92596303350001e-8f;      // log2(e) = L + Ll
@@ -86,13 +97,14 @@ __device__ __forceinline__ Scale scale_of(float temp, float top) {
     c.lo = __fdiv_rn(fmaf(-c.hi, temp, L) + Ll, temp);
     c.shift = c.at = 0.f;
     if (top == INFINITY) {
-        c.hi = c.lo = 0.f;                         // only infinite logits are kept, all alike
-        c.least = -3.4028234e38f;
+        c.shift = c.large = top;                   // only infinite logits are kept, all alike
+        c.hi = c.lo = c.least = 0.f;
     } else {
         const float p = __fmul_rn(top, c.hi);
         if (fabsf(p) < 2048.f) c.at = (ceilf(p * 1024.f) + 1.f) * (1.f / 1024);
         else c.shift = top;
         c.least = (top - c.shift) - __fdiv_rn(46.5f, c.hi);
+        c.large = __fsub_rd(top, __fdiv_ru(0.01f - kSmall, c.hi));
     }
     c.from = __fsub_rn(12288.0f, c.at);
     return c;
@@ -112,57 +124,53 @@ struct Weight {
     }
 };
 
-// Below 2^kSmall of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-38 of the top
-// weight, and few tokens are near that (all tokens' errors together are near 10^-12 of the sum).  At -7, 128 rows of
-// 100003 took 44.7 us, at -4 37.0: four tokens a thread share the branch, and seldom is none of 128 large.
-constexpr float kSmall = -4.0f;
-
-// The weights of N logits (of a masked one: 0).  A token's weight has to be the same wherever it is taken, so no product
-// and sum here is left to the compiler to contract or not.  (Several at once, so that they share the branch around what
-// only large ones need.)
+// The weights of N logits (of a masked one: 0), `most` the largest of them.  A token's weight has to be the same wherever
+// it is taken, so no product and sum here is left to the compiler to contract or not.  (Several at once, so that they
+// share the branch around what only large ones need.)
 template <int N>
-__device__ __forceinline__ void weights(const float *l, const Scale &c, const WeightTable &tab, Weight *w) {
+__device__ __forceinline__ void weights(const float *l, float most, const Scale &c, const WeightTable &tab, Weight *w) {
     constexpr float M = 12288.0f;                  // 1.5 * 2^13: its last place is 2^-10
     constexpr float L = 0.693147182464599609375f, Ll = -1.90465429995776804525e-9f;   // ln 2 = L + Ll
     float x[N], t[N], h[N], lw[N];
-    bool large = false;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        x[i] = fminf(fmaxf(__fsub_rn(l[i], c.shift), c.least), 3.4028234e38f);
+        x[i] = fmaxf(__fsub_rn(l[i], c.shift), c.least);
         t[i] = fmaf(x[i], c.hi, c.from);
-        const float at = __fadd_rn(c.at, __fsub_rn(t[i], M));
-        const float2 r = tab.r[__float_as_int(t[i]) & 1023];    // 1024 q is in the low bits: those of 12288 end in 22 zeros
-        // 2^g = 1 + b, b = a (1 + a / 2 + a^2 / 6) with g = y - q, a = g ln 2; (head + tail) 2^g = h + lw
+        const float at = __fsub_rn(t[i], c.from);  // at + q, exactly
+        const int n = __float_as_int(t[i]);        // 1024 q is in its low bits: those of 12288 end in 22 zeros
+        const WeightRow r = tab.r[n & 1023];
+        const float rx = __int_as_float(r.head + (n << 13));
+        // 2^g (1 + rest) = 1 + b to 2^-36, with g = y - q; the weight is rx (1 + b) = h + lw
         const float g = fmaf(x[i], c.lo, fmaf(x[i], c.hi, -at));
-        const float a = __fmul_rn(g, L), b = fmaf(__fmul_rn(a, fmaf(a, 0.16666667f, 0.5f)), a, a);
-        h[i] = fmaf(r.x, b, r.x);
-        lw[i] = __fadd_rn(fmaf(r.x, b, __fsub_rn(r.x, h[i])), r.y);
-        large |= t[i] > M + kSmall;
+        const float b = fmaf(g, fmaf(g, 0.2402265f, L), r.rest);
+        h[i] = fmaf(rx, b, rx);
+        lw[i] = fmaf(rx, b, __fsub_rn(rx, h[i]));
     }
-    if (large) {
+    if (most > c.large) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            // g, a and b as sums of two
-            const float at = __fadd_rn(c.at, __fsub_rn(t[i], M));
-            const float2 r = tab.r[__float_as_int(t[i]) & 1023];
+            // 2^g = 1 + b, b = a (1 + a / 2 + a^2 / 6) with a = g ln 2; g, a and b as sums of two
+            const float at = __fsub_rn(t[i], c.from);
+            const int n = __float_as_int(t[i]);
+            const WeightRow r = tab.r[n & 1023];
+            const float rx = __int_as_float(r.head + (n << 13));
             const float p = __fmul_rn(x[i], c.hi), g0 = __fsub_rn(p, at), ge = fmaf(x[i], c.lo, fmaf(x[i], c.hi, -p));
             const float gh = __fadd_rn(g0, ge), gl = __fadd_rn(__fsub_rn(g0, gh), ge);
             const float ah = __fmul_rn(gh, L), al = fmaf(gl, L, fmaf(gh, Ll, fmaf(gh, L, -ah)));
             const float z = __fmul_rn(__fmul_rn(ah, ah), fmaf(ah, 0.16666667f, 0.5f));
             const float bh = __fadd_rn(ah, z), bl = __fadd_rn(__fadd_rn(__fsub_rn(ah, bh), z), al);
-            const float hl = fmaf(r.x, bh, r.x);
-            const float ll = __fadd_rn(fmaf(r.x, bh, __fsub_rn(r.x, hl)), fmaf(r.x, bl, fmaf(r.y, bh, r.y)));
+            const float hl = fmaf(rx, bh, rx);
+            const float ll = fmaf(rx, __fadd_rn(bl, fmaf(bh, r.rest, r.rest)), fmaf(rx, bh, __fsub_rn(rx, hl)));
             h[i] = t[i] > M + kSmall ? hl : h[i];
             lw[i] = t[i] > M + kSmall ? ll : lw[i];
         }
     }
-    // times 2^n, then in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
+    // in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
     constexpr float M1 = 3.0f, M2 = 0x1.8p-21f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float f = __int_as_float(((__float_as_int(t[i]) & ~1023) << 13) + 0x3f800000);
-        const float hs = __fmul_rn(h[i], f), t1 = __fadd_rn(hs, M1);
-        const float t2 = __fadd_rn(fmaf(lw[i], f, __fsub_rn(hs, __fsub_rn(t1, M1))), M2);
+        const float t1 = __fadd_rn(h[i], M1);
+        const float t2 = __fadd_rn(__fadd_rn(lw[i], __fsub_rn(h[i], __fsub_rn(t1, M1))), M2);
         w[i] = {__float_as_uint(t1) - __float_as_uint(M1), __float_as_int(t2) - __float_as_int(M2)};
     }
 }

@@ -50,7 +50,8 @@ def check(logits, u, temp=None, top_k=None, top_p=None, min_p=None, T=1, vocab=N
         else:
             # x - ln(sum), both terms <= 0: x is a rounded quotient of a rounded difference (2 units of 2^-24 of it), the
             # logarithm is within 1 ulp (2 units) of a rounded argument (1 unit), their difference is rounded (1 unit): 4
-            # units of the whole at most; the sum itself is within 2^-44 of the top weight a token
+            # units of the whole at most; the sum itself is within 2^-44 of the top weight a token, and 2^-34 of those
+            # tokens' weights that are below 2^-4 of the top one: less than 2^-34 of ln(sum / top), which the token pays too
             assert abs(lph[i] - ref[1]) <= 4 * 2.0 ** -24 * abs(ref[1]) + V * 2.0 ** -44 + 1e-12, (i, lph[i], ref)
 
 
@@ -136,6 +137,19 @@ def test_ties_are_kept_by_index():
     zero = torch.zeros((4, 500), device="cuda")
     zero[:, ::2] = -0.0            # -0 equals 0: the lower index first
     check(zero, uniforms(4), temp=[0.0, 1.0, 1.0, 1.0], top_k=[0, 1, 2, 251])
+
+
+@pytest.mark.parametrize("base", [1e8, -1e30, 3e38])
+def test_large_logits(base):
+    # a place of the largest is wider than the differences that the temperature tells apart (but the last temperature)
+    V = 20001
+    g = torch.Generator(device="cuda").manual_seed(77)
+    step = 2.0 ** (np.floor(np.log2(abs(base))) - 23)
+    l = (torch.randint(0, 12, (8, V), generator=g, device="cuda").double() * step + base).float()
+    l[6:] = base                                      # all equal, as in a row of an additive mask
+    for temp in (1.0, min(4.0 * step, 2.0 ** 20)):
+        check(l, uniforms(8, seed=12), temp=[temp] * 8, top_p=[0.2, 0.5, 0.9, 0.99, 1.0, 1.0, 0.4, 0.9],
+              top_k=[0, 0, 0, 5000, 700, 0, 0, 3])
 
 
 def test_masks_infinities_and_lowest_values():
