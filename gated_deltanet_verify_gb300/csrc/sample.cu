@@ -231,17 +231,23 @@ struct Sampler {
             for (int e = 0; e < E; ++e) f(l[e], v * E - head + e);
         });
     }
-    // f(logit, weight, index in the vector, vector) for every element, four at a time, but those where all are below low
+    // f(logit, weight, index in the vector, vector) for every element, four at a time, but those where all are below low; a
+    // token is kept if the logit that f gets is at least low (that of one at low, but behind I, is -inf)
     template <typename F> __device__ __forceinline__ void each_weight(F f) const {
         each_vec([&](const float (&l)[E], int v) {
 #pragma unroll
             for (int e = 0; e < E; e += 4) {
-                const float most = fmaxf(fmaxf(l[e], l[e + 1]), fmaxf(l[e + 2], l[e + 3]));
+                float m[4] = {l[e], l[e + 1], l[e + 2], l[e + 3]};
+                if (I < V)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (m[j] == low && v * E - head + e + j > I) m[j] = -INFINITY;
+                const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 if (!(most >= low)) continue;      // none is kept
                 Weight w[4];
-                weights<4>(l + e, most, sc, s.table, w);
+                weights<4>(m, most, sc, s.table, w);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) f(l[e + j], w[j], e + j, v);
+                for (int j = 0; j < 4; ++j) f(m[j], w[j], e + j, v);
             }
         });
     }
@@ -317,17 +323,35 @@ struct Sampler {
         if (!open) clear();                      // at the start they are clear
         if (tid == 0) s.n_list = 0;
         __syncthreads();
-        each([&](float l, int i) {
-            if (!kept(l, i)) return;
-            // monotone in l; 0 for the top logit (inf - inf gives NaN, which converts to 0)
-            const float x = (top - l) * scale;
-            int b = __float2int_rz(x) - first;
-            if (open) {
-                if (b < kHead) atomicAdd(&s.hist_in[b], uint32_t(__float2int_rz((x - b) * 256.f)));
-                b = min(b, kBins - 1);
-            }
-            if (unsigned(b) < unsigned(kBins)) atomicAdd(&s.hist[b], 1u);
-        });
+        if (open && top < INFINITY) {
+            const uint32_t counts = smem_u32(s.hist) - 4u * 0x4b400000u;
+            const float heavy = top - __fdividef(kHead + 1.f, scale);
+            each_vec([&](const float (&l)[E], int) {
+                float most = l[0];
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    most = fmaxf(most, l[e]);
+                    // the bin in the low bits of a sum that is rounded down, its ulp 1
+                    const float x = fminf((top - l[e]) * scale, kBins - 0.5f);
+                    const uint32_t at = counts + 4u * __float_as_uint(__fadd_rz(x, 12582912.f));
+                    if (l[e] >= low) asm volatile("red.shared.add.u32 [%0], 1;\n" ::"r"(at) : "memory");
+                }
+                if (most > heavy)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float x = (top - l[e]) * scale;
+                        const int b = __float2int_rz(x);
+                        if (l[e] >= low && b < kHead) atomicAdd(&s.hist_in[b], uint32_t(__float2int_rz((x - b) * 256.f)));
+                    }
+            });
+        } else {
+            each([&](float l, int i) {
+                if (!kept(l, i)) return;
+                // 0 for the top logit (inf - inf gives NaN, which converts to 0)
+                const int b = __float2int_rz((top - l) * scale) - first;
+                if (unsigned(b) < unsigned(kBins)) atomicAdd(&s.hist[b], 1u);
+            });
+        }
         sync_cluster();
         const uint32_t *from = s.hist;
         if (n_cta > 1) {
@@ -579,11 +603,10 @@ struct Sampler {
         };
         if (MASS) {
             each_weight([&](float l, const Weight &w, int e, int v) {
-                const int i = v * E - head + e;
-                if (!kept(l, i)) return;
+                if (!(l >= low)) return;
                 w_all += w;
                 if (l > from) w_before += w;
-                else if (l > to) hold(l, i, w.units());
+                else if (l > to) hold(l, v * E - head + e, w.units());
             });
         } else {
             each([&](float l, int i) {
@@ -897,16 +920,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         know_mass = false;
     }
     if (!know_mass) {
-        // I is set where top-k or top-p ended among equals: else the logit alone decides
         Weight m{0, 0};
-        if (x.I == a.V)
-            x.each_weight([&](float l, const Weight &w, int, int) {
-                if (l >= x.low) m += w;
-            });
-        else
-            x.each_weight([&](float l, const Weight &w, int e, int v) {
-                if (x.kept(l, v * E - x.head + e)) m += w;
-            });
+        x.each_weight([&](float l, const Weight &w, int, int) {
+            if (l >= x.low) m += w;
+        });
         const u64 mine = x.warp_all(m.units(), Add());
         __syncthreads();
         if (x.lane == 0) s.warp_sum[x.wid] = mine;

@@ -76,10 +76,10 @@ struct __align__(16) WeightTable {
     }
 };
 
-// Below 2^kSmall of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-38 of the top
+// Below 2^kLarge of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-38 of the top
 // weight, and few tokens are near that (all tokens' errors together are near 10^-12 of the sum).  At -7, 128 rows of
 // 100003 took 44.7 us, at -4 37.0: four tokens a thread share the branch, and seldom is none of 128 large.
-constexpr float kSmall = -4.0f;
+constexpr float kLarge = -4.0f;
 
 // What the weights of a row share: y = x c - at with x = l - shift, c = hi + lo = log2(e) / T, and `at` (top - shift) c
 // rounded up to a multiple of 2^-10 (by one or two of them, so that y < 0).  With q a multiple of 2^-10 too, at + q is
@@ -88,7 +88,7 @@ constexpr float kSmall = -4.0f;
 struct Scale {
     float hi, lo, shift, at, from;                 // from: 12288 - at, where y is rounded to q
     float least;                                   // an x whose weight rounds to 0; lower ones (and NaN) count as it
-    float large;                                   // a little below the logits whose y is above kSmall
+    float large;                                   // a little below the logits whose y is above kLarge
 };
 __device__ __forceinline__ Scale scale_of(float temp, float top) {
     constexpr float L = 1.44269502162933349609375f, Ll = 1.92596303350001e-8f;      // log2(e) = L + Ll
@@ -104,7 +104,7 @@ __device__ __forceinline__ Scale scale_of(float temp, float top) {
         if (fabsf(p) < 2048.f) c.at = (ceilf(p * 1024.f) + 1.f) * (1.f / 1024);
         else c.shift = top;
         c.least = (top - c.shift) - __fdiv_rn(46.5f, c.hi);
-        c.large = __fsub_rd(top, __fdiv_ru(0.01f - kSmall, c.hi));
+        c.large = __fsub_rd(top, __fdiv_ru(0.01f - kLarge, c.hi));
     }
     c.from = __fsub_rn(12288.0f, c.at);
     return c;
@@ -161,8 +161,8 @@ __device__ __forceinline__ void weights(const float *l, float most, const Scale 
             const float bh = __fadd_rn(ah, z), bl = __fadd_rn(__fadd_rn(__fsub_rn(ah, bh), z), al);
             const float hl = fmaf(rx, bh, rx);
             const float ll = fmaf(rx, __fadd_rn(bl, fmaf(bh, r.rest, r.rest)), fmaf(rx, bh, __fsub_rn(rx, hl)));
-            h[i] = t[i] > M + kSmall ? hl : h[i];
-            lw[i] = t[i] > M + kSmall ? ll : lw[i];
+            h[i] = t[i] > M + kLarge ? hl : h[i];
+            lw[i] = t[i] > M + kLarge ? ll : lw[i];
         }
     }
     // in units of 2^-22 and of 2^-44 (the last places of 1.5 * 2 and of 1.5 * 2^-21), to nearest
