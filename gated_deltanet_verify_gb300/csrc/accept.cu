@@ -15,7 +15,7 @@
 // one load per lane and tensor (two past 32 tokens), then ballots; the walk
 // down a tree keeps its nodes in registers (two per lane), so a step costs two
 // ballots and a shuffle and no memory access.
-#include "internal.cuh"
+#include "step.cuh"
 
 namespace gdn {
 namespace {

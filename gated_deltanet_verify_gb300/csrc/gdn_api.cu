@@ -1,7 +1,7 @@
 // gdn_api.cu -- the C ABI declared in include/gdn_verify.h: argument
 // validation, launch-shape choice and error reporting.  No allocation, no
 // synchronisation: every call only enqueues work on the caller's stream.
-#include "internal.cuh"
+#include "step.cuh"
 
 #include <cstdarg>
 #include <cstdint>

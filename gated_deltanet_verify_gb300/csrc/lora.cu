@@ -18,7 +18,7 @@
 // a few loads at one slot; so K is split over a cluster of up to 8 CTAs and
 // their 8 warps, and the sums are joined through distributed shared memory in a
 // fixed order.
-#include "internal.cuh"
+#include "step.cuh"
 
 #include <cuda_bf16.h>
 

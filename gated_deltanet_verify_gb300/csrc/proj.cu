@@ -42,7 +42,7 @@
 //     the K blocks stream.
 //   * Every wait is bounded; a wait that gives up reports GDN_ERR_TIMEOUT on
 //     the caller's status word (when one is given) and the tile is skipped.
-#include "internal.cuh"
+#include "step.cuh"
 
 #include <cuda_bf16.h>
 #include <type_traits>

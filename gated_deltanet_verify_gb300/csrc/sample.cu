@@ -34,7 +34,7 @@
 // What bounds it: with many rows the exact weights, about 25 instructions a
 // token, and top-p's histogram; with few rows
 // latency -- a cluster barrier costs ~0.7 us, a block-wide sum ~0.5 us.
-#include "internal.cuh"
+#include "step.cuh"
 
 #include <cuda_bf16.h>
 
