@@ -18,6 +18,14 @@
 // a few loads at one slot; so K is split over a cluster of up to 8 CTAs and
 // their 8 warps, and the sums are joined through distributed shared memory in a
 // fixed order.
+//
+// Measured, a projection with adapters against the same without (captured graph):
+// input projection, hidden 5120, one slot of 16 rows, rank 16: 30.9 us against
+// 28.6; 32 slots: 95 against 87; 8 slots of rank 128: 48 against 34.7; output
+// projection, 8 slots of rank 64: 24.5 against 18.4.  This kernel runs beside the
+// projection's weight stream, which does not wait for it; what is left are loads
+// that take 4-5 us a round while that stream fills HBM's queues, and the adapters'
+// own tiles at the end of the projection's ring.
 #include "step.cuh"
 
 #include <cuda_bf16.h>
@@ -64,7 +72,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 // R8: the tiles of eight rank columns held in registers, at most; more than 64 columns go to CTAs by 64
 template <int R8>
 __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs a) {
-    extern __shared__ float part[];              // [warp][16][rl]; the first [16][rl] holds the CTA's sum afterwards
+    extern __shared__ float part[];              // [kWarps / 2][16][rl]; the first [16][rl] holds the CTA's sum afterwards
     // The projection starts once every CTA here has seen the kernel before complete, so it may read X at once; it
     // waits for this grid's results itself.
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -108,19 +116,28 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
                 mma16816(acc[n], p[h].z, q[h].z, p[h].w, q[h].w, b[h][n].z, b[h][n].w);
             }
     }
-    float *mine = part + wid * 16 * rl;
+    // the upper half of the warps leave their sums, the lower half add theirs: half the shared memory, so that a CTA of the
+    // projection finds room beside this one
+    float *mine = part + (wid & (kWarps / 2 - 1)) * 16 * rl;
 #pragma unroll
-    for (int n = 0; n < R8; ++n)
-        if (n < n8) {
-            *reinterpret_cast<float2 *>(mine + g * rl + n * 8 + 2 * t) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2 *>(mine + (g + 8) * rl + n * 8 + 2 * t) = make_float2(acc[n][2], acc[n][3]);
-        }
-    __syncthreads();
+    for (int half = 1; half >= 0; --half) {
+        if (wid / (kWarps / 2) == half)
+#pragma unroll
+            for (int n = 0; n < R8; ++n)
+                if (n < n8) {
+                    float2 *u = reinterpret_cast<float2 *>(mine + g * rl + n * 8 + 2 * t);
+                    float2 *v = reinterpret_cast<float2 *>(mine + (g + 8) * rl + n * 8 + 2 * t);
+                    const float2 x = half ? make_float2(0.f, 0.f) : *u, y = half ? make_float2(0.f, 0.f) : *v;
+                    *u = make_float2(x.x + acc[n][0], x.y + acc[n][1]);
+                    *v = make_float2(y.x + acc[n][2], y.y + acc[n][3]);
+                }
+        __syncthreads();
+    }
     for (int i = threadIdx.x; i < 16 * rl; i += kThreads) {
         float v = part[i];
 #pragma unroll
-        for (int q = 1; q < kWarps; ++q) v += part[q * 16 * rl + i];
-        part[i] = v;                             // only this thread reads or writes element i of any warp
+        for (int q = 1; q < kWarps / 2; ++q) v += part[q * 16 * rl + i];
+        part[i] = v;                             // only this thread reads or writes element i of any part
     }
     const float scale = a.scale ? a.scale[id] : 1.0f;
     if (S > 1) cluster_sync();
@@ -151,12 +168,25 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
 }
 
 template <int R8> cudaError_t launch_t(const ShrinkArgs &a, int pairs, int sms, cudaStream_t stream) {
-    // CTAs a pair and 64 rank columns: while all fit the SMs twice over, and every warp has a k step
+    // CTAs a pair and 64 rank columns: while there is an SM for each, and every warp has a k step (output projection,
+    // 8 slots of rank 64: 45, 32, 28, 24.5 us with 1, 2, 4, 8; 32 slots, two CTAs an SM: 62 us against 54)
     const int parts = (a.r + 63) / 64;
     int S = 1;
-    while (S < kMaxSplit && (long long)pairs * parts * S * 2 <= 2LL * sms && a.K >= 2 * S * kWarps * 32) S *= 2;
-    const size_t smem = size_t(kWarps) * 16 * (a.r < 64 ? a.r : 64) * 4;
+    while (S < kMaxSplit && (long long)pairs * parts * S * 2 <= sms && a.K >= 2 * S * kWarps * 32) S *= 2;
+    const size_t smem = size_t(kWarps / 2) * 16 * (a.r < 64 ? a.r : 64) * 4;
     auto kern = lora_shrink_kernel<R8>;
+    // An SM that has its shared memory divided for a small kernel takes none of the projection's CTAs until it is empty
+    // (input projection, 32 slots of one row: 40.5 us against 37; 32 of 16 rows: 97.6 against 95).  Function attributes
+    // belong to the context: set once in each.
+    static PerContext<int> attrs;
+    unsigned long long ctx = 0;
+    int set = 0;
+    if (!(current_context_id(&ctx) && attrs.get(ctx, &set))) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+        if (current_context_id(&ctx)) attrs.put(ctx, 1);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(pairs), unsigned(S), unsigned(parts));
     cfg.blockDim = dim3(kThreads, 1, 1);
