@@ -14,7 +14,8 @@
 // A few hundred bytes per slot, so launch latency bounds it: one warp per slot,
 // one load per lane and tensor (two past 32 tokens), then ballots; the walk
 // down a tree keeps its nodes in registers (two per lane), so a step costs two
-// ballots and a shuffle and no memory access.
+// ballots and a shuffle and no memory access.  In a captured graph a chain takes
+// 1.2 us (8 slots of 16 to 1024 of 64), a tree 1.6 to 2.5 us.
 #include "step.cuh"
 
 namespace gdn {

@@ -15,7 +15,7 @@
 // below (integer counts and masses) leave no trace of their order.
 //
 // A thread-block cluster of 1 to 16 CTAs takes a row and goes over it two or
-// three times; the first pass reads HBM, the others find it in L2 (each_vec):
+// three times; the first pass reads HBM, the others find it in L2:
 //   1. the top logit and its lowest index (all that temperature 0 needs);
 //   2. top-k: the tokens from a bound on, to the first CTA's list.  The bound is
 //      the k-th largest of the threads' own tops, so it lies just below the k-th
@@ -31,9 +31,16 @@
 //      top-k and top-p this pass only sums;
 //   5. the warp that holds the drawn place goes over its stretch once more.
 //
-// What bounds it: with many rows the exact weights, about 25 instructions a
-// token, and top-p's histogram; with few rows
-// latency -- a cluster barrier costs ~0.7 us, a block-wide sum ~0.5 us.
+// What bounds it: with many rows instruction issue (60 instructions a token in
+// all without filters, about 25 of them the exact weight; 64 % of the issue slots
+// used); with few rows latency -- a cluster barrier costs ~0.7 us, a block-wide
+// sum ~0.5 us, and code that is run once waits for its instructions.
+//
+// Measured, f32 (bf16), per call in a captured graph: one row of 32768, greedy
+// 3.7 us (3.5), no filter 8.3 (9.3), top-k + top-p + min-p 10.7 (10.5), top-p alone
+// 19.8 (24.4); 16 rows of 131072, top-p 37.5 (42.8); 128 rows of 100003, no filter
+// 34.0 (29.3), top-p 69.5 (82); 256 rows of 200000, greedy 37 us (5.5 TB/s), no
+// filter 113 (96), top-p 215 (199), mixed filters 157 (134).
 #include "step.cuh"
 
 #include <cuda_bf16.h>
@@ -853,7 +860,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
     if (bounded) {
         const float least = value_of(bound);
         x.each([&](float l, int i) {
-            if (l >= least) x.push(key_of(l + 0.0f), i, l >= x.low ? x.units(l) : 0);
+            if (l >= least) x.push(key_of(l + 0.0f), i, 0);
         });
         x.sync_cluster();
         const uint32_t n = ld_cluster32(map_cluster(&s.n_list, 0));
@@ -883,6 +890,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
         int place = 0;
         if (tid < n) {
             me = s.list[tid];
+            const float l = value_of(uint32_t(me.order >> 32));
+            s.list[tid].stat = me.stat = l >= x.low ? x.units(l) : 0;
+        }
+        __syncthreads();
+        if (tid < n) {
             for (int j = 0; j < n; ++j) {
                 const Item o = s.list[j];
                 if (o.order > me.order) {
@@ -951,14 +963,14 @@ struct Plan {
     int n_cta, threads;
 };
 Plan plan_of(int rows, int vocab, int sms) {
-    // few rows: one CTA of 512 threads per SM in all, 4096 tokens each at least (16 rows of 131072, top-p: 4, 8 and 16
-    // CTAs take 58, 50 and 75 us).  From a quarter to half as many rows as SMs, four CTAs, two per SM, even out rows of
-    // different cost (64 mixed rows: 45 us against 67 with two).
+    // few rows: one CTA of 512 threads per SM in all, 4096 tokens each at least (16 rows of 131072, top-p: 2, 4, 8 and 16
+    // CTAs take 55, 38, 38 and 62 us).  From a quarter to half as many rows as SMs, four CTAs, two per SM, even out rows of
+    // different cost (64 mixed rows: 40 us against 57 with two).
     int n = 1;
     while (n < kMaxCluster && (long long)rows * n * 2 <= sms && vocab / (2 * n) >= 4096) n *= 2;
     if (n == 2 && (long long)rows * 4 <= 2LL * sms && vocab / 4 >= 4096) n = 4;
-    // one CTA per row: 1024 threads while rows are fewer than two per SM (128 rows of 100003, top-p: 77 us against 98
-    // with 512; 512 rows of 50000: 177 against 148); a thread's weights add up in 32 bits for 1000 tokens
+    // one CTA per row: 1024 threads while rows are fewer than two per SM (128 rows of 100003, top-p: 70 us against 88
+    // with 512; 512 rows of 50000: 152 against 127); a thread's weights add up in 32 bits for 1000 tokens
     const bool wide = n == 1 && vocab > 8192 && (rows <= 2 * sms || vocab > 262144);
     return {n, wide ? 1024 : 512};
 }

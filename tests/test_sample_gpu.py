@@ -152,6 +152,13 @@ def test_large_logits(base):
               top_k=[0, 0, 0, 5000, 700, 0, 0, 3])
 
 
+def test_many_infinite_logits():
+    l = logits_of(6, 40003, seed=13)
+    l[:, ::2] = float("inf")
+    check(l, uniforms(6, seed=14), temp=[1.0] * 6, top_k=[1, 9000, 20001, 20002, 30000, 0],
+          top_p=[1.0, 0.5, 0.9, 1.0, 0.3, 0.7], min_p=[0.0, 0.0, 0.5, 0.0, 0.0, 1.0])
+
+
 def test_masks_infinities_and_lowest_values():
     V = 1537
     for dtype in (torch.float32, torch.bfloat16):
