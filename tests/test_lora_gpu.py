@@ -160,6 +160,22 @@ def test_repeats_graphs_and_streams():
     assert torch.equal(c.y[:c.M * c.N].view(c.M, c.N), c.run())
 
 
+def test_large_batches_back_to_back():
+    # several launches at once in flight, each one's weights asked for while the one before ends
+    c = Case(shape_of(n_slots=32, n_tokens=16, n_qk_heads=16, n_v_heads=48, d_k=128, d_v=128, n_embd=2048), "in", 4, 16,
+             [i % 5 - 1 for i in range(32)])
+    want, shared = c.run().clone(), c.plain()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [c.plain(), c.plain()]
+        c.run()
+        c.run()
+        got.append(c.plain())
+    torch.cuda.synchronize()
+    assert torch.equal(c.y[:c.M * c.N].view(c.M, c.N), want)
+    assert all(torch.equal(y, shared) for y in got)
+
+
 def _layer(shape, cases, which, x, status):
     """gdn_layer_verify_lora with adapters on the projections named in `which`; (y, act, out)."""
     dims = dims_of(shape)
