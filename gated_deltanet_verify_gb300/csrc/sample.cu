@@ -37,8 +37,8 @@
 // sum ~0.5 us, and code that is run once waits for its instructions.
 //
 // Measured, f32 (bf16), per call in a captured graph: one row of 32768, greedy
-// 3.7 us (3.5), no filter 8.3 (9.3), top-k + top-p + min-p 10.7 (10.5), top-p alone
-// 19.8 (24.4); 16 rows of 131072, top-p 37.5 (42.8); 128 rows of 100003, no filter
+// 3.4 us (3.3), no filter 7.9 (8.9), top-k + top-p + min-p 10.0 (9.8), top-p alone
+// 19.7 (23.4); 16 rows of 131072, top-p 37.5 (42.8); 128 rows of 100003, no filter
 // 34.0 (29.3), top-p 69.5 (82); 256 rows of 200000, greedy 37 us (5.5 TB/s), no
 // filter 113 (96), top-p 215 (199), mixed filters 157 (134).
 #include "step.cuh"
@@ -756,8 +756,8 @@ struct Sampler {
     }
 };
 
-template <typename L, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
+template <typename L, int NT, int PER_SM>
+__global__ void __launch_bounds__(NT, PER_SM) sample_kernel(const SampleArgs a, int n_cta, int cta_vecs) {
     extern __shared__ __align__(16) unsigned char smem[];
     Shared &s = *reinterpret_cast<Shared *>(smem);
     Sampler<L, NT> x{s, reinterpret_cast<uint4 *>(smem + kSharedBytes)};
@@ -958,9 +958,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) sample_kernel(const SampleArgs 
                [&](float l, int i) { finish(i, log_prob(l, x.top, temp, x.units(x.top), total)); });
 }
 
-// CTAs per row, a power of two up to 16, and threads per CTA
+// CTAs per row, a power of two up to 16, threads per CTA and the CTAs that an SM has registers for
 struct Plan {
-    int n_cta, threads;
+    int n_cta, threads, per_sm;
 };
 Plan plan_of(int rows, int vocab, int sms) {
     // few rows: one CTA of 512 threads per SM in all, 4096 tokens each at least (16 rows of 131072, top-p: 2, 4, 8 and 16
@@ -972,14 +972,16 @@ Plan plan_of(int rows, int vocab, int sms) {
     // one CTA per row: 1024 threads while rows are fewer than two per SM (128 rows of 100003, top-p: 70 us against 88
     // with 512; 512 rows of 50000: 152 against 127); a thread's weights add up in 32 bits for 1000 tokens
     const bool wide = n == 1 && vocab > 8192 && (rows <= 2 * sms || vocab > 262144);
-    return {n, wide ? 1024 : 512};
+    // up to half the SMs: twice the registers a thread (one row of 32768, top-k: 8.3 us against 9.0).  With more, clusters
+    // that get no two CTAs on an SM wait for each other (16 rows of 131072, top-p: 53 us against 37).
+    return {n, wide ? 1024 : 512, wide || (long long)rows * n * 2 <= sms ? 1 : 2};
 }
 
-template <typename L, int NT> cudaError_t launch_t(const SampleArgs &a, int n, cudaStream_t stream) {
+template <typename L, int NT, int PER_SM> cudaError_t launch_t(const SampleArgs &a, int n, cudaStream_t stream) {
     constexpr int E = 16 / sizeof(L);
     const int row_vecs = (a.V + 2 * E - 2) / E;              // whatever its first vector's alignment
     const int vecs = (row_vecs + n - 1) / n;
-    auto kern = sample_kernel<L, NT>;
+    auto kern = sample_kernel<L, NT, PER_SM>;
     const size_t smem = kSharedBytes + size_t(Sampler<L, NT>::kRing) * NT * 16;
     // function attributes belong to the context: set once in each
     static PerContext<int> attrs;
@@ -1012,11 +1014,13 @@ template <typename L, int NT> cudaError_t launch_t(const SampleArgs &a, int n, c
 
 cudaError_t launch_sample(const SampleArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream) {
     const Plan plan = plan_of(a.B * a.T, a.V, sm_count);
-    if (plan.threads == 1024)
-        return dtype == GDN_BF16 ? launch_t<__nv_bfloat16, 1024>(a, plan.n_cta, stream)
-                                 : launch_t<float, 1024>(a, plan.n_cta, stream);
-    return dtype == GDN_BF16 ? launch_t<__nv_bfloat16, 512>(a, plan.n_cta, stream)
-                             : launch_t<float, 512>(a, plan.n_cta, stream);
+    auto launch = [&](auto logit) {
+        using L = decltype(logit);
+        return plan.threads == 1024 ? launch_t<L, 1024, 1>(a, plan.n_cta, stream)
+               : plan.per_sm == 1   ? launch_t<L, 512, 1>(a, plan.n_cta, stream)
+                                    : launch_t<L, 512, 2>(a, plan.n_cta, stream);
+    };
+    return dtype == GDN_BF16 ? launch(__nv_bfloat16()) : launch(float());
 }
 
 }  // namespace gdn
