@@ -38,8 +38,8 @@
 //
 // Measured, f32 (bf16), per call in a captured graph: one row of 32768, greedy
 // 3.4 us (3.3), no filter 7.9 (8.9), top-k + top-p + min-p 10.0 (9.8), top-p alone
-// 19.7 (23.4); 16 rows of 131072, top-p 37.5 (42.8); 128 rows of 100003, no filter
-// 34.0 (29.3), top-p 69.5 (82); 256 rows of 200000, greedy 37 us (5.5 TB/s), no
+// 19.7 (23.4); 16 rows of 131072, top-p 36.2 (41.7); 128 rows of 100003, no filter
+// 34.0 (29.3), top-p 69.5 (83); 256 rows of 200000, greedy 37 us (5.5 TB/s), no
 // filter 113 (96), top-p 215 (199), mixed filters 157 (134).
 #include "step.cuh"
 
@@ -963,18 +963,21 @@ struct Plan {
     int n_cta, threads, per_sm;
 };
 Plan plan_of(int rows, int vocab, int sms) {
-    // few rows: one CTA of 512 threads per SM in all, 4096 tokens each at least (16 rows of 131072, top-p: 2, 4, 8 and 16
-    // CTAs take 55, 38, 38 and 62 us).  From a quarter to half as many rows as SMs, four CTAs, two per SM, even out rows of
-    // different cost (64 mixed rows: 40 us against 57 with two).
+    // Few rows: a cluster each, of CTAs with an SM and its registers to themselves (one row of 32768, top-k: 8.3 us against
+    // 9.0 with half the registers), 4096 tokens each at least.  Not every cluster finds that many SMs together: of four up
+    // to 27/32 of the SMs (32 rows of 131072, top-p: 40 us; 38 rows: 62 us against 48 with two CTAs an SM), larger ones up
+    // to 9/16 (10 rows, 8 CTAs: 31 us against 40 with 4; 16 rows: 54 against 36.5).
+    const int most4 = int(sms * 27LL / 32), most = int(sms * 9LL / 16);
     int n = 1;
-    while (n < kMaxCluster && (long long)rows * n * 2 <= sms && vocab / (2 * n) >= 4096) n *= 2;
-    if (n == 2 && (long long)rows * 4 <= 2LL * sms && vocab / 4 >= 4096) n = 4;
+    while (n < kMaxCluster && (long long)rows * n * 2 <= (n <= 2 ? most4 : most) && vocab / (2 * n) >= 4096) n *= 2;
+    // Up to almost half as many rows as SMs: four CTAs, two per SM, even out rows of different cost (64 mixed rows: 40 us
+    // against 57 with two CTAs a row, one per SM).  The last SMs hold no cluster of four: 74 rows of 131072 with top-k take
+    // 22 us, 76 would take 33, and 25 with one CTA a row.
+    if (n < 4 && (long long)rows * 4 <= 2LL * sms - 8 && vocab / 4 >= 4096) return {4, 512, 2};
     // one CTA per row: 1024 threads while rows are fewer than two per SM (128 rows of 100003, top-p: 70 us against 88
     // with 512; 512 rows of 50000: 152 against 127); a thread's weights add up in 32 bits for 1000 tokens
     const bool wide = n == 1 && vocab > 8192 && (rows <= 2 * sms || vocab > 262144);
-    // up to half the SMs: twice the registers a thread (one row of 32768, top-k: 8.3 us against 9.0).  With more, clusters
-    // that get no two CTAs on an SM wait for each other (16 rows of 131072, top-p: 53 us against 37).
-    return {n, wide ? 1024 : 512, wide || (long long)rows * n * 2 <= sms ? 1 : 2};
+    return {n, wide ? 1024 : 512, wide || n > 1 || rows <= most4 ? 1 : 2};
 }
 
 template <typename L, int NT, int PER_SM> cudaError_t launch_t(const SampleArgs &a, int n, cudaStream_t stream) {
