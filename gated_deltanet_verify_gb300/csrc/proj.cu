@@ -39,7 +39,8 @@
 //   * With low-rank adapters (LoraTerm) the ring goes on after the K blocks with
 //     the adapters' B tiles and the matching rows of h: the same MMAs with N = 16,
 //     each into the columns of its 16 activation rows.  Warp 3 lists them while
-//     the K blocks stream.
+//     the K blocks stream.  Only MMAs of one shape are ordered among themselves,
+//     so the K blocks' sums are waited for before the first of them.
 //   * Every wait is bounded; a wait that gives up reports GDN_ERR_TIMEOUT on
 //     the caller's status word (when one is given) and the tile is skipped.
 #include "step.cuh"
@@ -208,7 +209,8 @@ template <typename Term, int H>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs a,
                                                         const __grid_constant__ Term term) {
     extern __shared__ __align__(1024) unsigned char sm[];
-    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];   // full and empty by stage and half, done (2 arrivals), units
+    // full and empty by stage and half, done (2 arrivals), units listed, each issuer's K blocks summed
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 4];
     __shared__ uint32_t tslot;
     __shared__ int n_units;
     constexpr bool kLora = std::is_same<Term, LoraTerm>::value;
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     auto full = [&](int s, int h = 0) { return smem_u32(&bars[s * H + h]); };
     auto empty = [&](int s, int h = 0) { return smem_u32(&bars[kMaxStages + s * H + h]); };
     const uint32_t done = smem_u32(&bars[2 * kMaxStages]), listed = smem_u32(&bars[2 * kMaxStages + 1]);
+    auto summed = [&](int e) { return smem_u32(&bars[2 * kMaxStages + 2 + e]); };
     Unit *units = reinterpret_cast<Unit *>(sm + (sbase - smem_u32(sm)) + (size_t)S * stage_bytes);
 
     if (wid == 0) {
@@ -244,6 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         mbar_init(done, 2);
         mbar_init(listed, 1);
+        mbar_init(summed(0), 1);
+        mbar_init(summed(1), 1);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     fence_before_sync();
@@ -332,6 +337,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             const int n = ok ? n_units : 0;
             const int per = units_per_step(n, stage_bytes, term.width);
             const uint32_t ub = unit_bytes(term.width), hb = (uint32_t)kTileN * term.width * 2, tail = 32u * term.width;
+            // MMAs into the same accumulator follow one another in order only if their shapes are the same: before those
+            // of N = 16 the K blocks' (of N = Mt) have to be complete.  The units' tiles are on their way meanwhile.
+            if (n > 0 && a.Mt != 16) {
+                mma_commit(summed(e));
+                ok = ok && mbar_wait(summed(e), 0);
+                fence_after_sync();
+            }
             for (int i = nb, u0 = 0; u0 < n && ok; ++i, u0 += per) {
                 const int s = i % S, un = min(per, n - u0);
                 if ((s & 1) != e) continue;
