@@ -486,6 +486,25 @@ static int gemm_splits(int n_tiles, int m_blocks, int n_kb, int Mt, size_t smem,
     return splits < 1 ? 1 : splits;
 }
 
+constexpr uint32_t kRingBytes = 216u * 1024u;   // pipeline stages of a CTA
+// with 1024 bytes to align the tiles by, and the longest list of units (256 rows, a slot each, rank 128)
+template <typename Term> constexpr size_t max_smem() {
+    return kRingBytes + 1024 + (std::is_same<Term, LoraTerm>::value ? max_units(kMaxMt, 1, 128) * sizeof(Unit) : 0);
+}
+
+// The kernel's shared memory limit, which belongs to the context: set once in each, to the most that any launch asks for.
+// (Set to each launch's own size, one host thread's launch could meet the smaller limit of another's.)
+template <typename Term, int H> static cudaError_t raise_smem_limit() {
+    static PerContext<int> limits;
+    unsigned long long ctx = 0;
+    int set = 0;
+    if (current_context_id(&ctx) && limits.get(ctx, &set)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(gemm_kernel<Term, H>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)max_smem<Term>());
+    if (e == cudaSuccess && current_context_id(&ctx)) limits.put(ctx, 1);
+    return e;
+}
+
 template <typename Term>
 static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, Term &term,
                         int *d_status, cudaStream_t stream, std::string &why) {
@@ -515,7 +534,7 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
     // as many stages as fit in ~216 KB: a stage is held until its MMAs complete, so the bytes in flight per
     // SM set the intake (six 36 KB stages: output projection 14.6 us against 14.9 with five; two CTAs per SM
     // with 100 KB each, the K splits spread over every SM, measured slower: 26 us)
-    a.stages = (int)((216u * 1024u) / stage);
+    a.stages = (int)(kRingBytes / stage);
     if (a.stages > kMaxStages) a.stages = kMaxStages;
     if (a.stages < 2) {                                           // one for each MMA issuer
         why = "pipeline stage larger than shared memory";
@@ -523,7 +542,8 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
     }
     // a ring of two stages (more than 160 activation rows) moves by halves, so that three of its four are in flight
     // while one feeds the MMAs
-    auto kern = a.stages == 2 ? gemm_kernel<Term, kBoxes> : gemm_kernel<Term, 1>;
+    const bool halves = a.stages == 2;
+    auto kern = halves ? gemm_kernel<Term, kBoxes> : gemm_kernel<Term, 1>;
     size_t smem = (size_t)a.stages * stage + 1024;                // + room to align the tiles to 1024 bytes
     const int splits = gemm_splits(n_tiles, m_blocks, a.n_kb, a.Mt, smem - 1024, sms);
     if constexpr (kLora) {
@@ -557,7 +577,7 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
             return false;
         }
     }
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = halves ? raise_smem_limit<Term, kBoxes>() : raise_smem_limit<Term, 1>();
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n_tiles, m_blocks, a.splits);
