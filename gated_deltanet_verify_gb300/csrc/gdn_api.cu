@@ -177,14 +177,14 @@ const char *gdn_last_error(void) { return g_err.c_str(); }
 
 const char *gdn_version(void) { return GDN_CHECKED ? "gdn-verify 0.1.0 (sm_103a, checked)" : "gdn-verify 0.1.0 (sm_103a)"; }
 
-static int verify_impl(const gdn_dims *dims, const gdn_layer_params *params, const void *qkv, const void *z,
-                       const void *alpha, const void *beta_raw, const int32_t *d_parent, float *state,
-                       float *conv_state, float *cap_state, float *cap_conv, void *out, int *d_status,
-                       void *stream, int mode = gdn::kChain, const int32_t *d_trim = nullptr,
-                       const void *qkv_prev = nullptr, const void *alpha_prev = nullptr,
-                       const void *beta_prev = nullptr, long long ld_act = 0, const void *l2_next = nullptr,
-                       size_t l2_next_bytes = 0) {
-    g_err.clear();
+// Tokens the shared memory of a verify holds: a lazy one with a pending batch runs up to 2T of them.
+static int verify_tokens(const gdn_dims &d, bool pending) { return pending ? 2 * d.n_tokens : d.n_tokens; }
+
+// Every check of a verify; info and parts (CTAs per value head) are for its launch.
+static int check_verify(const gdn_dims *dims, const gdn_layer_params *params, const void *qkv, const void *z,
+                        const void *alpha, const void *beta_raw, const float *state, const float *conv_state,
+                        const float *cap_state, const float *cap_conv, const void *out, int mode, bool pending,
+                        const void *qkv_prev, const void *alpha_prev, const void *beta_prev, DevInfo &info, int &parts) {
     int rc = check_common(dims);
     if (rc) return rc;
     if ((rc = check_params(params))) return rc;
@@ -195,7 +195,6 @@ static int verify_impl(const gdn_dims *dims, const gdn_layer_params *params, con
     if (d.n_tokens > 64) return fail(GDN_ERR_SHAPE, "n_tokens must be <= 64 for verify (got %d)", d.n_tokens);
     if (d.n_slots > 65535) return fail(GDN_ERR_SHAPE, "n_slots must be <= 65535");
     const bool commit = mode == gdn::kCommit;
-    const bool pending = mode == gdn::kLazy && d_trim != nullptr;
     if (!qkv || (!z && !commit) || !alpha || !beta_raw || !state || !conv_state || (!out && !commit))
         return fail(GDN_ERR_ARG, "a required buffer pointer is NULL");
     if (pending && (!qkv_prev || !alpha_prev || !beta_prev))
@@ -205,18 +204,36 @@ static int verify_impl(const gdn_dims *dims, const gdn_layer_params *params, con
     for (const void *p : ptrs)
         if (p && !aligned16(p)) return fail(GDN_ERR_ALIGN, "buffer %p is not 16-byte aligned", p);
     const int r = d.n_v_heads / d.n_qk_heads;
-    const DevInfo info = dev_info();
-    const int P = gdn::verify_parts_per_head(d.n_slots, d.n_v_heads, r, d.d_v, info.sms);
-    if (P == 0)
+    info = dev_info();
+    parts = gdn::verify_parts_per_head(d.n_slots, d.n_v_heads, r, d.d_v, info.sms);
+    if (parts == 0)
         return fail(GDN_ERR_SHAPE, "H_v/H_k = %d heads of d_v = %d need more than 16 CTAs per thread-block cluster "
                     "(at most 8 warps of 8 value rows per CTA)", r, d.d_v);
-    const int act_bytes = d.act_dtype == GDN_BF16 ? 2 : 4;
-    // a lazy verify with a pending batch runs up to 2T tokens through shared memory
-    const int Tm = pending ? 2 * d.n_tokens : d.n_tokens;
-    const size_t smem = gdn::verify_smem_bytes(Tm, d.n_tokens, d.d_k, d.d_v, P, act_bytes, mode == gdn::kTree);
+    const size_t smem = gdn::verify_smem_bytes(verify_tokens(d, pending), d.n_tokens, d.d_k, d.d_v, parts,
+                                               d.act_dtype == GDN_BF16 ? 2 : 4, mode == gdn::kTree);
     if (info.smem_optin > 0 && smem > size_t(info.smem_optin))
         return fail(GDN_ERR_SHAPE, "verify needs %zu bytes of shared memory per CTA (max %d)", smem,
                     info.smem_optin);
+    return GDN_OK;
+}
+
+static int verify_impl(const gdn_dims *dims, const gdn_layer_params *params, const void *qkv, const void *z,
+                       const void *alpha, const void *beta_raw, const int32_t *d_parent, float *state,
+                       float *conv_state, float *cap_state, float *cap_conv, void *out, int *d_status,
+                       void *stream, int mode = gdn::kChain, const int32_t *d_trim = nullptr,
+                       const void *qkv_prev = nullptr, const void *alpha_prev = nullptr,
+                       const void *beta_prev = nullptr, long long ld_act = 0, const void *l2_next = nullptr,
+                       size_t l2_next_bytes = 0) {
+    g_err.clear();
+    const bool pending = mode == gdn::kLazy && d_trim != nullptr;
+    DevInfo info;
+    int P = 0;
+    int rc = check_verify(dims, params, qkv, z, alpha, beta_raw, state, conv_state, cap_state, cap_conv, out, mode, pending,
+                          qkv_prev, alpha_prev, beta_prev, info, P);
+    if (rc) return rc;
+    const gdn_dims &d = *dims;
+    const int r = d.n_v_heads / d.n_qk_heads, Tm = verify_tokens(d, pending);
+    const int act_bytes = d.act_dtype == GDN_BF16 ? 2 : 4;
 
     gdn::VerifyArgs a{};
     a.B = d.n_slots; a.Hk = d.n_qk_heads; a.Hv = d.n_v_heads; a.dk = d.d_k; a.dv = d.d_v;
@@ -568,8 +585,8 @@ size_t gdn_layer_workspace_bytes(const gdn_dims *dims, int n_embd) {
     return align256(M * size_t(gdn_proj_in_ld(dims)) * 2) + align256(M * size_t(dims->n_v_heads) * dims->d_v * 2);
 }
 
-// checks of one projection's adapters
-static int check_lora(const gdn_lora *l, const int32_t *d_adapter) {
+// checks of the adapters of a projection to N columns
+static int check_lora(const gdn_dims *dims, const gdn_lora *l, const int32_t *d_adapter, const char *what, int N) {
     if (!l || !d_adapter) return fail(GDN_ERR_ARG, "adapters or adapter ids are NULL");
     if (l->n_adapters < 1) return fail(GDN_ERR_SHAPE, "n_adapters must be positive (got %d)", l->n_adapters);
     if (l->rank < 8 || l->rank > 128 || l->rank % 8)
@@ -577,6 +594,10 @@ static int check_lora(const gdn_lora *l, const int32_t *d_adapter) {
     if (!l->a || !l->b) return fail(GDN_ERR_ARG, "an adapter weight pointer is NULL");
     if (!aligned16(l->a) || !aligned16(l->b) || !aligned16(l->scale) || !aligned16(d_adapter))
         return fail(GDN_ERR_ALIGN, "adapter weights, scales and ids must be 16-byte aligned");
+    const long long M = (long long)dims->n_slots * dims->n_tokens;
+    if ((long long)l->n_adapters * N > 0x7fffff00LL || M * 64 > 0x7fffff00LL)
+        return fail(GDN_ERR_SHAPE, "%s projection: %d adapters of %d columns, or %lld rows, are too many", what,
+                    l->n_adapters, N, M);
     return GDN_OK;
 }
 
@@ -587,7 +608,14 @@ static int check_workspace(const void *workspace, size_t ws_bytes, size_t need) 
     return GDN_OK;
 }
 
-// X [M][K] -> Y [M][N] (row stride ldc) with W, and with the slots' adapters where `lora` is given
+// one projection's rows in and out
+static int check_rows(const void *from, const void *to, const char *names) {
+    if (!from || !to) return fail(GDN_ERR_ARG, "%s is NULL", names);
+    if (!aligned16(from) || !aligned16(to)) return fail(GDN_ERR_ALIGN, "%s must be 16-byte aligned", names);
+    return GDN_OK;
+}
+
+// X [M][K] -> Y [M][N] (row stride ldc) with W, and with the slots' adapters where `lora` is given; all of it checked
 static int project(const char *what, const gdn_dims *dims, const void *W, const void *X, void *Y, int N, int K,
                    long long ldc, const gdn_lora *lora, const int32_t *d_adapter, void *scratch, int *d_status,
                    void *stream) {
@@ -598,9 +626,6 @@ static int project(const char *what, const gdn_dims *dims, const void *W, const 
     if (lora) {
         const gdn::LoraArgs a{lora->n_adapters, lora->rank, dims->n_tokens, lora->a, lora->b, lora->scale, d_adapter,
                               scratch};
-        if ((long long)lora->n_adapters * N > 0x7fffff00LL || (long long)M * 64 > 0x7fffff00LL)
-            return fail(GDN_ERR_SHAPE, "%s projection: %d adapters of %d columns, or %d rows, are too many", what,
-                        lora->n_adapters, N, M);
         ok = gdn::gemm_xwt_lora_bf16(W, X, Y, M, N, K, ldc, a, dev_info().sms, d_status, st, why);
     } else {
         ok = gdn::gemm_xwt_bf16(W, X, Y, M, N, K, ldc, d_status, st, why);
@@ -611,10 +636,6 @@ static int project(const char *what, const gdn_dims *dims, const void *W, const 
 static int project_in(const gdn_dims *dims, const gdn_proj_weights *w, const void *x, void *act, int *d_status,
                       void *stream, const gdn_lora *lora = nullptr, const int32_t *d_adapter = nullptr,
                       void *scratch = nullptr) {
-    int rc = check_proj(dims, w);
-    if (rc) return rc;
-    if (!x || !act) return fail(GDN_ERR_ARG, "x or act is NULL");
-    if (!aligned16(x) || !aligned16(act)) return fail(GDN_ERR_ALIGN, "x and act must be 16-byte aligned");
     return project("input", dims, w->w_in, x, act, int(proj_in_cols(*dims)), w->n_embd, gdn_proj_in_ld(dims), lora,
                    d_adapter, scratch, d_status, stream);
 }
@@ -622,10 +643,6 @@ static int project_in(const gdn_dims *dims, const gdn_proj_weights *w, const voi
 static int project_out(const gdn_dims *dims, const gdn_proj_weights *w, const void *out, void *y, int *d_status,
                        void *stream, const gdn_lora *lora = nullptr, const int32_t *d_adapter = nullptr,
                        void *scratch = nullptr) {
-    int rc = check_proj(dims, w);
-    if (rc) return rc;
-    if (!out || !y) return fail(GDN_ERR_ARG, "out or y is NULL");
-    if (!aligned16(out) || !aligned16(y)) return fail(GDN_ERR_ALIGN, "out and y must be 16-byte aligned");
     return project("output", dims, w->w_out, out, y, w->n_embd, dims->n_v_heads * dims->d_v, w->n_embd, lora, d_adapter,
                    scratch, d_status, stream);
 }
@@ -634,6 +651,8 @@ int gdn_project_in(const gdn_dims *dims, const gdn_proj_weights *w, const void *
                    size_t ws_bytes, void *stream) {
     g_err.clear();
     (void)workspace; (void)ws_bytes;            // the GEMM needs no scratch
+    int rc = check_proj(dims, w);
+    if (rc || (rc = check_rows(x, act, "x or act"))) return rc;
     return project_in(dims, w, x, act, nullptr, stream);
 }
 
@@ -641,24 +660,31 @@ int gdn_project_out(const gdn_dims *dims, const gdn_proj_weights *w, const void 
                     size_t ws_bytes, void *stream) {
     g_err.clear();
     (void)workspace; (void)ws_bytes;
+    int rc = check_proj(dims, w);
+    if (rc || (rc = check_rows(out, y, "out or y"))) return rc;
     return project_out(dims, w, out, y, nullptr, stream);
 }
 
-// the layer step in `workspace` (checked by the caller); lora_scratch: the adapters' part of it
+// the layer step in `workspace`, which the caller has checked, as it has the projections' weights and adapters;
+// lora_scratch: the adapters' part of it.  Everything else is checked before the first launch: the verify moves the state.
 static int layer_impl(const gdn_dims *dims, const gdn_layer_params *params, const gdn_proj_weights *w, const void *x,
                       float *state, float *conv_state, float *cap_state, float *cap_conv, void *y, void *workspace,
                       int *d_status, void *stream, const gdn_lora *lora_in = nullptr, const gdn_lora *lora_out = nullptr,
                       const int32_t *d_adapter = nullptr, void *lora_scratch = nullptr) {
-    int rc;
     const gdn_dims &d = *dims;
     const size_t M = size_t(d.n_slots) * d.n_tokens;
     const long long ld = gdn_proj_in_ld(dims);
     unsigned char *act = static_cast<unsigned char *>(workspace);
     unsigned char *out = act + align256(M * size_t(ld) * 2);
-    if ((rc = project_in(dims, w, x, act, d_status, stream, lora_in, d_adapter, lora_scratch))) return rc;
     // the verify reads q|k|v, z, alpha and beta_raw as column blocks of the activation matrix
     const long long C = conv_channels(dims), V = (long long)d.n_v_heads * d.d_v;
     unsigned char *z = act + C * 2, *alpha = act + (C + V) * 2, *beta = alpha + size_t(d.n_v_heads) * 2;
+    DevInfo info;
+    int parts = 0, rc = check_rows(x, y, "x or y");
+    if (rc || (rc = check_verify(dims, params, act, z, alpha, beta, state, conv_state, cap_state, cap_conv, out,
+                                 gdn::kChain, false, nullptr, nullptr, nullptr, info, parts)))
+        return rc;
+    if ((rc = project_in(dims, w, x, act, d_status, stream, lora_in, d_adapter, lora_scratch))) return rc;
     // the verify also warms L2 with the output projection's weights (read by the next launch)
     const size_t w_out_bytes = size_t(w->n_embd) * size_t(V) * 2;
     if ((rc = verify_impl(dims, params, act, z, alpha, beta, nullptr, state, conv_state, cap_state, cap_conv, out,
@@ -689,8 +715,9 @@ int gdn_project_in_lora(const gdn_dims *dims, const gdn_proj_weights *w, const g
                         const void *x, void *act, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
     g_err.clear();
     int rc = check_proj(dims, w);
-    if (rc || (rc = check_lora(lora, d_adapter))) return rc;
+    if (rc || (rc = check_lora(dims, lora, d_adapter, "input", int(proj_in_cols(*dims))))) return rc;
     if ((rc = check_workspace(workspace, ws_bytes, gdn_lora_workspace_bytes(dims, lora->rank)))) return rc;
+    if ((rc = check_rows(x, act, "x or act"))) return rc;
     return project_in(dims, w, x, act, d_status, stream, lora, d_adapter, workspace);
 }
 
@@ -698,8 +725,9 @@ int gdn_project_out_lora(const gdn_dims *dims, const gdn_proj_weights *w, const 
                          const void *out, void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
     g_err.clear();
     int rc = check_proj(dims, w);
-    if (rc || (rc = check_lora(lora, d_adapter))) return rc;
+    if (rc || (rc = check_lora(dims, lora, d_adapter, "output", w->n_embd))) return rc;
     if ((rc = check_workspace(workspace, ws_bytes, gdn_lora_workspace_bytes(dims, lora->rank)))) return rc;
+    if ((rc = check_rows(out, y, "out or y"))) return rc;
     return project_out(dims, w, out, y, d_status, stream, lora, d_adapter, workspace);
 }
 
@@ -716,8 +744,8 @@ int gdn_layer_verify_lora(const gdn_dims *dims, const gdn_layer_params *params, 
     int rc = check_proj(dims, w);
     if (rc) return rc;
     if (!lora_in && !lora_out) return fail(GDN_ERR_ARG, "both projections are without adapters");
-    if (lora_in && (rc = check_lora(lora_in, d_adapter))) return rc;
-    if (lora_out && (rc = check_lora(lora_out, d_adapter))) return rc;
+    if (lora_in && (rc = check_lora(dims, lora_in, d_adapter, "input", int(proj_in_cols(*dims))))) return rc;
+    if (lora_out && (rc = check_lora(dims, lora_out, d_adapter, "output", w->n_embd))) return rc;
     int rank = lora_in ? lora_in->rank : 0;
     if (lora_out && lora_out->rank > rank) rank = lora_out->rank;
     if ((rc = check_workspace(workspace, ws_bytes, gdn_layer_lora_workspace_bytes(dims, w->n_embd, rank)))) return rc;

@@ -505,9 +505,10 @@ template <typename Term, int H> static cudaError_t raise_smem_limit() {
     return e;
 }
 
-template <typename Term>
+// before(): what goes on the stream ahead of the kernel, once nothing but the launches themselves can fail
+template <typename Term, typename Before>
 static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, Term &term,
-                        int *d_status, cudaStream_t stream, std::string &why) {
+                        int *d_status, cudaStream_t stream, std::string &why, Before before) {
     constexpr bool kLora = std::is_same<Term, LoraTerm>::value;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) {
@@ -578,6 +579,7 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
         }
     }
     cudaError_t e = halves ? raise_smem_limit<Term, kBoxes>() : raise_smem_limit<Term, 1>();
+    if (e == cudaSuccess) e = before();
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(n_tiles, m_blocks, a.splits);
@@ -605,7 +607,7 @@ static bool gemm_launch(const void *W, const void *X, void *C, int M, int N, int
 bool gemm_xwt_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, int *d_status,
                    cudaStream_t stream, std::string &why) {
     NoTerm none;
-    return gemm_launch(W, X, C, M, N, K, ldc, none, d_status, stream, why);
+    return gemm_launch(W, X, C, M, N, K, ldc, none, d_status, stream, why, [] { return cudaSuccess; });
 }
 
 bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int K, long long ldc, const LoraArgs &lora,
@@ -638,12 +640,8 @@ bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int
         why = "adapter tensor map";
         return false;
     }
-    const cudaError_t e = launch_lora_shrink(X, M, K, lora, sms, d_status, stream);
-    if (e != cudaSuccess) {
-        why = std::string("adapter launch: ") + cudaGetErrorString(e);
-        return false;
-    }
-    return gemm_launch(W, X, C, M, N, K, ldc, term, d_status, stream, why);
+    return gemm_launch(W, X, C, M, N, K, ldc, term, d_status, stream, why,
+                       [&] { return launch_lora_shrink(X, M, K, lora, sms, d_status, stream); });
 }
 
 }  // namespace gdn

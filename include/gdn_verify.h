@@ -35,7 +35,9 @@
  *    CUDA graph.
  *  - Every device pointer must be 16-byte aligned (GDN_ERR_ALIGN otherwise).
  *  - A non-OK return means nothing was enqueued; gdn_last_error() (per
- *    thread) then describes the problem.  Problems only the device can see
+ *    thread) then describes the problem.  (Only where CUDA itself refuses a
+ *    launch, GDN_ERR_LAUNCH, may a call's earlier launches be on the stream.)
+ *    Problems only the device can see
  *    are written to *d_status (a device int the caller zeroes; may be NULL):
  *    the first error code wins.  No kernel traps, asserts or waits unbounded.
  *
