@@ -530,6 +530,14 @@ int gdn_verify_step_host(const gdn_dims *dims, const gdn_layer_params *params, i
     if (rollback_first != 0 && rollback_first != 1) return fail(GDN_ERR_ARG, "rollback_first must be 0 or 1");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char *din = static_cast<unsigned char *>(d_io), *dout = din + io.in_bytes;
+    // what the verify and the rollback would refuse, before the copy
+    if (!cap_state || !cap_conv) return fail(GDN_ERR_NO_CAPTURE, "the step rolls back: cap_state and cap_conv are needed");
+    DevInfo info;
+    int parts = 0;
+    if ((rc = check_verify(dims, params, din + io.qkv, din + io.z, din + io.alpha, din + io.beta_raw, state, conv_state,
+                           cap_state, cap_conv, dout, rollback_first ? gdn::kRolled : gdn::kChain, false, nullptr, nullptr,
+                           nullptr, info, parts)))
+        return rc;
     cudaError_t e = cudaMemcpyAsync(din, h_in, io.in_bytes, cudaMemcpyHostToDevice, st);
     if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "input copy failed: %s", cudaGetErrorString(e));
     const int32_t *trim = reinterpret_cast<const int32_t *>(din + io.trim);
