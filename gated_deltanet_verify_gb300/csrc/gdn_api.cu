@@ -564,6 +564,9 @@ static long long proj_in_cols(const gdn_dims &d) {
 
 static size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
 
+// rows of a projection: 65535 grid rows of 256
+constexpr long long kMaxProjRows = 65535LL * 256;
+
 // checks shared by the projection calls; M = B * T rows
 static int check_proj(const gdn_dims *dims, const gdn_proj_weights *w) {
     int rc = check_common(dims);
@@ -577,8 +580,9 @@ static int check_proj(const gdn_dims *dims, const gdn_proj_weights *w) {
     if (!w->w_in || !w->w_out) return fail(GDN_ERR_ARG, "a projection weight pointer is NULL");
     if (!aligned16(w->w_in) || !aligned16(w->w_out)) return fail(GDN_ERR_ALIGN, "weights must be 16-byte aligned");
     const long long M = (long long)dims->n_slots * dims->n_tokens;
-    if (M > (1LL << 30) || proj_in_cols(*dims) > (1LL << 30))
-        return fail(GDN_ERR_SHAPE, "projection sizes out of range");
+    if (M > kMaxProjRows || proj_in_cols(*dims) > (1LL << 30) || w->n_embd > (1 << 30))
+        return fail(GDN_ERR_SHAPE, "projection sizes out of range (%lld rows, %lld columns, n_embd %d)", M,
+                    proj_in_cols(*dims), w->n_embd);
     return GDN_OK;
 }
 
@@ -594,7 +598,7 @@ size_t gdn_layer_workspace_bytes(const gdn_dims *dims, int n_embd) {
 }
 
 // checks of the adapters of a projection to N columns
-static int check_lora(const gdn_dims *dims, const gdn_lora *l, const int32_t *d_adapter, const char *what, int N) {
+static int check_lora(const gdn_lora *l, const int32_t *d_adapter, const char *what, int N) {
     if (!l || !d_adapter) return fail(GDN_ERR_ARG, "adapters or adapter ids are NULL");
     if (l->n_adapters < 1) return fail(GDN_ERR_SHAPE, "n_adapters must be positive (got %d)", l->n_adapters);
     if (l->rank < 8 || l->rank > 128 || l->rank % 8)
@@ -602,10 +606,8 @@ static int check_lora(const gdn_dims *dims, const gdn_lora *l, const int32_t *d_
     if (!l->a || !l->b) return fail(GDN_ERR_ARG, "an adapter weight pointer is NULL");
     if (!aligned16(l->a) || !aligned16(l->b) || !aligned16(l->scale) || !aligned16(d_adapter))
         return fail(GDN_ERR_ALIGN, "adapter weights, scales and ids must be 16-byte aligned");
-    const long long M = (long long)dims->n_slots * dims->n_tokens;
-    if ((long long)l->n_adapters * N > 0x7fffff00LL || M * 64 > 0x7fffff00LL)
-        return fail(GDN_ERR_SHAPE, "%s projection: %d adapters of %d columns, or %lld rows, are too many", what,
-                    l->n_adapters, N, M);
+    if ((long long)l->n_adapters * N > 0x7fffff00LL)
+        return fail(GDN_ERR_SHAPE, "%s projection: %d adapters of %d columns are too many", what, l->n_adapters, N);
     return GDN_OK;
 }
 
@@ -715,7 +717,9 @@ int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const
 // ---- low-rank adapters beside the projections ------------------------------
 
 size_t gdn_lora_workspace_bytes(const gdn_dims *dims, int rank) {
-    if (!dims || dims->n_slots < 1 || dims->n_tokens < 1 || rank < 8 || rank > 128 || rank % 8) return 0;
+    if (!dims || dims->n_slots < 1 || dims->n_tokens < 1 || rank < 8 || rank > 128 || rank % 8 ||
+        (long long)dims->n_slots * dims->n_tokens > kMaxProjRows)
+        return 0;
     return align256(gdn::lora_scratch_bytes(dims->n_slots, dims->n_tokens, rank));
 }
 
@@ -723,7 +727,7 @@ int gdn_project_in_lora(const gdn_dims *dims, const gdn_proj_weights *w, const g
                         const void *x, void *act, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
     g_err.clear();
     int rc = check_proj(dims, w);
-    if (rc || (rc = check_lora(dims, lora, d_adapter, "input", int(proj_in_cols(*dims))))) return rc;
+    if (rc || (rc = check_lora(lora, d_adapter, "input", int(proj_in_cols(*dims))))) return rc;
     if ((rc = check_workspace(workspace, ws_bytes, gdn_lora_workspace_bytes(dims, lora->rank)))) return rc;
     if ((rc = check_rows(x, act, "x or act"))) return rc;
     return project_in(dims, w, x, act, d_status, stream, lora, d_adapter, workspace);
@@ -733,7 +737,7 @@ int gdn_project_out_lora(const gdn_dims *dims, const gdn_proj_weights *w, const 
                          const void *out, void *y, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
     g_err.clear();
     int rc = check_proj(dims, w);
-    if (rc || (rc = check_lora(dims, lora, d_adapter, "output", w->n_embd))) return rc;
+    if (rc || (rc = check_lora(lora, d_adapter, "output", w->n_embd))) return rc;
     if ((rc = check_workspace(workspace, ws_bytes, gdn_lora_workspace_bytes(dims, lora->rank)))) return rc;
     if ((rc = check_rows(out, y, "out or y"))) return rc;
     return project_out(dims, w, out, y, d_status, stream, lora, d_adapter, workspace);
@@ -752,8 +756,8 @@ int gdn_layer_verify_lora(const gdn_dims *dims, const gdn_layer_params *params, 
     int rc = check_proj(dims, w);
     if (rc) return rc;
     if (!lora_in && !lora_out) return fail(GDN_ERR_ARG, "both projections are without adapters");
-    if (lora_in && (rc = check_lora(dims, lora_in, d_adapter, "input", int(proj_in_cols(*dims))))) return rc;
-    if (lora_out && (rc = check_lora(dims, lora_out, d_adapter, "output", w->n_embd))) return rc;
+    if (lora_in && (rc = check_lora(lora_in, d_adapter, "input", int(proj_in_cols(*dims))))) return rc;
+    if (lora_out && (rc = check_lora(lora_out, d_adapter, "output", w->n_embd))) return rc;
     int rank = lora_in ? lora_in->rank : 0;
     if (lora_out && lora_out->rank > rank) rank = lora_out->rank;
     if ((rc = check_workspace(workspace, ws_bytes, gdn_layer_lora_workspace_bytes(dims, w->n_embd, rank)))) return rc;

@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 // K splits of a tile: enough CTAs to cover the SMs when the output tiles are few, while the other splits' partial tiles
 // would fit the pipeline buffers of one CTA (what its share of the columns takes of them is less)
 static int gemm_splits(int n_tiles, int m_blocks, int n_kb, int Mt, size_t smem, int sms) {
-    int splits = sms / (n_tiles * m_blocks);
+    int splits = (int)(sms / ((long long)n_tiles * m_blocks));
     if (splits > 8) splits = 8;
     if (splits > n_kb) splits = n_kb;
     while (splits > 1 && (size_t)(splits - 1) * Mt * kTileN * 4 > smem) --splits;

@@ -287,7 +287,8 @@ int gdn_commit_lazy(const gdn_dims *dims, const gdn_layer_params *params, const 
  * x and y are [B][T][n_embd] bf16.  The norm before the block, the residual
  * add after it and the rest of the model are not part of this library.
  * Limits: act_dtype GDN_BF16, n_embd a multiple of 8, n_v_heads a multiple of
- * 8 (GDN_ERR_DTYPE / GDN_ERR_SHAPE).
+ * 8, B*T at most 65535 * 256 rows, n_embd and the rows of w_in at most 2^30
+ * (GDN_ERR_DTYPE / GDN_ERR_SHAPE).
  */
 typedef struct {
     int n_embd;            /* hidden size */
@@ -342,7 +343,8 @@ int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const
  * others' rows of h are zero).  The pages have no adapters; the projections they
  * stand beside are those of internal.h, TargetLayer.
  *
- * Limits: those of gdn_project_in; rank a multiple of 8, 8..128 (GDN_ERR_SHAPE).
+ * Limits: those of gdn_project_in; rank a multiple of 8, 8..128; n_adapters
+ * times the projection's output columns below 2^31 - 256 (GDN_ERR_SHAPE).
  * workspace: gdn_lora_workspace_bytes (0 on bad arguments), 256-byte aligned;
  * it needs no initialisation, and calls that share it must be ordered.
  */
