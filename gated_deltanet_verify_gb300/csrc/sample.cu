@@ -10,9 +10,12 @@
 // A border of that last sum decides the token, so every sum is exact: a weight
 // is a 64-bit integer in units of about 2^-44 of the largest one (weight.cuh), and
 // the integer sums do not depend on the order they are taken in -- the token is
-// the same whatever the launch shape, and equals the one of 64-bit arithmetic
-// unless u lies within ~1e-11 of a border.  For the same reason the atomics
-// below (integer counts and masses) leave no trace of their order.
+// the same whatever the launch shape.  It equals the one of 64-bit arithmetic
+// unless u lies nearer to a border than the weights' errors together: ~1e-12 of
+// the sum as a rule, at most V 2^-45 + 2^-34 of it (1.5e-8 if 524288 light tokens
+// all round the same way; u itself comes in steps of 6e-8).  A token lighter than
+// half a unit is never drawn.  For the same reason the atomics below (integer
+// counts and masses) leave no trace of their order.
 //
 // A thread-block cluster of 1 to 16 CTAs takes a row and goes over it two or
 // three times; the first pass reads HBM, the others find it in L2:

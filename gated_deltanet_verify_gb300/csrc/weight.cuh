@@ -2,7 +2,9 @@
 //
 // weight(l) = exp((l - ref) / T) in units of 2^-44, rounded to nearest, where ref is the top logit or a little above:
 // at most 2^44, so 2^19 tokens sum to at most 2^63.  Only ratios of weights count, so ref need not be exact.  Integer
-// sums are exact and do not depend on their order.
+// sums are exact and do not depend on their order.  (The choice of the unit: the sum of the largest vocabulary fits 64
+// bits.  A weight below half a unit, e^-31.2 of the top one, is 0: with u = 0 too, such a token is not drawn, as the
+// masked token that a logit of the type's lowest value stands for must not be.)
 //
 // The exponential is table-driven (P. T. P. Tang, "Table-driven implementation
 // of the exponential function in IEEE floating-point arithmetic", ACM TOMS 15,
@@ -77,8 +79,9 @@ struct __align__(16) WeightTable {
 };
 
 // Below 2^kLarge of the top weight, rounding errors of 2^-34 of the weight are let be: they stay below 2^-38 of the top
-// weight, and few tokens are near that (all tokens' errors together are near 10^-12 of the sum).  At -7, 128 rows of
-// 100003 took 44.7 us, at -4 37.0: four tokens a thread share the branch, and seldom is none of 128 large.
+// weight, and few tokens are near that (all tokens' errors together are near 10^-12 of the sum as a rule; at most
+// 2^-34 of it, and 2^-45 of the top weight a token where all round the same way).  At -7, 128 rows of 100003 took 44.7 us,
+// at -4 37.0: four tokens a thread share the branch, and seldom is none of 128 large.
 constexpr float kLarge = -4.0f;
 
 // What the weights of a row share: y = x c - at with x = l - shift, c = hi + lo = log2(e) / T, and `at` (top - shift) c

@@ -392,10 +392,15 @@ int gdn_layer_verify_lora(const gdn_dims *dims, const gdn_layer_params *params, 
  *     min_p > 0 keeps tokens with w_i >= min_p (the top token has w = 1);
  *   - the row's token is the smallest i with sum_{j <= i, kept} w_j > u * sum_{kept} w_j;
  *     logprob (optional) is ln(w_token / sum_{kept} w_j).
- * temperature 0 takes the top token (logprob 0).  The sums are exact (64-bit
- * integers in units of 2^-44 of the top weight), so the result does not depend
- * on the launch shape and a repeated call gives the same tokens; of +inf logits
- * all are equally likely.
+ * temperature 0 takes the top token (logprob 0); of +inf logits all are equally
+ * likely.  Weights are rounded to multiples of 2^-44 of the top one, so a token
+ * lighter than half of that (x_i below -31.2) is never drawn, not even for u = 0:
+ * a mask made of the type's lowest value holds.  Sums of these weights are exact
+ * (64-bit integers), so the result does not depend on the launch shape and a
+ * repeated call gives the same tokens.  Against real arithmetic the rounding
+ * moves a sum by at most 2^-45 of the top weight a token, and the exponential by
+ * at most 2^-34 of the sum; only a u (or top_p) that near a border can then
+ * choose another token.
  *
  * The parameters are DEVICE arrays per slot (NULL: temperature 1, filters off).
  * A row gets token -1 and logprob -inf, and GDN_ERR_SAMPLE goes to *d_status,
