@@ -6,10 +6,11 @@
 //
 // Unit of work: a pair of a slot and one of the aligned groups of 16 rows of X
 // that its rows touch (rows of other slots count as zero), because the second
-// half is a product over such groups.  h is summed in fp32 and stored as two
-// bf16 numbers, head and tail, 2^-17 of it being lost at most: the two products
-// that this costs the tensor cores are cheaper than fp32 arithmetic, and one
-// bf16 alone would lose as much as the output's own rounding.
+// half is a product over such groups.  h is summed in fp32 and stored as three
+// bf16 numbers of 8 bits each, which together hold all 24 of it: the three
+// products that this costs the tensor cores are cheaper than fp32 arithmetic, and
+// h enters the output's sums unrounded.  (Two numbers, with 2^-17 of
+// h lost: 94.5 us against 94.7 at 32 slots of rank 16, 104 against 106 at rank 64.)
 //
 // X and A are read once each per pair, straight from global memory into the
 // fragments of mma.sync (m16n8k16, bf16, fp32 sums): with K permuted alike on
@@ -20,9 +21,9 @@
 // fixed order.
 //
 // Measured, a projection with adapters against the same without (captured graph):
-// input projection, hidden 5120, one slot of 16 rows, rank 16: 30.9 us against
-// 28.6; 32 slots: 95 against 87; 8 slots of rank 128: 48 against 34.7; output
-// projection, 8 slots of rank 64: 24.5 against 18.4.  This kernel runs beside the
+// input projection, hidden 5120, one slot of 16 rows, rank 16: 30.6 us against
+// 28.1; 32 slots: 94.7 against 86.7; 8 slots of rank 128: 49.4 against 34.6; output
+// projection, 8 slots of rank 64: 25.1 against 18.4.  This kernel runs beside the
 // projection's weight stream, which does not wait for it; what is left are loads
 // that take 4-5 us a round while that stream fills HBM's queues, and the adapters'
 // own tiles at the end of the projection's ring.
@@ -42,7 +43,7 @@ struct ShrinkArgs {
     int M, K, T, r, P, n_adapters;
     const int32_t *adapter;
     const float *scale;
-    __nv_bfloat16 *h;                // [pair][head, tail][16][r]
+    __nv_bfloat16 *h;                // [pair][high, middle, low][16][r]
     int *d_status;
 };
 
@@ -156,13 +157,15 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const ShrinkArgs 
         // rows of other slots are zero whatever the adapter holds
         const int m = group * 16 + i / rl;
         v = m >= lo && m < hi ? v * scale : 0.f;
-        const __nv_bfloat16 head = __float2bfloat16_rn(v);
-        const float rest = v - __bfloat162float(head);
-        // an infinite or NaN h stays what it is
-        const __nv_bfloat16 tail = __float2bfloat16_rn(rest - rest == 0.f ? rest : 0.f);
-        __nv_bfloat16 *to = a.h + ((size_t)pair * 32 + i / rl) * r + j0 + i % rl;
-        to[0] = head;
-        to[16 * r] = tail;
+        // cut off, not rounded: the differences are exact, and a finite h stays finite
+        const __nv_bfloat16 high = __float2bfloat16_rz(v);
+        float rest = v - __bfloat162float(high);
+        rest = rest - rest == 0.f ? rest : 0.f;  // an infinite or NaN h stays what it is
+        const __nv_bfloat16 middle = __float2bfloat16_rz(rest);
+        __nv_bfloat16 *to = a.h + ((size_t)pair * 48 + i / rl) * r + j0 + i % rl;
+        to[0] = high;
+        to[16 * r] = middle;
+        to[32 * r] = __float2bfloat16_rn(rest - __bfloat162float(middle));
     }
     if (S > 1) cluster_sync();                   // the peers have read this CTA's sums
 }
@@ -209,7 +212,7 @@ template <int R8> cudaError_t launch_t(const ShrinkArgs &a, int pairs, int sms, 
 int lora_groups_per_slot(int T) { return T % 16 == 0 ? T / 16 : (T + 14) / 16 + 1; }
 
 size_t lora_scratch_bytes(long long slots, int T, int rank) {
-    return size_t(slots) * lora_groups_per_slot(T) * 32 * rank * 2;
+    return size_t(slots) * lora_groups_per_slot(T) * 48 * rank * 2;
 }
 
 cudaError_t launch_lora_shrink(const void *X, int M, int K, const LoraArgs &l, int sms, int *d_status, cudaStream_t stream) {

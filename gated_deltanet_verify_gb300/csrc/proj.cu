@@ -73,16 +73,17 @@ struct GemmArgs {
 };
 
 // A low-rank term beside the product, by the slot (T rows of X) a row belongs to (h by lora.cu): units of an aligned
-// group of 16 rows, one slot's part of it and up to 64 rank columns, D[:, group] += B_tile (h_head + h_tail)^T.  They
+// group of 16 rows, one slot's part of it and up to 64 rank columns, D[:, group] += B_tile (h_high + h_middle + h_low)^T.  They
 // follow the K blocks through the same ring of stages; a stage holds several units (the B tile's box, 128 rows of
-// `width` columns, then the 32 rows of head and tail), whose swizzle is as wide as their rows: 32, 64 or 128 bytes.
+// `width` columns, then the 48 rows of h's three parts), whose swizzle is as wide as their rows: 32, 64 or 128 bytes.
 struct LoraTerm {
-    CUtensorMap b_map, h_map;           // [n_adapters * N][r]; [pairs * 32][r]
+    CUtensorMap b_map, h_map;           // [n_adapters * N][r]; [pairs * kPartRows][r]
     const int32_t *adapter;             // [slots]; outside [0, n_adapters): no term
     int n_adapters, r, T, P;            // P: groups a slot's rows may touch
     int width;                          // rank columns a unit: 16, 32 or 64
 };
 struct NoTerm {};
+constexpr int kParts = 3, kPartRows = 16 * kParts;   // of h: bf16 numbers that add up to it
 struct Unit {
     int h_row, b_row, column, box;      // column: of D
 };
@@ -93,7 +94,7 @@ __host__ __device__ constexpr int max_units(int Mt, int T, int r) {
 }
 // rank columns a unit, and its bytes
 __host__ __device__ constexpr int unit_width(int r) { return r <= 16 ? 16 : r <= 32 ? 32 : 64; }
-__host__ __device__ constexpr uint32_t unit_bytes(int width) { return (uint32_t)(kTileN + 32) * width * 2; }
+__host__ __device__ constexpr uint32_t unit_bytes(int width) { return (uint32_t)(kTileN + kPartRows) * width * 2; }
 // n units in steps of the ring: a stage's fill each, but both issuers busy
 __device__ __forceinline__ int units_per_step(int n, uint32_t stage_bytes, int width) {
     const int fill = (int)(stage_bytes / unit_bytes(width));
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             ok = ok && mbar_wait(listed, 0);
             const int n = ok ? n_units : 0;
             const int per = units_per_step(n, stage_bytes, term.width);
-            const uint32_t ub = unit_bytes(term.width), hb = (uint32_t)kTileN * term.width * 2, tail = 32u * term.width;
+            const uint32_t ub = unit_bytes(term.width), hb = (uint32_t)kTileN * term.width * 2, part = 32u * term.width;
             // MMAs into the same accumulator follow one another in order only if their shapes are the same: before those
             // of N = 16 the K blocks' (of N = Mt) have to be complete.  The units' tiles are on their way meanwhile.
             if (n > 0 && a.Mt != 16) {
@@ -355,8 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     const int steps = (min(64, term.r - 64 * q.box) + 15) / 16;
                     for (int j = 0; j < steps; ++j) {
                         const uint64_t bd = make_desc_sw(b + 32u * j, term.width);
-                        mma_bf16(acc + q.column, bd, make_desc_sw(h + 32u * j, term.width), idesc_bf16(16), 1u);
-                        mma_bf16(acc + q.column, bd, make_desc_sw(h + tail + 32u * j, term.width), idesc_bf16(16), 1u);
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p)
+                            mma_bf16(acc + q.column, bd, make_desc_sw(h + p * part + 32u * j, term.width), idesc_bf16(16), 1u);
                     }
                 }
                 for (int h = 0; h < H; ++h) mma_commit(empty(s, h));
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 for (int q = 0; q < mine; ++q) {
                     const int at = n + to - mine + q, g = g0 + q / boxes;
                     if (at % a.splits != split) continue;
-                    const Unit u{(s * term.P + g - first) * 32, id * a.N + n0, g * 16 - m0, q % boxes};
+                    const Unit u{(s * term.P + g - first) * kPartRows, id * a.N + n0, g * 16 - m0, q % boxes};
                     units[at / a.splits] = u;
                     // its B tile comes at the end of the ring: into L2 by then
                     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n" ::"l"(
@@ -625,7 +627,7 @@ bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int
     const CUtensorMapSwizzle swizzle = term.width == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
                                        : term.width == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
                                                           : CU_TENSOR_MAP_SWIZZLE_128B;
-    // boxes of `width` columns: 128 rows of B, the 16 + 16 rows of a pair's head and tail
+    // boxes of `width` columns: 128 rows of B, the rows of a pair's three parts of h
     const cuuint32_t estr[2] = {1, 1};
     auto map = [&](CUtensorMap *m, const void *p, cuuint64_t rows, cuuint32_t box_rows) {
         const cuuint64_t dims[2] = {(cuuint64_t)lora.rank, rows};
@@ -636,7 +638,7 @@ bool gemm_xwt_lora_bf16(const void *W, const void *X, void *C, int M, int N, int
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     if (!map(&term.b_map, lora.b, (cuuint64_t)lora.n_adapters * N, kTileN) ||
-        !map(&term.h_map, lora.h, (cuuint64_t)(M / lora.T) * term.P * 32, 32)) {
+        !map(&term.h_map, lora.h, (cuuint64_t)(M / lora.T) * term.P * kPartRows, kPartRows)) {
         why = "adapter tensor map";
         return false;
     }

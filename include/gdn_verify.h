@@ -333,8 +333,8 @@ int gdn_layer_verify(const gdn_dims *dims, const gdn_layer_params *params, const
  * run with an adapter of its own.  For row m of slot s, with a = d_adapter[s],
  *   act[m] = w_in x[m] + scale[a] * B[a] (A[a] x[m])
  * (and the same for the output projection), with fp32 sums and one rounding to
- * bf16; scale[a] * A[a] x is summed in fp32 and carried to 2^-17 of itself (as
- * two bf16 numbers).  d_adapter is a DEVICE int32[n_slots]: -1 runs the slot
+ * bf16; scale[a] * A[a] x is carried in the full fp32 of its sum (as three bf16
+ * numbers).  d_adapter is a DEVICE int32[n_slots]: -1 runs the slot
  * without an adapter (its rows then equal gdn_project_in's / gdn_project_out's);
  * another id outside [0, n_adapters) does the same and writes GDN_ERR_ADAPTER
  * to *d_status.  Several slots may name the same adapter.  Adapters of a lower
