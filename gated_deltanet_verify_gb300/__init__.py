@@ -186,19 +186,28 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
-_torch = None
+_current_stream = None
+
+
+def _current_stream_call():
+    """A function that returns the handle of torch's current stream on its current device."""
+    import torch
+    torch.cuda.current_stream()                  # initialises CUDA, or says why it cannot
+    # asking for the handle itself takes 0.2 us where building the Stream object takes 3, more than a launch; a torch
+    # without these two gets the public call
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # torch's current stream on its current device; asking for the handle itself takes 0.2 us where building the
-        # Stream object takes 3, more than a launch
-        global _torch
-        if _torch is None:
-            import torch
-            torch.cuda.current_stream()          # initialises CUDA, or says why it cannot
-            _torch = torch._C
-        return _torch._cuda_getCurrentRawStream(_torch._cuda_getDevice())
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _current_stream_call()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
