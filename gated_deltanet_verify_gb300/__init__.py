@@ -31,10 +31,12 @@ GDN_ERR_BOUNDS = 11
 GDN_ERR_SAMPLE = 12
 GDN_ERR_LENGTH = 13
 GDN_ERR_ADAPTER = 14
+GDN_ERR_PAGE = 15
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_ARG", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_ALIGN", 4: "GDN_ERR_DTYPE",
                 5: "GDN_ERR_TRIM_RANGE", 6: "GDN_ERR_NO_CAPTURE", 7: "GDN_ERR_LAUNCH", 8: "GDN_ERR_TIMEOUT",
                 9: "GDN_ERR_WORKSPACE", 10: "GDN_ERR_TREE",
-                11: "GDN_ERR_BOUNDS", 12: "GDN_ERR_SAMPLE", 13: "GDN_ERR_LENGTH", 14: "GDN_ERR_ADAPTER"}
+                11: "GDN_ERR_BOUNDS", 12: "GDN_ERR_SAMPLE", 13: "GDN_ERR_LENGTH", 14: "GDN_ERR_ADAPTER",
+                15: "GDN_ERR_PAGE"}
 
 GDN_F32 = 0
 GDN_BF16 = 1
@@ -45,6 +47,7 @@ EXPORTED_SYMBOLS = ("gdn_verify_forward", "gdn_verify_tree", "gdn_rollback", "gd
                     "gdn_project_in", "gdn_project_out", "gdn_layer_verify", "gdn_lora_workspace_bytes",
                     "gdn_project_in_lora", "gdn_project_out_lora", "gdn_layer_lora_workspace_bytes",
                     "gdn_layer_verify_lora", "gdn_sample", "gdn_accept", "gdn_accept_tree",
+                    "gdn_kv_append", "gdn_attend_workspace_bytes", "gdn_attend",
                     "gdn_prefill_workspace_bytes",
                     "gdn_prefill_chunked", "gdn_prefill_chunked_static", "gdn_prefill_static_scratch_bytes",
                     "gdn_last_error", "gdn_version")
@@ -91,6 +94,27 @@ class SampleDims(ctypes.Structure):
 class SampleParams(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
                 ("min_p", ctypes.c_void_p)]
+
+
+class AttnDims(ctypes.Structure):
+    _fields_ = [("n_slots", ctypes.c_int), ("n_tokens", ctypes.c_int), ("n_heads", ctypes.c_int),
+                ("n_kv_heads", ctypes.c_int), ("d_head", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int), ("page_stride", ctypes.c_longlong),
+                ("dtype", ctypes.c_int)]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("past", ctypes.c_void_p)]
+
+
+class QkParams(ctypes.Structure):
+    _fields_ = [("rope_dims", ctypes.c_int), ("adjacent", ctypes.c_int), ("freq", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("norm_eps", ctypes.c_float)]
+
+
+class AttnParams(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("window", ctypes.c_int), ("n_sink", ctypes.c_int)]
 
 
 def make_dims(n_slots: int, n_qk_heads: int, n_v_heads: int, d_k: int, d_v: int, n_tokens: int,
@@ -163,6 +187,14 @@ def lib() -> ctypes.CDLL:
         L.gdn_accept.restype = ip
         L.gdn_accept_tree.argtypes = [ctypes.POINTER(Dims)] + [vp] * 10
         L.gdn_accept_tree.restype = ip
+        L.gdn_kv_append.argtypes = ([ctypes.POINTER(AttnDims), ctypes.POINTER(KvCache), ctypes.POINTER(QkParams)] +
+                                    [vp] * 3 + [ctypes.c_longlong] * 3 + [vp] * 6)
+        L.gdn_kv_append.restype = ip
+        L.gdn_attend_workspace_bytes.argtypes = [ctypes.POINTER(AttnDims)]
+        L.gdn_attend_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_attend.argtypes = ([ctypes.POINTER(AttnDims), ctypes.POINTER(KvCache), ctypes.POINTER(AttnParams)] +
+                                 [vp] * 5 + [ctypes.c_size_t, vp, vp])
+        L.gdn_attend.restype = ip
         L.gdn_prefill_workspace_bytes.argtypes = [ctypes.POINTER(Dims)]
         L.gdn_prefill_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_prefill_chunked.argtypes = ([ctypes.POINTER(Dims), ctypes.POINTER(LayerParams)] + [vp] * 8 +
@@ -429,6 +461,54 @@ def gdn_accept_tree(dims: Dims, d_parent, draft, tokens, d_length, d_accept, d_n
     _check(lib().gdn_accept_tree(ctypes.byref(dims), _ptr(d_parent), _ptr(draft), _ptr(tokens), _ptr(d_length),
                                  _ptr(d_accept), _ptr(d_next), _ptr(d_emit), _ptr(d_path), _ptr(d_status),
                                  _stream(stream)))
+
+
+def make_attn_dims(n_slots: int, n_tokens: int, n_heads: int, n_kv_heads: int, d_head: int, page_tokens: int, n_pages: int,
+                   max_pages: int, page_stride: Optional[int] = None, dtype: int = GDN_BF16) -> AttnDims:
+    """A batch over a paged cache; page_stride None: pages follow one another."""
+    stride = n_kv_heads * page_tokens * d_head if page_stride is None else page_stride
+    return AttnDims(n_slots, n_tokens, n_heads, n_kv_heads, d_head, page_tokens, n_pages, max_pages, stride, dtype)
+
+
+def kv_cache(k, v, page_table, past) -> KvCache:
+    """One layer's pools [n_pages][n_kv_heads][page_tokens][d_head], the slots' pages [B][max_pages] and the positions
+    they hold before the batch [B] (int32)."""
+    c = KvCache(_ptr(k), _ptr(v), _ptr(page_table), _ptr(past))
+    c.tensors = (k, v, page_table, past)
+    return c
+
+
+def qk_params(rope_dims: int, freq=None, q_norm=None, k_norm=None, norm_eps: float = 1e-6,
+              adjacent: bool = False) -> QkParams:
+    """Rotation (freq: device f32[rope_dims/2], radians a position) and the heads' norms (device f32[d_head], or None)."""
+    p = QkParams(int(rope_dims), int(adjacent), _ptr(freq), _ptr(q_norm), _ptr(k_norm), norm_eps)
+    p.tensors = (freq, q_norm, k_norm)
+    return p
+
+
+def attn_params(scale: float, window: int = 0, n_sink: int = 0) -> AttnParams:
+    return AttnParams(scale, int(window), int(n_sink))
+
+
+def gdn_kv_append(dims: AttnDims, cache: KvCache, params: QkParams, q, k, v, ld_q: int, ld_k: int, ld_v: int, q_out,
+                  d_length=None, d_parent=None, d_path=None, d_status=None, stream=None) -> None:
+    """Rotates q into q_out (both may be None) and k into the cache, and appends v; with d_path the accepted path of a
+    tree goes to its final places."""
+    _check(lib().gdn_kv_append(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(params), _ptr(q), _ptr(k), _ptr(v),
+                               int(ld_q), int(ld_k), int(ld_v), _ptr(q_out), _ptr(d_length), _ptr(d_parent),
+                               _ptr(d_path), _ptr(d_status), _stream(stream)))
+
+
+def gdn_attend_workspace_bytes(dims: AttnDims) -> int:
+    return int(lib().gdn_attend_workspace_bytes(ctypes.byref(dims)))
+
+
+def gdn_attend(dims: AttnDims, cache: KvCache, params: AttnParams, q, out, workspace, ws_bytes: int, d_length=None,
+               d_parent=None, d_status=None, stream=None) -> None:
+    """Attention of the batch's tokens over the cache: q and out [B][T][n_heads][d_head]."""
+    _check(lib().gdn_attend(ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(params), _ptr(q), _ptr(out),
+                            _ptr(d_length), _ptr(d_parent), _ptr(workspace), int(ws_bytes), _ptr(d_status),
+                            _stream(stream)))
 
 
 def gdn_prefill_workspace_bytes(dims: Dims) -> int:

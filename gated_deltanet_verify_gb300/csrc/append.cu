@@ -1,0 +1,192 @@
+// append.cu -- a batch's queries and keys normalised and rotated by their positions, its keys and values appended to a
+// paged cache, in one pass.
+//
+// A head's vector x (D numbers) becomes x' = R(p) (x / sqrt(mean x^2 + eps) * w): R(p) turns pair i of the first
+// rope_dims numbers by the angle p * freq[i].  The new tokens' k' and v go to their slot's pages, q' to a dense matrix.
+//
+// Angles.  p * freq[i] in fp32 loses its turns at far positions (at p = 10^5 an error of 2^-8 radians).  Only the angle's
+// part of a full turn counts, so freq / 2 pi is held as a 64-bit fraction of a turn (rounded once, from fp64) and
+// multiplied by p in wrapping integers: exact but for that rounding, p * 2^-65 turns, and no fp64 in the loop (a CTA's SM
+// does two fp64 operations a cycle).  sincospif of the upper 32 bits follows.  A token's angles are computed once and
+// shared by its heads.
+//
+// Bytes bound it: every row is read once and written once.  A token is one CTA's: its threads take 8 numbers of a head
+// each (16-byte accesses in bf16), so D / 8 lanes hold a head, its norm is a few shuffles, and the other half of a
+// rotated pair comes by a shuffle too (rope_dims / 2 is a multiple of 8).
+#include "attn.cuh"
+
+#include <cuda_bf16.h>
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 8;               // numbers a thread holds
+constexpr unsigned kFull = 0xffffffffu;
+
+template <typename E> struct Vec;
+template <> struct Vec<float> {
+    float4 a, b;
+    __device__ __forceinline__ void get(float *x) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    __device__ __forceinline__ void set(const float *x) {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+template <> struct Vec<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void get(float *x) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ void set(const float *x) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        a = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+    constexpr int kLanes = D / kPer;              // threads a head
+    constexpr int kHeads = kThreads / kLanes;     // heads at a time
+    __shared__ float2 turn[D / 2];                // cos and sin of the token's angles
+    __shared__ int parents[64];
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int tid = threadIdx.x, sub = tid % kLanes, group = tid / kLanes;
+    const int half = a.rope_dims / 2, first = a.q ? 0 : a.H, heads = a.H + 2 * a.Hk;
+    const int page = 1 << a.kv.page_log2;
+    for (long long row = blockIdx.x; row < (long long)a.B * a.T; row += gridDim.x) {
+        const int s = int(row / a.T), t = int(row % a.T);
+        int past;
+        const int n = live_tokens(a.kv, a.length, a.T, s, past);
+        if (n < 0 && t == 0 && tid == 0) report(a.d_status, GDN_ERR_LENGTH);
+        if (t >= n) continue;
+        int source = t, depth = t;
+        if (a.path) {
+            source = a.path[row];
+            if (source == -1) continue;
+            if (source < 0 || source >= a.T) {
+                if (tid == 0) report(a.d_status, GDN_ERR_TREE);
+                continue;
+            }
+        }
+        __syncthreads();                          // the last token's angles are no longer read
+        if (a.parent) {
+            if (tid <= t) {
+                int p = a.parent[row - t + tid];
+                if (p < -1 || p >= tid) {         // as if it hung from the past
+                    if (tid == t) report(a.d_status, GDN_ERR_TREE);
+                    p = -1;
+                }
+                parents[tid] = p;
+            }
+            __syncthreads();
+            depth = 0;
+            for (int p = parents[t]; p >= 0; p = parents[p]) ++depth;
+        }
+        const unsigned long long position = (unsigned long long)(past + depth);
+        if (tid < half) {
+            // turns a position: the whole ones do not count, so the rest is a 64-bit fraction
+            const double f = (double)a.freq[tid] * 0.15915494309189533577;
+            const long long part = __double2ll_rn((f - rint(f)) * 18446744073709551616.0);
+            const int x = int((unsigned long long)part * position >> 32);
+            float sn, cs;
+            sincospif((float)x * 0x1p-31f, &sn, &cs);
+            turn[tid] = make_float2(cs, sn);
+        }
+        __syncthreads();
+        const int place = past + t;
+        const int id = a.kv.table[(size_t)s * a.kv.max_pages + (place >> a.kv.page_log2)];
+        const bool held = id >= 0 && id < a.kv.n_pages;
+        if (!held && tid == 0) report(a.d_status, GDN_ERR_PAGE);
+        const size_t from = (size_t)s * a.T + source;
+        for (int h0 = first; h0 < heads; h0 += kHeads) {
+            const int h = h0 + group;
+            const bool on = h < heads;
+            const int kind = h < a.H ? 0 : h < a.H + a.Hk ? 1 : 2;      // q, k, v
+            const int hk = h - a.H - (kind == 2 ? a.Hk : 0);
+            Vec<E> v{};
+            if (on) {
+                const E *base = kind == 0   ? static_cast<const E *>(a.q) + from * a.ld_q + (size_t)h * D
+                                : kind == 1 ? static_cast<const E *>(a.k) + from * a.ld_k + (size_t)hk * D
+                                            : static_cast<const E *>(a.v) + from * a.ld_v + (size_t)hk * D;
+                v = *reinterpret_cast<const Vec<E> *>(base + sub * kPer);
+            }
+            float x[kPer];
+            v.get(x);
+            const float *w = kind == 0 ? a.q_norm : a.k_norm;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) sum += x[i] * x[i];
+#pragma unroll
+            for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+            if (kind < 2 && w) {
+                const float r = rsqrtf(sum / D + a.eps);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) x[i] = x[i] * r * w[sub * kPer + i];
+            }
+            // the other half of each pair: rope_dims / 2 numbers further on, or beside it
+            const int step = half / kPer, i0 = sub * kPer;
+            const int lane = tid & 31;
+            const bool low = sub < step, turned = i0 < a.rope_dims && kind < 2;
+            float y[kPer];
+            if (!a.adjacent) {
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const float o = __shfl_sync(kFull, x[i], (low ? lane + step : lane - step) & 31);
+                    const float2 cs = turned ? turn[low ? i0 + i : i0 - half + i] : make_float2(1.f, 0.f);
+                    y[i] = turned ? (low ? x[i] * cs.x - o * cs.y : o * cs.y + x[i] * cs.x) : x[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; i += 2) {
+                    const float2 cs = turned ? turn[(i0 + i) / 2] : make_float2(1.f, 0.f);
+                    y[i] = turned ? x[i] * cs.x - x[i + 1] * cs.y : x[i];
+                    y[i + 1] = turned ? x[i] * cs.y + x[i + 1] * cs.x : x[i + 1];
+                }
+            }
+            if (kind < 2) v.set(y);               // v goes as it came
+            E *to = kind == 0 ? static_cast<E *>(a.q_out) + ((size_t)row * a.H + h) * D
+                              : static_cast<E *>(kind == 1 ? a.kv.k : a.kv.v) + (long long)id * a.kv.page_stride +
+                                    ((size_t)hk * page + (place & (page - 1))) * D;
+            if (on && (kind == 0 || held)) *reinterpret_cast<Vec<E> *>(to + sub * kPer) = v;
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+
+template <typename E>
+cudaError_t launch(const AppendArgs &a, int sms, cudaStream_t stream) {
+    auto kern = a.D == 64 ? append_kernel<E, 64> : a.D == 128 ? append_kernel<E, 128> : append_kernel<E, 256>;
+    cudaLaunchConfig_t cfg = {};
+    const long long rows = (long long)a.B * a.T, most = 8LL * sms;       // as many as the SMs hold at once
+    cfg.gridDim = dim3(unsigned(rows < most ? rows : most), 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream) {
+    return dtype == GDN_F32 ? launch<float>(a, sm_count, stream) : launch<__nv_bfloat16>(a, sm_count, stream);
+}
+
+}  // namespace gdn

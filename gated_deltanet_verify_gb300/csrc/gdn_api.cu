@@ -2,6 +2,7 @@
 // validation, launch-shape choice and error reporting.  No allocation, no
 // synchronisation: every call only enqueues work on the caller's stream.
 #include "step.cuh"
+#include "attn.cuh"
 
 #include <cstdarg>
 #include <cstdint>
@@ -827,6 +828,133 @@ int gdn_accept_tree(const gdn_dims *dims, const int32_t *d_parent, const int32_t
     g_err.clear();
     if (!d_parent) return fail(GDN_ERR_ARG, "parent ids are NULL");
     return accept_impl(dims, d_parent, draft, tokens, d_length, d_accept, d_next, d_emit, d_path, d_status, stream);
+}
+
+namespace {
+
+int check_attn_dims(const gdn_attn_dims *dims) {
+    if (!dims) return fail(GDN_ERR_ARG, "dims is NULL");
+    const gdn_attn_dims &d = *dims;
+    if (d.n_slots < 1 || d.n_tokens < 1 || (long long)d.n_slots * d.n_tokens > (1LL << 24))
+        return fail(GDN_ERR_SHAPE, "slots x tokens must be in [1, 2^24] (got %d x %d)", d.n_slots, d.n_tokens);
+    if (d.n_kv_heads < 1 || d.n_heads < d.n_kv_heads || d.n_heads > 65536 || d.n_heads % d.n_kv_heads ||
+        d.n_heads / d.n_kv_heads > 64)
+        return fail(GDN_ERR_SHAPE, "n_heads (%d) must be 1 .. 64 times n_kv_heads (%d), at most 65536", d.n_heads, d.n_kv_heads);
+    if (d.d_head != 64 && d.d_head != 128 && d.d_head != 256)
+        return fail(GDN_ERR_SHAPE, "d_head must be 64, 128 or 256 (got %d)", d.d_head);
+    if (d.page_tokens < 8 || d.page_tokens > 256 || (d.page_tokens & (d.page_tokens - 1)))
+        return fail(GDN_ERR_SHAPE, "page_tokens must be a power of two in [8, 256] (got %d)", d.page_tokens);
+    if (d.n_pages < 1 || d.max_pages < 1 || (long long)d.max_pages * d.page_tokens > (1LL << 30))
+        return fail(GDN_ERR_SHAPE, "n_pages and max_pages must be positive, max_pages * page_tokens at most 2^30 (got %d, %d)",
+                    d.n_pages, d.max_pages);
+    if (d.page_stride % 8 || d.page_stride >= (1LL << 38) ||
+        d.page_stride < (long long)d.n_kv_heads * d.page_tokens * d.d_head)
+        return fail(GDN_ERR_SHAPE, "page_stride must be a multiple of 8, at least a page and below 2^38 (got %lld)", d.page_stride);
+    if (d.dtype != GDN_F32 && d.dtype != GDN_BF16)
+        return fail(GDN_ERR_DTYPE, "dtype %d is neither GDN_F32 nor GDN_BF16", int(d.dtype));
+    return GDN_OK;
+}
+
+int check_kv_cache(const gdn_kv_cache *c) {
+    if (!c) return fail(GDN_ERR_ARG, "cache is NULL");
+    if (!c->k || !c->v || !c->page_table || !c->past) return fail(GDN_ERR_ARG, "a pointer of the cache is NULL");
+    const void *ptrs[] = {c->k, c->v, c->page_table, c->past};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return fail(GDN_ERR_ALIGN, "cache buffer %p is not 16-byte aligned", p);
+    return GDN_OK;
+}
+
+gdn::KvPages kv_pages(const gdn_attn_dims &d, const gdn_kv_cache &c) {
+    int log2 = 0;
+    while ((1 << log2) < d.page_tokens) ++log2;
+    return {c.k, c.v, c.page_table, c.past, d.page_stride, d.n_pages, d.max_pages, log2};
+}
+
+size_t attend_workspace(const gdn_attn_dims &d) {
+    const int rows = gdn::attend_block_rows(d.dtype, d.n_tokens, d.n_heads / d.n_kv_heads, d.d_head);
+    return gdn::attend_partial_bytes(rows, d.d_head) + gdn::attend_stats_bytes(rows);
+}
+
+}  // namespace
+
+int gdn_kv_append(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_qk_params *params, const void *q,
+                  const void *k, const void *v, long long ld_q, long long ld_k, long long ld_v, void *q_out,
+                  const int32_t *d_length, const int32_t *d_parent, const int32_t *d_path, int *d_status, void *stream) {
+    g_err.clear();
+    int rc = check_attn_dims(dims);
+    if (!rc) rc = check_kv_cache(cache);
+    if (rc) return rc;
+    if (!params) return fail(GDN_ERR_ARG, "params is NULL");
+    const gdn_attn_dims &d = *dims;
+    const gdn_qk_params &p = *params;
+    if (!k || !v || !q != !q_out) return fail(GDN_ERR_ARG, "k or v is NULL, or one of q and q_out without the other");
+    if (d_path && (q || d_parent)) return fail(GDN_ERR_ARG, "d_path goes with neither q nor d_parent");
+    if (d_parent && d.n_tokens > 64) return fail(GDN_ERR_SHAPE, "a tree has at most 64 tokens (got %d)", d.n_tokens);
+    if (p.rope_dims < 0 || p.rope_dims > d.d_head || p.rope_dims % 16)
+        return fail(GDN_ERR_SHAPE, "rope_dims must be a multiple of 16 in [0, d_head] (got %d)", p.rope_dims);
+    if (p.rope_dims && !p.freq) return fail(GDN_ERR_ARG, "freq is NULL");
+    if (!(p.norm_eps >= 0.f)) return fail(GDN_ERR_ARG, "norm_eps must be >= 0");
+    const int per16 = d.dtype == GDN_F32 ? 4 : 8;
+    const long long qw = (long long)d.n_heads * d.d_head, kw = (long long)d.n_kv_heads * d.d_head, most = 1LL << 38;
+    if ((q && (ld_q < qw || ld_q % per16 || ld_q >= most)) || ld_k < kw || ld_k % per16 || ld_k >= most || ld_v < kw ||
+        ld_v % per16 || ld_v >= most)
+        return fail(GDN_ERR_SHAPE, "a row stride is below its heads' width, no multiple of 16 bytes, or 2^38 or more "
+                    "(got %lld, %lld, %lld)", ld_q, ld_k, ld_v);
+    if (q && q == q_out && ld_q != qw) return fail(GDN_ERR_SHAPE, "q_out can only be q if ld_q is n_heads * d_head");
+    const void *ptrs[] = {q, k, v, q_out, p.freq, p.q_norm, p.k_norm, d_length, d_parent, d_path};
+    for (const void *x : ptrs)
+        if (!aligned16(x)) return fail(GDN_ERR_ALIGN, "buffer %p is not 16-byte aligned", x);
+    gdn::AppendArgs a{};
+    a.B = d.n_slots; a.T = d.n_tokens; a.H = d.n_heads; a.Hk = d.n_kv_heads; a.D = d.d_head;
+    a.kv = kv_pages(d, *cache);
+    a.q = q; a.k = k; a.v = v; a.ld_q = ld_q; a.ld_k = ld_k; a.ld_v = ld_v; a.q_out = q_out;
+    a.rope_dims = p.rope_dims; a.adjacent = p.adjacent != 0; a.freq = p.freq;
+    a.q_norm = p.q_norm; a.k_norm = p.k_norm; a.eps = p.norm_eps;
+    a.length = d_length; a.parent = d_parent; a.path = d_path; a.d_status = d_status;
+    const cudaError_t e = gdn::launch_append(a, d.dtype, dev_info().sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "append launch failed: %s", cudaGetErrorString(e));
+    return GDN_OK;
+}
+
+size_t gdn_attend_workspace_bytes(const gdn_attn_dims *dims) {
+    g_err.clear();
+    return check_attn_dims(dims) ? 0 : attend_workspace(*dims);
+}
+
+int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_attn_params *params, const void *q, void *out,
+               const int32_t *d_length, const int32_t *d_parent, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
+    g_err.clear();
+    int rc = check_attn_dims(dims);
+    if (!rc) rc = check_kv_cache(cache);
+    if (rc) return rc;
+    if (!params) return fail(GDN_ERR_ARG, "params is NULL");
+    const gdn_attn_dims &d = *dims;
+    if (!(params->scale > -INFINITY && params->scale < INFINITY)) return fail(GDN_ERR_ARG, "scale must be finite");
+    if (params->window < 0 || params->n_sink < 0)
+        return fail(GDN_ERR_ARG, "window and n_sink must be >= 0 (got %d, %d)", params->window, params->n_sink);
+    if (!q || !out) return fail(GDN_ERR_ARG, "q or out is NULL");
+    if (q == out) return fail(GDN_ERR_ARG, "out cannot be q");
+    if (d_parent && d.n_tokens > 64) return fail(GDN_ERR_SHAPE, "a tree has at most 64 tokens (got %d)", d.n_tokens);
+    const void *ptrs[] = {q, out, d_length, d_parent};
+    for (const void *x : ptrs)
+        if (!aligned16(x)) return fail(GDN_ERR_ALIGN, "buffer %p is not 16-byte aligned", x);
+    const size_t need = attend_workspace(d);
+    if (!workspace || ws_bytes < need)
+        return fail(GDN_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, workspace ? ws_bytes : (size_t)0);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(GDN_ERR_ALIGN, "workspace is not 256-byte aligned");
+    gdn::AttendArgs a{};
+    a.B = d.n_slots; a.T = d.n_tokens; a.H = d.n_heads; a.Hk = d.n_kv_heads; a.D = d.d_head; a.G = d.n_heads / d.n_kv_heads;
+    a.kv = kv_pages(d, *cache);
+    a.q = q; a.out = out; a.length = d_length; a.parent = d_parent; a.scale = params->scale;
+    a.window = params->window; a.n_sink = params->window ? params->n_sink : 0; a.d_status = d_status;
+    const int rows = gdn::attend_block_rows(d.dtype, a.T, a.G, a.D);
+    a.partial = static_cast<float *>(workspace);
+    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(rows, a.D));
+    const int sms = dev_info().sms;
+    const cudaError_t e = d.dtype == GDN_F32 ? gdn::launch_attend_f32(a, sms, static_cast<cudaStream_t>(stream))
+                                             : gdn::launch_attend_bf16_simple(a, sms, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "attention launch failed: %s", cudaGetErrorString(e));
+    return GDN_OK;
 }
 
 }  // extern "C"

@@ -78,8 +78,9 @@ typedef enum {
     GDN_ERR_TREE = 10,       /* (device) a parent id is outside [-1, t-1]; that token ran from the root */
     GDN_ERR_BOUNDS = 11,     /* (device, checked builds only) an access fell outside its buffer and was skipped */
     GDN_ERR_SAMPLE = 12,     /* (device) a row that cannot be sampled (see gdn_sample); its token is -1 */
-    GDN_ERR_LENGTH = 13,     /* (device) a slot's draft length is out of range; nothing of it is accepted */
-    GDN_ERR_ADAPTER = 14     /* (device) an adapter id names none; the slot ran without one */
+    GDN_ERR_LENGTH = 13,     /* (device) a slot's length (or past) is out of range; nothing of it is accepted (or run) */
+    GDN_ERR_ADAPTER = 14,    /* (device) an adapter id names none; the slot ran without one */
+    GDN_ERR_PAGE = 15        /* (device) a page id names none; its positions were not written, or read as zeros */
 } gdn_status;
 
 typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
@@ -470,6 +471,117 @@ int gdn_accept(const gdn_dims *dims, const int32_t *draft, const int32_t *tokens
 int gdn_accept_tree(const gdn_dims *dims, const int32_t *d_parent, const int32_t *draft, const int32_t *tokens,
                     const int32_t *d_length, int32_t *d_accept, int32_t *d_next, int32_t *d_emit, int32_t *d_path,
                     int *d_status, void *stream);
+
+/*
+ * The full-attention layers of the model run over the same batch between the
+ * GDN layers (internal.h, "Target weights": full attention every fourth layer).
+ * Their keys and values lie in a paged cache that the caller owns, one pool of
+ * pages per layer: position p of slot s and kv head h is the row
+ *   k + page_table[s][p / page_tokens] * page_stride + (h * page_tokens + p % page_tokens) * d_head
+ * (elements; the same in v).  past[s] is the number of positions a slot holds
+ * before the batch (internal.h, "Target forward graph": QwenGraphInputs::kv_start);
+ * the batch's token t is appended at past[s] + t.  The caller advances past by
+ * the tokens that it keeps: positions behind it are never read, so a rollback of
+ * the cache moves nothing.  page_table entries of positions that a call neither
+ * writes nor may see are not read; slots may share pages that none of them writes.
+ *
+ * Limits: d_head 64, 128 or 256; n_heads a multiple of n_kv_heads, at most 64
+ * times as many; page_tokens a power of two, 8 .. 256; page_stride a multiple of
+ * 8, at least n_kv_heads * page_tokens * d_head and below 2^38; max_pages *
+ * page_tokens at most 2^30; B*T at most 2^24; n_heads at most 65536 (GDN_ERR_SHAPE).
+ * Activations and cache are all f32 or all bf16.  d_length (optional, DEVICE
+ * int32[B]): a slot's real tokens, 0 .. T; the rows behind them are neither read
+ * nor written.  A length or a past outside [0, T] or [0, max_pages * page_tokens -
+ * length] skips the slot and writes GDN_ERR_LENGTH to *d_status.  A page id
+ * outside [0, n_pages) writes GDN_ERR_PAGE: its positions are not written, and
+ * read as zeros (keys and values).  d_parent (optional, DEVICE int32[B][T], T <=
+ * 64): the batch is a draft tree as in gdn_verify_tree; node t lies at past +
+ * depth (its number of ancestors in the batch) but is stored at past + t.  A parent outside
+ * [-1, t-1] writes GDN_ERR_TREE and its node hangs from the past.
+ */
+typedef struct {
+    int n_slots;           /* B */
+    int n_tokens;          /* T: new tokens per slot, 1 .. */
+    int n_heads;           /* query heads */
+    int n_kv_heads;
+    int d_head;
+    int page_tokens;       /* positions a page */
+    int n_pages;           /* pages in the pools */
+    int max_pages;         /* entries of a slot's row of the page table */
+    long long page_stride; /* elements from one page of a pool to the next (K and V may interleave) */
+    gdn_dtype dtype;       /* of q, k, v, the cache and the output */
+} gdn_attn_dims;
+
+typedef struct {
+    void *k, *v;                  /* the pools */
+    const int32_t *page_table;    /* [B][max_pages] */
+    const int32_t *past;          /* [B] */
+} gdn_kv_cache;
+
+typedef struct {
+    int rope_dims;         /* leading numbers of a head that are rotated: 0, or a multiple of 16 up to d_head */
+    int adjacent;          /* pairs (2i, 2i+1) if nonzero, else (i, i + rope_dims/2) */
+    const float *freq;     /* [rope_dims/2] f32: pair i turns by freq[i] radians a position */
+    const float *q_norm;   /* [d_head] f32 weight of the RMS norm over a head of q, or NULL: none */
+    const float *k_norm;   /* the same for k */
+    float norm_eps;
+} gdn_qk_params;
+
+/*
+ * Before the attention: q and k are normalised (if asked) and rotated by their
+ * positions, and k and v go into the cache (internal.h, "Target forward graph":
+ * QwenGraphInputs::positions and kv_write_rows; hf2q qwen35_target.rs,
+ * positions_for_range: the text positions, the same on every axis).  q, k and v are rows of n_heads, n_kv_heads
+ * and n_kv_heads heads, ld_q, ld_k and ld_v elements apart (multiples of 16
+ * bytes), so they may be column blocks of one projection's output.  q_out
+ * [B][T][n_heads][d_head] may be q itself if ld_q is n_heads * d_head; q NULL:
+ * keys and values alone.  Sums, norms and rotations are fp32, the angles exact
+ * to 2^-24 of a turn at any position; one rounding at the end.  v is copied.
+ *
+ * d_path (optional, DEVICE int32[B][T], with q and d_parent NULL): commits the
+ * accepted path of a draft tree, as gdn_accept_tree's d_path gives it, from the
+ * same k and v: row i of the slot comes from token d_path[s][i] and goes to
+ * position past + i; -1 rows are left out.  (The tree's own append stored node t
+ * at past + t, so the path's rows have to move; from the batch's rows the call
+ * can be repeated.)  Another entry outside [0, T) writes GDN_ERR_TREE and is
+ * left out.
+ */
+int gdn_kv_append(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_qk_params *params,
+                  const void *q, const void *k, const void *v, long long ld_q, long long ld_k, long long ld_v,
+                  void *q_out, const int32_t *d_length, const int32_t *d_parent, const int32_t *d_path,
+                  int *d_status, void *stream);
+
+typedef struct {
+    float scale;           /* of the scores (1/sqrt(d_head) is common); finite */
+    int window;            /* 0: none; else a token sees the last `window` positions, its own among them */
+    int n_sink;            /* with a window: the first positions that stay visible */
+} gdn_attn_params;
+
+/* Device workspace of gdn_attend: partial sums of rows whose keys several CTAs
+ * share (0 on bad dims).  Its size does not depend on the lengths. */
+size_t gdn_attend_workspace_bytes(const gdn_attn_dims *dims);
+
+/*
+ * Attention of the batch's tokens over the cache, after gdn_kv_append:
+ *   out[s][t][h] = sum_p w_p v_p / sum_p w_p,  w_p = exp(scale * q[s][t][h] . k_p)
+ * over the positions p that token t sees: every p < past and, of the batch,
+ * itself and the tokens before it (in a tree: its ancestors).  With a window
+ * (internal.h, QwenGraphInputs::fa_window) those of them that are less than
+ * `window` positions back, or among the first n_sink; a tree's nodes count by
+ * their depth.  Query head h reads kv head h / (n_heads / n_kv_heads).  Any T >= 1:
+ * single tokens, verify batches, a prompt's chunk.
+ *
+ * Scores, maxima and sums are fp32.  In bf16 the weights w_p, scaled to at most
+ * 2^8, are rounded to bf16 for the product with v (fp32 sums) and the output
+ * once more.  What lies at positions that no token of the slot sees is never
+ * used; k and v of the others must be finite.  q and out [B][T][n_heads][d_head]
+ * do not overlap.  workspace: gdn_attend_workspace_bytes, 256-byte aligned; it
+ * needs no initialisation, and calls that share it must be ordered.  The sums'
+ * order, so the last bits of a row, depends on the lengths of the whole batch.
+ */
+int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_attn_params *params,
+               const void *q, void *out, const int32_t *d_length, const int32_t *d_parent,
+               void *workspace, size_t ws_bytes, int *d_status, void *stream);
 
 /*
  * One verify step from host memory: the inputs of the step arrive as one
