@@ -1,0 +1,696 @@
+// attend.cu -- attention of a batch of new tokens over a paged cache, bf16, on the tensor cores.
+//
+// Rows: the G query heads that share a kv head times a block's tokens, 128 to a tile (a chain's verify of 16 tokens with
+// G = 6 fills 96), so that a key and a value are read once for all of them.  Per tile of 128 keys
+//   S = Q K^T            (128 x 128, fp32 in tensor memory)
+//   P = 2^(S scale log2 e - m)   rounded to bf16, in place of S; the row sums stay fp32
+//   O += P V             (128 x D, fp32 in tensor memory)
+// with the running maximum m: one pass over the cache.  m is only moved (and O rescaled) when it has grown by more than 2^8,
+// so weights reach 2^8 and the rescale is rare; the rounding of P to bf16 (half a step, 2^-8, of each weight, and of the output as
+// a mean of them) is what the tensor cores take, and of the order of the output's own rounding.
+//
+//   * A warp streams keys and values through a ring of 16 or 32 KB stages: one TMA box a page, straight into the tensor
+//     cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
+//     side by side, so that boxes of any page size leave the same layout: group stride (D / 64) KB, chunk stride 1 KB.  It is
+//     K-major for K (8-row groups by the stride offset) and, read the other way, MN-major for V.
+//   * A warp issues the MMAs; S has two buffers.  With one row tile they alternate by key tile, so that the next S is
+//     made while this one's softmax runs; with two row tiles (D <= 128 and more than 128 rows a slot) each has its own.
+//   * 128 threads a row tile do the softmax, a row each (tensor memory's lane), so no value crosses threads.
+//   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
+//     at the ends of its share are joined with its neighbours' parts by attend_join.cuh.
+//
+// Positions that no row of the block sees are not loaded by whole pages, and their rows of V are cleared in shared memory
+// before the MMA (0 x NaN would be NaN); scores that a row may not see are replaced, whatever was there.
+//
+// Every wait is bounded; one that gives up reports GDN_ERR_TIMEOUT and the CTA ends.
+#include "attend_join.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kTile = 128;            // keys a tile
+constexpr int kRowTile = 128;         // rows a tile (tensor memory's lanes)
+constexpr int kSpin = 1 << 22;        // mbarrier polls before a wait gives up
+constexpr float kSlack = 8.f;         // powers of two by which a maximum may grow unmoved
+
+template <int D, int RT> struct Shape {
+    static constexpr int kChunks = D / 64;                         // 128-byte columns of a row
+    static constexpr int kStage = D == 64 ? 16384 : 32768;         // bytes
+    static constexpr int kKChunks = kChunks < 2 ? kChunks : 2;     // of K in a stage: 128 keys x 64 kKChunks
+    static constexpr int kKStages = kChunks / kKChunks;
+    static constexpr int kVTokens = kStage / (2 * D);              // of V in a stage: kVTokens keys x D
+    static constexpr int kVStages = kTile / kVTokens;
+    static constexpr int kQBytes = RT * kRowTile * D * 2;
+    static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
+    static constexpr int kThreads = 128 * RT + 64;
+    static constexpr size_t kSmem = 1024 + kQBytes + size_t(kRing) * kStage;
+    static_assert(RT == 1 || D <= 128, "tensor memory: two S and the row tiles' O");
+    static_assert(kRing >= 5, "a tile's V, the next one's K, and one more");
+};
+
+struct TcArgs {
+    CUtensorMap q_map, k_map, v_map;
+    AttendArgs a;
+    int tt;                           // tokens a row tile holds
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.release.cta.shared::cta.b64 st, [%0], %1;\n\t}\n" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.release.cta.shared::cta.b64 st, [%0];\n\t}\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// bounded wait; false if it gave up
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+    for (int i = 0; i < kSpin; ++i)
+        if (mbar_try(bar, parity)) return true;
+    return false;
+}
+// the same by a whole warp, with one answer for all its lanes
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void tma_box5(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::
+            "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+// shared-memory matrix descriptor in the 128-byte swizzle, atoms of 8 rows x 128 bytes.  K-major: `stride` from one
+// 8-row group to the next (one MMA's 16 columns lie inside a row; lead unused).  MN-major: `lead` from one 64-column chunk
+// to the next, `stride` from one group of 8 k to the next.
+__device__ __forceinline__ uint64_t make_desc(uint32_t saddr, uint32_t lead, uint32_t stride) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(stride >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+// instruction descriptor: kind::f16, bf16 A and B, fp32 D, M = 128, A K-major, B K-major or MN-major
+__host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(id), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(id), "r"(acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+#define GDN_R32(r) \
+    "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), \
+    "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), \
+    "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), \
+    "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+#define GDN_I32(r) \
+    "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), \
+    "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), \
+    "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), \
+    "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+// 32 columns of this thread's tensor-memory lane (wait_ld / wait_st before the registers or the columns are used)
+__device__ __forceinline__ void tmem_ld32(uint32_t at, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+                 "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+                 : GDN_R32(r)
+                 : "r"(at));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+                 "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::GDN_I32(r),
+                 "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// bits [0, n) of a word, n any int
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// A CTA's blocks of rows, one after the other: each role walks them by itself.
+struct Walk {
+    long long left;
+    int pair, kvh, j0, j1;
+    Span span;
+    bool first, whole;
+    __device__ __forceinline__ Walk(const AttendArgs &a, const Place &at, long long tiles) : left(tiles), pair(at.pair), first(true) {
+        span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
+        kvh = int(at.offset / span.n);
+        j0 = int(at.offset % span.n);
+        cut();
+    }
+    __device__ __forceinline__ void cut() {
+        j1 = int(min((long long)span.n, j0 + left));
+        whole = j0 == 0 && j1 == span.n;
+    }
+    __device__ __forceinline__ bool next(const AttendArgs &a) {
+        left -= j1 - j0;
+        first = false;
+        j0 = 0;
+        if (left <= 0) return false;
+        if (++kvh == a.Hk) {
+            kvh = 0;
+            do {
+                if (++pair == a.B * a.n_tb) return false;      // never, unless the lengths change under the call
+                span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
+            } while (span.n == 0);
+        }
+        cut();
+        return true;
+    }
+};
+
+template <int D, int RT>
+__global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
+    using Sh = Shape<D, RT>;
+    extern __shared__ unsigned char sm[];
+    __shared__ __align__(8) uint64_t bars[2 * Sh::kRing + 10];
+    __shared__ uint32_t tslot;
+    __shared__ long long scratch[Sh::kThreads / 32 + 4];
+    __shared__ int parents[RT][64];
+    __shared__ unsigned char depths[RT][64];
+    const AttendArgs &a = args.a;
+    const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31, c = blockIdx.x;
+    const uint32_t qbase = (smem_u32(sm) + 1023u) & ~1023u, ring = qbase + Sh::kQBytes;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto full = [&](uint32_t s) { return bar(s); };
+    auto empty = [&](uint32_t s) { return bar(Sh::kRing + s); };
+    constexpr int kB = 2 * Sh::kRing;
+    const uint32_t q_full = bar(kB), q_empty = bar(kB + 1);
+    auto s_full = [&](int b) { return bar(kB + 2 + b); };      // S is there
+    auto p_full = [&](int b) { return bar(kB + 4 + b); };      // P is there
+    auto o_done = [&](int b) { return bar(kB + 6 + b); };      // P V is done: O is whole so far, the buffer free
+    auto o_free = [&](int i) { return bar(kB + 8 + i); };      // a row tile's O has been read out
+
+    if (wid == 4 * RT + 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tslot)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    if (tid == 128 * RT) {
+        for (int s = 0; s < 2 * Sh::kRing + 4; ++s) mbar_init(bar(s), 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(p_full(b), 128);
+            mbar_init(o_done(b), 1);
+            mbar_init(o_free(b), 128);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        prefetch_map(&args.q_map);
+        prefetch_map(&args.k_map);
+        prefetch_map(&args.v_map);
+    }
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    Share share;
+    fence_before();
+    const Place at = find_place<kTile, Sh::kThreads>(a, c, share, scratch);     // two barriers of the CTA in it
+    fence_after();
+    const uint32_t tmem = tslot;
+    bool ok = true;
+    if (c == 0)
+        for (int s = tid; s < a.B; s += Sh::kThreads) {
+            int past;
+            if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
+        }
+
+    if (c < share.ctas) {
+        const long long tiles = share.start(c + 1) - share.start(c);
+        Walk w(a, at, tiles);
+        if (wid == 4 * RT) {
+            // ---- the loads
+            const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
+            uint32_t r = 0;                       // stages filled
+            int blocks = 0;
+            do {
+                const int s = w.pair / a.n_tb, sink = min(a.n_sink, w.span.lo), lo = w.span.lo, hi = w.span.hi;
+                const int32_t *table = a.kv.table + (size_t)s * a.kv.max_pages;
+                // page p of a tile is lane p's (a page of more than a tile: lane 0's)
+                auto page_id = [&](int j) {
+                    if (j >= w.j1) return -1;
+                    const int from = w.span.tile(j) * kTile + (lane << page_log2), to = from + min(page, kTile);
+                    const bool on = lane < max(1, kTile >> page_log2) && ((from < hi && to > lo) || from < sink);
+                    return on ? table[from >> page_log2] : -1;
+                };
+                auto put = [&](const CUtensorMap *map, int j, int id, int part, bool value) {
+                    // a stage: kKChunks columns of all keys, or all columns of kVTokens keys
+                    const uint32_t st = r % Sh::kRing;
+                    if (r >= Sh::kRing) ok = ok && warp_wait(empty(st), ((r / Sh::kRing) - 1) & 1);
+                    ++r;
+                    if (!ok) return;
+                    const int tokens = value ? Sh::kVTokens : kTile, box = min(page, tokens);
+                    const int k0 = w.span.tile(j) * kTile + (value ? part * Sh::kVTokens : 0);
+                    const int from = k0 + lane * box, to = from + box;
+                    const bool on = lane < tokens / box && ((from < hi && to > lo) || from < sink);
+                    const int at_page = (from >> page_log2) - ((w.span.tile(j) * kTile) >> page_log2);
+                    int g = __shfl_sync(0xffffffffu, id, at_page & 31);
+                    if (on && (g < 0 || g >= a.kv.n_pages)) {
+                        report(a.d_status, GDN_ERR_PAGE);
+                        g = a.kv.n_pages;         // outside the tensor: zeros
+                    }
+                    const uint32_t box_bytes = (uint32_t)box * (value ? D : 64 * Sh::kKChunks) * 2;
+                    const uint32_t n = __popc(__ballot_sync(0xffffffffu, on));
+                    if (lane == 0) mbar_expect(full(st), n * box_bytes);
+                    __syncwarp();
+                    if (on)
+                        tma_box5(ring + st * Sh::kStage + lane * box_bytes, map, 0, 0, value ? 0 : part * Sh::kKChunks,
+                                 ((w.kvh << page_log2) + (from & (page - 1))) >> 3, g, full(st));
+                };
+                auto put_k = [&](int j, int id) {
+#pragma unroll
+                    for (int p = 0; p < Sh::kKStages; ++p) put(&args.k_map, j, id, p, false);
+                };
+                auto put_v = [&](int j, int id) {
+#pragma unroll
+                    for (int p = 0; p < Sh::kVStages; ++p) put(&args.v_map, j, id, p, true);
+                };
+                int id = page_id(w.j0), id1 = page_id(w.j0 + 1);
+                if (blocks > 0) ok = ok && warp_wait(q_empty, (blocks - 1) & 1);
+                if (ok && lane == 0) {
+                    const uint32_t bytes = (uint32_t)args.tt * a.G * 128;
+                    mbar_expect(q_full, bytes * RT * Sh::kChunks);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int q = 0; q < Sh::kChunks; ++q)
+                            tma_box5(qbase + (i * Sh::kChunks + q) * (kRowTile * 128), &args.q_map, 0, q, w.kvh * a.G,
+                                     w.span.t0 + i * args.tt, s, q_full);
+                }
+                __syncwarp();
+                ++blocks;
+                // in the order in which the MMAs take them
+                if (RT == 1) put_k(w.j0, id);
+                for (int j = w.j0; j < w.j1 && ok; ++j) {
+                    const int id2 = page_id(j + 2);
+                    if (RT == 2) put_k(j, id);
+                    else if (j + 1 < w.j1) put_k(j + 1, id1);
+                    put_v(j, id);
+                    id = id1;
+                    id1 = id2;
+                }
+            } while (ok && w.next(a));
+            if (!ok)                              // the copies in flight land before the CTA ends
+                for (uint32_t i = r > Sh::kRing ? r - Sh::kRing : 0; i < r; ++i) mbar_wait(full(i % Sh::kRing), (i / Sh::kRing) & 1);
+        } else if (wid == 4 * RT + 1) {
+            // ---- the MMAs
+            const bool leader = elect_one();      // one thread issues all of them, so that its commits cover them
+            uint32_t r = 0, u = 0;                // stages taken, units (S buffers filled) begun before this block
+            int blocks = 0;
+            // S buffer b: rows of row tile i
+            auto qk = [&](int i, int b, bool release) {
+#pragma unroll
+                for (int p = 0; p < Sh::kKStages; ++p) {
+                    const uint32_t st = (r + p) % Sh::kRing;
+                    ok = ok && warp_wait(full(st), ((r + p) / Sh::kRing) & 1);
+                    fence_after();
+                    if (ok && leader) {
+                        const uint32_t kb = ring + st * Sh::kStage;
+#pragma unroll
+                        for (int k = 0; k < 4 * Sh::kKChunks; ++k)
+                            mma_ss(tmem + b * 128,
+                                   make_desc(qbase + (i * Sh::kChunks + p * Sh::kKChunks + k / 4) * (kRowTile * 128) + (k & 3) * 32, 16, 1024),
+                                   make_desc(kb + (k / 4) * 1024 + (k & 3) * 32, 16, Sh::kKChunks * 1024), idesc(kTile, false),
+                                   p > 0 || k > 0);
+                        if (release) mma_commit(empty(st));
+                    }
+                    __syncwarp();
+                }
+                if (ok && leader) mma_commit(s_full(b));
+                __syncwarp();
+            };
+            auto pv = [&](int i, int b, uint32_t rv, bool fresh, bool release) {
+#pragma unroll
+                for (int p = 0; p < Sh::kVStages; ++p) {
+                    const uint32_t st = (rv + p) % Sh::kRing;
+                    ok = ok && warp_wait(full(st), ((rv + p) / Sh::kRing) & 1);
+                    fence_after();
+                    if (ok && leader) {
+                        const uint32_t vb = ring + st * Sh::kStage;
+#pragma unroll
+                        for (int k = 0; k < Sh::kVTokens / 16; ++k)
+                            mma_ts(tmem + 256 + i * 128, tmem + b * 128 + (p * Sh::kVTokens / 16 + k) * 8,
+                                   make_desc(vb + k * 2 * Sh::kChunks * 1024, 1024, Sh::kChunks * 1024), idesc(D, true),
+                                   !fresh || p > 0 || k > 0);
+                        if (release) mma_commit(empty(st));
+                    }
+                    __syncwarp();
+                }
+                if (ok && leader) mma_commit(o_done(b));
+                __syncwarp();
+            };
+            do {
+                ok = ok && warp_wait(q_full, blocks & 1);
+                const int n = w.j1 - w.j0;
+                if constexpr (RT == 1) {
+                    // unit u + t in buffer (u + t) & 1, free once the P V of two units before is done
+                    auto next_qk = [&](int t) {
+                        const uint32_t v = u + t;
+                        if (v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
+                        qk(0, v & 1, true);
+                        r += Sh::kKStages;
+                        if (t == n - 1 && ok && leader) mma_commit(q_empty);
+                        __syncwarp();
+                    };
+                    next_qk(0);
+                    for (int t = 0; t < n && ok; ++t) {
+                        if (t + 1 < n) next_qk(t + 1);
+                        const uint32_t v = u + t;
+                        ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
+                        if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
+                        pv(0, v & 1, r, t == 0, true);
+                        r += Sh::kVStages;
+                    }
+                } else {
+                    // each row tile has its own buffer, free once its P V is done
+                    for (int t = 0; t <= n && ok; ++t) {
+                        const uint32_t v = u + t;
+                        // of tile t: K in stages r .., V of tile t - 1 in the stages before them
+                        const uint32_t rv = r - Sh::kVStages;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (t > 0) {
+                                ok = ok && warp_wait(p_full(i), (v - 1) & 1);
+                                if (t == 1 && blocks > 0) ok = ok && warp_wait(o_free(i), (blocks - 1) & 1);
+                                pv(i, i, rv, t == 1, i == 1);
+                            }
+                            if (t < n) {
+                                if (v > 0) ok = ok && warp_wait(o_done(i), (v - 1) & 1);
+                                qk(i, i, i == 1);
+                                if (t == n - 1 && i == 1 && ok && leader) mma_commit(q_empty);
+                                __syncwarp();
+                            }
+                        }
+                        if (t < n) r += Sh::kKStages + Sh::kVStages;
+                    }
+                }
+                u += n;
+                ++blocks;
+            } while (ok && w.next(a));
+        } else {
+            // ---- the softmax: thread = row
+            const int i = wid >> 2, row = tid & 127;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * (wid & 3)) << 16), o_at = lanes + 256 + i * 128;
+            const bool negative = a.scale < 0.f;
+            // a scale of zero leaves all weights alike, and masked ones at none
+            const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+            uint32_t u = 0, r = 0;
+            int last_pair = -1;
+            unsigned long long line = 0;          // a tree's nodes that this row sees
+            int position = 0;
+            do {
+                const int s = w.pair / a.n_tb, past = w.span.past, n = w.j1 - w.j0;
+                const int first_t = w.span.t0 + i * args.tt, last_t = min(w.span.t1, first_t + args.tt) - 1;
+                const int t = row < args.tt * a.G ? first_t + row / a.G : w.span.t1;
+                const bool on = t < w.span.t1;
+                const bool busy = __any_sync(0xffffffffu, on);
+                if (w.pair != last_pair) {
+                    last_pair = w.pair;
+                    position = past + t;
+                    if (a.parent) {
+                        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                        if (row < w.span.t1) {
+                            int p = a.parent[(size_t)s * a.T + row];
+                            if (p < -1 || p >= row) {             // it hangs from the past
+                                report(a.d_status, GDN_ERR_TREE);
+                                p = -1;
+                            }
+                            parents[i][row] = p;
+                        }
+                        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                        if (row < w.span.t1) {
+                            int d = 0;
+                            for (int p = parents[i][row]; p >= 0; p = parents[i][p]) ++d;
+                            depths[i][row] = (unsigned char)d;
+                        }
+                        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                        line = 0;
+                        if (on) {
+                            const int mine = depths[i][t];
+                            position = past + mine;
+                            for (int p = t; p >= 0; p = parents[i][p]) {
+                                const int d = depths[i][p];
+                                if (!a.window || mine - d < a.window || past + d < a.n_sink) line |= 1ull << p;
+                            }
+                        }
+                    }
+                }
+                const int lim = a.parent ? past : position + 1;   // positions below: by the rule of a chain
+                const int low = a.window ? position - a.window + 1 : 0;
+                const int sink = min(a.n_sink, w.span.lo);
+                float m = -INFINITY, l = 0.f;
+                for (int q = 0; q < n; ++q) {
+                    const uint32_t v = u + q;
+                    const int b = RT == 1 ? (v & 1) : i;
+                    const uint32_t phase = RT == 1 ? (v >> 1) & 1 : v & 1;
+                    const int k0 = w.span.tile(w.j0 + q) * kTile;
+                    ok = ok && warp_wait(s_full(b), phase);
+                    if (!ok) break;
+                    fence_after();
+                    // O is whole up to the tile before
+                    auto wait_o = [&] {
+                        if constexpr (RT == 1) return warp_wait(o_done((v - 1) & 1), ((v - 1) >> 1) & 1);
+                        else return warp_wait(o_done(i), (v - 1) & 1);
+                    };
+                    if (busy) {
+                        const uint32_t s_at = lanes + b * 128;
+                        uint32_t x[128];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) tmem_ld32(s_at + 32 * e, x + 32 * e);
+                        wait_ld();
+                        if (negative)
+#pragma unroll
+                            for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
+                        // does every row see all of the tile?
+                        const bool all = k0 + kTile <= past + (a.parent ? 0 : first_t + 1) &&
+                                         (!a.window || k0 > past + last_t - a.window);
+                        if (!__all_sync(0xffffffffu, all || !on)) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int at0 = k0 + 32 * e;
+                                uint32_t see = below(lim - at0);
+                                if (a.window) see &= ~below(low - at0) | below(a.n_sink - at0);
+                                if (a.parent) {
+                                    const int sh = past - at0;            // node 0's bit
+                                    if (sh > -64 && sh < 32) see |= (uint32_t)(sh >= 0 ? line << sh : line >> -sh);
+                                }
+#pragma unroll
+                                for (int f = 0; f < 32; ++f)
+                                    if (!(see >> f & 1)) x[32 * e + f] = 0xff800000u;
+                            }
+                        }
+                        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
+                        const float to = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        const bool grows = on && (to - m) * sc > kSlack;
+                        if (q == 0) {
+                            m = fmaxf(m, to);
+                        } else if (__any_sync(0xffffffffu, grows)) {
+                            const float up = fmaxf(m, to), f = m == up ? 1.f : ex2((m - up) * sc);
+                            ok = ok && wait_o();
+                            fence_after();
+                            l *= f;
+                            m = up;
+#pragma unroll 1
+                            for (int e = 0; e < D; e += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(o_at + e, o);
+                                wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st32(o_at + e, o);
+                            }
+                        }
+                        const float base = m == -INFINITY ? 0.f : -m * sc;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t p[32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                const float y0 = ex2(fmaf(__uint_as_float(x[64 * e + 2 * k]), sc, base));
+                                const float y1 = ex2(fmaf(__uint_as_float(x[64 * e + 2 * k + 1]), sc, base));
+                                sum[2 * (k & 1)] += y0;
+                                sum[2 * (k & 1) + 1] += y1;
+                                p[k] = pack_bf16(y0, y1);
+                            }
+                            tmem_st32(s_at + 32 * e, p);
+                        }
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        wait_st();
+                    }
+                    // ---- rows of V that no row of the block sees
+                    if (k0 + kTile > w.span.hi || (k0 < w.span.lo && k0 + kTile > sink)) {
+                        const int key = k0 + row, part = row / Sh::kVTokens, g = row % Sh::kVTokens;
+                        // after the P V of the tile before, whose stages come ahead of this one's in the ring
+                        if (v > 0) ok = ok && wait_o();
+                        const uint32_t rv = r + ((RT == 2 || q == 0) + (RT == 1 && q + 1 < n)) * Sh::kKStages + part;
+                        ok = ok && warp_wait(full(rv % Sh::kRing), (rv / Sh::kRing) & 1);
+                        if (ok && !(key < w.span.hi && (key >= w.span.lo || key < sink))) {
+                            const uint32_t to = ring + (rv % Sh::kRing) * Sh::kStage + (g >> 3) * (Sh::kChunks * 1024) + (g & 7) * 128;
+#pragma unroll
+                            for (int e = 0; e < Sh::kChunks; ++e)
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to + e * 1024 + k * 16), "r"(0) : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                    }
+                    // what the ring has moved on by, with this tile's V: K before V, and with one row tile the next tile's K too
+                    if constexpr (RT == 1) r += (q == 0 ? Sh::kKStages : 0) + (q + 1 < n ? Sh::kKStages : 0) + Sh::kVStages;
+                    else r += Sh::kKStages + Sh::kVStages;
+                    fence_before();
+                    mbar_arrive(p_full(b));
+                }
+                u += n;
+                // ---- the block's sums: its output, or a part of it
+                if (ok) {
+                    if constexpr (RT == 1) ok = warp_wait(o_done((u - 1) & 1), ((u - 1) >> 1) & 1);
+                    else ok = warp_wait(o_done(i), (u - 1) & 1);
+                }
+                fence_after();
+                if (ok && busy) {
+                    const int in_block = i * args.tt * a.G + row, g = row % a.G;
+                    const size_t part = size_t(2 * c + (w.first ? 0 : 1)) * (a.TB * a.G) + in_block;
+                    const float inv = 1.f / l;
+                    if (!w.whole && on) a.stats[part] = make_float2(m * sc, l);
+#pragma unroll 1
+                    for (int e = 0; e < D; e += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o_at + e, o);
+                        wait_ld();
+                        if (!on) continue;
+                        if (w.whole) {
+                            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                                   (((size_t)s * a.T + t) * a.H + (size_t)w.kvh * a.G + g) * D + e);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int f = 0; f < 4; ++f)
+                                    y[f] = pack_bf16(__uint_as_float(o[8 * k + 2 * f]) * inv, __uint_as_float(o[8 * k + 2 * f + 1]) * inv);
+                                out[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        } else {
+                            uint4 *to = reinterpret_cast<uint4 *>(a.partial + part * D + e);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                    }
+                }
+                fence_before();
+                mbar_arrive(o_free(i));
+            } while (ok && w.next(a));
+        }
+    }
+    if (!ok && lane == 0) report(a.d_status, GDN_ERR_TIMEOUT);
+    __syncwarp();
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (wid == 4 * RT + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+}
+
+template <int D, int RT> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
+    using Sh = Shape<D, RT>;
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const AttendArgs &a = t.a;
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+    auto map = [&](CUtensorMap *m, const void *p, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+        return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(p), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    const cuuint64_t es = 2, page = 1ull << a.kv.page_log2;
+    {
+        // a row tile: G heads of tt tokens of one slot (tokens past T read zeros)
+        const cuuint64_t dims[5] = {64, D / 64, (cuuint64_t)a.H, (cuuint64_t)a.T, (cuuint64_t)a.B};
+        const cuuint64_t strides[4] = {128, D * es, a.H * D * es, (cuuint64_t)a.T * a.H * D * es};
+        const cuuint32_t box[5] = {64, 1, (cuuint32_t)a.G, (cuuint32_t)t.tt, 1};
+        if (!map(&t.q_map, a.q, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    // a page of a kv head: groups of 8 tokens, in each the 64-column chunks, in each 8 rows
+    const cuuint64_t dims[5] = {64, 8, D / 64, (cuuint64_t)a.Hk * (page / 8), (cuuint64_t)a.kv.n_pages};
+    const cuuint64_t strides[4] = {D * es, 128, 8 * D * es, (cuuint64_t)a.kv.page_stride * es};
+    const cuuint32_t kbox[5] = {64, 8, Sh::kKChunks, (cuuint32_t)(page < kTile ? page / 8 : kTile / 8), 1};
+    const cuuint32_t vbox[5] = {64, 8, D / 64, (cuuint32_t)(page < Sh::kVTokens ? page / 8 : Sh::kVTokens / 8), 1};
+    if (!map(&t.k_map, a.kv.k, dims, strides, kbox) || !map(&t.v_map, a.kv.v, dims, strides, vbox)) return cudaErrorInvalidValue;
+
+    static PerContext<int> limits;
+    unsigned long long ctx = 0;
+    int set = 0;
+    if (!current_context_id(&ctx) || !limits.get(ctx, &set)) {
+        const cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+        if (e != cudaSuccess) return e;
+        if (current_context_id(&ctx)) limits.put(ctx, 1);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(a.ctas), 1, 1);
+    cfg.blockDim = dim3(Sh::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, RT>, t);
+    return e != cudaSuccess ? e : launch_join<__nv_bfloat16, D, kTile>(a, stream);
+}
+
+// row tiles of a CTA: two where a slot's rows fill more than one and tensor memory holds both tiles' O
+int row_tiles(int T, int G, int D) { return D <= 128 && T > kRowTile / G ? 2 : 1; }
+
+}  // namespace
+
+int attend_bf16_block_rows(int T, int G, int D) { return row_tiles(T, G, D) * kRowTile; }
+
+cudaError_t launch_attend_bf16(const AttendArgs &args, int sm_count, cudaStream_t stream) {
+    TcArgs t{};
+    AttendArgs &a = t.a;
+    a = args;
+    const int rt = row_tiles(a.T, a.G, a.D);
+    t.tt = kRowTile / a.G < a.T ? kRowTile / a.G : a.T;
+    a.TB = rt * t.tt;
+    a.n_tb = (a.T + a.TB - 1) / a.TB;
+    a.ctas = sm_count < kAttendCtas ? sm_count : kAttendCtas;
+    if (rt == 2) return a.D == 64 ? launch<64, 2>(t, stream) : launch<128, 2>(t, stream);
+    return a.D == 64 ? launch<64, 1>(t, stream) : a.D == 128 ? launch<128, 1>(t, stream) : launch<256, 1>(t, stream);
+}
+
+}  // namespace gdn

@@ -311,23 +311,14 @@ template <typename E, int BM> cudaError_t launch_d(const AttendArgs &a, cudaStre
 }  // namespace
 
 // rows of a block: 16 where a slot has no more (a wider block would spend its time on rows that are not there), else 64
-static int block_rows(int T, int G) { return (long long)T * G <= 16 ? 16 : 64; }
-int attend_block_rows(gdn_dtype, int T, int G, int) { return block_rows(T, G); }
+int attend_f32_block_rows(int T, int G) { return (long long)T * G <= 16 ? 16 : 64; }
 
 cudaError_t launch_attend_f32(AttendArgs a, int sm_count, cudaStream_t stream) {
-    const int rows = block_rows(a.T, a.G);
+    const int rows = attend_f32_block_rows(a.T, a.G);
     a.TB = rows / a.G < a.T ? rows / a.G : a.T;
     a.n_tb = (a.T + a.TB - 1) / a.TB;
     a.ctas = sm_count < kAttendCtas ? sm_count : kAttendCtas;
     return rows == 16 ? launch_d<float, 16>(a, stream) : launch_d<float, 64>(a, stream);
-}
-
-cudaError_t launch_attend_bf16_simple(AttendArgs a, int sm_count, cudaStream_t stream) {
-    const int rows = block_rows(a.T, a.G);
-    a.TB = rows / a.G < a.T ? rows / a.G : a.T;
-    a.n_tb = (a.T + a.TB - 1) / a.TB;
-    a.ctas = sm_count < kAttendCtas ? sm_count : kAttendCtas;
-    return rows == 16 ? launch_d<__nv_bfloat16, 16>(a, stream) : launch_d<__nv_bfloat16, 64>(a, stream);
 }
 
 }  // namespace gdn

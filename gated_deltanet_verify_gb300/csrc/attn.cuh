@@ -50,16 +50,16 @@ struct AttendArgs {
 
 // What the workspace holds; rows: of a block, at most.
 constexpr int kAttendCtas = 152;      // CTAs of a launch, at most: one on every SM
-constexpr int kAttendRows = 256;      // rows of a block, at most
 inline size_t attend_partial_bytes(int rows, int D) { return size_t(2) * kAttendCtas * rows * D * sizeof(float); }
 inline size_t attend_stats_bytes(int rows) { return size_t(2) * kAttendCtas * rows * sizeof(float2); }
 
 // Return a cudaError_t of the launch (cudaSuccess when enqueued).
 cudaError_t launch_append(const AppendArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream);
 cudaError_t launch_attend_f32(AttendArgs a, int sm_count, cudaStream_t stream);
-cudaError_t launch_attend_bf16_simple(AttendArgs a, int sm_count, cudaStream_t stream);
+cudaError_t launch_attend_bf16(const AttendArgs &a, int sm_count, cudaStream_t stream);
 // rows of a block at most, for the workspace
-int attend_block_rows(gdn_dtype dtype, int T, int G, int D);
+int attend_f32_block_rows(int T, int G);
+int attend_bf16_block_rows(int T, int G, int D);
 
 #ifdef __CUDACC__
 

@@ -870,8 +870,14 @@ gdn::KvPages kv_pages(const gdn_attn_dims &d, const gdn_kv_cache &c) {
     return {c.k, c.v, c.page_table, c.past, d.page_stride, d.n_pages, d.max_pages, log2};
 }
 
+// rows of a block of the work, at most
+int attend_rows(const gdn_attn_dims &d) {
+    const int G = d.n_heads / d.n_kv_heads;
+    return d.dtype == GDN_F32 ? gdn::attend_f32_block_rows(d.n_tokens, G) : gdn::attend_bf16_block_rows(d.n_tokens, G, d.d_head);
+}
+
 size_t attend_workspace(const gdn_attn_dims &d) {
-    const int rows = gdn::attend_block_rows(d.dtype, d.n_tokens, d.n_heads / d.n_kv_heads, d.d_head);
+    const int rows = attend_rows(d);
     return gdn::attend_partial_bytes(rows, d.d_head) + gdn::attend_stats_bytes(rows);
 }
 
@@ -947,12 +953,11 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     a.kv = kv_pages(d, *cache);
     a.q = q; a.out = out; a.length = d_length; a.parent = d_parent; a.scale = params->scale;
     a.window = params->window; a.n_sink = params->window ? params->n_sink : 0; a.d_status = d_status;
-    const int rows = gdn::attend_block_rows(d.dtype, a.T, a.G, a.D);
     a.partial = static_cast<float *>(workspace);
-    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(rows, a.D));
+    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(attend_rows(d), a.D));
     const int sms = dev_info().sms;
     const cudaError_t e = d.dtype == GDN_F32 ? gdn::launch_attend_f32(a, sms, static_cast<cudaStream_t>(stream))
-                                             : gdn::launch_attend_bf16_simple(a, sms, static_cast<cudaStream_t>(stream));
+                                             : gdn::launch_attend_bf16(a, sms, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "attention launch failed: %s", cudaGetErrorString(e));
     return GDN_OK;
 }
