@@ -24,7 +24,8 @@ CHECKED_BUILD = os.path.join(PKG, "_build_checked")
 CHECKED_LIB = os.path.join(PKG, "libgdn_verify_checked.so")
 
 SOURCES = ["gdn_api.cu", "verify.cu", "rollback.cu", "prefill.cu", "proj.cu", "lora.cu", "sample.cu", "accept.cu",
-           "append.cu", "attend.cu", "attend_f32.cu"]
+           "append.cu", "attend.cu", "attend_f32.cu",
+           "attend_join.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

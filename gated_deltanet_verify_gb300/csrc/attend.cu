@@ -17,35 +17,56 @@
 //     made while this one's softmax runs; with two row tiles (D <= 128 and more than 128 rows a slot) each has its own.
 //   * 128 threads a row tile do the softmax, a row each (tensor memory's lane), so no value crosses threads.
 //   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
-//     at the ends of its share are joined with its neighbours' parts by attend_join.cuh.
+//     at the ends of its share are joined with its neighbours' parts by attend_join.cu.
 //
 // Positions that no row of the block sees are not loaded by whole pages, and their rows of V are cleared in shared memory
 // before the MMA (0 x NaN would be NaN); scores that a row may not see are replaced, whatever was there.
 //
 // Every wait is bounded; one that gives up reports GDN_ERR_TIMEOUT and the CTA ends.
-#include "attend_join.cuh"
+#include "attn.cuh"
+
+#include <cuda_bf16.h>
 
 namespace gdn {
 namespace {
 
-constexpr int kTile = 128;            // keys a tile
-constexpr int kRowTile = 128;         // rows a tile (tensor memory's lanes)
+constexpr int kTile = kTileBf16;
+constexpr int kLanes = 128;           // tensor memory's: rows of a row tile
 constexpr int kSpin = 1 << 22;        // mbarrier polls before a wait gives up
 constexpr float kSlack = 8.f;         // powers of two by which a maximum may grow unmoved
 
-template <int D, int RT> struct Shape {
+// RT: row tiles.  C: copies of a row tile's rows, 128 / C of them, side by side in tensor memory; copy i takes the i-th
+// C-th of every tile's keys.
+template <int D, int RT, int C> struct Shape {
     static constexpr int kChunks = D / 64;                         // 128-byte columns of a row
     static constexpr int kStage = D == 64 ? 16384 : 32768;         // bytes
     static constexpr int kKChunks = kChunks < 2 ? kChunks : 2;     // of K in a stage: 128 keys x 64 kKChunks
     static constexpr int kKStages = kChunks / kKChunks;
     static constexpr int kVTokens = kStage / (2 * D);              // of V in a stage: kVTokens keys x D
     static constexpr int kVStages = kTile / kVTokens;
-    static constexpr int kQBytes = RT * kRowTile * D * 2;
+    static constexpr int kQBytes = RT * kLanes * D * 2;
     static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
-    static constexpr int kThreads = 128 * RT + 64;
-    static constexpr size_t kSmem = 1024 + kQBytes + size_t(kRing) * kStage;
-    static_assert(RT == 1 || D <= 128, "tensor memory: two S and the row tiles' O");
+    static constexpr int kThreads = RT == 1 ? 192 : 384;
+    static constexpr int kRows = kLanes / C;                       // of a row tile
+    static constexpr int kKeys = kTile / C;                        // of a tile that a copy takes
+    // a row's sums on their way out: two stages are shared out among the softmax threads
+    static constexpr int kOut = 2 * kStage / (RT * kLanes);
+    static_assert(RT == 1 || (D <= 128 && C == 1), "tensor memory: two S and the row tiles' O");
     static_assert(kRing >= 5, "a tile's V, the next one's K, and one more");
+};
+
+// What a CTA keeps beside its tiles, behind them.
+template <int RT, int RING> struct Control {
+    uint64_t full[RING], empty[RING];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2];    // S is there; P is there
+    uint64_t o_done[2];               // P V is done: O is whole so far, the buffer free
+    uint64_t o_free[2];               // a row tile's O has been read out
+    int scratch[4 * RT + 6];
+    uint32_t tmem;
+    float2 stats[RT][kLanes];         // a row's maximum and sum, by copy
+    int parents[RT][64];
+    unsigned char depths[RT][64];
 };
 
 struct TcArgs {
@@ -151,6 +172,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r) {
                  "r"(at)
                  : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n" ::
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                     "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+                 : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -165,18 +192,17 @@ __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 
 
 // A CTA's blocks of rows, one after the other: each role walks them by itself.
 struct Walk {
-    long long left;
-    int pair, kvh, j0, j1;
+    int left, pair, kvh, j0, j1;
     Span span;
     bool first, whole;
-    __device__ __forceinline__ Walk(const AttendArgs &a, const Place &at, long long tiles) : left(tiles), pair(at.pair), first(true) {
+    __device__ __forceinline__ Walk(const AttendArgs &a, const Place &at, int tiles) : left(tiles), pair(at.pair), first(true) {
         span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
-        kvh = int(at.offset / span.n);
-        j0 = int(at.offset % span.n);
+        kvh = at.offset / span.n;
+        j0 = at.offset % span.n;
         cut();
     }
     __device__ __forceinline__ void cut() {
-        j1 = int(min((long long)span.n, j0 + left));
+        j1 = min(span.n, j0 + left);
         whole = j0 == 0 && j1 == span.n;
     }
     __device__ __forceinline__ bool next(const AttendArgs &a) {
@@ -196,237 +222,63 @@ struct Walk {
     }
 };
 
-template <int D, int RT>
-__global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
-    using Sh = Shape<D, RT>;
-    extern __shared__ unsigned char sm[];
-    __shared__ __align__(8) uint64_t bars[2 * Sh::kRing + 10];
-    __shared__ uint32_t tslot;
-    __shared__ long long scratch[Sh::kThreads / 32 + 4];
-    __shared__ int parents[RT][64];
-    __shared__ unsigned char depths[RT][64];
+template <int D, int RT, int C>
+__global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
+    using Sh = Shape<D, RT, C>;
+    using Ctl = Control<RT, Sh::kRing>;
+    extern __shared__ __align__(1024) unsigned char sm[];         // no other shared memory, so that it starts at a swizzle atom
+    Ctl &ctl = *reinterpret_cast<Ctl *>(sm + Sh::kQBytes + Sh::kRing * Sh::kStage);
     const AttendArgs &a = args.a;
     const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31, c = blockIdx.x;
-    const uint32_t qbase = (smem_u32(sm) + 1023u) & ~1023u, ring = qbase + Sh::kQBytes;
-    auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    auto full = [&](uint32_t s) { return bar(s); };
-    auto empty = [&](uint32_t s) { return bar(Sh::kRing + s); };
-    constexpr int kB = 2 * Sh::kRing;
-    const uint32_t q_full = bar(kB), q_empty = bar(kB + 1);
-    auto s_full = [&](int b) { return bar(kB + 2 + b); };      // S is there
-    auto p_full = [&](int b) { return bar(kB + 4 + b); };      // P is there
-    auto o_done = [&](int b) { return bar(kB + 6 + b); };      // P V is done: O is whole so far, the buffer free
-    auto o_free = [&](int i) { return bar(kB + 8 + i); };      // a row tile's O has been read out
+    const uint32_t qbase = smem_u32(sm), ring = qbase + Sh::kQBytes;
+    auto full = [&](uint32_t s) { return smem_u32(&ctl.full[s]); };
+    auto empty = [&](uint32_t s) { return smem_u32(&ctl.empty[s]); };
+    const uint32_t q_full = smem_u32(&ctl.q_full), q_empty = smem_u32(&ctl.q_empty);
+    auto s_full = [&](int b) { return smem_u32(&ctl.s_full[b]); };
+    auto p_full = [&](int b) { return smem_u32(&ctl.p_full[b]); };
+    auto o_done = [&](int b) { return smem_u32(&ctl.o_done[b]); };
+    auto o_free = [&](int i) { return smem_u32(&ctl.o_free[i]); };
 
     if (wid == 4 * RT + 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tslot)));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&ctl.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    }
-    if (tid == 128 * RT) {
-        for (int s = 0; s < 2 * Sh::kRing + 4; ++s) mbar_init(bar(s), 1);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(p_full(b), 128);
-            mbar_init(o_done(b), 1);
-            mbar_init(o_free(b), 128);
+    } else if (wid == 4 * RT) {
+        if (lane < Sh::kRing) {
+            mbar_init(full(lane), 1);
+            mbar_init(empty(lane), 1);
+        }
+        if (lane < 2) {
+            mbar_init(s_full(lane), 1);
+            mbar_init(p_full(lane), 128);
+            mbar_init(o_done(lane), 1);
+            mbar_init(o_free(lane), 128);
+            mbar_init(lane ? q_full : q_empty, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-        prefetch_map(&args.q_map);
-        prefetch_map(&args.k_map);
-        prefetch_map(&args.v_map);
+        if (lane < 3) prefetch_map(lane == 0 ? &args.q_map : lane == 1 ? &args.k_map : &args.v_map);
     }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     Share share;
+    const Place at = find_place<kTile, Sh::kThreads>(a, c, share, ctl.scratch);
     fence_before();
-    const Place at = find_place<kTile, Sh::kThreads>(a, c, share, scratch);     // two barriers of the CTA in it
+    __syncthreads();
     fence_after();
-    const uint32_t tmem = tslot;
+    const uint32_t tmem = ctl.tmem;
     bool ok = true;
-    if (c == 0)
-        for (int s = tid; s < a.B; s += Sh::kThreads) {
-            int past;
-            if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
-        }
-
     if (c < share.ctas) {
-        const long long tiles = share.start(c + 1) - share.start(c);
-        Walk w(a, at, tiles);
-        if (wid == 4 * RT) {
-            // ---- the loads
-            const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
-            uint32_t r = 0;                       // stages filled
-            int blocks = 0;
-            do {
-                const int s = w.pair / a.n_tb, sink = min(a.n_sink, w.span.lo), lo = w.span.lo, hi = w.span.hi;
-                const int32_t *table = a.kv.table + (size_t)s * a.kv.max_pages;
-                // page p of a tile is lane p's (a page of more than a tile: lane 0's)
-                auto page_id = [&](int j) {
-                    if (j >= w.j1) return -1;
-                    const int from = w.span.tile(j) * kTile + (lane << page_log2), to = from + min(page, kTile);
-                    const bool on = lane < max(1, kTile >> page_log2) && ((from < hi && to > lo) || from < sink);
-                    return on ? table[from >> page_log2] : -1;
-                };
-                auto put = [&](const CUtensorMap *map, int j, int id, int part, bool value) {
-                    // a stage: kKChunks columns of all keys, or all columns of kVTokens keys
-                    const uint32_t st = r % Sh::kRing;
-                    if (r >= Sh::kRing) ok = ok && warp_wait(empty(st), ((r / Sh::kRing) - 1) & 1);
-                    ++r;
-                    if (!ok) return;
-                    const int tokens = value ? Sh::kVTokens : kTile, box = min(page, tokens);
-                    const int k0 = w.span.tile(j) * kTile + (value ? part * Sh::kVTokens : 0);
-                    const int from = k0 + lane * box, to = from + box;
-                    const bool on = lane < tokens / box && ((from < hi && to > lo) || from < sink);
-                    const int at_page = (from >> page_log2) - ((w.span.tile(j) * kTile) >> page_log2);
-                    int g = __shfl_sync(0xffffffffu, id, at_page & 31);
-                    if (on && (g < 0 || g >= a.kv.n_pages)) {
-                        report(a.d_status, GDN_ERR_PAGE);
-                        g = a.kv.n_pages;         // outside the tensor: zeros
-                    }
-                    const uint32_t box_bytes = (uint32_t)box * (value ? D : 64 * Sh::kKChunks) * 2;
-                    const uint32_t n = __popc(__ballot_sync(0xffffffffu, on));
-                    if (lane == 0) mbar_expect(full(st), n * box_bytes);
-                    __syncwarp();
-                    if (on)
-                        tma_box5(ring + st * Sh::kStage + lane * box_bytes, map, 0, 0, value ? 0 : part * Sh::kKChunks,
-                                 ((w.kvh << page_log2) + (from & (page - 1))) >> 3, g, full(st));
-                };
-                auto put_k = [&](int j, int id) {
-#pragma unroll
-                    for (int p = 0; p < Sh::kKStages; ++p) put(&args.k_map, j, id, p, false);
-                };
-                auto put_v = [&](int j, int id) {
-#pragma unroll
-                    for (int p = 0; p < Sh::kVStages; ++p) put(&args.v_map, j, id, p, true);
-                };
-                int id = page_id(w.j0), id1 = page_id(w.j0 + 1);
-                if (blocks > 0) ok = ok && warp_wait(q_empty, (blocks - 1) & 1);
-                if (ok && lane == 0) {
-                    const uint32_t bytes = (uint32_t)args.tt * a.G * 128;
-                    mbar_expect(q_full, bytes * RT * Sh::kChunks);
-#pragma unroll
-                    for (int i = 0; i < RT; ++i)
-#pragma unroll
-                        for (int q = 0; q < Sh::kChunks; ++q)
-                            tma_box5(qbase + (i * Sh::kChunks + q) * (kRowTile * 128), &args.q_map, 0, q, w.kvh * a.G,
-                                     w.span.t0 + i * args.tt, s, q_full);
-                }
-                __syncwarp();
-                ++blocks;
-                // in the order in which the MMAs take them
-                if (RT == 1) put_k(w.j0, id);
-                for (int j = w.j0; j < w.j1 && ok; ++j) {
-                    const int id2 = page_id(j + 2);
-                    if (RT == 2) put_k(j, id);
-                    else if (j + 1 < w.j1) put_k(j + 1, id1);
-                    put_v(j, id);
-                    id = id1;
-                    id1 = id2;
-                }
-            } while (ok && w.next(a));
-            if (!ok)                              // the copies in flight land before the CTA ends
-                for (uint32_t i = r > Sh::kRing ? r - Sh::kRing : 0; i < r; ++i) mbar_wait(full(i % Sh::kRing), (i / Sh::kRing) & 1);
-        } else if (wid == 4 * RT + 1) {
-            // ---- the MMAs
-            const bool leader = elect_one();      // one thread issues all of them, so that its commits cover them
-            uint32_t r = 0, u = 0;                // stages taken, units (S buffers filled) begun before this block
-            int blocks = 0;
-            // S buffer b: rows of row tile i
-            auto qk = [&](int i, int b, bool release) {
-#pragma unroll
-                for (int p = 0; p < Sh::kKStages; ++p) {
-                    const uint32_t st = (r + p) % Sh::kRing;
-                    ok = ok && warp_wait(full(st), ((r + p) / Sh::kRing) & 1);
-                    fence_after();
-                    if (ok && leader) {
-                        const uint32_t kb = ring + st * Sh::kStage;
-#pragma unroll
-                        for (int k = 0; k < 4 * Sh::kKChunks; ++k)
-                            mma_ss(tmem + b * 128,
-                                   make_desc(qbase + (i * Sh::kChunks + p * Sh::kKChunks + k / 4) * (kRowTile * 128) + (k & 3) * 32, 16, 1024),
-                                   make_desc(kb + (k / 4) * 1024 + (k & 3) * 32, 16, Sh::kKChunks * 1024), idesc(kTile, false),
-                                   p > 0 || k > 0);
-                        if (release) mma_commit(empty(st));
-                    }
-                    __syncwarp();
-                }
-                if (ok && leader) mma_commit(s_full(b));
-                __syncwarp();
-            };
-            auto pv = [&](int i, int b, uint32_t rv, bool fresh, bool release) {
-#pragma unroll
-                for (int p = 0; p < Sh::kVStages; ++p) {
-                    const uint32_t st = (rv + p) % Sh::kRing;
-                    ok = ok && warp_wait(full(st), ((rv + p) / Sh::kRing) & 1);
-                    fence_after();
-                    if (ok && leader) {
-                        const uint32_t vb = ring + st * Sh::kStage;
-#pragma unroll
-                        for (int k = 0; k < Sh::kVTokens / 16; ++k)
-                            mma_ts(tmem + 256 + i * 128, tmem + b * 128 + (p * Sh::kVTokens / 16 + k) * 8,
-                                   make_desc(vb + k * 2 * Sh::kChunks * 1024, 1024, Sh::kChunks * 1024), idesc(D, true),
-                                   !fresh || p > 0 || k > 0);
-                        if (release) mma_commit(empty(st));
-                    }
-                    __syncwarp();
-                }
-                if (ok && leader) mma_commit(o_done(b));
-                __syncwarp();
-            };
-            do {
-                ok = ok && warp_wait(q_full, blocks & 1);
-                const int n = w.j1 - w.j0;
-                if constexpr (RT == 1) {
-                    // unit u + t in buffer (u + t) & 1, free once the P V of two units before is done
-                    auto next_qk = [&](int t) {
-                        const uint32_t v = u + t;
-                        if (v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
-                        qk(0, v & 1, true);
-                        r += Sh::kKStages;
-                        if (t == n - 1 && ok && leader) mma_commit(q_empty);
-                        __syncwarp();
-                    };
-                    next_qk(0);
-                    for (int t = 0; t < n && ok; ++t) {
-                        if (t + 1 < n) next_qk(t + 1);
-                        const uint32_t v = u + t;
-                        ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
-                        if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
-                        pv(0, v & 1, r, t == 0, true);
-                        r += Sh::kVStages;
-                    }
-                } else {
-                    // each row tile has its own buffer, free once its P V is done
-                    for (int t = 0; t <= n && ok; ++t) {
-                        const uint32_t v = u + t;
-                        // of tile t: K in stages r .., V of tile t - 1 in the stages before them
-                        const uint32_t rv = r - Sh::kVStages;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (t > 0) {
-                                ok = ok && warp_wait(p_full(i), (v - 1) & 1);
-                                if (t == 1 && blocks > 0) ok = ok && warp_wait(o_free(i), (blocks - 1) & 1);
-                                pv(i, i, rv, t == 1, i == 1);
-                            }
-                            if (t < n) {
-                                if (v > 0) ok = ok && warp_wait(o_done(i), (v - 1) & 1);
-                                qk(i, i, i == 1);
-                                if (t == n - 1 && i == 1 && ok && leader) mma_commit(q_empty);
-                                __syncwarp();
-                            }
-                        }
-                        if (t < n) r += Sh::kKStages + Sh::kVStages;
-                    }
-                }
-                u += n;
-                ++blocks;
-            } while (ok && w.next(a));
-        } else {
-            // ---- the softmax: thread = row
-            const int i = wid >> 2, row = tid & 127;
+        Walk w(a, at, share.start(c + 1) - share.start(c));
+        // With two row tiles 384 threads start with 168 registers each, and the softmax warps take what the others do not need
+        // (216 x 256 + 72 x 128 = 168 x 384).
+        if (wid < 4 * RT) {
+            if constexpr (RT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+            // ---- the softmax: thread = tensor memory's lane = row (of one of C copies)
+            const int i = wid >> 2, tl = tid & 127, copy = tl / Sh::kRows, row = tl % Sh::kRows;
             const uint32_t lanes = tmem + ((uint32_t)(32 * (wid & 3)) << 16), o_at = lanes + 256 + i * 128;
             const bool negative = a.scale < 0.f;
             // a scale of zero leaves all weights alike, and masked ones at none
             const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-            uint32_t u = 0, r = 0;
+            uint32_t u = 0, r = 0;                // S buffers taken, stages passed before this block
             int last_pair = -1;
             unsigned long long line = 0;          // a tree's nodes that this row sees
             int position = 0;
@@ -435,33 +287,33 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(co
                 const int first_t = w.span.t0 + i * args.tt, last_t = min(w.span.t1, first_t + args.tt) - 1;
                 const int t = row < args.tt * a.G ? first_t + row / a.G : w.span.t1;
                 const bool on = t < w.span.t1;
-                const bool busy = __any_sync(0xffffffffu, on);
+                const bool busy = __any_sync(kWarp, on);
                 if (w.pair != last_pair) {
                     last_pair = w.pair;
                     position = past + t;
                     if (a.parent) {
                         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
-                        if (row < w.span.t1) {
-                            int p = a.parent[(size_t)s * a.T + row];
-                            if (p < -1 || p >= row) {             // it hangs from the past
+                        if (tl < w.span.t1) {
+                            int p = a.parent[(size_t)s * a.T + tl];
+                            if (p < -1 || p >= tl) {              // it hangs from the past
                                 report(a.d_status, GDN_ERR_TREE);
                                 p = -1;
                             }
-                            parents[i][row] = p;
+                            ctl.parents[i][tl] = p;
                         }
                         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
-                        if (row < w.span.t1) {
+                        if (tl < w.span.t1) {
                             int d = 0;
-                            for (int p = parents[i][row]; p >= 0; p = parents[i][p]) ++d;
-                            depths[i][row] = (unsigned char)d;
+                            for (int p = ctl.parents[i][tl]; p >= 0; p = ctl.parents[i][p]) ++d;
+                            ctl.depths[i][tl] = (unsigned char)d;
                         }
                         asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
                         line = 0;
                         if (on) {
-                            const int mine = depths[i][t];
+                            const int mine = ctl.depths[i][t];
                             position = past + mine;
-                            for (int p = t; p >= 0; p = parents[i][p]) {
-                                const int d = depths[i][p];
+                            for (int p = t; p >= 0; p = ctl.parents[i][p]) {
+                                const int d = ctl.depths[i][p];
                                 if (!a.window || mine - d < a.window || past + d < a.n_sink) line |= 1ull << p;
                             }
                         }
@@ -471,12 +323,15 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(co
                 const int low = a.window ? position - a.window + 1 : 0;
                 const int sink = min(a.n_sink, w.span.lo);
                 float m = -INFINITY, l = 0.f;
-                for (int q = 0; q < n; ++q) {
+                // Before the first tile comes a dry pass on whatever tensor memory holds, while the first keys are on their way:
+                // a launch starts with a cold instruction cache, and the first pass takes 4000 cycles where the next ones take
+                // 1400.  It writes into O, which the first P V overwrites.
+                for (int q = w.first ? -1 : 0; q < n; ++q) {
+                    const bool dry = q < 0;
                     const uint32_t v = u + q;
                     const int b = RT == 1 ? (v & 1) : i;
-                    const uint32_t phase = RT == 1 ? (v >> 1) & 1 : v & 1;
-                    const int k0 = w.span.tile(w.j0 + q) * kTile;
-                    ok = ok && warp_wait(s_full(b), phase);
+                    const int k0 = dry ? w.span.lo : w.span.tile(w.j0 + q) * kTile, mine0 = k0 + copy * Sh::kKeys;
+                    if (!dry) ok = ok && warp_wait(s_full(b), RT == 1 ? (v >> 1) & 1 : v & 1);
                     if (!ok) break;
                     fence_after();
                     // O is whole up to the tile before
@@ -485,21 +340,29 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(co
                         else return warp_wait(o_done(i), (v - 1) & 1);
                     };
                     if (busy) {
-                        const uint32_t s_at = lanes + b * 128;
-                        uint32_t x[128];
+                        const uint32_t s_at = lanes + b * 128 + copy * Sh::kKeys, p_at = dry ? o_at : lanes + b * 128;
+                        uint32_t x[Sh::kKeys];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) tmem_ld32(s_at + 32 * e, x + 32 * e);
+                        for (int e = 0; e < Sh::kKeys; e += 32) tmem_ld32(s_at + e, x + e);
+                        if (C > 1) {              // the other copies' keys
+                            const uint32_t zero[16] = {};
+#pragma unroll
+                            for (int e = 1; e < C; ++e)
+#pragma unroll
+                                for (int f = 0; f < Sh::kKeys / 2; f += 16)
+                                    tmem_st16(p_at + ((copy + e) & (C - 1)) * (Sh::kKeys / 2) + f, zero);
+                        }
                         wait_ld();
                         if (negative)
 #pragma unroll
-                            for (int e = 0; e < 128; ++e) x[e] ^= 0x80000000u;
-                        // does every row see all of the tile?
-                        const bool all = k0 + kTile <= past + (a.parent ? 0 : first_t + 1) &&
-                                         (!a.window || k0 > past + last_t - a.window);
-                        if (!__all_sync(0xffffffffu, all || !on)) {
+                            for (int e = 0; e < Sh::kKeys; ++e) x[e] ^= 0x80000000u;
+                        // does every row see all of the keys?
+                        const bool all = mine0 + Sh::kKeys <= past + (a.parent ? 0 : first_t + 1) &&
+                                         (!a.window || mine0 > past + last_t - a.window);
+                        if (!__all_sync(kWarp, all || !on)) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int at0 = k0 + 32 * e;
+                            for (int e = 0; e < Sh::kKeys; e += 32) {
+                                const int at0 = mine0 + e;
                                 uint32_t see = below(lim - at0);
                                 if (a.window) see &= ~below(low - at0) | below(a.n_sink - at0);
                                 if (a.parent) {
@@ -508,17 +371,17 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(co
                                 }
 #pragma unroll
                                 for (int f = 0; f < 32; ++f)
-                                    if (!(see >> f & 1)) x[32 * e + f] = 0xff800000u;
+                                    if (!(see >> f & 1)) x[e + f] = 0xff800000u;
                             }
                         }
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 128; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
+                        for (int e = 0; e < Sh::kKeys; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
                         const float to = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         const bool grows = on && (to - m) * sc > kSlack;
-                        if (q == 0) {
+                        if (q <= 0) {
                             m = fmaxf(m, to);
-                        } else if (__any_sync(0xffffffffu, grows)) {
+                        } else if (__any_sync(kWarp, grows)) {
                             const float up = fmaxf(m, to), f = m == up ? 1.f : ex2((m - up) * sc);
                             ok = ok && wait_o();
                             fence_after();
@@ -537,31 +400,36 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(co
                         const float base = m == -INFINITY ? 0.f : -m * sc;
                         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t p[32];
+                        for (int e = 0; e < Sh::kKeys; e += 32) {
+                            uint32_t p[16];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                const float y0 = ex2(fmaf(__uint_as_float(x[64 * e + 2 * k]), sc, base));
-                                const float y1 = ex2(fmaf(__uint_as_float(x[64 * e + 2 * k + 1]), sc, base));
+                            for (int k = 0; k < 16; ++k) {
+                                const float y0 = ex2(fmaf(__uint_as_float(x[e + 2 * k]), sc, base));
+                                const float y1 = ex2(fmaf(__uint_as_float(x[e + 2 * k + 1]), sc, base));
                                 sum[2 * (k & 1)] += y0;
                                 sum[2 * (k & 1) + 1] += y1;
                                 p[k] = pack_bf16(y0, y1);
                             }
-                            tmem_st32(s_at + 32 * e, p);
+                            tmem_st16(p_at + copy * (Sh::kKeys / 2) + e / 2, p);
                         }
                         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                         wait_st();
                     }
+                    if (dry) {
+                        m = -INFINITY;
+                        l = 0.f;
+                        continue;
+                    }
                     // ---- rows of V that no row of the block sees
                     if (k0 + kTile > w.span.hi || (k0 < w.span.lo && k0 + kTile > sink)) {
-                        const int key = k0 + row, part = row / Sh::kVTokens, g = row % Sh::kVTokens;
+                        const int key = k0 + tl, part = tl / Sh::kVTokens, g = tl % Sh::kVTokens;
                         // after the P V of the tile before, whose stages come ahead of this one's in the ring
                         if (v > 0) ok = ok && wait_o();
                         const uint32_t rv = r + ((RT == 2 || q == 0) + (RT == 1 && q + 1 < n)) * Sh::kKStages + part;
                         ok = ok && warp_wait(full(rv % Sh::kRing), (rv / Sh::kRing) & 1);
                         if (ok && !(key < w.span.hi && (key >= w.span.lo || key < sink))) {
                             const uint32_t to = ring + (rv % Sh::kRing) * Sh::kStage + (g >> 3) * (Sh::kChunks * 1024) + (g & 7) * 128;
-#pragma unroll
+#pragma unroll 1
                             for (int e = 0; e < Sh::kChunks; ++e)
 #pragma unroll
                                 for (int k = 0; k < 8; ++k)
@@ -577,56 +445,291 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, 1) attend_tc_kernel(co
                 }
                 u += n;
                 // ---- the block's sums: its output, or a part of it
+                float factor = 1.f;
+                if constexpr (C > 1) {
+                    // copies to a common maximum
+                    ctl.stats[i][tl] = make_float2(m, l);
+                    asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                    const float own = m;
+                    m = -INFINITY;
+                    l = 0.f;
+#pragma unroll
+                    for (int e = 0; e < C; ++e) m = fmaxf(m, ctl.stats[i][e * Sh::kRows + row].x);
+#pragma unroll
+                    for (int e = 0; e < C; ++e) {
+                        const float2 st = ctl.stats[i][e * Sh::kRows + row];
+                        l += st.x == -INFINITY ? 0.f : st.y * ex2((st.x - m) * sc);
+                    }
+                    factor = own == -INFINITY ? 0.f : ex2((own - m) * sc);
+                }
+                if (w.whole) factor /= l;
+                const size_t part0 = size_t(2 * c + (w.first ? 0 : 1)) * a.part_rows + i * args.tt * a.G;
+                if (!w.whole && on && copy == 0) a.stats[part0 + row] = make_float2(m * sc, l);
                 if (ok) {
                     if constexpr (RT == 1) ok = warp_wait(o_done((u - 1) & 1), ((u - 1) >> 1) & 1);
                     else ok = warp_wait(o_done(i), (u - 1) & 1);
                 }
                 fence_after();
-                if (ok && busy) {
-                    const int in_block = i * args.tt * a.G + row, g = row % a.G;
-                    const size_t part = size_t(2 * c + (w.first ? 0 : 1)) * (a.TB * a.G) + in_block;
-                    const float inv = 1.f / l;
-                    if (!w.whole && on) a.stats[part] = make_float2(m * sc, l);
+                // Rows go through the two stages, each turned by its number of 16 bytes (so that 32 lanes write 32 rows
+                // without conflicts), and leave side by side.  (Written by its own lane, 16 bytes a row at a time, 96 rows of
+                // 256 took 7400 cycles; as two bulk copies a row, 11500.)
+                constexpr int kStagesRt = 2 / RT, kLanesStage = kLanes / kStagesRt;
+                constexpr int kCols = Sh::kOut / 4 < D ? Sh::kOut / 4 : D, kPieces = kCols / 4;
+                auto out_row = [&](int lane_row) {
+                    const uint32_t st = (r + (RT == 1 ? lane_row / kLanesStage : i)) % Sh::kRing;
+                    return ring + st * Sh::kStage + (lane_row % kLanesStage) * Sh::kOut;
+                };
+#pragma unroll
+                for (int p = 0; p < kStagesRt; ++p) {
+                    const uint32_t st = r + (RT == 1 ? p : i);
+                    ok = ok && warp_wait(full(st % Sh::kRing), (st / Sh::kRing) & 1);
+                }
+                const int rows = ok ? max(0, last_t + 1 - first_t) * a.G : 0;      // as in every warp, unless a wait gave up
 #pragma unroll 1
-                    for (int e = 0; e < D; e += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o_at + e, o);
-                        wait_ld();
-                        if (!on) continue;
-                        if (w.whole) {
-                            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                                   (((size_t)s * a.T + t) * a.H + (size_t)w.kvh * a.G + g) * D + e);
+                for (int at0 = 0; at0 < D; at0 += kCols) {
+                    if (at0 > 0) asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                    if (ok && busy) {
+                        const uint32_t mine = out_row(tl);
+#pragma unroll 1
+                        for (int e = 0; e < kCols; e += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o_at + at0 + e, o);
+                            wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                uint32_t y[4];
-#pragma unroll
-                                for (int f = 0; f < 4; ++f)
-                                    y[f] = pack_bf16(__uint_as_float(o[8 * k + 2 * f]) * inv, __uint_as_float(o[8 * k + 2 * f + 1]) * inv);
-                                out[k] = make_uint4(y[0], y[1], y[2], y[3]);
+                            for (int k = 0; k < 8; ++k) {
+                                const int spot = (e / 4 + k + lane) & (kPieces - 1);
+                                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(mine + spot * 16),
+                                             "f"(__uint_as_float(o[4 * k]) * factor), "f"(__uint_as_float(o[4 * k + 1]) * factor),
+                                             "f"(__uint_as_float(o[4 * k + 2]) * factor), "f"(__uint_as_float(o[4 * k + 3]) * factor)
+                                             : "memory");
                             }
-                        } else {
-                            uint4 *to = reinterpret_cast<uint4 *>(a.partial + part * D + e);
+                        }
+                    }
+                    if (at0 + kCols == D) {
+                        fence_before();
+                        mbar_arrive(o_free(i));
+                    }
+                    asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+#pragma unroll 2
+                    for (int x = tl; x < rows * kPieces; x += 128) {
+                        const int rr = x / kPieces, piece = x % kPieces;
+                        float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) to[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        for (int e = 0; e < C; ++e) {
+                            const int from = e * Sh::kRows + rr;
+                            float z[4];
+                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                                         : "=f"(z[0]), "=f"(z[1]), "=f"(z[2]), "=f"(z[3])
+                                         : "r"(out_row(from) + ((piece + from) & (kPieces - 1)) * 16));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) y[k] += z[k];
+                        }
+                        if (w.whole) {
+                            const size_t to = (((size_t)s * a.T + first_t + rr / a.G) * a.H + (size_t)w.kvh * a.G + rr % a.G) * D;
+                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + to + at0 + 4 * piece) =
+                                make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                        } else {
+                            *reinterpret_cast<float4 *>(a.partial + (part0 + rr) * D + at0 + 4 * piece) = make_float4(y[0], y[1], y[2], y[3]);
                         }
                     }
                 }
-                fence_before();
-                mbar_arrive(o_free(i));
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+                asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                if (tl < kStagesRt) mbar_arrive(empty((r + (RT == 1 ? tl : i)) % Sh::kRing));
+                r += 2;
             } while (ok && w.next(a));
+        } else {
+            if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+            if (wid == 4 * RT) {
+                // ---- the loads
+                const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
+                uint32_t r = 0;                   // stages filled
+                int blocks = 0;
+                do {
+                    const int s = w.pair / a.n_tb, sink = min(a.n_sink, w.span.lo), lo = w.span.lo, hi = w.span.hi;
+                    const int32_t *table = a.kv.table + (size_t)s * a.kv.max_pages;
+                    // page p of a tile is lane p's (a page of more than a tile: lane 0's)
+                    auto page_id = [&](int j) {
+                        if (j >= w.j1) return -1;
+                        const int from = w.span.tile(j) * kTile + (lane << page_log2), to = from + min(page, kTile);
+                        const bool on = lane < max(1, kTile >> page_log2) && ((from < hi && to > lo) || from < sink);
+                        return on ? table[from >> page_log2] : -1;
+                    };
+                    // a tile's K or V: of a stage kKChunks columns of all keys, or all columns of kVTokens keys
+                    auto put = [&](int j, int id, bool value) {
+                        const CUtensorMap *map = value ? &args.v_map : &args.k_map;
+                        const int tokens = value ? Sh::kVTokens : kTile, box = min(page, tokens), stages = value ? Sh::kVStages : Sh::kKStages;
+                        const uint32_t box_bytes = (uint32_t)box * (value ? D : 64 * Sh::kKChunks) * 2;
+                        const int tile0 = w.span.tile(j) * kTile;
+#pragma unroll 1
+                        for (int part = 0; part < stages; ++part, ++r) {
+                            const uint32_t st = r % Sh::kRing;
+                            if (r >= Sh::kRing) ok = ok && warp_wait(empty(st), ((r / Sh::kRing) - 1) & 1);
+                            if (!ok) return;
+                            const int from = tile0 + (value ? part * Sh::kVTokens : 0) + lane * box, to = from + box;
+                            const bool on = lane < tokens / box && ((from < hi && to > lo) || from < sink);
+                            int g = __shfl_sync(kWarp, id, ((from >> page_log2) - (tile0 >> page_log2)) & 31);
+                            if (on && (g < 0 || g >= a.kv.n_pages)) {
+                                report(a.d_status, GDN_ERR_PAGE);
+                                g = a.kv.n_pages; // outside the tensor: zeros
+                            }
+                            const uint32_t boxes = __popc(__ballot_sync(kWarp, on));
+                            if (lane == 0) mbar_expect(full(st), boxes * box_bytes);
+                            __syncwarp();
+                            if (on)
+                                tma_box5(ring + st * Sh::kStage + lane * box_bytes, map, 0, 0, value ? 0 : part * Sh::kKChunks,
+                                         ((w.kvh << page_log2) + (from & (page - 1))) >> 3, g, full(st));
+                        }
+                    };
+                    int id = page_id(w.j0), id1 = page_id(w.j0 + 1);
+                    if (blocks > 0) ok = ok && warp_wait(q_empty, (blocks - 1) & 1);
+                    if (ok) {
+                        // lane: copy, chunk, row tile
+                        const int q = (lane / C) % Sh::kChunks, i = lane / (C * Sh::kChunks);
+                        if (lane == 0) mbar_expect(q_full, (uint32_t)args.tt * a.G * 128 * (RT * Sh::kChunks * C));
+                        __syncwarp();
+                        if (i < RT)
+                            tma_box5(qbase + (i * Sh::kChunks + q) * (kLanes * 128) + (lane % C) * (Sh::kRows * 128), &args.q_map, 0, q,
+                                     w.kvh * a.G, w.span.t0 + i * args.tt, s, q_full);
+                    }
+                    __syncwarp();
+                    ++blocks;
+                    // in the order in which the MMAs take them
+                    if (RT == 1) put(w.j0, id, false);
+#pragma unroll 1
+                    for (int j = w.j0; j < w.j1 && ok; ++j) {
+                        const int id2 = page_id(j + 2);
+                        if (RT == 2 || j + 1 < w.j1) put(RT == 2 ? j : j + 1, RT == 2 ? id : id1, false);
+                        put(j, id, true);
+                        id = id1;
+                        id1 = id2;
+                    }
+                    // two stages for the block's sums on their way out
+                    for (int p = 0; p < 2; ++p, ++r) {
+                        if (r >= Sh::kRing) ok = ok && warp_wait(empty(r % Sh::kRing), ((r / Sh::kRing) - 1) & 1);
+                        if (ok && lane == 0) mbar_arrive(full(r % Sh::kRing));
+                    }
+                } while (ok && w.next(a));
+                if (!ok)                          // the copies in flight land before the CTA ends
+                    for (uint32_t i = r > Sh::kRing ? r - Sh::kRing : 0; i < r; ++i) mbar_wait(full(i % Sh::kRing), (i / Sh::kRing) & 1);
+            } else if (wid == 4 * RT + 1) {
+                // ---- the MMAs
+                const bool leader = elect_one();  // one thread issues all of them, so that its commits cover them
+                uint32_t r = 0, u = 0;            // stages taken, units (S buffers filled) begun before this block
+                int blocks = 0;
+                // S buffer b: rows of row tile i
+                auto qk = [&](int i, int b, bool release) {
+#pragma unroll 1
+                    for (int p = 0; p < Sh::kKStages; ++p) {
+                        const uint32_t st = (r + p) % Sh::kRing;
+                        ok = ok && warp_wait(full(st), ((r + p) / Sh::kRing) & 1);
+                        fence_after();
+                        if (ok && leader) {
+                            const uint32_t kb = ring + st * Sh::kStage;
+#pragma unroll
+                            for (int k = 0; k < 4 * Sh::kKChunks; ++k)
+                                mma_ss(tmem + b * 128,
+                                       make_desc(qbase + (i * Sh::kChunks + p * Sh::kKChunks + k / 4) * (kLanes * 128) + (k & 3) * 32, 16, 1024),
+                                       make_desc(kb + (k / 4) * 1024 + (k & 3) * 32, 16, Sh::kKChunks * 1024), idesc(kTile, false),
+                                       p > 0 || k > 0);
+                            if (release) mma_commit(empty(st));
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && leader) mma_commit(s_full(b));
+                    __syncwarp();
+                };
+                auto pv = [&](int i, int b, uint32_t rv, bool fresh, bool release) {
+#pragma unroll 1
+                    for (int p = 0; p < Sh::kVStages; ++p) {
+                        const uint32_t st = (rv + p) % Sh::kRing;
+                        ok = ok && warp_wait(full(st), ((rv + p) / Sh::kRing) & 1);
+                        fence_after();
+                        if (ok && leader) {
+                            const uint32_t vb = ring + st * Sh::kStage;
+#pragma unroll
+                            for (int k = 0; k < Sh::kVTokens / 16; ++k)
+                                mma_ts(tmem + 256 + i * 128, tmem + b * 128 + (p * Sh::kVTokens / 16 + k) * 8,
+                                       make_desc(vb + k * 2 * Sh::kChunks * 1024, 1024, Sh::kChunks * 1024), idesc(D, true),
+                                       !fresh || p > 0 || k > 0);
+                            if (release) mma_commit(empty(st));
+                        }
+                        __syncwarp();
+                    }
+                    if (ok && leader) mma_commit(o_done(b));
+                    __syncwarp();
+                };
+                do {
+                    ok = ok && warp_wait(q_full, blocks & 1);
+                    const int n = w.j1 - w.j0;
+                    // Q is free for the next block once the last S is made
+                    auto q_done = [&](int t) {
+                        if (t == n - 1 && ok && leader) mma_commit(q_empty);
+                        __syncwarp();
+                    };
+                    if constexpr (RT == 1) {
+                        // unit u + t in buffer (u + t) & 1, free once the P V of two units before is done
+#pragma unroll 1
+                        for (int t = -1; t < n && ok; ++t) {
+                            if (t + 1 < n) {
+                                const uint32_t v = u + t + 1;
+                                if (v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
+                                qk(0, v & 1, true);
+                                r += Sh::kKStages;
+                                q_done(t + 1);
+                            }
+                            if (t >= 0) {
+                                const uint32_t v = u + t;
+                                ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
+                                if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
+                                pv(0, v & 1, r, t == 0, true);
+                                r += Sh::kVStages;
+                            }
+                        }
+                    } else {
+                        // each row tile has its own buffer, free once its P V is done
+#pragma unroll 1
+                        for (int t = 0; t <= n && ok; ++t) {
+                            const uint32_t v = u + t;
+                            // of tile t: K in stages r .., V of tile t - 1 in the stages before them
+                            const uint32_t rv = r - Sh::kVStages;
+#pragma unroll 1
+                            for (int i = 0; i < 2; ++i) {
+                                if (t > 0) {
+                                    ok = ok && warp_wait(p_full(i), (v - 1) & 1);
+                                    if (t == 1 && blocks > 0) ok = ok && warp_wait(o_free(i), (blocks - 1) & 1);
+                                    pv(i, i, rv, t == 1, i == 1);
+                                }
+                                if (t < n) {
+                                    if (v > 0) ok = ok && warp_wait(o_done(i), (v - 1) & 1);
+                                    qk(i, i, i == 1);
+                                    if (i == 1) q_done(t);
+                                }
+                            }
+                            if (t < n) r += Sh::kKStages + Sh::kVStages;
+                        }
+                    }
+                    u += n;
+                    r += 2;                       // those of the sums on their way out
+                    ++blocks;
+                } while (ok && w.next(a));
+            }
         }
     }
     if (!ok && lane == 0) report(a.d_status, GDN_ERR_TIMEOUT);
-    __syncwarp();
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (c == share.ctas - 1 || share.ctas == 0)
+        for (int s = tid; s < a.B; s += Sh::kThreads) {
+            int past;
+            if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
+        }
     fence_before();
     __syncthreads();
     fence_after();
     if (wid == 4 * RT + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }
 
-template <int D, int RT> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
-    using Sh = Shape<D, RT>;
+template <int D, int RT, int C> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
+    using Sh = Shape<D, RT, C>;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     const AttendArgs &a = t.a;
@@ -651,46 +754,54 @@ template <int D, int RT> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
     const cuuint32_t vbox[5] = {64, 8, D / 64, (cuuint32_t)(page < Sh::kVTokens ? page / 8 : Sh::kVTokens / 8), 1};
     if (!map(&t.k_map, a.kv.k, dims, strides, kbox) || !map(&t.v_map, a.kv.v, dims, strides, vbox)) return cudaErrorInvalidValue;
 
+    constexpr size_t smem = Sh::kQBytes + Sh::kRing * Sh::kStage + sizeof(Control<RT, Sh::kRing>);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     static PerContext<int> limits;
     unsigned long long ctx = 0;
     int set = 0;
     if (!current_context_id(&ctx) || !limits.get(ctx, &set)) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, RT, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (current_context_id(&ctx)) limits.put(ctx, 1);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.ctas), 1, 1);
     cfg.blockDim = dim3(Sh::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, RT>, t);
-    return e != cudaSuccess ? e : launch_join<__nv_bfloat16, D, kTile>(a, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, RT, C>, t);
+    return e != cudaSuccess ? e : launch_attend_join(a, GDN_BF16, stream);
 }
 
-// row tiles of a CTA: two where a slot's rows fill more than one and tensor memory holds both tiles' O
-int row_tiles(int T, int G, int D) { return D <= 128 && T > kRowTile / G ? 2 : 1; }
+// Row tiles of a CTA: two where a slot's rows fill more than one and tensor memory holds both tiles' O.
+int row_tiles(int T, int G, int D) { return D <= 128 && T > kLanes / G ? 2 : 1; }
+// Copies of the rows: four where a slot has at most 32.
+int copies(int T, int G) { return (long long)T * G <= 32 ? 4 : 1; }
+
+template <int D> cudaError_t launch_d(TcArgs &t, int rt, int c, cudaStream_t stream) {
+    if constexpr (D <= 128)
+        if (rt == 2) return launch<D, 2, 1>(t, stream);
+    return c == 4 ? launch<D, 1, 4>(t, stream) : launch<D, 1, 1>(t, stream);
+}
 
 }  // namespace
 
-int attend_bf16_block_rows(int T, int G, int D) { return row_tiles(T, G, D) * kRowTile; }
+AttendBlock attend_bf16_block(int T, int G, int D) {
+    const int rt = row_tiles(T, G, D), rows = kLanes / copies(T, G), tt = rows / G < T ? rows / G : T;
+    return {rt * rows, rt * tt};
+}
 
-cudaError_t launch_attend_bf16(const AttendArgs &args, int sm_count, cudaStream_t stream) {
+cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t stream) {
     TcArgs t{};
-    AttendArgs &a = t.a;
-    a = args;
-    const int rt = row_tiles(a.T, a.G, a.D);
-    t.tt = kRowTile / a.G < a.T ? kRowTile / a.G : a.T;
-    a.TB = rt * t.tt;
-    a.n_tb = (a.T + a.TB - 1) / a.TB;
-    a.ctas = sm_count < kAttendCtas ? sm_count : kAttendCtas;
-    if (rt == 2) return a.D == 64 ? launch<64, 2>(t, stream) : launch<128, 2>(t, stream);
-    return a.D == 64 ? launch<64, 1>(t, stream) : a.D == 128 ? launch<128, 1>(t, stream) : launch<256, 1>(t, stream);
+    t.a = a;
+    const int rt = row_tiles(a.T, a.G, a.D), c = copies(a.T, a.G);
+    t.tt = a.TB / rt;
+    return a.D == 64 ? launch_d<64>(t, rt, c, stream) : a.D == 128 ? launch_d<128>(t, rt, c, stream) : launch_d<256>(t, rt, c, stream);
 }
 
 }  // namespace gdn

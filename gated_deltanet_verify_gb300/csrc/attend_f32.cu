@@ -9,21 +9,19 @@
 // weighted sum of the values (a lane D / 32 columns of BM / 8 rows).  Tiles stream through two buffers of asynchronous
 // copies.  Positions that no row may see are filled with zeros, and the scores of those that a row may not see are
 // replaced, so what lies there does not matter.
-#include "attend_join.cuh"
+#include "attn.cuh"
 
 namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTile = 32;             // keys a tile: a lane each in the softmax
+constexpr int kTile = kTileF32;       // a lane each in the softmax
 constexpr unsigned kFull = 0xffffffffu;
 
-template <typename E> __device__ __forceinline__ float4 read4(const E *p);
-template <> __device__ __forceinline__ float4 read4<float>(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-template <> __device__ __forceinline__ float4 read4<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xffff0000u));
+__device__ __forceinline__ float4 read4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+template <int N> __device__ __forceinline__ void store_row(float *to, const float *x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[i] = x[i];
 }
 
 template <int D, int BM> struct Smem {
@@ -36,10 +34,10 @@ template <int D, int BM> struct Smem {
     int at[BM];                       // a row's token, -1: none
     int position[BM];                 // where a row's token is
     int parents[64], depth[64];
-    long long scratch[kThreads / 32 + 4];
+    int scratch[kThreads / 32 + 2];
 };
 
-template <typename E, int D, int BM>
+template <int D, int BM>
 __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     Smem<D, BM> &sm = *reinterpret_cast<Smem<D, BM> *>(raw);
@@ -52,8 +50,9 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
             int past;
             if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
         }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (c >= share.ctas) return;
-    long long left = share.start(c + 1) - share.start(c);
+    int left = share.start(c + 1) - share.start(c);
     const int page = 1 << a.kv.page_log2;
     const float scale2 = a.scale * 1.4426950408889634f;
 
@@ -64,11 +63,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
     bool first_block = true;
     int pair = at.pair;
     Span span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
-    int kvh = int(at.offset / span.n), j = int(at.offset % span.n);
+    int kvh = at.offset / span.n, j = at.offset % span.n;
     while (left > 0) {
         const int s = pair / a.n_tb;
         const int rows = (span.t1 - span.t0) * a.G;
-        const int j0 = j, j1 = int(min((long long)span.n, j0 + left));
+        const int j0 = j, j1 = min(span.n, j0 + left);
         const int32_t *table = a.kv.table + (size_t)s * a.kv.max_pages;
         const int sink = min(a.n_sink, span.lo);
 
@@ -86,20 +85,14 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
                 }
                 const long long off = (long long)(on ? id : 0) * a.kv.page_stride +
                                       ((size_t)kvh * page + (key & (page - 1))) * D + x;
-                const E *kp = static_cast<const E *>(a.kv.k) + off, *vp = static_cast<const E *>(a.kv.v) + off;
+                const float *kp = static_cast<const float *>(a.kv.k) + off, *vp = static_cast<const float *>(a.kv.v) + off;
                 float *ks = &sm.k[buf][r][x], *vs = &sm.v[buf][r][x];
-                if constexpr (sizeof(E) == 4) {
-                    const int bytes = on ? 16 : 0;               // of the 16 written, those that are read
-                    const void *kg = on ? (const void *)kp : a.kv.k, *vg = on ? (const void *)vp : a.kv.v;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                                     (uint32_t)__cvta_generic_to_shared(ks)), "l"(kg), "r"(bytes) : "memory");
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                                     (uint32_t)__cvta_generic_to_shared(vs)), "l"(vg), "r"(bytes) : "memory");
-                } else {
-                    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    *reinterpret_cast<float4 *>(ks) = on ? read4<E>(kp) : z;
-                    *reinterpret_cast<float4 *>(vs) = on ? read4<E>(vp) : z;
-                }
+                const int bytes = on ? 16 : 0;                   // of the 16 written, those that are read
+                const void *kg = on ? (const void *)kp : a.kv.k, *vg = on ? (const void *)vp : a.kv.v;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(ks)), "l"(kg), "r"(bytes) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(vs)), "l"(vg), "r"(bytes) : "memory");
             }
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         };
@@ -111,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
             const int r = i / (D / 4), x = (i % (D / 4)) * 4;
             float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows)
-                f = read4<E>(static_cast<const E *>(a.q) +
+                f = read4(static_cast<const float *>(a.q) +
                              (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D + x);
             *reinterpret_cast<float4 *>(&sm.q[r][x]) = f;
         }
@@ -241,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         }
         // ---- the block's sums: its output, or a part of it
         const bool whole = j0 == 0 && j1 == span.n;
-        const size_t part = size_t(2 * c + (first_block ? 0 : 1)) * (a.TB * a.G);
+        const size_t part = size_t(2 * c + (first_block ? 0 : 1)) * a.part_rows;
         constexpr int V = kCols < 4 ? kCols : 4;
 #pragma unroll
         for (int i = 0; i < kRowsW; ++i) {
@@ -249,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
             if (r >= rows) continue;
             const float l = sm.l[r];
             if (whole) {
-                E *out = static_cast<E *>(a.out) +
+                float *out = static_cast<float *>(a.out) +
                          (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D;
                 const float inv = 1.f / l;
 #pragma unroll
@@ -277,16 +270,15 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         }
     }
     asm volatile("cp.async.wait_all;\n" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
 
-template <typename E, int D, int BM> cudaError_t launch(AttendArgs a, cudaStream_t stream) {
+template <int D, int BM> cudaError_t launch(const AttendArgs &a, cudaStream_t stream) {
     const int smem = int(sizeof(Smem<D, BM>));
     static PerContext<int> limits;
     unsigned long long ctx = 0;
     int set = 0;
     if (!current_context_id(&ctx) || !limits.get(ctx, &set)) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<E, D, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (current_context_id(&ctx)) limits.put(ctx, 1);
     }
@@ -300,25 +292,26 @@ template <typename E, int D, int BM> cudaError_t launch(AttendArgs a, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<E, D, BM>, a);
-    return e != cudaSuccess ? e : launch_join<E, D, kTile>(a, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_kernel<D, BM>, a);
+    return e != cudaSuccess ? e : launch_attend_join(a, GDN_F32, stream);
 }
 
-template <typename E, int BM> cudaError_t launch_d(const AttendArgs &a, cudaStream_t stream) {
-    return a.D == 64 ? launch<E, 64, BM>(a, stream) : a.D == 128 ? launch<E, 128, BM>(a, stream) : launch<E, 256, BM>(a, stream);
+template <int BM> cudaError_t launch_d(const AttendArgs &a, cudaStream_t stream) {
+    return a.D == 64 ? launch<64, BM>(a, stream) : a.D == 128 ? launch<128, BM>(a, stream) : launch<256, BM>(a, stream);
 }
 
 }  // namespace
 
 // rows of a block: 16 where a slot has no more (a wider block would spend its time on rows that are not there), else 64
-int attend_f32_block_rows(int T, int G) { return (long long)T * G <= 16 ? 16 : 64; }
+static int block_rows(int T, int G) { return (long long)T * G <= 16 ? 16 : 64; }
 
-cudaError_t launch_attend_f32(AttendArgs a, int sm_count, cudaStream_t stream) {
-    const int rows = attend_f32_block_rows(a.T, a.G);
-    a.TB = rows / a.G < a.T ? rows / a.G : a.T;
-    a.n_tb = (a.T + a.TB - 1) / a.TB;
-    a.ctas = sm_count < kAttendCtas ? sm_count : kAttendCtas;
-    return rows == 16 ? launch_d<float, 16>(a, stream) : launch_d<float, 64>(a, stream);
+AttendBlock attend_f32_block(int T, int G) {
+    const int rows = block_rows(T, G);
+    return {rows, rows / G < T ? rows / G : T};
+}
+
+cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t stream) {
+    return block_rows(a.T, a.G) == 16 ? launch_d<16>(a, stream) : launch_d<64>(a, stream);
 }
 
 }  // namespace gdn

@@ -43,23 +43,33 @@ struct AttendArgs {
     int window, n_sink;
     int TB, n_tb;                     // tokens a block of rows takes (TB * G rows), blocks a slot
     int ctas;
-    float *partial;                   // [2 * ctas][TB * G][D]: unnormalised sums of split blocks
-    float2 *stats;                    // [2 * ctas][TB * G]: their maxima (in powers of two) and sums
+    int part_rows;                    // rows of a part in the workspace
+    float *partial;                   // [2 * ctas][part_rows][D]: unnormalised sums of split blocks
+    float2 *stats;                    // [2 * ctas][part_rows]: their maxima (in powers of two) and sums
     int *d_status;
 };
+
+constexpr int kTileF32 = 32, kTileBf16 = 128;   // keys a tile
 
 // What the workspace holds; rows: of a block, at most.
 constexpr int kAttendCtas = 152;      // CTAs of a launch, at most: one on every SM
 inline size_t attend_partial_bytes(int rows, int D) { return size_t(2) * kAttendCtas * rows * D * sizeof(float); }
 inline size_t attend_stats_bytes(int rows) { return size_t(2) * kAttendCtas * rows * sizeof(float2); }
 
+// How the rows of a slot and a kv head are cut up.
+struct AttendBlock {
+    int rows;                         // of a block, at most (what a part of the workspace holds)
+    int tokens;                       // that a block takes
+};
+AttendBlock attend_f32_block(int T, int G);
+AttendBlock attend_bf16_block(int T, int G, int D);
+
 // Return a cudaError_t of the launch (cudaSuccess when enqueued).
 cudaError_t launch_append(const AppendArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream);
-cudaError_t launch_attend_f32(AttendArgs a, int sm_count, cudaStream_t stream);
-cudaError_t launch_attend_bf16(const AttendArgs &a, int sm_count, cudaStream_t stream);
-// rows of a block at most, for the workspace
-int attend_f32_block_rows(int T, int G);
-int attend_bf16_block_rows(int T, int G, int D);
+cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t stream);
+cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t stream);
+// the rows of blocks that several CTAs shared, from their parts
+cudaError_t launch_attend_join(const AttendArgs &a, gdn_dtype dtype, cudaStream_t stream);
 
 #ifdef __CUDACC__
 
@@ -103,64 +113,115 @@ __device__ __forceinline__ Span block_span(const AttendArgs &a, int s, int tb) {
     return p;
 }
 
-// The whole work is a row of tiles: blocks of rows in the order (slot, token block), kv heads within one, key tiles
-// within one.  CTA c of n takes the tiles [start(c), start(c + 1)), so every SM has the same share whatever the
-// lengths; the block at either end of its share may be split with its neighbours, whose partial sums are joined later.
+// The whole work is a row of tiles (fewer than 2^31, as the host checks): blocks of rows in the order (slot, token block), kv
+// heads within one, key tiles within one.  Of n CTAs, CTA c takes the tiles [start(c), start(c + 1)), so every SM has the
+// same share whatever the lengths; the block at either end of its share may be split with its neighbours, whose partial
+// sums are joined later.
 struct Share {
-    long long total;
-    int ctas;
-    __device__ __forceinline__ long long start(int c) const { return total * c / ctas; }
+    int total, ctas, base, more;      // the first `more` CTAs take base + 1 tiles, the others base
+    __device__ __forceinline__ void set(int t, int n) {
+        total = t;
+        ctas = min(n, t);
+        base = ctas ? t / ctas : 0;
+        more = t - base * ctas;
+    }
+    __device__ __forceinline__ int start(int c) const { return base * c + min(c, more); }
     // the CTA that has this tile
-    __device__ __forceinline__ int owner(long long tile) const {
-        int c = int(min((long long)ctas - 1, tile * ctas / total));
-        while (c + 1 < ctas && start(c + 1) <= tile) ++c;
-        while (c > 0 && start(c) > tile) --c;
-        return c;
+    __device__ __forceinline__ int owner(int tile) const {
+        const int wide = (base + 1) * more;
+        return tile < wide ? tile / (base + 1) : more + (tile - wide) / base;
     }
 };
 
 // Where a tile lies: pair = slot * n_tb + token block, then tile `offset` of its Hk * n.
 struct Place {
-    int pair;
-    long long offset;
+    int pair, offset;
 };
 
-// Found by the whole CTA together (THREADS of them): the sum of all tiles, then the pair that tile `share.start(c)` is
-// in.  scratch: THREADS / 32 + 4 long longs of shared memory.
-template <int TK, int THREADS>
-__device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &share, long long *scratch) {
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, pairs = a.B * a.n_tb;
-    const int chunk = (pairs + THREADS - 1) / THREADS;
-    const int i0 = min(pairs, tid * chunk), i1 = min(pairs, i0 + chunk);
-    long long mine = 0;
-    for (int i = i0; i < i1; ++i) mine += block_span<TK>(a, i / a.n_tb, i % a.n_tb).n;
-    mine *= a.Hk;
-    long long upto = mine;
+// A warp finds its way by itself where there are at most kScanPairs pairs; more take the whole CTA.  (Rolled loops: a launch
+// starts with a cold instruction cache, and unrolled by 8 this took 4600 cycles for one pair.)
+constexpr int kScanPairs = 256;
+constexpr unsigned kWarp = 0xffffffffu;
+
+template <int TK> __device__ __forceinline__ int pair_tiles(const AttendArgs &a, int pair) {
+    return pair < a.B * a.n_tb ? block_span<TK>(a, pair / a.n_tb, pair % a.n_tb).n * a.Hk : 0;
+}
+__device__ __forceinline__ int scan_warp(int v) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += o;
+        const int o = __shfl_up_sync(kWarp, v, d);
+        if ((threadIdx.x & 31) >= d) v += o;
     }
+    return v;
+}
+template <int TK> __device__ __forceinline__ int scan_total(const AttendArgs &a) {
+    int sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < a.B * a.n_tb; i += 32) sum += pair_tiles<TK>(a, i + (threadIdx.x & 31));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kWarp, sum, d);
+    return sum;
+}
+// the pair that a tile (below the total) is in
+template <int TK> __device__ __forceinline__ Place scan_find(const AttendArgs &a, int tile) {
+    int before = 0, i = 0;
+#pragma unroll 1
+    for (;; i += 32) {
+        const int n = pair_tiles<TK>(a, i + (threadIdx.x & 31)), upto = before + scan_warp(n);
+        const unsigned past = __ballot_sync(kWarp, upto > tile);
+        if (past || i + 32 >= a.B * a.n_tb) {
+            const int l = past ? __ffs(past) - 1 : 0;
+            return Place{i + l, tile - __shfl_sync(kWarp, upto - n, l)};
+        }
+        before = __shfl_sync(kWarp, upto, 31);
+    }
+}
+// the first tile of a pair
+template <int TK> __device__ __forceinline__ int scan_begin(const AttendArgs &a, int pair) {
+    int before = 0;
+#pragma unroll 1
+    for (int i = 0; i < pair; i += 32) {
+        const int at = i + (threadIdx.x & 31);
+        before += at < pair ? pair_tiles<TK>(a, at) : 0;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) before += __shfl_xor_sync(kWarp, before, d);
+    return before;
+}
+
+// The sum of all tiles, then the pair that tile `share.start(c)` is in; called by the whole CTA (THREADS of them).
+// scratch: THREADS / 32 + 2 words of shared memory.
+template <int TK, int THREADS>
+__device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &share, int *scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, pairs = a.B * a.n_tb;
+    if (pairs <= kScanPairs) {
+        share.set(scan_total<TK>(a), a.ctas);
+        return c < share.ctas ? scan_find<TK>(a, share.start(c)) : Place{0, 0};
+    }
+    const int chunk = (pairs + THREADS - 1) / THREADS;
+    const int i0 = min(pairs, tid * chunk), i1 = min(pairs, i0 + chunk);
+    int mine = 0;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) mine += pair_tiles<TK>(a, i);
+    const int upto = scan_warp(mine);
     if (lane == 31) scratch[wid] = upto;
     __syncthreads();
-    long long before = 0, total = 0;
+    int before = upto - mine, total = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
-        const long long v = scratch[w];
+        const int v = scratch[w];
         before += w < wid ? v : 0;
         total += v;
     }
-    share.total = total;
-    share.ctas = int(min((long long)a.ctas, total));
-    long long *found = scratch + THREADS / 32;
-    if (total > 0 && c < share.ctas) {
-        const long long target = share.start(c);
-        before += upto - mine;
-        if (mine > 0 && target >= before && target < before + mine) {
-            long long at = target - before;
+    share.set(total, a.ctas);
+    int *found = scratch + THREADS / 32;
+    if (c < share.ctas) {
+        int at = share.start(c) - before;
+        if (at >= 0 && at < mine) {
             int i = i0;
+#pragma unroll 1
             for (;; ++i) {
-                const long long n = (long long)block_span<TK>(a, i / a.n_tb, i % a.n_tb).n * a.Hk;
-                if (at < n) break;
+                const int n = pair_tiles<TK>(a, i);
+                if (at < n || i + 1 == i1) break;
                 at -= n;
             }
             found[0] = i;
@@ -168,7 +229,7 @@ __device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &s
         }
     }
     __syncthreads();
-    return Place{int(found[0]), found[1]};
+    return Place{found[0], found[1]};
 }
 
 #endif  // __CUDACC__

@@ -870,15 +870,23 @@ gdn::KvPages kv_pages(const gdn_attn_dims &d, const gdn_kv_cache &c) {
     return {c.k, c.v, c.page_table, c.past, d.page_stride, d.n_pages, d.max_pages, log2};
 }
 
-// rows of a block of the work, at most
-int attend_rows(const gdn_attn_dims &d) {
+gdn::AttendBlock attend_block(const gdn_attn_dims &d) {
     const int G = d.n_heads / d.n_kv_heads;
-    return d.dtype == GDN_F32 ? gdn::attend_f32_block_rows(d.n_tokens, G) : gdn::attend_bf16_block_rows(d.n_tokens, G, d.d_head);
+    return d.dtype == GDN_F32 ? gdn::attend_f32_block(d.n_tokens, G) : gdn::attend_bf16_block(d.n_tokens, G, d.d_head);
 }
 
 size_t attend_workspace(const gdn_attn_dims &d) {
-    const int rows = attend_rows(d);
+    const int rows = attend_block(d).rows;
     return gdn::attend_partial_bytes(rows, d.d_head) + gdn::attend_stats_bytes(rows);
+}
+
+// key tiles of all blocks of rows, at most
+int check_attend_work(const gdn_attn_dims &d) {
+    const long long tb = attend_block(d).tokens, tile = d.dtype == GDN_F32 ? gdn::kTileF32 : gdn::kTileBf16;
+    const long long blocks = (d.n_tokens + tb - 1) / tb * d.n_slots, tiles = ((long long)d.max_pages * d.page_tokens + tile - 1) / tile;
+    if ((double)blocks * d.n_kv_heads * (double)tiles >= 2147483648.0)
+        return fail(GDN_ERR_SHAPE, "%lld blocks of rows x %d kv heads x %lld key tiles are 2^31 or more", blocks, d.n_kv_heads, tiles);
+    return GDN_OK;
 }
 
 }  // namespace
@@ -924,13 +932,14 @@ int gdn_kv_append(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gd
 
 size_t gdn_attend_workspace_bytes(const gdn_attn_dims *dims) {
     g_err.clear();
-    return check_attn_dims(dims) ? 0 : attend_workspace(*dims);
+    return check_attn_dims(dims) || check_attend_work(*dims) ? 0 : attend_workspace(*dims);
 }
 
 int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_attn_params *params, const void *q, void *out,
                const int32_t *d_length, const int32_t *d_parent, void *workspace, size_t ws_bytes, int *d_status, void *stream) {
     g_err.clear();
     int rc = check_attn_dims(dims);
+    if (!rc) rc = check_attend_work(*dims);
     if (!rc) rc = check_kv_cache(cache);
     if (rc) return rc;
     if (!params) return fail(GDN_ERR_ARG, "params is NULL");
@@ -953,11 +962,16 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     a.kv = kv_pages(d, *cache);
     a.q = q; a.out = out; a.length = d_length; a.parent = d_parent; a.scale = params->scale;
     a.window = params->window; a.n_sink = params->window ? params->n_sink : 0; a.d_status = d_status;
-    a.partial = static_cast<float *>(workspace);
-    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(attend_rows(d), a.D));
+    const gdn::AttendBlock block = attend_block(d);
+    a.part_rows = block.rows;
+    a.TB = block.tokens;
+    a.n_tb = (a.T + a.TB - 1) / a.TB;
     const int sms = dev_info().sms;
-    const cudaError_t e = d.dtype == GDN_F32 ? gdn::launch_attend_f32(a, sms, static_cast<cudaStream_t>(stream))
-                                             : gdn::launch_attend_bf16(a, sms, static_cast<cudaStream_t>(stream));
+    a.ctas = sms < gdn::kAttendCtas ? sms : gdn::kAttendCtas;
+    a.partial = static_cast<float *>(workspace);
+    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(a.part_rows, a.D));
+    const cudaError_t e = d.dtype == GDN_F32 ? gdn::launch_attend_f32(a, static_cast<cudaStream_t>(stream))
+                                             : gdn::launch_attend_bf16(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "attention launch failed: %s", cudaGetErrorString(e));
     return GDN_OK;
 }

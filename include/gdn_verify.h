@@ -578,6 +578,9 @@ size_t gdn_attend_workspace_bytes(const gdn_attn_dims *dims);
  * do not overlap.  workspace: gdn_attend_workspace_bytes, 256-byte aligned; it
  * needs no initialisation, and calls that share it must be ordered.  The sums'
  * order, so the last bits of a row, depends on the lengths of the whole batch.
+ * Limit: the slots' blocks of rows (a block: 128 rows of a kv head's queries at
+ * the least, 16 in f32) times n_kv_heads times the key tiles of max_pages pages
+ * (128 positions, 32 in f32) below 2^31 (GDN_ERR_SHAPE).
  */
 int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_attn_params *params,
                const void *q, void *out, const int32_t *d_length, const int32_t *d_parent,
