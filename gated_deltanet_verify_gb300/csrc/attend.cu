@@ -44,7 +44,9 @@ template <int D, int RT, int C> struct Shape {
     static constexpr int kKStages = kChunks / kKChunks;
     static constexpr int kVTokens = kStage / (2 * D);              // of V in a stage: kVTokens keys x D
     static constexpr int kVStages = kTile / kVTokens;
-    static constexpr int kQBytes = RT * kLanes * D * 2;
+    static constexpr int kQTile = RT * kLanes * D * 2;
+    static constexpr int kQBuffers = RT == 1 && D == 64 ? 2 : 1;   // where there is room, the next block's Q comes early
+    static constexpr int kQBytes = kQBuffers * kQTile;
     static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
     static constexpr int kThreads = RT == 1 ? 192 : 384;
     static constexpr int kRows = kLanes / C;                       // of a row tile
@@ -58,7 +60,7 @@ template <int D, int RT, int C> struct Shape {
 // What a CTA keeps beside its tiles, behind them.
 template <int RT, int RING> struct Control {
     uint64_t full[RING], empty[RING];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2];    // S is there; P is there
     uint64_t o_done[2];               // P V is done: O is whole so far, the buffer free
     uint64_t o_free[2];               // a row tile's O has been read out
@@ -190,25 +192,55 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // bits [0, n) of a word, n any int
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
+// A place in the ring of N stages: the stage, and how often the ring has gone round.
+template <int N> struct Ring {
+    uint32_t stage = 0, round = 0;
+    __device__ __forceinline__ void next(int n = 1) {
+        stage += n;
+        if (stage >= N) {
+            stage -= N;
+            ++round;
+        }
+    }
+    __device__ __forceinline__ Ring after(int n) const {
+        Ring x = *this;
+        x.next(n);
+        return x;
+    }
+};
+
 // A CTA's blocks of rows, one after the other: each role walks them by itself.
 struct Walk {
     int left, pair, kvh, j0, j1;
     Span span;
     bool first, whole;
-    __device__ __forceinline__ Walk(const AttendArgs &a, const Place &at, int tiles) : left(tiles), pair(at.pair), first(true) {
-        span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
-        kvh = at.offset / span.n;
-        j0 = at.offset % span.n;
-        cut();
+    // a block of one tile, of no slot
+    __device__ __forceinline__ void none() {
+        span = Span{0, 0, 1 << 20, 0, kTile, 0, 0, 1};
+        left = j1 = 1;
+        pair = kvh = j0 = 0;
+        first = whole = true;
     }
-    __device__ __forceinline__ void cut() {
-        j1 = min(span.n, j0 + left);
+    // the first block with tiles of a share of `tiles` tiles; false if there is none
+    __device__ __forceinline__ bool begin(const AttendArgs &a, const Place &at, int tiles) {
+        left = tiles;
+        pair = at.pair;
+        first = true;
+        span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
+        kvh = at.offset / (span.n + a.pad);
+        return cut(a, at.offset % (span.n + a.pad));
+    }
+    // from the block's tile `from`, the first a.pad of which are not there
+    __device__ __forceinline__ bool cut(const AttendArgs &a, int from) {
+        const int to = min(span.n + a.pad, from + left);
+        left -= to - from;
+        j0 = max(0, from - a.pad);
+        j1 = max(0, to - a.pad);
         whole = j0 == 0 && j1 == span.n;
+        return j1 > j0;
     }
     __device__ __forceinline__ bool next(const AttendArgs &a) {
-        left -= j1 - j0;
         first = false;
-        j0 = 0;
         if (left <= 0) return false;
         if (++kvh == a.Hk) {
             kvh = 0;
@@ -217,8 +249,7 @@ struct Walk {
                 span = block_span<kTile>(a, pair / a.n_tb, pair % a.n_tb);
             } while (span.n == 0);
         }
-        cut();
-        return true;
+        return cut(a, 0);
     }
 };
 
@@ -233,7 +264,8 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
     const uint32_t qbase = smem_u32(sm), ring = qbase + Sh::kQBytes;
     auto full = [&](uint32_t s) { return smem_u32(&ctl.full[s]); };
     auto empty = [&](uint32_t s) { return smem_u32(&ctl.empty[s]); };
-    const uint32_t q_full = smem_u32(&ctl.q_full), q_empty = smem_u32(&ctl.q_empty);
+    auto q_full = [&](int b) { return smem_u32(&ctl.q_full[b]); };
+    auto q_empty = [&](int b) { return smem_u32(&ctl.q_empty[b]); };
     auto s_full = [&](int b) { return smem_u32(&ctl.s_full[b]); };
     auto p_full = [&](int b) { return smem_u32(&ctl.p_full[b]); };
     auto o_done = [&](int b) { return smem_u32(&ctl.o_done[b]); };
@@ -252,22 +284,34 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
             mbar_init(p_full(lane), 128);
             mbar_init(o_done(lane), 1);
             mbar_init(o_free(lane), 128);
-            mbar_init(lane ? q_full : q_empty, 1);
+            mbar_init(q_full(lane), 1);
+            mbar_init(q_empty(lane), 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane < 3) prefetch_map(lane == 0 ? &args.q_map : lane == 1 ? &args.k_map : &args.v_map);
     }
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    Share share;
-    const Place at = find_place<kTile, Sh::kThreads>(a, c, share, ctl.scratch);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = ctl.tmem;
     bool ok = true;
-    if (c < share.ctas) {
-        Walk w(a, at, share.start(c + 1) - share.start(c));
+    // What comes before the wait for the kernel ahead runs beside its end: for the softmax warps a dry pass through their
+    // loop.  (Where the whole CTA looks for its work together there is none.)
+    const bool together = a.B * a.n_tb > kScanPairs;
+    Share share;
+    Place at{0, 0};
+    auto begin = [&] {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+        if (together) return;
+        share.set(scan_total<kTile>(a), a);
+        if (c < share.ctas) at = scan_find<kTile>(a, share.start(c));
+    };
+    if (together) {
+        begin();
+        at = find_place<kTile, Sh::kThreads>(a, c, share, ctl.scratch);
+    }
+    {
         // With two row tiles 384 threads start with 168 registers each, and the softmax warps take what the others do not need
         // (216 x 256 + 72 x 128 = 168 x 384).
         if (wid < 4 * RT) {
@@ -278,17 +322,25 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
             const bool negative = a.scale < 0.f;
             // a scale of zero leaves all weights alike, and masked ones at none
             const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-            uint32_t u = 0, r = 0;                // S buffers taken, stages passed before this block
+            uint32_t u = 0;                       // S buffers taken before this block
+            Ring<Sh::kRing> r;                    // the first stage of this tile
             int last_pair = -1;
             unsigned long long line = 0;          // a tree's nodes that this row sees
             int position = 0;
+            Walk w;
+            // A launch starts with a cold instruction cache: the first pass through this loop takes 4000 cycles and more where
+            // the next ones take 1400.  So it is a dry one, on a block of one tile that is not there, over whatever tensor
+            // memory holds; it writes into O, which the first P V overwrites.
+            bool dry = !together;
+            if (dry) w.none();
+            if (dry || (c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c))))
             do {
                 const int s = w.pair / a.n_tb, past = w.span.past, n = w.j1 - w.j0;
                 const int first_t = w.span.t0 + i * args.tt, last_t = min(w.span.t1, first_t + args.tt) - 1;
                 const int t = row < args.tt * a.G ? first_t + row / a.G : w.span.t1;
                 const bool on = t < w.span.t1;
                 const bool busy = __any_sync(kWarp, on);
-                if (w.pair != last_pair) {
+                if (w.pair != last_pair && !dry) {
                     last_pair = w.pair;
                     position = past + t;
                     if (a.parent) {
@@ -323,14 +375,10 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                 const int low = a.window ? position - a.window + 1 : 0;
                 const int sink = min(a.n_sink, w.span.lo);
                 float m = -INFINITY, l = 0.f;
-                // Before the first tile comes a dry pass on whatever tensor memory holds, while the first keys are on their way:
-                // a launch starts with a cold instruction cache, and the first pass takes 4000 cycles where the next ones take
-                // 1400.  It writes into O, which the first P V overwrites.
-                for (int q = w.first ? -1 : 0; q < n; ++q) {
-                    const bool dry = q < 0;
+                for (int q = 0; q < n; ++q) {
                     const uint32_t v = u + q;
                     const int b = RT == 1 ? (v & 1) : i;
-                    const int k0 = dry ? w.span.lo : w.span.tile(w.j0 + q) * kTile, mine0 = k0 + copy * Sh::kKeys;
+                    const int k0 = w.span.tile(w.j0 + q) * kTile, mine0 = k0 + copy * Sh::kKeys;
                     if (!dry) ok = ok && warp_wait(s_full(b), RT == 1 ? (v >> 1) & 1 : v & 1);
                     if (!ok) break;
                     fence_after();
@@ -379,7 +427,7 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         for (int e = 0; e < Sh::kKeys; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
                         const float to = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         const bool grows = on && (to - m) * sc > kSlack;
-                        if (q <= 0) {
+                        if (q == 0) {
                             m = fmaxf(m, to);
                         } else if (__any_sync(kWarp, grows)) {
                             const float up = fmaxf(m, to), f = m == up ? 1.f : ex2((m - up) * sc);
@@ -415,33 +463,38 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                         wait_st();
                     }
-                    if (dry) {
-                        m = -INFINITY;
-                        l = 0.f;
-                        continue;
-                    }
+                    if (dry) break;
                     // ---- rows of V that no row of the block sees
                     if (k0 + kTile > w.span.hi || (k0 < w.span.lo && k0 + kTile > sink)) {
                         const int key = k0 + tl, part = tl / Sh::kVTokens, g = tl % Sh::kVTokens;
                         // after the P V of the tile before, whose stages come ahead of this one's in the ring
                         if (v > 0) ok = ok && wait_o();
-                        const uint32_t rv = r + ((RT == 2 || q == 0) + (RT == 1 && q + 1 < n)) * Sh::kKStages + part;
-                        ok = ok && warp_wait(full(rv % Sh::kRing), (rv / Sh::kRing) & 1);
+                        const Ring<Sh::kRing> rv = r.after(((RT == 2 || q == 0) + (RT == 1 && q + 1 < n)) * Sh::kKStages + part);
+                        ok = ok && warp_wait(full(rv.stage), rv.round & 1);
                         if (ok && !(key < w.span.hi && (key >= w.span.lo || key < sink))) {
-                            const uint32_t to = ring + (rv % Sh::kRing) * Sh::kStage + (g >> 3) * (Sh::kChunks * 1024) + (g & 7) * 128;
+                            const uint32_t to = ring + rv.stage * Sh::kStage + (g >> 3) * (Sh::kChunks * 1024) + (g & 7) * 128;
 #pragma unroll 1
                             for (int e = 0; e < Sh::kChunks; ++e)
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to + e * 1024 + k * 16), "r"(0) : "memory");
+                                for (int k = 0; k < 8; ++k)       // (turned, so that lanes do not meet in a bank)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to + e * 1024 + ((k + g) & 7) * 16), "r"(0)
+                                                 : "memory");
                         }
                         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     }
                     // what the ring has moved on by, with this tile's V: K before V, and with one row tile the next tile's K too
-                    if constexpr (RT == 1) r += (q == 0 ? Sh::kKStages : 0) + (q + 1 < n ? Sh::kKStages : 0) + Sh::kVStages;
-                    else r += Sh::kKStages + Sh::kVStages;
+                    if (RT == 2 || q == 0) r.next(Sh::kKStages);
+                    if (RT == 1 && q + 1 < n) r.next(Sh::kKStages);
+                    r.next(Sh::kVStages);
                     fence_before();
                     mbar_arrive(p_full(b));
+                }
+                if (dry) {
+                    dry = false;
+                    begin();
+                    if (c >= share.ctas || !w.begin(a, at, share.start(c + 1) - share.start(c))) break;
+                    last_pair = -1;
+                    continue;
                 }
                 u += n;
                 // ---- the block's sums: its output, or a part of it
@@ -471,38 +524,40 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                 }
                 fence_after();
                 // Rows go through the two stages, each turned by its number of 16 bytes (so that 32 lanes write 32 rows
-                // without conflicts), and leave side by side.  (Written by its own lane, 16 bytes a row at a time, 96 rows of
-                // 256 took 7400 cycles; as two bulk copies a row, 11500.)
+                // without conflicts), and leave side by side, four 16-byte pieces a thread in flight.  (Written by its own
+                // lane, 16 bytes a row at a time, 96 rows of 256 took 7400 cycles; as two bulk copies a row, 11500.)
                 constexpr int kStagesRt = 2 / RT, kLanesStage = kLanes / kStagesRt;
-                constexpr int kCols = Sh::kOut / 4 < D ? Sh::kOut / 4 : D, kPieces = kCols / 4;
-                auto out_row = [&](int lane_row) {
-                    const uint32_t st = (r + (RT == 1 ? lane_row / kLanesStage : i)) % Sh::kRing;
-                    return ring + st * Sh::kStage + (lane_row % kLanesStage) * Sh::kOut;
-                };
+                constexpr int kCols = Sh::kOut / 4 < D ? Sh::kOut / 4 : D, kPieces = kCols / 4, kStep = 128 / kPieces;
+                unsigned char *stage[kStagesRt];
 #pragma unroll
                 for (int p = 0; p < kStagesRt; ++p) {
-                    const uint32_t st = r + (RT == 1 ? p : i);
-                    ok = ok && warp_wait(full(st % Sh::kRing), (st / Sh::kRing) & 1);
+                    const Ring<Sh::kRing> st = r.after(RT == 1 ? p : i);
+                    ok = ok && warp_wait(full(st.stage), st.round & 1);
+                    stage[p] = sm + Sh::kQBytes + st.stage * Sh::kStage;
                 }
+                // row `from` of tensor memory, its 16-byte piece p
+                auto spot = [&](int from, int p) {
+                    unsigned char *at_stage = RT == 2 || from < kLanesStage ? stage[0] : stage[kStagesRt - 1];
+                    return reinterpret_cast<float4 *>(at_stage + (from & (kLanesStage - 1)) * Sh::kOut + ((p + from) & (kPieces - 1)) * 16);
+                };
                 const int rows = ok ? max(0, last_t + 1 - first_t) * a.G : 0;      // as in every warp, unless a wait gave up
+                const int piece = tl % kPieces, row0 = tl / kPieces;
+                unsigned char *out0 = w.whole ? reinterpret_cast<unsigned char *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                    (((size_t)s * a.T + first_t) * a.H + (size_t)w.kvh * a.G) * D + 4 * piece)
+                                              : reinterpret_cast<unsigned char *>(a.partial + (part0 + row0) * D + 4 * piece);
 #pragma unroll 1
                 for (int at0 = 0; at0 < D; at0 += kCols) {
                     if (at0 > 0) asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
                     if (ok && busy) {
-                        const uint32_t mine = out_row(tl);
 #pragma unroll 1
                         for (int e = 0; e < kCols; e += 32) {
                             uint32_t o[32];
                             tmem_ld32(o_at + at0 + e, o);
                             wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int spot = (e / 4 + k + lane) & (kPieces - 1);
-                                asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(mine + spot * 16),
-                                             "f"(__uint_as_float(o[4 * k]) * factor), "f"(__uint_as_float(o[4 * k + 1]) * factor),
-                                             "f"(__uint_as_float(o[4 * k + 2]) * factor), "f"(__uint_as_float(o[4 * k + 3]) * factor)
-                                             : "memory");
-                            }
+                            for (int k = 0; k < 8; ++k)
+                                *spot(tl, e / 4 + k) = make_float4(__uint_as_float(o[4 * k]) * factor, __uint_as_float(o[4 * k + 1]) * factor,
+                                                                  __uint_as_float(o[4 * k + 2]) * factor, __uint_as_float(o[4 * k + 3]) * factor);
                         }
                     }
                     if (at0 + kCols == D) {
@@ -510,40 +565,53 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         mbar_arrive(o_free(i));
                     }
                     asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
-#pragma unroll 2
-                    for (int x = tl; x < rows * kPieces; x += 128) {
-                        const int rr = x / kPieces, piece = x % kPieces;
-                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int x = row0; x < rows; x += 4 * kStep) {
+                        float4 y[4];
 #pragma unroll
-                        for (int e = 0; e < C; ++e) {
-                            const int from = e * Sh::kRows + rr;
-                            float z[4];
-                            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
-                                         : "=f"(z[0]), "=f"(z[1]), "=f"(z[2]), "=f"(z[3])
-                                         : "r"(out_row(from) + ((piece + from) & (kPieces - 1)) * 16));
+                        for (int k = 0; k < 4; ++k) {
+                            const int rr = min(x + k * kStep, rows - 1);
+                            y[k] = *spot(rr, piece);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) y[k] += z[k];
+                            for (int e = 1; e < C; ++e) {
+                                const float4 z = *spot(e * Sh::kRows + rr, piece);
+                                y[k].x += z.x; y[k].y += z.y; y[k].z += z.z; y[k].w += z.w;
+                            }
                         }
-                        if (w.whole) {
-                            const size_t to = (((size_t)s * a.T + first_t + rr / a.G) * a.H + (size_t)w.kvh * a.G + rr % a.G) * D;
-                            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + to + at0 + 4 * piece) =
-                                make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
-                        } else {
-                            *reinterpret_cast<float4 *>(a.partial + (part0 + rr) * D + at0 + 4 * piece) = make_float4(y[0], y[1], y[2], y[3]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int rr = x + k * kStep;
+                            if (rr >= rows) break;
+                            if (w.whole) {
+                                const int tt = rr / a.G;
+                                *reinterpret_cast<uint2 *>(out0 + (((size_t)tt * a.H + rr - tt * a.G) * D + at0) * 2) =
+                                    make_uint2(pack_bf16(y[k].x, y[k].y), pack_bf16(y[k].z, y[k].w));
+                            } else {
+                                *reinterpret_cast<float4 *>(out0 + ((rr - row0) * D + at0) * 4) = y[k];
+                            }
                         }
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
-                if (tl < kStagesRt) mbar_arrive(empty((r + (RT == 1 ? tl : i)) % Sh::kRing));
-                r += 2;
-            } while (ok && w.next(a));
+                if (tl < kStagesRt) mbar_arrive(empty(r.after(RT == 1 ? tl : i).stage));
+                r.next(2);
+                if (!ok || !w.next(a)) break;
+            } while (true);
         } else {
+            if (!together) begin();
+            Walk w;
+            const bool some = c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c));
             if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
-            if (wid == 4 * RT) {
+            if (!some) {
+                // nothing to do: fewer tiles than CTAs
+            } else if (wid == 4 * RT) {
                 // ---- the loads
                 const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
-                uint32_t r = 0;                   // stages filled
+                Ring<Sh::kRing> r;                // the next stage to fill
+                auto free_stage = [&] {
+                    if (r.round > 0) ok = ok && warp_wait(empty(r.stage), (r.round - 1) & 1);
+                };
                 int blocks = 0;
                 do {
                     const int s = w.pair / a.n_tb, sink = min(a.n_sink, w.span.lo), lo = w.span.lo, hi = w.span.hi;
@@ -562,9 +630,9 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         const uint32_t box_bytes = (uint32_t)box * (value ? D : 64 * Sh::kKChunks) * 2;
                         const int tile0 = w.span.tile(j) * kTile;
 #pragma unroll 1
-                        for (int part = 0; part < stages; ++part, ++r) {
-                            const uint32_t st = r % Sh::kRing;
-                            if (r >= Sh::kRing) ok = ok && warp_wait(empty(st), ((r / Sh::kRing) - 1) & 1);
+                        for (int part = 0; part < stages; ++part, r.next()) {
+                            const uint32_t st = r.stage;
+                            free_stage();
                             if (!ok) return;
                             const int from = tile0 + (value ? part * Sh::kVTokens : 0) + lane * box, to = from + box;
                             const bool on = lane < tokens / box && ((from < hi && to > lo) || from < sink);
@@ -582,15 +650,16 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         }
                     };
                     int id = page_id(w.j0), id1 = page_id(w.j0 + 1);
-                    if (blocks > 0) ok = ok && warp_wait(q_empty, (blocks - 1) & 1);
+                    const int qb = blocks % Sh::kQBuffers, uses = blocks / Sh::kQBuffers;
+                    if (uses > 0) ok = ok && warp_wait(q_empty(qb), (uses - 1) & 1);
                     if (ok) {
                         // lane: copy, chunk, row tile
                         const int q = (lane / C) % Sh::kChunks, i = lane / (C * Sh::kChunks);
-                        if (lane == 0) mbar_expect(q_full, (uint32_t)args.tt * a.G * 128 * (RT * Sh::kChunks * C));
+                        if (lane == 0) mbar_expect(q_full(qb), (uint32_t)args.tt * a.G * 128 * (RT * Sh::kChunks * C));
                         __syncwarp();
                         if (i < RT)
-                            tma_box5(qbase + (i * Sh::kChunks + q) * (kLanes * 128) + (lane % C) * (Sh::kRows * 128), &args.q_map, 0, q,
-                                     w.kvh * a.G, w.span.t0 + i * args.tt, s, q_full);
+                            tma_box5(qbase + qb * Sh::kQTile + (i * Sh::kChunks + q) * (kLanes * 128) + (lane % C) * (Sh::kRows * 128), &args.q_map, 0, q,
+                                     w.kvh * a.G, w.span.t0 + i * args.tt, s, q_full(qb));
                     }
                     __syncwarp();
                     ++blocks;
@@ -605,66 +674,65 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         id1 = id2;
                     }
                     // two stages for the block's sums on their way out
-                    for (int p = 0; p < 2; ++p, ++r) {
-                        if (r >= Sh::kRing) ok = ok && warp_wait(empty(r % Sh::kRing), ((r / Sh::kRing) - 1) & 1);
-                        if (ok && lane == 0) mbar_arrive(full(r % Sh::kRing));
+                    for (int p = 0; p < 2 && ok; ++p, r.next()) {
+                        free_stage();
+                        if (ok && lane == 0) mbar_arrive(full(r.stage));
                     }
                 } while (ok && w.next(a));
                 if (!ok)                          // the copies in flight land before the CTA ends
-                    for (uint32_t i = r > Sh::kRing ? r - Sh::kRing : 0; i < r; ++i) mbar_wait(full(i % Sh::kRing), (i / Sh::kRing) & 1);
+                    for (int i = 0; i < Sh::kRing; ++i) {
+                        const uint32_t fills = r.round + (i < (int)r.stage);      // of stage i
+                        if (fills > 0) mbar_wait(full(i), (fills - 1) & 1);
+                    }
             } else if (wid == 4 * RT + 1) {
                 // ---- the MMAs
                 const bool leader = elect_one();  // one thread issues all of them, so that its commits cover them
-                uint32_t r = 0, u = 0;            // stages taken, units (S buffers filled) begun before this block
+                Ring<Sh::kRing> r;                // the next stage to take
+                uint32_t u = 0;                   // S buffers filled before this block
                 int blocks = 0;
                 // S buffer b: rows of row tile i
                 auto qk = [&](int i, int b, bool release) {
-#pragma unroll 1
-                    for (int p = 0; p < Sh::kKStages; ++p) {
-                        const uint32_t st = (r + p) % Sh::kRing;
-                        ok = ok && warp_wait(full(st), ((r + p) / Sh::kRing) & 1);
+                    Ring<Sh::kRing> x = r;
+#pragma unroll
+                    for (int p = 0; p < Sh::kKStages; ++p, x.next()) {
+                        ok = ok && warp_wait(full(x.stage), x.round & 1);
                         fence_after();
                         if (ok && leader) {
-                            const uint32_t kb = ring + st * Sh::kStage;
+                            const uint64_t qd = make_desc(qbase + (blocks % Sh::kQBuffers) * Sh::kQTile + (i * Sh::kChunks + p * Sh::kKChunks) * (kLanes * 128), 16, 1024);
+                            const uint64_t kd = make_desc(ring + x.stage * Sh::kStage, 16, Sh::kKChunks * 1024);
 #pragma unroll
                             for (int k = 0; k < 4 * Sh::kKChunks; ++k)
-                                mma_ss(tmem + b * 128,
-                                       make_desc(qbase + (i * Sh::kChunks + p * Sh::kKChunks + k / 4) * (kLanes * 128) + (k & 3) * 32, 16, 1024),
-                                       make_desc(kb + (k / 4) * 1024 + (k & 3) * 32, 16, Sh::kKChunks * 1024), idesc(kTile, false),
-                                       p > 0 || k > 0);
-                            if (release) mma_commit(empty(st));
+                                mma_ss(tmem + b * 128, qd + ((k / 4) * (kLanes * 128) + (k & 3) * 32) / 16, kd + ((k / 4) * 1024 + (k & 3) * 32) / 16,
+                                       idesc(kTile, false), p > 0 || k > 0);
+                            if (release) mma_commit(empty(x.stage));
+                            if (p + 1 == Sh::kKStages) mma_commit(s_full(b));
                         }
                         __syncwarp();
                     }
-                    if (ok && leader) mma_commit(s_full(b));
-                    __syncwarp();
                 };
-                auto pv = [&](int i, int b, uint32_t rv, bool fresh, bool release) {
-#pragma unroll 1
-                    for (int p = 0; p < Sh::kVStages; ++p) {
-                        const uint32_t st = (rv + p) % Sh::kRing;
-                        ok = ok && warp_wait(full(st), ((rv + p) / Sh::kRing) & 1);
+                auto pv = [&](int i, int b, Ring<Sh::kRing> x, bool fresh, bool release) {
+#pragma unroll
+                    for (int p = 0; p < Sh::kVStages; ++p, x.next()) {
+                        ok = ok && warp_wait(full(x.stage), x.round & 1);
                         fence_after();
                         if (ok && leader) {
-                            const uint32_t vb = ring + st * Sh::kStage;
+                            const uint64_t vd = make_desc(ring + x.stage * Sh::kStage, 1024, Sh::kChunks * 1024);
 #pragma unroll
                             for (int k = 0; k < Sh::kVTokens / 16; ++k)
                                 mma_ts(tmem + 256 + i * 128, tmem + b * 128 + (p * Sh::kVTokens / 16 + k) * 8,
-                                       make_desc(vb + k * 2 * Sh::kChunks * 1024, 1024, Sh::kChunks * 1024), idesc(D, true),
-                                       !fresh || p > 0 || k > 0);
-                            if (release) mma_commit(empty(st));
+                                       vd + k * 2 * Sh::kChunks * 1024 / 16, idesc(D, true), !fresh || p > 0 || k > 0);
+                            if (release) mma_commit(empty(x.stage));
+                            if (p + 1 == Sh::kVStages) mma_commit(o_done(b));
                         }
                         __syncwarp();
                     }
-                    if (ok && leader) mma_commit(o_done(b));
-                    __syncwarp();
                 };
                 do {
-                    ok = ok && warp_wait(q_full, blocks & 1);
+                    ok = ok && warp_wait(q_full(blocks % Sh::kQBuffers), (blocks / Sh::kQBuffers) & 1);
                     const int n = w.j1 - w.j0;
                     // Q is free for the next block once the last S is made
                     auto q_done = [&](int t) {
-                        if (t == n - 1 && ok && leader) mma_commit(q_empty);
+                        if (t == n - 1 && ok && leader) mma_commit(q_empty(blocks % Sh::kQBuffers));
                         __syncwarp();
                     };
                     if constexpr (RT == 1) {
@@ -675,7 +743,7 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                                 const uint32_t v = u + t + 1;
                                 if (v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
                                 qk(0, v & 1, true);
-                                r += Sh::kKStages;
+                                r.next(Sh::kKStages);
                                 q_done(t + 1);
                             }
                             if (t >= 0) {
@@ -683,16 +751,16 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                                 ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
                                 if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
                                 pv(0, v & 1, r, t == 0, true);
-                                r += Sh::kVStages;
+                                r.next(Sh::kVStages);
                             }
                         }
                     } else {
                         // each row tile has its own buffer, free once its P V is done
+                        Ring<Sh::kRing> rv;
 #pragma unroll 1
                         for (int t = 0; t <= n && ok; ++t) {
                             const uint32_t v = u + t;
-                            // of tile t: K in stages r .., V of tile t - 1 in the stages before them
-                            const uint32_t rv = r - Sh::kVStages;
+                            // r: tile t's K, and rv the V of tile t - 1 right before it
 #pragma unroll 1
                             for (int i = 0; i < 2; ++i) {
                                 if (t > 0) {
@@ -706,18 +774,22 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                                     if (i == 1) q_done(t);
                                 }
                             }
-                            if (t < n) r += Sh::kKStages + Sh::kVStages;
+                            if (t < n) {
+                                r.next(Sh::kKStages);
+                                rv = r;
+                                r.next(Sh::kVStages);
+                            }
                         }
                     }
                     u += n;
-                    r += 2;                       // those of the sums on their way out
+                    r.next(2);                    // those of the sums on their way out
                     ++blocks;
                 } while (ok && w.next(a));
             }
         }
     }
     if (!ok && lane == 0) report(a.d_status, GDN_ERR_TIMEOUT);
-    if (c == share.ctas - 1 || share.ctas == 0)
+    if (c + 1 == a.ctas)
         for (int s = tid; s < a.B; s += Sh::kThreads) {
             int past;
             if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
@@ -792,8 +864,10 @@ template <int D> cudaError_t launch_d(TcArgs &t, int rt, int c, cudaStream_t str
 }  // namespace
 
 AttendBlock attend_bf16_block(int T, int G, int D) {
-    const int rt = row_tiles(T, G, D), rows = kLanes / copies(T, G), tt = rows / G < T ? rows / G : T;
-    return {rt * rows, rt * tt};
+    const int rt = row_tiles(T, G, D), c = copies(T, G), rows = kLanes / c, tt = rows / G < T ? rows / G : T;
+    // A part of many rows costs as much as a tile's keys and values.  A block's beginning and end take 3 to 5 us, a tile of 128
+    // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).
+    return {rt * rows, rt * tt, c > 1 ? 1 : 3, D == 64 ? 4 : D == 128 ? 2 : 1};
 }
 
 cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t stream) {

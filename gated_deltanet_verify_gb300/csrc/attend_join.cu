@@ -4,7 +4,7 @@
 // O_i = sum 2^(x - m_i) v; with m = max m_i the row is sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in the order of the parts.
 // A part in which the row sees nothing has l_i = 0 and m_i = -inf.  The partial sums are still in L2, so round trips to
 // it are what costs: a warp takes 128 columns of a row, its lanes fetch the parts' m and l at once (a part each), and
-// eight parts' sums are in flight together.
+// sixteen parts' sums are in flight together.
 #include "attn.cuh"
 
 #include <cuda_bf16.h>
@@ -37,28 +37,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     int begin = 0;
     Span span;
     if (by_item) {                                  // few blocks of rows: one after the other
-        share.set(scan_total<TK>(a), a.ctas);
+        share.set(scan_total<TK>(a), a);
         const int pair = blockIdx.x / a.Hk;
         s = pair / a.n_tb;
         span = block_span<TK>(a, s, pair % a.n_tb);
         kvh = blockIdx.x % a.Hk;
-        begin = scan_begin<TK>(a, pair) + kvh * span.n;
-        c = span.n ? share.owner(begin) : 0;
-        if (span.n) parts = share.owner(begin + span.n - 1) - c + 1;
+        begin = scan_begin<TK>(a, pair) + kvh * (span.n + a.pad);
+        c = span.n ? share.owner(begin + a.pad) : 0;
+        if (span.n) parts = share.owner(begin + a.pad + span.n - 1) - c + 1;
     } else {                                        // the one that CTA c's share ends in
         c = blockIdx.x;
         const Place at = find_place<TK, kJoinThreads>(a, c + 1, share, scratch);
         s = at.pair / a.n_tb;
         span = block_span<TK>(a, s, at.pair % a.n_tb);
         if (c + 1 < share.ctas) {
-            kvh = at.offset / span.n;
-            begin = share.start(c + 1) - (at.offset - kvh * span.n);
+            kvh = at.offset / (span.n + a.pad);
+            begin = share.start(c + 1) - (at.offset - kvh * (span.n + a.pad));
             // else it begins there, or an earlier CTA has its beginning
-            if (begin >= share.start(c) && begin < share.start(c + 1)) parts = share.owner(begin + span.n - 1) - c + 1;
+            if (share.owner(begin + a.pad) == c) parts = share.owner(begin + a.pad + span.n - 1) - c + 1;
         }
     }
     // (every thread waits, so that this kernel does not end before the one whose sums are joined)
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (parts == 1) return;
     const int rows = (span.t1 - span.t0) * a.G, stride = a.part_rows;
     const size_t first = size_t(2 * c + (begin > share.start(c) ? 1 : 0)) * stride;
@@ -87,10 +88,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         for (int e = 0; e < V; ++e) o[e] = 0.f;
 #pragma unroll
         for (int k = 0; k < kPartWords; ++k)
-            for (int i0 = 32 * k; i0 < min(parts, 32 * k + 32); i0 += 8) {
-                float x[8][V];
+            for (int i0 = 32 * k; i0 < min(parts, 32 * k + 32); i0 += 16) {
+                float x[16][V];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < 16; ++q) {
                     const float *from = a.partial + part(min(i0 + q, parts - 1)) * D + column;
                     if constexpr (V == 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(from);
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {       // past the last part the weight is 0
+                for (int q = 0; q < 16; ++q) {      // past the last part the weight is 0
                     const float f = __shfl_sync(kWarp, w[k], (i0 + q) & 31);
 #pragma unroll
                     for (int e = 0; e < V; ++e) o[e] += f == 0.f ? 0.f : f * x[q][e];
@@ -115,13 +116,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 }
 
 template <typename E, int D, int TK> cudaError_t launch(const AttendArgs &a, cudaStream_t stream) {
-    // with no more blocks of rows than CTAs, a column of the grid for each; else one for each border between two CTAs, where
-    // a block has two or three parts
+    // With no more blocks of rows than CTAs, a column of the grid for each; else one for each border between two CTAs, where
+    // a block has two or three parts.  Some eight CTAs an SM: each looks for its block first.
     const long long items = (long long)a.B * a.n_tb * a.Hk;
     const bool by_item = items <= a.ctas;
+    const int columns = by_item ? (int)items : a.ctas, most = 8 * kAttendCtas / columns;
     const int rows_cta = kJoinWarps / (D > 128 ? D / 128 : 1), groups = (a.TB * a.G + rows_cta - 1) / rows_cta;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(by_item ? unsigned(items) : unsigned(a.ctas), unsigned(by_item || groups < 8 ? groups : 8), 1);
+    cfg.gridDim = dim3(unsigned(columns), unsigned(groups < most ? groups : most), 1);
     cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

@@ -42,7 +42,9 @@ struct AttendArgs {
     float scale;
     int window, n_sink;
     int TB, n_tb;                     // tokens a block of rows takes (TB * G rows), blocks a slot
-    int ctas;
+    int ctas;                         // of the launch
+    int least;                        // tiles of a CTA's share, at least (if there are so many)
+    int pad;                          // what a block costs beside its tiles, in tiles
     int part_rows;                    // rows of a part in the workspace
     float *partial;                   // [2 * ctas][part_rows][D]: unnormalised sums of split blocks
     float2 *stats;                    // [2 * ctas][part_rows]: their maxima (in powers of two) and sums
@@ -60,6 +62,8 @@ inline size_t attend_stats_bytes(int rows) { return size_t(2) * kAttendCtas * ro
 struct AttendBlock {
     int rows;                         // of a block, at most (what a part of the workspace holds)
     int tokens;                       // that a block takes
+    int least;                        // tiles a CTA takes at least
+    int pad;                          // what a block costs beside its tiles, in tiles
 };
 AttendBlock attend_f32_block(int T, int G);
 AttendBlock attend_bf16_block(int T, int G, int D);
@@ -116,12 +120,13 @@ __device__ __forceinline__ Span block_span(const AttendArgs &a, int s, int tb) {
 // The whole work is a row of tiles (fewer than 2^31, as the host checks): blocks of rows in the order (slot, token block), kv
 // heads within one, key tiles within one.  Of n CTAs, CTA c takes the tiles [start(c), start(c + 1)), so every SM has the
 // same share whatever the lengths; the block at either end of its share may be split with its neighbours, whose partial
-// sums are joined later.
+// sums are joined later.  A block begins with `pad` tiles that are not there, for what it costs beside its tiles: without
+// them the CTAs with the most blocks ended last (a window's blocks of 10 tiles: 60 us where most took 50).
 struct Share {
     int total, ctas, base, more;      // the first `more` CTAs take base + 1 tiles, the others base
-    __device__ __forceinline__ void set(int t, int n) {
+    __device__ __forceinline__ void set(int t, const AttendArgs &a) {
         total = t;
-        ctas = min(n, t);
+        ctas = min(a.ctas, (t + a.least - 1) / a.least);
         base = ctas ? t / ctas : 0;
         more = t - base * ctas;
     }
@@ -133,7 +138,7 @@ struct Share {
     }
 };
 
-// Where a tile lies: pair = slot * n_tb + token block, then tile `offset` of its Hk * n.
+// Where a tile lies: pair = slot * n_tb + token block, then tile `offset` of its Hk * (pad + n).
 struct Place {
     int pair, offset;
 };
@@ -144,7 +149,8 @@ constexpr int kScanPairs = 256;
 constexpr unsigned kWarp = 0xffffffffu;
 
 template <int TK> __device__ __forceinline__ int pair_tiles(const AttendArgs &a, int pair) {
-    return pair < a.B * a.n_tb ? block_span<TK>(a, pair / a.n_tb, pair % a.n_tb).n * a.Hk : 0;
+    const int n = pair < a.B * a.n_tb ? block_span<TK>(a, pair / a.n_tb, pair % a.n_tb).n : 0;
+    return n ? (n + a.pad) * a.Hk : 0;
 }
 __device__ __forceinline__ int scan_warp(int v) {
 #pragma unroll
@@ -195,7 +201,7 @@ template <int TK, int THREADS>
 __device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &share, int *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, pairs = a.B * a.n_tb;
     if (pairs <= kScanPairs) {
-        share.set(scan_total<TK>(a), a.ctas);
+        share.set(scan_total<TK>(a), a);
         return c < share.ctas ? scan_find<TK>(a, share.start(c)) : Place{0, 0};
     }
     const int chunk = (pairs + THREADS - 1) / THREADS;
@@ -212,7 +218,7 @@ __device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &s
         before += w < wid ? v : 0;
         total += v;
     }
-    share.set(total, a.ctas);
+    share.set(total, a);
     int *found = scratch + THREADS / 32;
     if (c < share.ctas) {
         int at = share.start(c) - before;

@@ -883,7 +883,7 @@ size_t attend_workspace(const gdn_attn_dims &d) {
 // key tiles of all blocks of rows, at most
 int check_attend_work(const gdn_attn_dims &d) {
     const long long tb = attend_block(d).tokens, tile = d.dtype == GDN_F32 ? gdn::kTileF32 : gdn::kTileBf16;
-    const long long blocks = (d.n_tokens + tb - 1) / tb * d.n_slots, tiles = ((long long)d.max_pages * d.page_tokens + tile - 1) / tile;
+    const long long blocks = (d.n_tokens + tb - 1) / tb * d.n_slots, tiles = ((long long)d.max_pages * d.page_tokens + tile - 1) / tile + attend_block(d).pad;
     if ((double)blocks * d.n_kv_heads * (double)tiles >= 2147483648.0)
         return fail(GDN_ERR_SHAPE, "%lld blocks of rows x %d kv heads x %lld key tiles are 2^31 or more", blocks, d.n_kv_heads, tiles);
     return GDN_OK;
@@ -965,6 +965,8 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     const gdn::AttendBlock block = attend_block(d);
     a.part_rows = block.rows;
     a.TB = block.tokens;
+    a.least = block.least;
+    a.pad = block.pad;
     a.n_tb = (a.T + a.TB - 1) / a.TB;
     const int sms = dev_info().sms;
     a.ctas = sms < gdn::kAttendCtas ? sms : gdn::kAttendCtas;
