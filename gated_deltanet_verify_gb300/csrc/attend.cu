@@ -13,7 +13,7 @@
 //     cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
 //     side by side, so that boxes of any page size leave the same layout: group stride (D / 64) KB, chunk stride 1 KB.  It is
 //     K-major for K (8-row groups by the stride offset) and, read the other way, MN-major for V.
-//   * A warp issues the MMAs; S has two buffers.  With one row tile they alternate by key tile, so that the next S is
+//   * Two warps issue the MMAs; S has two buffers.  With one row tile they alternate by key tile, so that the next S is
 //     made while this one's softmax runs; with two row tiles (D <= 128 and more than 128 rows a slot) each has its own.
 //   * 128 threads a row tile do the softmax, a row each (tensor memory's lane), so no value crosses threads.
 //   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
@@ -48,7 +48,7 @@ template <int D, int RT, int C> struct Shape {
     static constexpr int kQBuffers = RT == 1 && D == 64 ? 2 : 1;   // where there is room, the next block's Q comes early
     static constexpr int kQBytes = kQBuffers * kQTile;
     static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
-    static constexpr int kThreads = RT == 1 ? 192 : 384;
+    static constexpr int kThreads = RT == 1 ? 224 : 384;
     static constexpr int kRows = kLanes / C;                       // of a row tile
     static constexpr int kKeys = kTile / C;                        // of a tile that a copy takes
     // a row's sums on their way out: two stages are shared out among the softmax threads
@@ -64,6 +64,7 @@ template <int RT, int RING> struct Control {
     uint64_t s_full[2], p_full[2];    // S is there; P is there
     uint64_t o_done[2];               // P V is done: O is whole so far, the buffer free
     uint64_t o_free[2];               // a row tile's O has been read out
+    uint64_t turn[2];                 // a row tile's warps may take their exponentials
     int scratch[4 * RT + 6];
     uint32_t tmem;
     float2 stats[RT][kLanes];         // a row's maximum and sum, by copy
@@ -189,6 +190,32 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// pairs of fp32 in one instruction
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // bits [0, n) of a word, n any int
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -270,6 +297,7 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
     auto p_full = [&](int b) { return smem_u32(&ctl.p_full[b]); };
     auto o_done = [&](int b) { return smem_u32(&ctl.o_done[b]); };
     auto o_free = [&](int i) { return smem_u32(&ctl.o_free[i]); };
+    auto turn = [&](int i) { return smem_u32(&ctl.turn[i]); };
 
     if (wid == 4 * RT + 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&ctl.tmem)));
@@ -277,15 +305,16 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
     } else if (wid == 4 * RT) {
         if (lane < Sh::kRing) {
             mbar_init(full(lane), 1);
-            mbar_init(empty(lane), 1);
+            mbar_init(empty(lane), RT);           // by the MMAs of each row tile
         }
         if (lane < 2) {
             mbar_init(s_full(lane), 1);
             mbar_init(p_full(lane), 128);
             mbar_init(o_done(lane), 1);
             mbar_init(o_free(lane), 128);
+            mbar_init(turn(lane), 4);
             mbar_init(q_full(lane), 1);
-            mbar_init(q_empty(lane), 1);
+            mbar_init(q_empty(lane), RT);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane < 3) prefetch_map(lane == 0 ? &args.q_map : lane == 1 ? &args.k_map : &args.v_map);
@@ -424,8 +453,9 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         }
                         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < Sh::kKeys; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(x[e]));
-                        const float to = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        for (int e = 0; e < Sh::kKeys; e += 2)
+                            top[e / 2 & 3] = max3(top[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        const float to = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                         const bool grows = on && (to - m) * sc > kSlack;
                         if (q == 0) {
                             m = fmaxf(m, to);
@@ -446,24 +476,32 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                             }
                         }
                         const float base = m == -INFINITY ? 0.f : -m * sc;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        // Two row tiles take their exponentials in turns, so that one's MMAs run beside the other's softmax:
+                        // left to themselves they run in step (5600 cycles for a tile of both).
+                        if (RT == 2 && !dry && (i == 1 || v > 0)) ok = ok && warp_wait(turn(i), (i == 1 ? v : v - 1) & 1);
+                        const uint64_t sc2 = pair2(sc, sc), base2 = pair2(base, base);
+                        uint64_t sum[2] = {0, 0};
 #pragma unroll
                         for (int e = 0; e < Sh::kKeys; e += 32) {
                             uint32_t p[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                const float y0 = ex2(fmaf(__uint_as_float(x[e + 2 * k]), sc, base));
-                                const float y1 = ex2(fmaf(__uint_as_float(x[e + 2 * k + 1]), sc, base));
-                                sum[2 * (k & 1)] += y0;
-                                sum[2 * (k & 1) + 1] += y1;
+                                const float2 z = split2(fma2(pair2(__uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1])), sc2, base2));
+                                const float y0 = ex2(z.x), y1 = ex2(z.y);
+                                sum[k & 1] = add2(sum[k & 1], pair2(y0, y1));
                                 p[k] = pack_bf16(y0, y1);
                             }
                             tmem_st16(p_at + copy * (Sh::kKeys / 2) + e / 2, p);
                         }
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        const float2 all2 = split2(add2(sum[0], sum[1]));
+                        l += all2.x + all2.y;
                         wait_st();
                     }
                     if (dry) break;
+                    if (RT == 2) {                // (a warp without rows passes its turn on as it comes)
+                        if (!busy && (i == 1 || v > 0)) ok = ok && warp_wait(turn(i), (i == 1 ? v : v - 1) & 1);
+                        if (lane == 0) mbar_arrive(turn(i ^ 1));
+                    }
                     // ---- rows of V that no row of the block sees
                     if (k0 + kTile > w.span.hi || (k0 < w.span.lo && k0 + kTile > sink)) {
                         const int key = k0 + tl, part = tl / Sh::kVTokens, g = tl % Sh::kVTokens;
@@ -594,15 +632,15 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                 }
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
-                if (tl < kStagesRt) mbar_arrive(empty(r.after(RT == 1 ? tl : i).stage));
+                if (tl < 2) mbar_arrive(empty(r.after(RT == 1 ? tl : i).stage));      // (twice where each row tile arrives)
                 r.next(2);
                 if (!ok || !w.next(a)) break;
             } while (true);
         } else {
+            if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
             if (!together) begin();
             Walk w;
             const bool some = c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c));
-            if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
             if (!some) {
                 // nothing to do: fewer tiles than CTAs
             } else if (wid == 4 * RT) {
@@ -684,44 +722,49 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         const uint32_t fills = r.round + (i < (int)r.stage);      // of stage i
                         if (fills > 0) mbar_wait(full(i), (fills - 1) & 1);
                     }
-            } else if (wid == 4 * RT + 1) {
-                // ---- the MMAs
-                const bool leader = elect_one();  // one thread issues all of them, so that its commits cover them
-                Ring<Sh::kRing> r;                // the next stage to take
+            } else if (wid <= 4 * RT + 2) {
+                // ---- the MMAs, from two warps: an MMA's end is known some 400 cycles after it, and what one warp waits for the
+                // other need not.  With one row tile a warp makes S and the other takes P V; with two, each has one of them.
+                // Both wait for every stage of the ring in its order, whether theirs or not: a stage's barrier tells the last
+                // round from the one before it only to who has seen all of them.
+                const int part = wid - (4 * RT + 1);
+                const bool leader = elect_one();  // one thread issues all of a warp's, so that its commits cover them
+                Ring<Sh::kRing> r;                // the next stage
                 uint32_t u = 0;                   // S buffers filled before this block
                 int blocks = 0;
-                // S buffer b: rows of row tile i
-                auto qk = [&](int i, int b, bool release) {
-                    Ring<Sh::kRing> x = r;
+                auto arrived = [&](uint32_t st, uint32_t round) {
+                    ok = ok && warp_wait(full(st), round & 1);
+                    fence_after();
+                };
+                // S buffer b: rows of row tile i.  The stages are passed by
+                auto qk = [&](int i, int b, bool mine) {
 #pragma unroll
-                    for (int p = 0; p < Sh::kKStages; ++p, x.next()) {
-                        ok = ok && warp_wait(full(x.stage), x.round & 1);
-                        fence_after();
-                        if (ok && leader) {
+                    for (int p = 0; p < Sh::kKStages; ++p, r.next()) {
+                        arrived(r.stage, r.round);
+                        if (ok && leader && mine) {
                             const uint64_t qd = make_desc(qbase + (blocks % Sh::kQBuffers) * Sh::kQTile + (i * Sh::kChunks + p * Sh::kKChunks) * (kLanes * 128), 16, 1024);
-                            const uint64_t kd = make_desc(ring + x.stage * Sh::kStage, 16, Sh::kKChunks * 1024);
+                            const uint64_t kd = make_desc(ring + r.stage * Sh::kStage, 16, Sh::kKChunks * 1024);
 #pragma unroll
                             for (int k = 0; k < 4 * Sh::kKChunks; ++k)
                                 mma_ss(tmem + b * 128, qd + ((k / 4) * (kLanes * 128) + (k & 3) * 32) / 16, kd + ((k / 4) * 1024 + (k & 3) * 32) / 16,
                                        idesc(kTile, false), p > 0 || k > 0);
-                            if (release) mma_commit(empty(x.stage));
+                            mma_commit(empty(r.stage));
                             if (p + 1 == Sh::kKStages) mma_commit(s_full(b));
                         }
                         __syncwarp();
                     }
                 };
-                auto pv = [&](int i, int b, Ring<Sh::kRing> x, bool fresh, bool release) {
+                auto pv = [&](int i, int b, bool fresh, bool mine) {
 #pragma unroll
-                    for (int p = 0; p < Sh::kVStages; ++p, x.next()) {
-                        ok = ok && warp_wait(full(x.stage), x.round & 1);
-                        fence_after();
-                        if (ok && leader) {
-                            const uint64_t vd = make_desc(ring + x.stage * Sh::kStage, 1024, Sh::kChunks * 1024);
+                    for (int p = 0; p < Sh::kVStages; ++p, r.next()) {
+                        arrived(r.stage, r.round);
+                        if (ok && leader && mine) {
+                            const uint64_t vd = make_desc(ring + r.stage * Sh::kStage, 1024, Sh::kChunks * 1024);
 #pragma unroll
                             for (int k = 0; k < Sh::kVTokens / 16; ++k)
                                 mma_ts(tmem + 256 + i * 128, tmem + b * 128 + (p * Sh::kVTokens / 16 + k) * 8,
                                        vd + k * 2 * Sh::kChunks * 1024 / 16, idesc(D, true), !fresh || p > 0 || k > 0);
-                            if (release) mma_commit(empty(x.stage));
+                            mma_commit(empty(r.stage));
                             if (p + 1 == Sh::kVStages) mma_commit(o_done(b));
                         }
                         __syncwarp();
@@ -741,48 +784,34 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         for (int t = -1; t < n && ok; ++t) {
                             if (t + 1 < n) {
                                 const uint32_t v = u + t + 1;
-                                if (v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
-                                qk(0, v & 1, true);
-                                r.next(Sh::kKStages);
-                                q_done(t + 1);
+                                if (part == 0 && v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
+                                qk(0, v & 1, part == 0);
+                                if (part == 0) q_done(t + 1);
                             }
                             if (t >= 0) {
                                 const uint32_t v = u + t;
-                                ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
-                                if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
-                                pv(0, v & 1, r, t == 0, true);
-                                r.next(Sh::kVStages);
+                                if (part == 1) {
+                                    ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
+                                    if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
+                                }
+                                pv(0, v & 1, t == 0, part == 1);
                             }
                         }
                     } else {
-                        // each row tile has its own buffer, free once its P V is done
-                        Ring<Sh::kRing> rv;
+                        // a row tile's own buffer is free once its P V is done
 #pragma unroll 1
-                        for (int t = 0; t <= n && ok; ++t) {
+                        for (int t = 0; t < n && ok; ++t) {
                             const uint32_t v = u + t;
-                            // r: tile t's K, and rv the V of tile t - 1 right before it
-#pragma unroll 1
-                            for (int i = 0; i < 2; ++i) {
-                                if (t > 0) {
-                                    ok = ok && warp_wait(p_full(i), (v - 1) & 1);
-                                    if (t == 1 && blocks > 0) ok = ok && warp_wait(o_free(i), (blocks - 1) & 1);
-                                    pv(i, i, rv, t == 1, i == 1);
-                                }
-                                if (t < n) {
-                                    if (v > 0) ok = ok && warp_wait(o_done(i), (v - 1) & 1);
-                                    qk(i, i, i == 1);
-                                    if (i == 1) q_done(t);
-                                }
-                            }
-                            if (t < n) {
-                                r.next(Sh::kKStages);
-                                rv = r;
-                                r.next(Sh::kVStages);
-                            }
+                            if (v > 0) ok = ok && warp_wait(o_done(part), (v - 1) & 1);
+                            qk(part, part, true);
+                            q_done(t);
+                            ok = ok && warp_wait(p_full(part), v & 1);
+                            if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(part), (blocks - 1) & 1);
+                            pv(part, part, t == 0, true);
                         }
                     }
+                    for (int p = 0; p < 2; ++p, r.next()) arrived(r.stage, r.round);      // those of the sums on their way out
                     u += n;
-                    r.next(2);                    // those of the sums on their way out
                     ++blocks;
                 } while (ok && w.next(a));
             }
@@ -867,7 +896,7 @@ AttendBlock attend_bf16_block(int T, int G, int D) {
     const int rt = row_tiles(T, G, D), c = copies(T, G), rows = kLanes / c, tt = rows / G < T ? rows / G : T;
     // A part of many rows costs as much as a tile's keys and values.  A block's beginning and end take 3 to 5 us, a tile of 128
     // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).
-    return {rt * rows, rt * tt, c > 1 ? 1 : 3, D == 64 ? 4 : D == 128 ? 2 : 1};
+    return {rt * rows, rt * tt, c > 1 ? 1 : 3, D == 64 ? 4 : 3};
 }
 
 cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t stream) {

@@ -4,7 +4,7 @@
 // O_i = sum 2^(x - m_i) v; with m = max m_i the row is sum 2^(m_i - m) O_i / sum 2^(m_i - m) l_i, in the order of the parts.
 // A part in which the row sees nothing has l_i = 0 and m_i = -inf.  The partial sums are still in L2, so round trips to
 // it are what costs: a warp takes 128 columns of a row, its lanes fetch the parts' m and l at once (a part each), and
-// sixteen parts' sums are in flight together.
+// eight parts' sums are in flight together.
 #include "attn.cuh"
 
 #include <cuda_bf16.h>
@@ -88,10 +88,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         for (int e = 0; e < V; ++e) o[e] = 0.f;
 #pragma unroll
         for (int k = 0; k < kPartWords; ++k)
-            for (int i0 = 32 * k; i0 < min(parts, 32 * k + 32); i0 += 16) {
-                float x[16][V];
+            for (int i0 = 32 * k; i0 < min(parts, 32 * k + 32); i0 += 8) {
+                float x[8][V];
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {
+                for (int q = 0; q < 8; ++q) {
                     const float *from = a.partial + part(min(i0 + q, parts - 1)) * D + column;
                     if constexpr (V == 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(from);
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                     }
                 }
 #pragma unroll
-                for (int q = 0; q < 16; ++q) {      // past the last part the weight is 0
+                for (int q = 0; q < 8; ++q) {       // past the last part the weight is 0
                     const float f = __shfl_sync(kWarp, w[k], (i0 + q) & 31);
 #pragma unroll
                     for (int e = 0; e < V; ++e) o[e] += f == 0.f ? 0.f : f * x[q][e];
