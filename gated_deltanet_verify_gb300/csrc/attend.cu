@@ -13,9 +13,13 @@
 //     cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
 //     side by side, so that boxes of any page size leave the same layout: group stride (D / 64) KB, chunk stride 1 KB.  It is
 //     K-major for K (8-row groups by the stride offset) and, read the other way, MN-major for V.
-//   * Two warps issue the MMAs; S has two buffers.  With one row tile they alternate by key tile, so that the next S is
-//     made while this one's softmax runs; with two row tiles (D <= 128 and more than 128 rows a slot) each has its own.
-//   * 128 threads a row tile do the softmax, a row each (tensor memory's lane), so no value crosses threads.
+//   * Two warps issue the MMAs, one those of S and one those of P V; S has as many buffers as tensor memory holds beside O
+//     (three, or two for D = 256), so that the next S is made while this one's softmax runs.  (Two row tiles a CTA, each with
+//     its own S, O and softmax warps, halve what the keys and values cost in shared memory, but ran slower: the chains
+//     of one tile's S, softmax and P V are what binds, and two of them took 4950 cycles where a single one takes 2200.)
+//   * 128 threads do the softmax, a row each (tensor memory's lane), so no value crosses threads.  Where a slot has at most
+//     32 rows they lie there four times, and each copy's warp takes a quarter of every tile's keys (its other weights are
+//     zeros); the four sums are added up at the end.  One warp with all the keys took 1400 cycles a tile, this takes 600.
 //   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
 //     at the ends of its share are joined with its neighbours' parts by attend_join.cu.
 //
@@ -31,51 +35,49 @@ namespace gdn {
 namespace {
 
 constexpr int kTile = kTileBf16;
-constexpr int kLanes = 128;           // tensor memory's: rows of a row tile
+constexpr int kLanes = 128;           // tensor memory's: rows of a block
+constexpr int kThreads = 7 * 32;      // four warps of softmax, one of loads, two of MMAs
 constexpr int kSpin = 1 << 22;        // mbarrier polls before a wait gives up
 constexpr float kSlack = 8.f;         // powers of two by which a maximum may grow unmoved
 
-// RT: row tiles.  C: copies of a row tile's rows, 128 / C of them, side by side in tensor memory; copy i takes the i-th
-// C-th of every tile's keys.
-template <int D, int RT, int C> struct Shape {
+// C: copies of the rows, 128 / C of them, side by side in tensor memory; copy i takes the i-th C-th of every tile's keys.
+template <int D, int C> struct Shape {
     static constexpr int kChunks = D / 64;                         // 128-byte columns of a row
     static constexpr int kStage = D == 64 ? 16384 : 32768;         // bytes
     static constexpr int kKChunks = kChunks < 2 ? kChunks : 2;     // of K in a stage: 128 keys x 64 kKChunks
     static constexpr int kKStages = kChunks / kKChunks;
     static constexpr int kVTokens = kStage / (2 * D);              // of V in a stage: kVTokens keys x D
     static constexpr int kVStages = kTile / kVTokens;
-    static constexpr int kQTile = RT * kLanes * D * 2;
-    static constexpr int kQBuffers = RT == 1 && D == 64 ? 2 : 1;   // where there is room, the next block's Q comes early
+    static constexpr int kQTile = kLanes * D * 2;
+    static constexpr int kQBuffers = D == 64 ? 2 : 1;   // where there is room, the next block's Q comes early
     static constexpr int kQBytes = kQBuffers * kQTile;
     static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
-    static constexpr int kThreads = RT == 1 ? 224 : 384;
-    static constexpr int kRows = kLanes / C;                       // of a row tile
+    static constexpr int kBuffers = D == 256 ? 2 : 3;              // of S, in tensor memory beside O
+    static constexpr int kOColumn = 128 * 2;                       // O, between the second S and the third
+    static constexpr int kRows = kLanes / C;                       // of a block
     static constexpr int kKeys = kTile / C;                        // of a tile that a copy takes
     // a row's sums on their way out: two stages are shared out among the softmax threads
-    static constexpr int kOut = 2 * kStage / (RT * kLanes);
-    static_assert(RT == 1 || (D <= 128 && C == 1), "tensor memory: two S and the row tiles' O");
+    static constexpr int kOut = 2 * kStage / kLanes;
     static_assert(kRing >= 5, "a tile's V, the next one's K, and one more");
 };
 
 // What a CTA keeps beside its tiles, behind them.
-template <int RT, int RING> struct Control {
+template <int RING> struct Control {
     uint64_t full[RING], empty[RING];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2];    // S is there; P is there
-    uint64_t o_done[2];               // P V is done: O is whole so far, the buffer free
-    uint64_t o_free[2];               // a row tile's O has been read out
-    uint64_t turn[2];                 // a row tile's warps may take their exponentials
-    int scratch[4 * RT + 6];
+    uint64_t s_full[3], p_full[3];    // S is there; P is there
+    uint64_t o_done[3];               // P V is done: O is whole so far, the buffer free
+    uint64_t o_free;                  // O has been read out
+    int scratch[kThreads / 32 + 2];
     uint32_t tmem;
-    float2 stats[RT][kLanes];         // a row's maximum and sum, by copy
-    int parents[RT][64];
-    unsigned char depths[RT][64];
+    float2 stats[kLanes];             // a row's maximum and sum, by copy
+    int parents[64];
+    unsigned char depths[64];
 };
 
 struct TcArgs {
     CUtensorMap q_map, k_map, v_map;
     AttendArgs a;
-    int tt;                           // tokens a row tile holds
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
@@ -181,6 +183,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
                      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
                  : "memory");
 }
+// the four softmax warps
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -219,7 +223,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // bits [0, n) of a word, n any int
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// A place in the ring of N stages: the stage, and how often the ring has gone round.
+// A place in a ring of N stages (of keys and values, or S buffers): the stage, and how often the ring has gone round.
 template <int N> struct Ring {
     uint32_t stage = 0, round = 0;
     __device__ __forceinline__ void next(int n = 1) {
@@ -280,10 +284,10 @@ struct Walk {
     }
 };
 
-template <int D, int RT, int C>
-__global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
-    using Sh = Shape<D, RT, C>;
-    using Ctl = Control<RT, Sh::kRing>;
+template <int D, int C>
+__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
+    using Sh = Shape<D, C>;
+    using Ctl = Control<Sh::kRing>;
     extern __shared__ __align__(1024) unsigned char sm[];         // no other shared memory, so that it starts at a swizzle atom
     Ctl &ctl = *reinterpret_cast<Ctl *>(sm + Sh::kQBytes + Sh::kRing * Sh::kStage);
     const AttendArgs &a = args.a;
@@ -296,25 +300,25 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
     auto s_full = [&](int b) { return smem_u32(&ctl.s_full[b]); };
     auto p_full = [&](int b) { return smem_u32(&ctl.p_full[b]); };
     auto o_done = [&](int b) { return smem_u32(&ctl.o_done[b]); };
-    auto o_free = [&](int i) { return smem_u32(&ctl.o_free[i]); };
-    auto turn = [&](int i) { return smem_u32(&ctl.turn[i]); };
+    const uint32_t o_free = smem_u32(&ctl.o_free);
 
-    if (wid == 4 * RT + 1) {
+    if (wid == 5) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&ctl.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    } else if (wid == 4 * RT) {
+    } else if (wid == 4) {
         if (lane < Sh::kRing) {
             mbar_init(full(lane), 1);
-            mbar_init(empty(lane), RT);           // by the MMAs of each row tile
+            mbar_init(empty(lane), 1);
         }
-        if (lane < 2) {
+        if (lane < 3) {
             mbar_init(s_full(lane), 1);
             mbar_init(p_full(lane), 128);
             mbar_init(o_done(lane), 1);
-            mbar_init(o_free(lane), 128);
-            mbar_init(turn(lane), 4);
+        }
+        if (lane < 2) {
             mbar_init(q_full(lane), 1);
-            mbar_init(q_empty(lane), RT);
+            mbar_init(q_empty(lane), 1);
+            if (lane) mbar_init(o_free, 128);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane < 3) prefetch_map(lane == 0 ? &args.q_map : lane == 1 ? &args.k_map : &args.v_map);
@@ -338,20 +342,18 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
     };
     if (together) {
         begin();
-        at = find_place<kTile, Sh::kThreads>(a, c, share, ctl.scratch);
+        at = find_place<kTile, kThreads>(a, c, share, ctl.scratch);
     }
     {
-        // With two row tiles 384 threads start with 168 registers each, and the softmax warps take what the others do not need
-        // (216 x 256 + 72 x 128 = 168 x 384).
-        if (wid < 4 * RT) {
-            if constexpr (RT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+        if (wid < 4) {
             // ---- the softmax: thread = tensor memory's lane = row (of one of C copies)
-            const int i = wid >> 2, tl = tid & 127, copy = tl / Sh::kRows, row = tl % Sh::kRows;
-            const uint32_t lanes = tmem + ((uint32_t)(32 * (wid & 3)) << 16), o_at = lanes + 256 + i * 128;
+            const int tl = tid, copy = tl / Sh::kRows, row = tl % Sh::kRows;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * wid) << 16), o_at = lanes + Sh::kOColumn;
             const bool negative = a.scale < 0.f;
             // a scale of zero leaves all weights alike, and masked ones at none
             const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-            uint32_t u = 0;                       // S buffers taken before this block
+            Ring<Sh::kBuffers> u, before;         // this tile's S, and the tile's before it
+            bool any = false;                     // was there one?
             Ring<Sh::kRing> r;                    // the first stage of this tile
             int last_pair = -1;
             unsigned long long line = 0;          // a tree's nodes that this row sees
@@ -365,36 +367,36 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
             if (dry || (c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c))))
             do {
                 const int s = w.pair / a.n_tb, past = w.span.past, n = w.j1 - w.j0;
-                const int first_t = w.span.t0 + i * args.tt, last_t = min(w.span.t1, first_t + args.tt) - 1;
-                const int t = row < args.tt * a.G ? first_t + row / a.G : w.span.t1;
+                const int first_t = w.span.t0, last_t = w.span.t1 - 1;
+                const int t = row < a.TB * a.G ? first_t + row / a.G : w.span.t1;
                 const bool on = t < w.span.t1;
                 const bool busy = __any_sync(kWarp, on);
                 if (w.pair != last_pair && !dry) {
                     last_pair = w.pair;
                     position = past + t;
                     if (a.parent) {
-                        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                        softmax_sync();
                         if (tl < w.span.t1) {
                             int p = a.parent[(size_t)s * a.T + tl];
                             if (p < -1 || p >= tl) {              // it hangs from the past
                                 report(a.d_status, GDN_ERR_TREE);
                                 p = -1;
                             }
-                            ctl.parents[i][tl] = p;
+                            ctl.parents[tl] = p;
                         }
-                        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                        softmax_sync();
                         if (tl < w.span.t1) {
                             int d = 0;
-                            for (int p = ctl.parents[i][tl]; p >= 0; p = ctl.parents[i][p]) ++d;
-                            ctl.depths[i][tl] = (unsigned char)d;
+                            for (int p = ctl.parents[tl]; p >= 0; p = ctl.parents[p]) ++d;
+                            ctl.depths[tl] = (unsigned char)d;
                         }
-                        asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                        softmax_sync();
                         line = 0;
                         if (on) {
-                            const int mine = ctl.depths[i][t];
+                            const int mine = ctl.depths[t];
                             position = past + mine;
-                            for (int p = t; p >= 0; p = ctl.parents[i][p]) {
-                                const int d = ctl.depths[i][p];
+                            for (int p = t; p >= 0; p = ctl.parents[p]) {
+                                const int d = ctl.depths[p];
                                 if (!a.window || mine - d < a.window || past + d < a.n_sink) line |= 1ull << p;
                             }
                         }
@@ -405,19 +407,15 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                 const int sink = min(a.n_sink, w.span.lo);
                 float m = -INFINITY, l = 0.f;
                 for (int q = 0; q < n; ++q) {
-                    const uint32_t v = u + q;
-                    const int b = RT == 1 ? (v & 1) : i;
+                    const uint32_t s_column = u.stage * 128 + (u.stage == 2 ? 128 : 0);
                     const int k0 = w.span.tile(w.j0 + q) * kTile, mine0 = k0 + copy * Sh::kKeys;
-                    if (!dry) ok = ok && warp_wait(s_full(b), RT == 1 ? (v >> 1) & 1 : v & 1);
+                    if (!dry) ok = ok && warp_wait(s_full(u.stage), u.round & 1);
                     if (!ok) break;
                     fence_after();
                     // O is whole up to the tile before
-                    auto wait_o = [&] {
-                        if constexpr (RT == 1) return warp_wait(o_done((v - 1) & 1), ((v - 1) >> 1) & 1);
-                        else return warp_wait(o_done(i), (v - 1) & 1);
-                    };
+                    auto wait_o = [&] { return warp_wait(o_done(before.stage), before.round & 1); };
                     if (busy) {
-                        const uint32_t s_at = lanes + b * 128 + copy * Sh::kKeys, p_at = dry ? o_at : lanes + b * 128;
+                        const uint32_t s_at = lanes + s_column + copy * Sh::kKeys, p_at = dry ? o_at : lanes + s_column;
                         uint32_t x[Sh::kKeys];
 #pragma unroll
                         for (int e = 0; e < Sh::kKeys; e += 32) tmem_ld32(s_at + e, x + e);
@@ -476,9 +474,6 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                             }
                         }
                         const float base = m == -INFINITY ? 0.f : -m * sc;
-                        // Two row tiles take their exponentials in turns, so that one's MMAs run beside the other's softmax:
-                        // left to themselves they run in step (5600 cycles for a tile of both).
-                        if (RT == 2 && !dry && (i == 1 || v > 0)) ok = ok && warp_wait(turn(i), (i == 1 ? v : v - 1) & 1);
                         const uint64_t sc2 = pair2(sc, sc), base2 = pair2(base, base);
                         uint64_t sum[2] = {0, 0};
 #pragma unroll
@@ -498,16 +493,12 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         wait_st();
                     }
                     if (dry) break;
-                    if (RT == 2) {                // (a warp without rows passes its turn on as it comes)
-                        if (!busy && (i == 1 || v > 0)) ok = ok && warp_wait(turn(i), (i == 1 ? v : v - 1) & 1);
-                        if (lane == 0) mbar_arrive(turn(i ^ 1));
-                    }
                     // ---- rows of V that no row of the block sees
                     if (k0 + kTile > w.span.hi || (k0 < w.span.lo && k0 + kTile > sink)) {
                         const int key = k0 + tl, part = tl / Sh::kVTokens, g = tl % Sh::kVTokens;
                         // after the P V of the tile before, whose stages come ahead of this one's in the ring
-                        if (v > 0) ok = ok && wait_o();
-                        const Ring<Sh::kRing> rv = r.after(((RT == 2 || q == 0) + (RT == 1 && q + 1 < n)) * Sh::kKStages + part);
+                        if (any) ok = ok && wait_o();
+                        const Ring<Sh::kRing> rv = r.after(((q == 0) + (q + 1 < n)) * Sh::kKStages + part);
                         ok = ok && warp_wait(full(rv.stage), rv.round & 1);
                         if (ok && !(key < w.span.hi && (key >= w.span.lo || key < sink))) {
                             const uint32_t to = ring + rv.stage * Sh::kStage + (g >> 3) * (Sh::kChunks * 1024) + (g & 7) * 128;
@@ -520,12 +511,15 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         }
                         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                     }
-                    // what the ring has moved on by, with this tile's V: K before V, and with one row tile the next tile's K too
-                    if (RT == 2 || q == 0) r.next(Sh::kKStages);
-                    if (RT == 1 && q + 1 < n) r.next(Sh::kKStages);
+                    // what the ring has moved on by, with this tile's V: the next tile's K comes before it
+                    if (q == 0) r.next(Sh::kKStages);
+                    if (q + 1 < n) r.next(Sh::kKStages);
                     r.next(Sh::kVStages);
                     fence_before();
-                    mbar_arrive(p_full(b));
+                    mbar_arrive(p_full(u.stage));
+                    before = u;
+                    any = true;
+                    u.next();
                 }
                 if (dry) {
                     dry = false;
@@ -534,58 +528,53 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                     last_pair = -1;
                     continue;
                 }
-                u += n;
                 // ---- the block's sums: its output, or a part of it
                 float factor = 1.f;
                 if constexpr (C > 1) {
                     // copies to a common maximum
-                    ctl.stats[i][tl] = make_float2(m, l);
-                    asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                    ctl.stats[tl] = make_float2(m, l);
+                    softmax_sync();
                     const float own = m;
                     m = -INFINITY;
                     l = 0.f;
 #pragma unroll
-                    for (int e = 0; e < C; ++e) m = fmaxf(m, ctl.stats[i][e * Sh::kRows + row].x);
+                    for (int e = 0; e < C; ++e) m = fmaxf(m, ctl.stats[e * Sh::kRows + row].x);
 #pragma unroll
                     for (int e = 0; e < C; ++e) {
-                        const float2 st = ctl.stats[i][e * Sh::kRows + row];
+                        const float2 st = ctl.stats[e * Sh::kRows + row];
                         l += st.x == -INFINITY ? 0.f : st.y * ex2((st.x - m) * sc);
                     }
                     factor = own == -INFINITY ? 0.f : ex2((own - m) * sc);
                 }
                 if (w.whole) factor /= l;
-                const size_t part0 = size_t(2 * c + (w.first ? 0 : 1)) * a.part_rows + i * args.tt * a.G;
+                const size_t part0 = size_t(2 * c + (w.first ? 0 : 1)) * a.part_rows;
                 if (!w.whole && on && copy == 0) a.stats[part0 + row] = make_float2(m * sc, l);
-                if (ok) {
-                    if constexpr (RT == 1) ok = warp_wait(o_done((u - 1) & 1), ((u - 1) >> 1) & 1);
-                    else ok = warp_wait(o_done(i), (u - 1) & 1);
-                }
+                ok = ok && warp_wait(o_done(before.stage), before.round & 1);
                 fence_after();
                 // Rows go through the two stages, each turned by its number of 16 bytes (so that 32 lanes write 32 rows
                 // without conflicts), and leave side by side, four 16-byte pieces a thread in flight.  (Written by its own
                 // lane, 16 bytes a row at a time, 96 rows of 256 took 7400 cycles; as two bulk copies a row, 11500.)
-                constexpr int kStagesRt = 2 / RT, kLanesStage = kLanes / kStagesRt;
                 constexpr int kCols = Sh::kOut / 4 < D ? Sh::kOut / 4 : D, kPieces = kCols / 4, kStep = 128 / kPieces;
-                unsigned char *stage[kStagesRt];
+                unsigned char *stage[2];
 #pragma unroll
-                for (int p = 0; p < kStagesRt; ++p) {
-                    const Ring<Sh::kRing> st = r.after(RT == 1 ? p : i);
+                for (int p = 0; p < 2; ++p) {
+                    const Ring<Sh::kRing> st = r.after(p);
                     ok = ok && warp_wait(full(st.stage), st.round & 1);
                     stage[p] = sm + Sh::kQBytes + st.stage * Sh::kStage;
                 }
                 // row `from` of tensor memory, its 16-byte piece p
                 auto spot = [&](int from, int p) {
-                    unsigned char *at_stage = RT == 2 || from < kLanesStage ? stage[0] : stage[kStagesRt - 1];
-                    return reinterpret_cast<float4 *>(at_stage + (from & (kLanesStage - 1)) * Sh::kOut + ((p + from) & (kPieces - 1)) * 16);
+                    return reinterpret_cast<float4 *>((from < kLanes / 2 ? stage[0] : stage[1]) + from % (kLanes / 2) * Sh::kOut +
+                                                      ((p + from) & (kPieces - 1)) * 16);
                 };
-                const int rows = ok ? max(0, last_t + 1 - first_t) * a.G : 0;      // as in every warp, unless a wait gave up
+                const int rows = ok ? (last_t + 1 - first_t) * a.G : 0;            // as in every warp, unless a wait gave up
                 const int piece = tl % kPieces, row0 = tl / kPieces;
                 unsigned char *out0 = w.whole ? reinterpret_cast<unsigned char *>(static_cast<__nv_bfloat16 *>(a.out) +
                                                     (((size_t)s * a.T + first_t) * a.H + (size_t)w.kvh * a.G) * D + 4 * piece)
                                               : reinterpret_cast<unsigned char *>(a.partial + (part0 + row0) * D + 4 * piece);
 #pragma unroll 1
                 for (int at0 = 0; at0 < D; at0 += kCols) {
-                    if (at0 > 0) asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                    if (at0 > 0) softmax_sync();
                     if (ok && busy) {
 #pragma unroll 1
                         for (int e = 0; e < kCols; e += 32) {
@@ -600,9 +589,9 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                     }
                     if (at0 + kCols == D) {
                         fence_before();
-                        mbar_arrive(o_free(i));
+                        mbar_arrive(o_free);
                     }
-                    asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
+                    softmax_sync();
 #pragma unroll 1
                     for (int x = row0; x < rows; x += 4 * kStep) {
                         float4 y[4];
@@ -631,19 +620,18 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                asm volatile("bar.sync %0, 128;\n" ::"r"(1 + i) : "memory");
-                if (tl < 2) mbar_arrive(empty(r.after(RT == 1 ? tl : i).stage));      // (twice where each row tile arrives)
+                softmax_sync();
+                if (tl < 2) mbar_arrive(empty(r.after(tl).stage));
                 r.next(2);
                 if (!ok || !w.next(a)) break;
             } while (true);
         } else {
-            if constexpr (RT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
             if (!together) begin();
             Walk w;
             const bool some = c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c));
             if (!some) {
                 // nothing to do: fewer tiles than CTAs
-            } else if (wid == 4 * RT) {
+            } else if (wid == 4) {
                 // ---- the loads
                 const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
                 Ring<Sh::kRing> r;                // the next stage to fill
@@ -691,22 +679,21 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                     const int qb = blocks % Sh::kQBuffers, uses = blocks / Sh::kQBuffers;
                     if (uses > 0) ok = ok && warp_wait(q_empty(qb), (uses - 1) & 1);
                     if (ok) {
-                        // lane: copy, chunk, row tile
-                        const int q = (lane / C) % Sh::kChunks, i = lane / (C * Sh::kChunks);
-                        if (lane == 0) mbar_expect(q_full(qb), (uint32_t)args.tt * a.G * 128 * (RT * Sh::kChunks * C));
+                        const int q = lane / C;   // lane: chunk, copy
+                        if (lane == 0) mbar_expect(q_full(qb), (uint32_t)(a.TB * a.G * 128 * (Sh::kChunks * C)));
                         __syncwarp();
-                        if (i < RT)
-                            tma_box5(qbase + qb * Sh::kQTile + (i * Sh::kChunks + q) * (kLanes * 128) + (lane % C) * (Sh::kRows * 128), &args.q_map, 0, q,
-                                     w.kvh * a.G, w.span.t0 + i * args.tt, s, q_full(qb));
+                        if (q < Sh::kChunks)
+                            tma_box5(qbase + qb * Sh::kQTile + q * (kLanes * 128) + (lane % C) * (Sh::kRows * 128), &args.q_map, 0, q,
+                                     w.kvh * a.G, w.span.t0, s, q_full(qb));
                     }
                     __syncwarp();
                     ++blocks;
                     // in the order in which the MMAs take them
-                    if (RT == 1) put(w.j0, id, false);
+                    put(w.j0, id, false);
 #pragma unroll 1
                     for (int j = w.j0; j < w.j1 && ok; ++j) {
                         const int id2 = page_id(j + 2);
-                        if (RT == 2 || j + 1 < w.j1) put(RT == 2 ? j : j + 1, RT == 2 ? id : id1, false);
+                        if (j + 1 < w.j1) put(j + 1, id1, false);
                         put(j, id, true);
                         id = id1;
                         id1 = id2;
@@ -722,39 +709,39 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         const uint32_t fills = r.round + (i < (int)r.stage);      // of stage i
                         if (fills > 0) mbar_wait(full(i), (fills - 1) & 1);
                     }
-            } else if (wid <= 4 * RT + 2) {
+            } else if (wid <= 6) {
                 // ---- the MMAs, from two warps: an MMA's end is known some 400 cycles after it, and what one warp waits for the
-                // other need not.  With one row tile a warp makes S and the other takes P V; with two, each has one of them.
-                // Both wait for every stage of the ring in its order, whether theirs or not: a stage's barrier tells the last
+                // other need not: one makes S, the other takes P V.  Both wait for every stage of the ring in its order, whether theirs or not: a stage's barrier tells the last
                 // round from the one before it only to who has seen all of them.
-                const int part = wid - (4 * RT + 1);
+                const int part = wid - 5;
                 const bool leader = elect_one();  // one thread issues all of a warp's, so that its commits cover them
                 Ring<Sh::kRing> r;                // the next stage
-                uint32_t u = 0;                   // S buffers filled before this block
+                Ring<Sh::kBuffers> x;             // this warp's next S
                 int blocks = 0;
                 auto arrived = [&](uint32_t st, uint32_t round) {
                     ok = ok && warp_wait(full(st), round & 1);
                     fence_after();
                 };
-                // S buffer b: rows of row tile i.  The stages are passed by
-                auto qk = [&](int i, int b, bool mine) {
+                // S.  Who does not take the stages passes them by
+                auto column = [&] { return tmem + x.stage * 128 + (x.stage == 2 ? 128 : 0); };
+                auto qk = [&](bool mine) {
 #pragma unroll
                     for (int p = 0; p < Sh::kKStages; ++p, r.next()) {
                         arrived(r.stage, r.round);
                         if (ok && leader && mine) {
-                            const uint64_t qd = make_desc(qbase + (blocks % Sh::kQBuffers) * Sh::kQTile + (i * Sh::kChunks + p * Sh::kKChunks) * (kLanes * 128), 16, 1024);
+                            const uint64_t qd = make_desc(qbase + (blocks % Sh::kQBuffers) * Sh::kQTile + p * Sh::kKChunks * (kLanes * 128), 16, 1024);
                             const uint64_t kd = make_desc(ring + r.stage * Sh::kStage, 16, Sh::kKChunks * 1024);
 #pragma unroll
                             for (int k = 0; k < 4 * Sh::kKChunks; ++k)
-                                mma_ss(tmem + b * 128, qd + ((k / 4) * (kLanes * 128) + (k & 3) * 32) / 16, kd + ((k / 4) * 1024 + (k & 3) * 32) / 16,
+                                mma_ss(column(), qd + ((k / 4) * (kLanes * 128) + (k & 3) * 32) / 16, kd + ((k / 4) * 1024 + (k & 3) * 32) / 16,
                                        idesc(kTile, false), p > 0 || k > 0);
                             mma_commit(empty(r.stage));
-                            if (p + 1 == Sh::kKStages) mma_commit(s_full(b));
+                            if (p + 1 == Sh::kKStages) mma_commit(s_full(x.stage));
                         }
                         __syncwarp();
                     }
                 };
-                auto pv = [&](int i, int b, bool fresh, bool mine) {
+                auto pv = [&](bool fresh, bool mine) {
 #pragma unroll
                     for (int p = 0; p < Sh::kVStages; ++p, r.next()) {
                         arrived(r.stage, r.round);
@@ -762,10 +749,10 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                             const uint64_t vd = make_desc(ring + r.stage * Sh::kStage, 1024, Sh::kChunks * 1024);
 #pragma unroll
                             for (int k = 0; k < Sh::kVTokens / 16; ++k)
-                                mma_ts(tmem + 256 + i * 128, tmem + b * 128 + (p * Sh::kVTokens / 16 + k) * 8,
+                                mma_ts(tmem + Sh::kOColumn, column() + (p * Sh::kVTokens / 16 + k) * 8,
                                        vd + k * 2 * Sh::kChunks * 1024 / 16, idesc(D, true), !fresh || p > 0 || k > 0);
                             mma_commit(empty(r.stage));
-                            if (p + 1 == Sh::kVStages) mma_commit(o_done(b));
+                            if (p + 1 == Sh::kVStages) mma_commit(o_done(x.stage));
                         }
                         __syncwarp();
                     }
@@ -778,40 +765,27 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
                         if (t == n - 1 && ok && leader) mma_commit(q_empty(blocks % Sh::kQBuffers));
                         __syncwarp();
                     };
-                    if constexpr (RT == 1) {
-                        // unit u + t in buffer (u + t) & 1, free once the P V of two units before is done
 #pragma unroll 1
-                        for (int t = -1; t < n && ok; ++t) {
-                            if (t + 1 < n) {
-                                const uint32_t v = u + t + 1;
-                                if (part == 0 && v >= 2) ok = ok && warp_wait(o_done(v & 1), ((v >> 1) - 1) & 1);
-                                qk(0, v & 1, part == 0);
-                                if (part == 0) q_done(t + 1);
-                            }
-                            if (t >= 0) {
-                                const uint32_t v = u + t;
-                                if (part == 1) {
-                                    ok = ok && warp_wait(p_full(v & 1), (v >> 1) & 1);
-                                    if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(0), (blocks - 1) & 1);
-                                }
-                                pv(0, v & 1, t == 0, part == 1);
+                    for (int t = -1; t < n && ok; ++t) {
+                        if (t + 1 < n) {
+                            // an S buffer is free once the P V of its last use is done
+                            if (part == 0 && x.round > 0) ok = ok && warp_wait(o_done(x.stage), (x.round - 1) & 1);
+                            qk(part == 0);
+                            if (part == 0) {
+                                q_done(t + 1);
+                                x.next();
                             }
                         }
-                    } else {
-                        // a row tile's own buffer is free once its P V is done
-#pragma unroll 1
-                        for (int t = 0; t < n && ok; ++t) {
-                            const uint32_t v = u + t;
-                            if (v > 0) ok = ok && warp_wait(o_done(part), (v - 1) & 1);
-                            qk(part, part, true);
-                            q_done(t);
-                            ok = ok && warp_wait(p_full(part), v & 1);
-                            if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free(part), (blocks - 1) & 1);
-                            pv(part, part, t == 0, true);
+                        if (t >= 0) {
+                            if (part == 1) {
+                                ok = ok && warp_wait(p_full(x.stage), x.round & 1);
+                                if (t == 0 && blocks > 0) ok = ok && warp_wait(o_free, (blocks - 1) & 1);
+                            }
+                            pv(t == 0, part == 1);
+                            if (part == 1) x.next();
                         }
                     }
                     for (int p = 0; p < 2; ++p, r.next()) arrived(r.stage, r.round);      // those of the sums on their way out
-                    u += n;
                     ++blocks;
                 } while (ok && w.next(a));
             }
@@ -819,18 +793,18 @@ __global__ void __launch_bounds__(Shape<D, RT, C>::kThreads, 1) attend_tc_kernel
     }
     if (!ok && lane == 0) report(a.d_status, GDN_ERR_TIMEOUT);
     if (c + 1 == a.ctas)
-        for (int s = tid; s < a.B; s += Sh::kThreads) {
+        for (int s = tid; s < a.B; s += kThreads) {
             int past;
             if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
         }
     fence_before();
     __syncthreads();
     fence_after();
-    if (wid == 4 * RT + 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+    if (wid == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }
 
-template <int D, int RT, int C> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
-    using Sh = Shape<D, RT, C>;
+template <int D, int C> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
+    using Sh = Shape<D, C>;
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     const AttendArgs &a = t.a;
@@ -842,10 +816,10 @@ template <int D, int RT, int C> cudaError_t launch(TcArgs &t, cudaStream_t strea
     };
     const cuuint64_t es = 2, page = 1ull << a.kv.page_log2;
     {
-        // a row tile: G heads of tt tokens of one slot (tokens past T read zeros)
+        // a block's rows: G heads of TB tokens of one slot (tokens past T read zeros)
         const cuuint64_t dims[5] = {64, D / 64, (cuuint64_t)a.H, (cuuint64_t)a.T, (cuuint64_t)a.B};
         const cuuint64_t strides[4] = {128, D * es, a.H * D * es, (cuuint64_t)a.T * a.H * D * es};
-        const cuuint32_t box[5] = {64, 1, (cuuint32_t)a.G, (cuuint32_t)t.tt, 1};
+        const cuuint32_t box[5] = {64, 1, (cuuint32_t)a.G, (cuuint32_t)a.TB, 1};
         if (!map(&t.q_map, a.q, dims, strides, box)) return cudaErrorInvalidValue;
     }
     // a page of a kv head: groups of 8 tokens, in each the 64-column chunks, in each 8 rows
@@ -855,19 +829,19 @@ template <int D, int RT, int C> cudaError_t launch(TcArgs &t, cudaStream_t strea
     const cuuint32_t vbox[5] = {64, 8, D / 64, (cuuint32_t)(page < Sh::kVTokens ? page / 8 : Sh::kVTokens / 8), 1};
     if (!map(&t.k_map, a.kv.k, dims, strides, kbox) || !map(&t.v_map, a.kv.v, dims, strides, vbox)) return cudaErrorInvalidValue;
 
-    constexpr size_t smem = Sh::kQBytes + Sh::kRing * Sh::kStage + sizeof(Control<RT, Sh::kRing>);
+    constexpr size_t smem = Sh::kQBytes + Sh::kRing * Sh::kStage + sizeof(Control<Sh::kRing>);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     static PerContext<int> limits;
     unsigned long long ctx = 0;
     int set = 0;
     if (!current_context_id(&ctx) || !limits.get(ctx, &set)) {
-        const cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, RT, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel<D, C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
         if (current_context_id(&ctx)) limits.put(ctx, 1);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.ctas), 1, 1);
-    cfg.blockDim = dim3(Sh::kThreads, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -875,36 +849,30 @@ template <int D, int RT, int C> cudaError_t launch(TcArgs &t, cudaStream_t strea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, RT, C>, t);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, attend_tc_kernel<D, C>, t);
     return e != cudaSuccess ? e : launch_attend_join(a, GDN_BF16, stream);
 }
 
-// Row tiles of a CTA: two where a slot's rows fill more than one and tensor memory holds both tiles' O.
-int row_tiles(int T, int G, int D) { return D <= 128 && T > kLanes / G ? 2 : 1; }
 // Copies of the rows: four where a slot has at most 32.
 int copies(int T, int G) { return (long long)T * G <= 32 ? 4 : 1; }
 
-template <int D> cudaError_t launch_d(TcArgs &t, int rt, int c, cudaStream_t stream) {
-    if constexpr (D <= 128)
-        if (rt == 2) return launch<D, 2, 1>(t, stream);
-    return c == 4 ? launch<D, 1, 4>(t, stream) : launch<D, 1, 1>(t, stream);
+template <int D> cudaError_t launch_d(TcArgs &t, cudaStream_t stream) {
+    return copies(t.a.T, t.a.G) == 4 ? launch<D, 4>(t, stream) : launch<D, 1>(t, stream);
 }
 
 }  // namespace
 
 AttendBlock attend_bf16_block(int T, int G, int D) {
-    const int rt = row_tiles(T, G, D), c = copies(T, G), rows = kLanes / c, tt = rows / G < T ? rows / G : T;
+    const int c = copies(T, G), rows = kLanes / c;
     // A part of many rows costs as much as a tile's keys and values.  A block's beginning and end take 3 to 5 us, a tile of 128
     // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).
-    return {rt * rows, rt * tt, c > 1 ? 1 : 3, D == 64 ? 4 : 3};
+    return {rows, rows / G < T ? rows / G : T, c > 1 ? 1 : 3, D == 64 ? 4 : 3};
 }
 
 cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t stream) {
     TcArgs t{};
     t.a = a;
-    const int rt = row_tiles(a.T, a.G, a.D), c = copies(a.T, a.G);
-    t.tt = a.TB / rt;
-    return a.D == 64 ? launch_d<64>(t, rt, c, stream) : a.D == 128 ? launch_d<128>(t, rt, c, stream) : launch_d<256>(t, rt, c, stream);
+    return a.D == 64 ? launch_d<64>(t, stream) : a.D == 128 ? launch_d<128>(t, stream) : launch_d<256>(t, stream);
 }
 
 }  // namespace gdn
