@@ -21,7 +21,8 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 8;               // numbers a thread holds
+constexpr int kPer = 8;               // numbers a thread holds of a head
+constexpr int kBatch = 4;             // heads that a thread has in flight
 constexpr unsigned kFull = 0xffffffffu;
 
 template <typename E> struct Vec;
@@ -58,14 +59,16 @@ template <> struct Vec<__nv_bfloat16> {
 };
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kLanes = D / kPer;              // threads a head
     constexpr int kHeads = kThreads / kLanes;     // heads at a time
     __shared__ float2 turn[D / 2];                // cos and sin of the token's angles
     __shared__ int parents[64];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int tid = threadIdx.x, sub = tid % kLanes, group = tid / kLanes;
-    const int half = a.rope_dims / 2, first = a.q ? 0 : a.H, heads = a.H + 2 * a.Hk;
+    const int half = a.rope_dims / 2, heads = a.H + 2 * a.Hk;
+    // this CTA's heads: of every gridDim.y groups of kHeads one, kBatch of them in flight
+    const int head0 = (a.q ? 0 : a.H) + blockIdx.y * kHeads + group, step = gridDim.y * kHeads;
     const int page = 1 << a.kv.page_log2;
     for (long long row = blockIdx.x; row < (long long)a.B * a.T; row += gridDim.x) {
         const int s = int(row / a.T), t = int(row % a.T);
@@ -82,6 +85,24 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
                 continue;
             }
         }
+        const size_t from = (size_t)s * a.T + source;
+        auto kind_of = [&](int h) { return h < a.H ? 0 : h < a.H + a.Hk ? 1 : 2; };     // q, k, v
+        auto load = [&](int h) {
+            const int kind = kind_of(h), hk = h - a.H - (kind == 2 ? a.Hk : 0);
+            const E *base = kind == 0   ? static_cast<const E *>(a.q) + from * a.ld_q + (size_t)h * D
+                            : kind == 1 ? static_cast<const E *>(a.k) + from * a.ld_k + (size_t)hk * D
+                                        : static_cast<const E *>(a.v) + from * a.ld_v + (size_t)hk * D;
+            return *reinterpret_cast<const Vec<E> *>(base + sub * kPer);
+        };
+        // the first rows are on their way while the angles are computed
+        Vec<E> v[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (head0 + b * step < heads) v[b] = load(head0 + b * step);
+        const int place = past + t;
+        const int id = a.kv.table[(size_t)s * a.kv.max_pages + (place >> a.kv.page_log2)];
+        const bool held = id >= 0 && id < a.kv.n_pages;
+        if (!held && tid == 0) report(a.d_status, GDN_ERR_PAGE);
         __syncthreads();                          // the last token's angles are no longer read
         if (a.parent) {
             if (tid <= t) {
@@ -96,72 +117,67 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
             depth = 0;
             for (int p = parents[t]; p >= 0; p = parents[p]) ++depth;
         }
-        const unsigned long long position = (unsigned long long)(past + depth);
         if (tid < half) {
             // turns a position: the whole ones do not count, so the rest is a 64-bit fraction
             const double f = (double)a.freq[tid] * 0.15915494309189533577;
             const long long part = __double2ll_rn((f - rint(f)) * 18446744073709551616.0);
-            const int x = int((unsigned long long)part * position >> 32);
+            const int x = int((unsigned long long)part * (unsigned long long)(past + depth) >> 32);
             float sn, cs;
             sincospif((float)x * 0x1p-31f, &sn, &cs);
             turn[tid] = make_float2(cs, sn);
         }
         __syncthreads();
-        const int place = past + t;
-        const int id = a.kv.table[(size_t)s * a.kv.max_pages + (place >> a.kv.page_log2)];
-        const bool held = id >= 0 && id < a.kv.n_pages;
-        if (!held && tid == 0) report(a.d_status, GDN_ERR_PAGE);
-        const size_t from = (size_t)s * a.T + source;
-        for (int h0 = first; h0 < heads; h0 += kHeads) {
-            const int h = h0 + group;
-            const bool on = h < heads;
-            const int kind = h < a.H ? 0 : h < a.H + a.Hk ? 1 : 2;      // q, k, v
-            const int hk = h - a.H - (kind == 2 ? a.Hk : 0);
-            Vec<E> v{};
-            if (on) {
-                const E *base = kind == 0   ? static_cast<const E *>(a.q) + from * a.ld_q + (size_t)h * D
-                                : kind == 1 ? static_cast<const E *>(a.k) + from * a.ld_k + (size_t)hk * D
-                                            : static_cast<const E *>(a.v) + from * a.ld_v + (size_t)hk * D;
-                v = *reinterpret_cast<const Vec<E> *>(base + sub * kPer);
-            }
-            float x[kPer];
-            v.get(x);
-            const float *w = kind == 0 ? a.q_norm : a.k_norm;
-            float sum = 0.f;
+        // where this thread's numbers are turned: pairs half apart (or beside one another), the lower ones first
+        const int i0 = sub * kPer, apart = half / kPer, lane = tid & 31;
+        const bool low = sub < apart, turned = i0 < a.rope_dims;
+        const int other = (low ? lane + apart : lane - apart) & 31;
+        for (int h0 = head0 - group; h0 < heads; h0 += kBatch * step) {        // (the same in all lanes: they shuffle)
+            if (h0 != head0 - group)
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) sum += x[i] * x[i];
+                for (int b = 0; b < kBatch; ++b)
+                    if (h0 + group + b * step < heads) v[b] = load(h0 + group + b * step);
 #pragma unroll
-            for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-            if (kind < 2 && w) {
-                const float r = rsqrtf(sum / D + a.eps);
+            for (int b = 0; b < kBatch; ++b) {
+                if (h0 + b * step >= heads) break;
+                const int h = h0 + group + b * step, kind = kind_of(h), hk = h - a.H - (kind == 2 ? a.Hk : 0);
+                float x[kPer], y[kPer];
+                v[b].get(x);
+                const float *w = kind == 0 ? a.q_norm : a.k_norm;
+                if (a.q_norm || a.k_norm) {
+                    float sum = 0.f;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) x[i] = x[i] * r * w[sub * kPer + i];
-            }
-            // the other half of each pair: rope_dims / 2 numbers further on, or beside it
-            const int step = half / kPer, i0 = sub * kPer;
-            const int lane = tid & 31;
-            const bool low = sub < step, turned = i0 < a.rope_dims && kind < 2;
-            float y[kPer];
-            if (!a.adjacent) {
+                    for (int i = 0; i < kPer; ++i) sum += x[i] * x[i];
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const float o = __shfl_sync(kFull, x[i], (low ? lane + step : lane - step) & 31);
-                    const float2 cs = turned ? turn[low ? i0 + i : i0 - half + i] : make_float2(1.f, 0.f);
-                    y[i] = turned ? (low ? x[i] * cs.x - o * cs.y : o * cs.y + x[i] * cs.x) : x[i];
+                    for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+                    if (kind < 2 && w) {
+                        const float r = rsqrtf(sum / D + a.eps);
+                        const float4 w0 = *reinterpret_cast<const float4 *>(w + i0), w1 = *reinterpret_cast<const float4 *>(w + i0 + 4);
+                        const float ww[kPer] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                        for (int i = 0; i < kPer; ++i) x[i] = x[i] * r * ww[i];
+                    }
                 }
-            } else {
+                if (!a.adjacent) {
 #pragma unroll
-                for (int i = 0; i < kPer; i += 2) {
-                    const float2 cs = turned ? turn[(i0 + i) / 2] : make_float2(1.f, 0.f);
-                    y[i] = turned ? x[i] * cs.x - x[i + 1] * cs.y : x[i];
-                    y[i + 1] = turned ? x[i] * cs.y + x[i + 1] * cs.x : x[i + 1];
+                    for (int i = 0; i < kPer; ++i) {
+                        const float o = __shfl_sync(kFull, x[i], other);
+                        const float2 cs = turned ? turn[low ? i0 + i : i0 - half + i] : make_float2(1.f, 0.f);
+                        y[i] = turned ? (low ? x[i] * cs.x - o * cs.y : o * cs.y + x[i] * cs.x) : x[i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kPer; i += 2) {
+                        const float2 cs = turned ? turn[(i0 + i) / 2] : make_float2(1.f, 0.f);
+                        y[i] = turned ? x[i] * cs.x - x[i + 1] * cs.y : x[i];
+                        y[i + 1] = turned ? x[i] * cs.y + x[i + 1] * cs.x : x[i + 1];
+                    }
                 }
+                if (kind < 2) v[b].set(y);        // v goes as it came
+                E *to = kind == 0 ? static_cast<E *>(a.q_out) + ((size_t)row * a.H + h) * D
+                                  : static_cast<E *>(kind == 1 ? a.kv.k : a.kv.v) + (long long)id * a.kv.page_stride +
+                                        ((size_t)hk * page + (place & (page - 1))) * D;
+                if (h < heads && (kind == 0 || held)) *reinterpret_cast<Vec<E> *>(to + i0) = v[b];
             }
-            if (kind < 2) v.set(y);               // v goes as it came
-            E *to = kind == 0 ? static_cast<E *>(a.q_out) + ((size_t)row * a.H + h) * D
-                              : static_cast<E *>(kind == 1 ? a.kv.k : a.kv.v) + (long long)id * a.kv.page_stride +
-                                    ((size_t)hk * page + (place & (page - 1))) * D;
-            if (on && (kind == 0 || held)) *reinterpret_cast<Vec<E> *>(to + sub * kPer) = v;
         }
     }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -171,8 +187,11 @@ template <typename E>
 cudaError_t launch(const AppendArgs &a, int sms, cudaStream_t stream) {
     auto kern = a.D == 64 ? append_kernel<E, 64> : a.D == 128 ? append_kernel<E, 128> : append_kernel<E, 256>;
     cudaLaunchConfig_t cfg = {};
-    const long long rows = (long long)a.B * a.T, most = 8LL * sms;       // as many as the SMs hold at once
-    cfg.gridDim = dim3(unsigned(rows < most ? rows : most), 1, 1);
+    // as many CTAs as the SMs hold at once: of tokens, and with few tokens of their heads too
+    const long long rows = (long long)a.B * a.T, most = 8LL * sms;
+    const int groups = ((a.q ? a.H : 0) + 2 * a.Hk + kThreads * kPer / a.D - 1) / (kThreads * kPer / a.D);
+    const long long spare = most / rows;
+    cfg.gridDim = dim3(unsigned(rows < most ? rows : most), unsigned(spare < 1 ? 1 : spare < groups ? spare : groups), 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
