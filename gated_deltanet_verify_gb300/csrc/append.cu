@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 8;               // numbers a thread holds of a head
-constexpr int kBatch = 4;             // heads that a thread has in flight
+constexpr int kBatch = 3;             // heads that a thread has in flight
 constexpr unsigned kFull = 0xffffffffu;
 
 template <typename E> struct Vec;
@@ -58,11 +58,14 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
-template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+template <typename E, int D, bool ADJACENT>
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kLanes = D / kPer;              // threads a head
     constexpr int kHeads = kThreads / kLanes;     // heads at a time
-    __shared__ float2 turn[D / 2];                // cos and sin of the token's angles
+    // cos and sin of the token's angles; a thread's pairs are as far apart as there are threads, so that they do not meet in a bank
+    __shared__ float2 turn[D / 2];
+    constexpr int kPairs = ADJACENT ? kPer / 2 : kPer, kApart = D / 2 / kPairs;
+    auto spot = [](int pair) { return pair % kPairs * kApart + pair / kPairs; };
     __shared__ int parents[64];
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int tid = threadIdx.x, sub = tid % kLanes, group = tid / kLanes;
@@ -70,8 +73,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     // this CTA's heads: of every gridDim.y groups of kHeads one, kBatch of them in flight
     const int head0 = (a.q ? 0 : a.H) + blockIdx.y * kHeads + group, step = gridDim.y * kHeads;
     const int page = 1 << a.kv.page_log2;
-    for (long long row = blockIdx.x; row < (long long)a.B * a.T; row += gridDim.x) {
-        const int s = int(row / a.T), t = int(row % a.T);
+    // where this thread's numbers are turned: pairs half apart (or beside one another), the lower ones first
+    const int i0 = sub * kPer, apart = half / kPer, lane = tid & 31;
+    const bool low = sub < apart, turned = i0 < a.rope_dims;
+    const int other = (low ? lane + apart : lane - apart) & 31;
+    const bool norms = a.q_norm || a.k_norm;
+    // turns a position: the whole ones do not count, so the rest is a 64-bit fraction
+    unsigned long long part = 0;
+    if (tid < half) {
+        const double f = (double)a.freq[tid] * 0.15915494309189533577;
+        part = (unsigned long long)__double2ll_rn((f - rint(f)) * 18446744073709551616.0);
+    }
+    for (int row = blockIdx.x; row < a.B * a.T; row += gridDim.x) {
+        const int s = row / a.T, t = row - s * a.T;
         int past;
         const int n = live_tokens(a.kv, a.length, a.T, s, past);
         if (n < 0 && t == 0 && tid == 0) report(a.d_status, GDN_ERR_LENGTH);
@@ -86,13 +100,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             }
         }
         const size_t from = (size_t)s * a.T + source;
-        auto kind_of = [&](int h) { return h < a.H ? 0 : h < a.H + a.Hk ? 1 : 2; };     // q, k, v
+        const int k_head = a.H, v_head = a.H + a.Hk;  // heads in one row: q, then k, then v
+        const E *from_q = static_cast<const E *>(a.q) + from * a.ld_q + i0;
+        const E *from_k = static_cast<const E *>(a.k) + from * a.ld_k - (size_t)k_head * D + i0;
+        const E *from_v = static_cast<const E *>(a.v) + from * a.ld_v - (size_t)v_head * D + i0;
         auto load = [&](int h) {
-            const int kind = kind_of(h), hk = h - a.H - (kind == 2 ? a.Hk : 0);
-            const E *base = kind == 0   ? static_cast<const E *>(a.q) + from * a.ld_q + (size_t)h * D
-                            : kind == 1 ? static_cast<const E *>(a.k) + from * a.ld_k + (size_t)hk * D
-                                        : static_cast<const E *>(a.v) + from * a.ld_v + (size_t)hk * D;
-            return *reinterpret_cast<const Vec<E> *>(base + sub * kPer);
+            return *reinterpret_cast<const Vec<E> *>((h < k_head ? from_q : h < v_head ? from_k : from_v) + (size_t)h * D);
         };
         // the first rows are on their way while the angles are computed
         Vec<E> v[kBatch];
@@ -118,19 +131,24 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             for (int p = parents[t]; p >= 0; p = parents[p]) ++depth;
         }
         if (tid < half) {
-            // turns a position: the whole ones do not count, so the rest is a 64-bit fraction
-            const double f = (double)a.freq[tid] * 0.15915494309189533577;
-            const long long part = __double2ll_rn((f - rint(f)) * 18446744073709551616.0);
-            const int x = int((unsigned long long)part * (unsigned long long)(past + depth) >> 32);
+            const int x = int(part * (unsigned long long)(past + depth) >> 32);
             float sn, cs;
             sincospif((float)x * 0x1p-31f, &sn, &cs);
-            turn[tid] = make_float2(cs, sn);
+            turn[spot(tid)] = make_float2(cs, sn);
         }
         __syncthreads();
-        // where this thread's numbers are turned: pairs half apart (or beside one another), the lower ones first
-        const int i0 = sub * kPer, apart = half / kPer, lane = tid & 31;
-        const bool low = sub < apart, turned = i0 < a.rope_dims;
-        const int other = (low ? lane + apart : lane - apart) & 31;
+        // the same for every head: y = x cos + (the pair's other number) sin, with the sine's sign
+        float cs[kPer], sn[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const bool first = ADJACENT ? !(i & 1) : low;
+            const float2 f = turned ? turn[spot(ADJACENT ? (i0 + i) / 2 : low ? i0 + i : i0 - half + i)] : make_float2(1.f, 0.f);
+            cs[i] = f.x;
+            sn[i] = first ? -f.y : f.y;
+        }
+        E *to_q = static_cast<E *>(a.q_out) + (size_t)row * a.H * D + i0;
+        const long long at = (long long)id * a.kv.page_stride + (size_t)(place & (page - 1)) * D + i0;
+        E *to_k = static_cast<E *>(a.kv.k) + at - (size_t)k_head * page * D, *to_v = static_cast<E *>(a.kv.v) + at - (size_t)v_head * page * D;
         for (int h0 = head0 - group; h0 < heads; h0 += kBatch * step) {        // (the same in all lanes: they shuffle)
             if (h0 != head0 - group)
 #pragma unroll
@@ -139,44 +157,34 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 if (h0 + b * step >= heads) break;
-                const int h = h0 + group + b * step, kind = kind_of(h), hk = h - a.H - (kind == 2 ? a.Hk : 0);
-                float x[kPer], y[kPer];
-                v[b].get(x);
-                const float *w = kind == 0 ? a.q_norm : a.k_norm;
-                if (a.q_norm || a.k_norm) {
-                    float sum = 0.f;
+                const int h = h0 + group + b * step;
+                if (h0 + b * step < v_head) {     // not all are v, which goes as it came
+                    float x[kPer], y[kPer];
+                    v[b].get(x);
+                    if (norms) {
+                        const float *w = h < k_head ? a.q_norm : a.k_norm;
+                        float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kPer; ++i) sum += x[i] * x[i];
+                        for (int i = 0; i < kPer; ++i) sum += x[i] * x[i];
 #pragma unroll
-                    for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-                    if (kind < 2 && w) {
-                        const float r = rsqrtf(sum / D + a.eps);
-                        const float4 w0 = *reinterpret_cast<const float4 *>(w + i0), w1 = *reinterpret_cast<const float4 *>(w + i0 + 4);
-                        const float ww[kPer] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                        for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
+                        if (w) {
+                            const float r = rsqrtf(sum / D + a.eps);
+                            const float4 w0 = *reinterpret_cast<const float4 *>(w + i0), w1 = *reinterpret_cast<const float4 *>(w + i0 + 4);
+                            const float ww[kPer] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                        for (int i = 0; i < kPer; ++i) x[i] = x[i] * r * ww[i];
+                            for (int i = 0; i < kPer; ++i) x[i] = x[i] * r * ww[i];
+                        }
                     }
-                }
-                if (!a.adjacent) {
 #pragma unroll
                     for (int i = 0; i < kPer; ++i) {
-                        const float o = __shfl_sync(kFull, x[i], other);
-                        const float2 cs = turned ? turn[low ? i0 + i : i0 - half + i] : make_float2(1.f, 0.f);
-                        y[i] = turned ? (low ? x[i] * cs.x - o * cs.y : o * cs.y + x[i] * cs.x) : x[i];
+                        const float o = ADJACENT ? x[i ^ 1] : __shfl_sync(kFull, x[i], other);
+                        y[i] = turned ? fmaf(o, sn[i], x[i] * cs[i]) : x[i];
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kPer; i += 2) {
-                        const float2 cs = turned ? turn[(i0 + i) / 2] : make_float2(1.f, 0.f);
-                        y[i] = turned ? x[i] * cs.x - x[i + 1] * cs.y : x[i];
-                        y[i + 1] = turned ? x[i] * cs.y + x[i + 1] * cs.x : x[i + 1];
-                    }
+                    if (h < v_head) v[b].set(y);
                 }
-                if (kind < 2) v[b].set(y);        // v goes as it came
-                E *to = kind == 0 ? static_cast<E *>(a.q_out) + ((size_t)row * a.H + h) * D
-                                  : static_cast<E *>(kind == 1 ? a.kv.k : a.kv.v) + (long long)id * a.kv.page_stride +
-                                        ((size_t)hk * page + (place & (page - 1))) * D;
-                if (h < heads && (kind == 0 || held)) *reinterpret_cast<Vec<E> *>(to + i0) = v[b];
+                E *to = h < k_head ? to_q + (size_t)h * D : (h < v_head ? to_k : to_v) + (size_t)h * page * D;
+                if (h < heads && (h < k_head || held)) *reinterpret_cast<Vec<E> *>(to) = v[b];
             }
         }
     }
@@ -185,12 +193,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 
 template <typename E>
 cudaError_t launch(const AppendArgs &a, int sms, cudaStream_t stream) {
-    auto kern = a.D == 64 ? append_kernel<E, 64> : a.D == 128 ? append_kernel<E, 128> : append_kernel<E, 256>;
+    auto kern = a.D == 64    ? (a.adjacent ? append_kernel<E, 64, true> : append_kernel<E, 64, false>)
+                : a.D == 128 ? (a.adjacent ? append_kernel<E, 128, true> : append_kernel<E, 128, false>)
+                             : (a.adjacent ? append_kernel<E, 256, true> : append_kernel<E, 256, false>);
     cudaLaunchConfig_t cfg = {};
-    // as many CTAs as the SMs hold at once: of tokens, and with few tokens of their heads too
-    const long long rows = (long long)a.B * a.T, most = 8LL * sms;
+    // As many CTAs as the SMs hold at once, which share out the tokens; with few tokens their heads too, twice as many then
+    // (32 x 16 tokens: 6.1 us, with one CTA a token 7.5).
+    const long long rows = (long long)a.B * a.T, most = 4LL * sms, spare = 2 * most / rows;
     const int groups = ((a.q ? a.H : 0) + 2 * a.Hk + kThreads * kPer / a.D - 1) / (kThreads * kPer / a.D);
-    const long long spare = most / rows;
     cfg.gridDim = dim3(unsigned(rows < most ? rows : most), unsigned(spare < 1 ? 1 : spare < groups ? spare : groups), 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.stream = stream;
