@@ -37,7 +37,7 @@ namespace {
 constexpr int kTile = kTileBf16;
 constexpr int kLanes = 128;           // tensor memory's: rows of a block
 constexpr int kThreads = 7 * 32;      // four warps of softmax, one of loads, two of MMAs
-constexpr int kSpin = 1 << 22;        // mbarrier polls before a wait gives up
+constexpr int kSpin = 1 << 20;        // mbarrier polls before a wait gives up
 constexpr float kSlack = 8.f;         // powers of two by which a maximum may grow unmoved
 
 // C: copies of the rows, 128 / C of them, side by side in tensor memory; copy i takes the i-th C-th of every tile's keys.
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     } else if (wid == 4) {
         if (lane < Sh::kRing) {
             mbar_init(full(lane), 1);
-            mbar_init(empty(lane), 1);
+            mbar_init(empty(lane), 2);            // by both MMA warps
         }
         if (lane < 3) {
             mbar_init(s_full(lane), 1);
@@ -337,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
         if (together) return;
-        share.set(scan_total<kTile>(a), a);
-        if (c < share.ctas) at = scan_find<kTile>(a, share.start(c));
+        at = warp_place<kTile>(a, c, share);
     };
     if (together) {
         begin();
@@ -621,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 }
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
                 softmax_sync();
-                if (tl < 2) mbar_arrive(empty(r.after(tl).stage));
+                if (tl < 4) mbar_arrive(empty(r.after(tl / 2).stage));
                 r.next(2);
                 if (!ok || !w.next(a)) break;
             } while (true);
@@ -711,23 +710,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     }
             } else if (wid <= 6) {
                 // ---- the MMAs, from two warps: an MMA's end is known some 400 cycles after it, and what one warp waits for the
-                // other need not: one makes S, the other takes P V.  Both wait for every stage of the ring in its order, whether theirs or not: a stage's barrier tells the last
-                // round from the one before it only to who has seen all of them.
+                // other need not: one makes S, the other takes P V.  Both pass every stage of the ring in its order, whether theirs or
+                // not, and a stage is only filled again when both have: its barrier has two phases, so that who falls a
+                // round behind would wait for ever, and who runs ahead would take the last round's for this one's.
                 const int part = wid - 5;
                 const bool leader = elect_one();  // one thread issues all of a warp's, so that its commits cover them
                 Ring<Sh::kRing> r;                // the next stage
                 Ring<Sh::kBuffers> x;             // this warp's next S
                 int blocks = 0;
-                auto arrived = [&](uint32_t st, uint32_t round) {
-                    ok = ok && warp_wait(full(st), round & 1);
+                auto arrived = [&](bool mine) {
+                    ok = ok && warp_wait(full(r.stage), r.round & 1);
                     fence_after();
+                    if (ok && leader && !mine) mbar_arrive(empty(r.stage));
                 };
                 // S.  Who does not take the stages passes them by
                 auto column = [&] { return tmem + x.stage * 128 + (x.stage == 2 ? 128 : 0); };
                 auto qk = [&](bool mine) {
 #pragma unroll
                     for (int p = 0; p < Sh::kKStages; ++p, r.next()) {
-                        arrived(r.stage, r.round);
+                        arrived(mine);
                         if (ok && leader && mine) {
                             const uint64_t qd = make_desc(qbase + (blocks % Sh::kQBuffers) * Sh::kQTile + p * Sh::kKChunks * (kLanes * 128), 16, 1024);
                             const uint64_t kd = make_desc(ring + r.stage * Sh::kStage, 16, Sh::kKChunks * 1024);
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 auto pv = [&](bool fresh, bool mine) {
 #pragma unroll
                     for (int p = 0; p < Sh::kVStages; ++p, r.next()) {
-                        arrived(r.stage, r.round);
+                        arrived(mine);
                         if (ok && leader && mine) {
                             const uint64_t vd = make_desc(ring + r.stage * Sh::kStage, 1024, Sh::kChunks * 1024);
 #pragma unroll
@@ -758,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     }
                 };
                 do {
-                    ok = ok && warp_wait(q_full(blocks % Sh::kQBuffers), (blocks / Sh::kQBuffers) & 1);
+                    if (part == 0) ok = ok && warp_wait(q_full(blocks % Sh::kQBuffers), (blocks / Sh::kQBuffers) & 1);
                     const int n = w.j1 - w.j0;
                     // Q is free for the next block once the last S is made
                     auto q_done = [&](int t) {
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                             if (part == 1) x.next();
                         }
                     }
-                    for (int p = 0; p < 2; ++p, r.next()) arrived(r.stage, r.round);      // those of the sums on their way out
+                    r.next(2);                    // those of the sums on their way out, which the softmax warps pass
                     ++blocks;
                 } while (ok && w.next(a));
             }

@@ -195,15 +195,25 @@ template <int TK> __device__ __forceinline__ int scan_begin(const AttendArgs &a,
     return before;
 }
 
+// a warp by itself, with at most kScanPairs pairs
+template <int TK> __device__ __forceinline__ Place warp_place(const AttendArgs &a, int c, Share &share) {
+    if (a.B * a.n_tb > 32) {
+        share.set(scan_total<TK>(a), a);
+        return c < share.ctas ? scan_find<TK>(a, share.start(c)) : Place{0, 0};
+    }
+    const int n = pair_tiles<TK>(a, threadIdx.x & 31), upto = scan_warp(n);
+    share.set(__shfl_sync(kWarp, upto, 31), a);
+    if (c >= share.ctas) return Place{0, 0};
+    const int tile = share.start(c), l = __ffs(__ballot_sync(kWarp, upto > tile)) - 1;
+    return Place{l, tile - __shfl_sync(kWarp, upto - n, l)};
+}
+
 // The sum of all tiles, then the pair that tile `share.start(c)` is in; called by the whole CTA (THREADS of them).
 // scratch: THREADS / 32 + 2 words of shared memory.
 template <int TK, int THREADS>
 __device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &share, int *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, pairs = a.B * a.n_tb;
-    if (pairs <= kScanPairs) {
-        share.set(scan_total<TK>(a), a);
-        return c < share.ctas ? scan_find<TK>(a, share.start(c)) : Place{0, 0};
-    }
+    if (pairs <= kScanPairs) return warp_place<TK>(a, c, share);
     const int chunk = (pairs + THREADS - 1) / THREADS;
     const int i0 = min(pairs, tid * chunk), i1 = min(pairs, i0 + chunk);
     int mine = 0;

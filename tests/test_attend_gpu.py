@@ -97,6 +97,10 @@ CASES = {
     "window over tree": dict(T=40, H=6, Hk=2, D=128, page=16, past=[0, 200, 1000], window=7, n_sink=3, tree=True),
     "window over tree, no sinks": dict(T=64, H=6, Hk=2, D=64, page=16, past=[3, 130], window=2, tree=True),
     "many slots": dict(T=2, H=8, Hk=2, D=64, page=16, past=[(37 * i) % 400 for i in range(170)]),
+    "one slot, long": dict(T=16, H=6, Hk=1, D=256, page=64, past=[13001]),
+    "one slot, longer": dict(T=1, H=8, Hk=2, D=128, page=128, past=[26000]),
+    "one slot, small heads, long": dict(T=2, H=8, Hk=4, D=64, page=16, past=[50011]),
+    "three slots, one long": dict(T=4, H=8, Hk=4, D=128, page=32, past=[25000, 7, 300], length=[3, 4, 0]),
     "one long, many short": dict(T=1, H=8, Hk=2, D=128, page=64, past=[9000] + [i % 50 for i in range(40)]),
     "large scores": dict(T=3, H=4, Hk=2, D=64, page=16, past=[300], scale=6.0),
     "negative scale": dict(T=3, H=4, Hk=2, D=128, page=16, past=[300], scale=-0.2),
@@ -224,6 +228,25 @@ def test_two_streams_with_their_own_workspaces(dtype):
             r.call(stream=s)
     for r in runs:
         r.check()
+
+
+@pytest.mark.parametrize("sizes", [dict(T=16, H=32, Hk=8, D=128, page=128, past=[8000]),
+                                   dict(T=16, H=24, Hk=4, D=256, page=64, past=[5000]),
+                                   dict(T=40, H=8, Hk=4, D=64, page=64, past=[9000, 300])])
+def test_launch_after_launch(sizes):
+    """Hundreds of launches with nothing between them: the warps of a CTA meet in every order."""
+    r = Run(Case(**sizes))
+    r.call()
+    first = r.got().clone()
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        for _ in range(20):
+            r.call(stream=stream)
+    for _ in range(20):
+        graph.replay()
+    assert torch.equal(first, r.got())
+    r.check()
 
 
 def test_far_pages():
