@@ -17,9 +17,10 @@
 //     (three, or two for D = 256), so that the next S is made while this one's softmax runs.  (Two row tiles a CTA, each with
 //     its own S, O and softmax warps, halve what the keys and values cost in shared memory, but ran slower: the chains
 //     of one tile's S, softmax and P V are what binds, and two of them took 4950 cycles where a single one takes 2200.)
-//   * 128 threads do the softmax, a row each (tensor memory's lane), so no value crosses threads.  Where a slot has at most
-//     32 rows they lie there four times, and each copy's warp takes a quarter of every tile's keys (its other weights are
-//     zeros); the four sums are added up at the end.  One warp with all the keys took 1400 cycles a tile, this takes 600.
+//   * Two threads do the softmax of a row (tensor memory's lane), half of the keys each, and exchange their maxima: S, softmax
+//     and P V of a tile follow one another, so its time counts (1400 cycles with one thread a row, XXX with two).  Where a slot
+//     has at most 32 rows they lie there four times instead, and each copy's warp takes a quarter of every tile's keys (its
+//     other weights are zeros); the four sums are added up at the end.
 //   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
 //     at the ends of its share are joined with its neighbours' parts by attend_join.cu.
 //
@@ -36,7 +37,6 @@ namespace {
 
 constexpr int kTile = kTileBf16;
 constexpr int kLanes = 128;           // tensor memory's: rows of a block
-constexpr int kThreads = 7 * 32;      // four warps of softmax, one of loads, two of MMAs
 constexpr int kSpin = 1 << 20;        // mbarrier polls before a wait gives up
 constexpr float kSlack = 8.f;         // powers of two by which a maximum may grow unmoved
 
@@ -55,22 +55,30 @@ template <int D, int C> struct Shape {
     static constexpr int kBuffers = D == 256 ? 2 : 3;              // of S, in tensor memory beside O
     static constexpr int kOColumn = 128 * 2;                       // O, between the second S and the third
     static constexpr int kRows = kLanes / C;                       // of a block
-    static constexpr int kKeys = kTile / C;                        // of a tile that a copy takes
+    // Without copies two threads share a row, each with half of a tile's keys (and of O where it is moved).
+    static constexpr int kShare = C == 1 ? 2 : 1;
+    static constexpr int kKeys = kTile / (C * kShare);             // of a tile that a thread takes
+    static constexpr int kSoftmax = kShare * kLanes;               // threads
+    static constexpr int kLoads = kSoftmax / 32, kMmas = kLoads + 1;   // warps: one of loads, two of MMAs
+    static constexpr int kThreads = kSoftmax + 96;
     // a row's sums on their way out: two stages are shared out among the softmax threads
     static constexpr int kOut = 2 * kStage / kLanes;
     static_assert(kRing >= 5, "a tile's V, the next one's K, and one more");
 };
 
 // What a CTA keeps beside its tiles, behind them.
-template <int RING> struct Control {
+template <int RING, int THREADS> struct Control {
     uint64_t full[RING], empty[RING];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[3], p_full[3];    // S is there; P is there
     uint64_t o_done[3];               // P V is done: O is whole so far, the buffer free
     uint64_t o_free;                  // O has been read out
-    int scratch[kThreads / 32 + 2];
+    int scratch[THREADS / 32 + 2];
     uint32_t tmem;
-    float2 stats[kLanes];             // a row's maximum and sum, by copy
+    union {                           // of a row:
+        float2 stats[kLanes];         // maximum and sum, by copy
+        float each[2][kLanes];        // each thread's maximum of a tile, at the end its sum
+    };
     int parents[64];
     unsigned char depths[64];
 };
@@ -183,8 +191,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r) {
                      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
                  : "memory");
 }
-// the four softmax warps
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+// the softmax warps
+template <int THREADS> __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(THREADS) : "memory"); }
+template <int THREADS> __device__ __forceinline__ bool softmax_all(bool ok) {
+    int r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}\n" :
+                     "=r"(r) : "r"((int)ok), "n"(THREADS) : "memory");
+    return r != 0;
+}
+// the two warps that share 32 rows
+__device__ __forceinline__ void rows_sync(int warp) { asm volatile("bar.sync %0, 64;\n" ::"r"(2 + (warp & 3)) : "memory"); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -285,9 +301,10 @@ struct Walk {
 };
 
 template <int D, int C>
-__global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
+__global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(const __grid_constant__ TcArgs args) {
     using Sh = Shape<D, C>;
-    using Ctl = Control<Sh::kRing>;
+    constexpr int kThreads = Sh::kThreads;
+    using Ctl = Control<Sh::kRing, kThreads>;
     extern __shared__ __align__(1024) unsigned char sm[];         // no other shared memory, so that it starts at a swizzle atom
     Ctl &ctl = *reinterpret_cast<Ctl *>(sm + Sh::kQBytes + Sh::kRing * Sh::kStage);
     const AttendArgs &a = args.a;
@@ -302,23 +319,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     auto o_done = [&](int b) { return smem_u32(&ctl.o_done[b]); };
     const uint32_t o_free = smem_u32(&ctl.o_free);
 
-    if (wid == 5) {
+    if (wid == Sh::kMmas) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&ctl.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
-    } else if (wid == 4) {
+    } else if (wid == Sh::kLoads) {
         if (lane < Sh::kRing) {
             mbar_init(full(lane), 1);
             mbar_init(empty(lane), 2);            // by both MMA warps
         }
         if (lane < 3) {
             mbar_init(s_full(lane), 1);
-            mbar_init(p_full(lane), 128);
+            mbar_init(p_full(lane), Sh::kSoftmax);
             mbar_init(o_done(lane), 1);
         }
         if (lane < 2) {
             mbar_init(q_full(lane), 1);
             mbar_init(q_empty(lane), 1);
-            if (lane) mbar_init(o_free, 128);
+            if (lane) mbar_init(o_free, Sh::kSoftmax);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane < 3) prefetch_map(lane == 0 ? &args.q_map : lane == 1 ? &args.k_map : &args.v_map);
@@ -344,10 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
         at = find_place<kTile, kThreads>(a, c, share, ctl.scratch);
     }
     {
-        if (wid < 4) {
-            // ---- the softmax: thread = tensor memory's lane = row (of one of C copies)
-            const int tl = tid, copy = tl / Sh::kRows, row = tl % Sh::kRows;
-            const uint32_t lanes = tmem + ((uint32_t)(32 * wid) << 16), o_at = lanes + Sh::kOColumn;
+        if (wid < Sh::kLoads) {
+            // ---- the softmax: tensor memory's lane = row (of one of C copies), a thread or two for each
+            const int tl = tid % kLanes, half = tid / kLanes, copy = tl / Sh::kRows, row = tl % Sh::kRows;
+            const uint32_t lanes = tmem + ((uint32_t)(32 * (wid & 3)) << 16), o_at = lanes + Sh::kOColumn;
             const bool negative = a.scale < 0.f;
             // a scale of zero leaves all weights alike, and masked ones at none
             const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
@@ -374,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     last_pair = w.pair;
                     position = past + t;
                     if (a.parent) {
-                        softmax_sync();
-                        if (tl < w.span.t1) {
+                        softmax_sync<Sh::kSoftmax>();
+                        if (half == 0 && tl < w.span.t1) {
                             int p = a.parent[(size_t)s * a.T + tl];
                             if (p < -1 || p >= tl) {              // it hangs from the past
                                 report(a.d_status, GDN_ERR_TREE);
@@ -383,13 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                             }
                             ctl.parents[tl] = p;
                         }
-                        softmax_sync();
-                        if (tl < w.span.t1) {
+                        softmax_sync<Sh::kSoftmax>();
+                        if (half == 0 && tl < w.span.t1) {
                             int d = 0;
                             for (int p = ctl.parents[tl]; p >= 0; p = ctl.parents[p]) ++d;
                             ctl.depths[tl] = (unsigned char)d;
                         }
-                        softmax_sync();
+                        softmax_sync<Sh::kSoftmax>();
                         line = 0;
                         if (on) {
                             const int mine = ctl.depths[t];
@@ -407,14 +424,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 float m = -INFINITY, l = 0.f;
                 for (int q = 0; q < n; ++q) {
                     const uint32_t s_column = u.stage * 128 + (u.stage == 2 ? 128 : 0);
-                    const int k0 = w.span.tile(w.j0 + q) * kTile, mine0 = k0 + copy * Sh::kKeys;
+                    const int k0 = w.span.tile(w.j0 + q) * kTile, mine = (copy + half) * Sh::kKeys, mine0 = k0 + mine;
                     if (!dry) ok = ok && warp_wait(s_full(u.stage), u.round & 1);
-                    if (!ok) break;
+                    // (after a wait that gave up all go on without waiting, as the barriers among them want, and leave together)
                     fence_after();
                     // O is whole up to the tile before
                     auto wait_o = [&] { return warp_wait(o_done(before.stage), before.round & 1); };
                     if (busy) {
-                        const uint32_t s_at = lanes + s_column + copy * Sh::kKeys, p_at = dry ? o_at : lanes + s_column;
+                        const uint32_t s_at = lanes + s_column + mine, p_at = dry ? o_at : lanes + s_column;
                         uint32_t x[Sh::kKeys];
 #pragma unroll
                         for (int e = 0; e < Sh::kKeys; e += 32) tmem_ld32(s_at + e, x + e);
@@ -452,7 +469,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
 #pragma unroll
                         for (int e = 0; e < Sh::kKeys; e += 2)
                             top[e / 2 & 3] = max3(top[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                        const float to = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+                        float to = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+                        if constexpr (Sh::kShare == 2) {
+                            ctl.each[half][tl] = to;
+                            rows_sync(wid);
+                            to = fmaxf(to, ctl.each[half ^ 1][tl]);
+                            rows_sync(wid);
+                        }
                         const bool grows = on && (to - m) * sc > kSlack;
                         if (q == 0) {
                             m = fmaxf(m, to);
@@ -463,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                             l *= f;
                             m = up;
 #pragma unroll 1
-                            for (int e = 0; e < D; e += 32) {
+                            for (int e = half * (D / Sh::kShare); e < (half + 1) * (D / Sh::kShare); e += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(o_at + e, o);
                                 wait_ld();
@@ -485,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                                 sum[k & 1] = add2(sum[k & 1], pair2(y0, y1));
                                 p[k] = pack_bf16(y0, y1);
                             }
-                            tmem_st16(p_at + copy * (Sh::kKeys / 2) + e / 2, p);
+                            tmem_st16(p_at + mine / 2 + e / 2, p);
                         }
                         const float2 all2 = split2(add2(sum[0], sum[1]));
                         l += all2.x + all2.y;
@@ -502,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                         if (ok && !(key < w.span.hi && (key >= w.span.lo || key < sink))) {
                             const uint32_t to = ring + rv.stage * Sh::kStage + (g >> 3) * (Sh::kChunks * 1024) + (g & 7) * 128;
 #pragma unroll 1
-                            for (int e = 0; e < Sh::kChunks; ++e)
+                            for (int e = half; e < Sh::kChunks; e += Sh::kShare)
 #pragma unroll
                                 for (int k = 0; k < 8; ++k)       // (turned, so that lanes do not meet in a bank)
                                     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(to + e * 1024 + ((k + g) & 7) * 16), "r"(0)
@@ -532,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                 if constexpr (C > 1) {
                     // copies to a common maximum
                     ctl.stats[tl] = make_float2(m, l);
-                    softmax_sync();
+                    softmax_sync<Sh::kSoftmax>();
                     const float own = m;
                     m = -INFINITY;
                     l = 0.f;
@@ -545,15 +568,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     }
                     factor = own == -INFINITY ? 0.f : ex2((own - m) * sc);
                 }
+                if constexpr (Sh::kShare == 2) {
+                    ctl.each[half][tl] = l;
+                    softmax_sync<Sh::kSoftmax>();
+                    l = ctl.each[0][tl] + ctl.each[1][tl];
+                }
                 if (w.whole) factor /= l;
                 const size_t part0 = size_t(2 * c + (w.first ? 0 : 1)) * a.part_rows;
-                if (!w.whole && on && copy == 0) a.stats[part0 + row] = make_float2(m * sc, l);
+                if (!w.whole && on && copy == 0 && half == 0) a.stats[part0 + row] = make_float2(m * sc, l);
                 ok = ok && warp_wait(o_done(before.stage), before.round & 1);
                 fence_after();
                 // Rows go through the two stages, each turned by its number of 16 bytes (so that 32 lanes write 32 rows
                 // without conflicts), and leave side by side, four 16-byte pieces a thread in flight.  (Written by its own
                 // lane, 16 bytes a row at a time, 96 rows of 256 took 7400 cycles; as two bulk copies a row, 11500.)
-                constexpr int kCols = Sh::kOut / 4 < D ? Sh::kOut / 4 : D, kPieces = kCols / 4, kStep = 128 / kPieces;
+                constexpr int kCols = Sh::kOut / 4 < D ? Sh::kOut / 4 : D, kPieces = kCols / 4, kStep = Sh::kSoftmax / kPieces;
                 unsigned char *stage[2];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
@@ -567,16 +595,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                                                       ((p + from) & (kPieces - 1)) * 16);
                 };
                 const int rows = ok ? (last_t + 1 - first_t) * a.G : 0;            // as in every warp, unless a wait gave up
-                const int piece = tl % kPieces, row0 = tl / kPieces;
+                const int piece = tid % kPieces, row0 = tid / kPieces;
                 unsigned char *out0 = w.whole ? reinterpret_cast<unsigned char *>(static_cast<__nv_bfloat16 *>(a.out) +
                                                     (((size_t)s * a.T + first_t) * a.H + (size_t)w.kvh * a.G) * D + 4 * piece)
                                               : reinterpret_cast<unsigned char *>(a.partial + (part0 + row0) * D + 4 * piece);
 #pragma unroll 1
                 for (int at0 = 0; at0 < D; at0 += kCols) {
-                    if (at0 > 0) softmax_sync();
+                    if (at0 > 0) softmax_sync<Sh::kSoftmax>();
                     if (ok && busy) {
 #pragma unroll 1
-                        for (int e = 0; e < kCols; e += 32) {
+                        for (int e = half * (kCols / Sh::kShare); e < (half + 1) * (kCols / Sh::kShare); e += 32) {
                             uint32_t o[32];
                             tmem_ld32(o_at + at0 + e, o);
                             wait_ld();
@@ -590,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                         fence_before();
                         mbar_arrive(o_free);
                     }
-                    softmax_sync();
+                    softmax_sync<Sh::kSoftmax>();
 #pragma unroll 1
                     for (int x = row0; x < rows; x += 4 * kStep) {
                         float4 y[4];
@@ -619,8 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-                softmax_sync();
-                if (tl < 4) mbar_arrive(empty(r.after(tl / 2).stage));
+                ok = softmax_all<Sh::kSoftmax>(ok);
+                if (tid < 4) mbar_arrive(empty(r.after(tid / 2).stage));
                 r.next(2);
                 if (!ok || !w.next(a)) break;
             } while (true);
@@ -630,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
             const bool some = c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c));
             if (!some) {
                 // nothing to do: fewer tiles than CTAs
-            } else if (wid == 4) {
+            } else if (wid == Sh::kLoads) {
                 // ---- the loads
                 const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
                 Ring<Sh::kRing> r;                // the next stage to fill
@@ -708,12 +736,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
                         const uint32_t fills = r.round + (i < (int)r.stage);      // of stage i
                         if (fills > 0) mbar_wait(full(i), (fills - 1) & 1);
                     }
-            } else if (wid <= 6) {
+            } else {
                 // ---- the MMAs, from two warps: an MMA's end is known some 400 cycles after it, and what one warp waits for the
                 // other need not: one makes S, the other takes P V.  Both pass every stage of the ring in its order, whether theirs or
                 // not, and a stage is only filled again when both have: its barrier has two phases, so that who falls a
                 // round behind would wait for ever, and who runs ahead would take the last round's for this one's.
-                const int part = wid - 5;
+                const int part = wid - Sh::kMmas;
                 const bool leader = elect_one();  // one thread issues all of a warp's, so that its commits cover them
                 Ring<Sh::kRing> r;                // the next stage
                 Ring<Sh::kBuffers> x;             // this warp's next S
@@ -801,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const __grid_con
     fence_before();
     __syncthreads();
     fence_after();
-    if (wid == 5) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+    if (wid == Sh::kMmas) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }
 
 template <int D, int C> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
@@ -830,7 +858,7 @@ template <int D, int C> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
     const cuuint32_t vbox[5] = {64, 8, D / 64, (cuuint32_t)(page < Sh::kVTokens ? page / 8 : Sh::kVTokens / 8), 1};
     if (!map(&t.k_map, a.kv.k, dims, strides, kbox) || !map(&t.v_map, a.kv.v, dims, strides, vbox)) return cudaErrorInvalidValue;
 
-    constexpr size_t smem = Sh::kQBytes + Sh::kRing * Sh::kStage + sizeof(Control<Sh::kRing>);
+    constexpr size_t smem = Sh::kQBytes + Sh::kRing * Sh::kStage + sizeof(Control<Sh::kRing, Sh::kThreads>);
     static_assert(smem <= 227 * 1024, "shared memory of a CTA");
     static PerContext<int> limits;
     unsigned long long ctx = 0;
@@ -842,7 +870,7 @@ template <int D, int C> cudaError_t launch(TcArgs &t, cudaStream_t stream) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.ctas), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(Sh::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
