@@ -29,7 +29,6 @@ struct AppendArgs {
     float eps;
     const int32_t *length, *parent, *path;
     int *d_status;
-    size_t ext_kv, ext_table;         // bytes, for a checked build
 };
 
 // Attention of a batch over the cache (attend.cu, attend_f32.cu).
@@ -220,7 +219,9 @@ __device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &s
 #pragma unroll 1
     for (int i = i0; i < i1; ++i) mine += pair_tiles<TK>(a, i);
     const int upto = scan_warp(mine);
+    int *found = scratch + THREADS / 32;
     if (lane == 31) scratch[wid] = upto;
+    if (tid < 2) found[tid] = 0;          // what a CTA without a share gets: a place that is there
     __syncthreads();
     int before = upto - mine, total = 0;
     for (int w = 0; w < THREADS / 32; ++w) {
@@ -229,7 +230,6 @@ __device__ __forceinline__ Place find_place(const AttendArgs &a, int c, Share &s
         total += v;
     }
     share.set(total, a);
-    int *found = scratch + THREADS / 32;
     if (c < share.ctas) {
         int at = share.start(c) - before;
         if (at >= 0 && at < mine) {

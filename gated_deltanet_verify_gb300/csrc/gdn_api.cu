@@ -842,6 +842,8 @@ int check_attn_dims(const gdn_attn_dims *dims) {
         return fail(GDN_ERR_SHAPE, "n_heads (%d) must be 1 .. 64 times n_kv_heads (%d), at most 65536", d.n_heads, d.n_kv_heads);
     if (d.d_head != 64 && d.d_head != 128 && d.d_head != 256)
         return fail(GDN_ERR_SHAPE, "d_head must be 64, 128 or 256 (got %d)", d.d_head);
+    if ((long long)d.n_tokens * d.n_heads * d.d_head >= (1LL << 38))
+        return fail(GDN_ERR_SHAPE, "n_tokens * n_heads * d_head must be below 2^38 (got %d, %d, %d)", d.n_tokens, d.n_heads, d.d_head);
     if (d.page_tokens < 8 || d.page_tokens > 256 || (d.page_tokens & (d.page_tokens - 1)))
         return fail(GDN_ERR_SHAPE, "page_tokens must be a power of two in [8, 256] (got %d)", d.page_tokens);
     if (d.n_pages < 1 || d.max_pages < 1 || (long long)d.max_pages * d.page_tokens > (1LL << 30))

@@ -488,7 +488,8 @@ int gdn_accept_tree(const gdn_dims *dims, const int32_t *d_parent, const int32_t
  * Limits: d_head 64, 128 or 256; n_heads a multiple of n_kv_heads, at most 64
  * times as many; page_tokens a power of two, 8 .. 256; page_stride a multiple of
  * 8, at least n_kv_heads * page_tokens * d_head and below 2^38; max_pages *
- * page_tokens at most 2^30; B*T at most 2^24; n_heads at most 65536 (GDN_ERR_SHAPE).
+ * page_tokens at most 2^30; B*T at most 2^24; n_heads at most 65536; T * n_heads *
+ * d_head below 2^38 (GDN_ERR_SHAPE).
  * Activations and cache are all f32 or all bf16.  d_length (optional, DEVICE
  * int32[B]): a slot's real tokens, 0 .. T; the rows behind them are neither read
  * nor written.  A length or a past outside [0, T] or [0, max_pages * page_tokens -

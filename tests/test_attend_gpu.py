@@ -1,4 +1,6 @@
 """gdn_attend against plain 64-bit sums: chains, trees, windows, chunks, pages in any order, NaN wherever nothing may look."""
+import threading
+
 import pytest
 import torch
 
@@ -97,6 +99,8 @@ CASES = {
     "window over tree": dict(T=40, H=6, Hk=2, D=128, page=16, past=[0, 200, 1000], window=7, n_sink=3, tree=True),
     "window over tree, no sinks": dict(T=64, H=6, Hk=2, D=64, page=16, past=[3, 130], window=2, tree=True),
     "many slots": dict(T=2, H=8, Hk=2, D=64, page=16, past=[(37 * i) % 400 for i in range(170)]),
+    "more slots than a warp looks through": dict(T=1, H=4, Hk=2, D=128, page=8, past=[(91 * i) % 300 for i in range(300)]),
+    "more blocks than a warp looks through": dict(T=1100, H=32, Hk=1, D=64, page=64, past=[40]),
     "one slot, long": dict(T=16, H=6, Hk=1, D=256, page=64, past=[13001]),
     "one slot, longer": dict(T=1, H=8, Hk=2, D=128, page=128, past=[26000]),
     "one slot, small heads, long": dict(T=2, H=8, Hk=4, D=64, page=16, past=[50011]),
@@ -247,6 +251,35 @@ def test_launch_after_launch(sizes):
         graph.replay()
     assert torch.equal(first, r.got())
     r.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_host_threads(dtype):
+    """Several host threads, each with its own stream, buffers and shape of kernel."""
+    shapes = [dict(T=1, H=8, Hk=2, D=64, page=16, past=[900, 4]), dict(T=16, H=24, Hk=4, D=256, page=64, past=[1000]),
+              dict(T=5, H=8, Hk=2, D=128, page=32, past=[700, 70]), dict(T=2, H=6, Hk=1, D=256, page=16, past=[300])]
+    runs = [Run(Case(dtype=dtype, seed=i, **x)) for i, x in enumerate(shapes)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(r):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            for _ in range(50):
+                r.call(stream=stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(r,)) for r in runs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for r in runs:
+        r.check()
 
 
 def test_far_pages():

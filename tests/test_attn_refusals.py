@@ -29,7 +29,8 @@ def cache(**kw):
 
 
 BAD_DIMS = [dict(n_slots=0), dict(n_tokens=0), dict(n_slots=2 ** 13, n_tokens=2 ** 12), dict(n_heads=7), dict(n_heads=0),
-            dict(n_kv_heads=0), dict(n_heads=130, n_kv_heads=2), dict(n_heads=2 ** 17, n_kv_heads=2 ** 16), dict(d_head=96),
+            dict(n_kv_heads=0), dict(n_heads=130, n_kv_heads=2), dict(n_heads=2 ** 17, n_kv_heads=2 ** 16),
+            dict(n_slots=1, n_tokens=2 ** 23, n_heads=2 ** 10, n_kv_heads=2 ** 5), dict(d_head=96),
             dict(d_head=0), dict(page_tokens=4), dict(page_tokens=24), dict(page_tokens=512), dict(n_pages=0),
             dict(max_pages=0), dict(max_pages=2 ** 27), dict(page_stride=2 * 16 * 64 - 8), dict(page_stride=2 * 16 * 64 + 4),
             dict(page_stride=2 ** 38)]
@@ -119,6 +120,15 @@ def test_append(code, kw):
 ])
 def test_attend(code, kw):
     refused(code, call_attend, **kw)
+
+
+@pytest.mark.parametrize("dtype", [gdn.GDN_F32, gdn.GDN_BF16])
+def test_more_work_than_a_launch_counts(dtype):
+    """Blocks of rows times kv heads times key tiles past 2^31."""
+    kw = dict(n_slots=2 ** 10, n_tokens=2 ** 10, n_heads=64, n_kv_heads=64, page_tokens=256, max_pages=2 ** 12, dtype=dtype)
+    refused(gdn.GDN_ERR_SHAPE, call_attend, d=dims(**kw))
+    assert gdn.gdn_attend_workspace_bytes(dims(**kw)) == 0
+    assert gdn.gdn_attend_workspace_bytes(dims(**{**kw, "n_slots": 1})) > 0
 
 
 def test_workspace_is_asked_for_in_full():
