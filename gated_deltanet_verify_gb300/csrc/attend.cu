@@ -54,6 +54,8 @@ template <int D, int C> struct Shape {
     static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
     static constexpr int kBuffers = D == 256 ? 2 : 3;              // of S, in tensor memory beside O
     static constexpr int kOColumn = 128 * 2;                       // O, between the second S and the third
+    // a ring that reaches back to the tile before this S buffer's use, even if a block ends with each
+    static constexpr bool kLongRing = kRing >= kBuffers * (kKStages + kVStages + 2);
     static constexpr int kRows = kLanes / C;                       // of a block
     // Without copies two threads share a row, each with half of a tile's keys (and of O where it is moved).
     static constexpr int kShare = C == 1 ? 2 : 1;
@@ -518,8 +520,9 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                     // ---- rows of V that no row of the block sees
                     if (k0 + kTile > w.span.hi || (k0 < w.span.lo && k0 + kTile > sink)) {
                         const int key = k0 + tl, part = tl / Sh::kVTokens, g = tl % Sh::kVTokens;
-                        // after the P V of the tile before, whose stages come ahead of this one's in the ring
-                        if (any) ok = ok && wait_o();
+                        // The stage's last round has to be over (see the MMAs): it is where the ring is long, as the P V before
+                        // this S buffer's is done; else the P V of the tile before is waited for, whose stages come ahead.
+                        if (!Sh::kLongRing && any) ok = ok && wait_o();
                         const Ring<Sh::kRing> rv = r.after(((q == 0) + (q + 1 < n)) * Sh::kKStages + part);
                         ok = ok && warp_wait(full(rv.stage), rv.round & 1);
                         if (ok && !(key < w.span.hi && (key >= w.span.lo || key < sink))) {
