@@ -895,10 +895,13 @@ template <int D> cudaError_t launch_d(TcArgs &t, cudaStream_t stream) {
 }  // namespace
 
 AttendBlock attend_bf16_block(int T, int G, int D) {
-    const int c = copies(T, G), rows = kLanes / c;
+    const int c = copies(T, G), rows = kLanes / c, tokens = rows / G < T ? rows / G : T;
     // A part of many rows costs as much as a tile's keys and values.  A block's beginning and end take 3 to 5 us, a tile of 128
-    // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).
-    return {rows, rows / G < T ? rows / G : T, c > 1 ? 1 : 3, D == 64 ? 4 : 3};
+    // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).  Where a slot is one block the cache's bytes bind, and 128 CTAs take them a little
+    // faster than one on each of 152 SMs (8 slots of 20000 positions: 101.5 and 107.4 us for one token with D = 128, 111.2 and
+    // 115.0 for 16 with D = 256); with D = 64 (155 and 134 us) or several blocks (a prompt: 579 and 499) they do not.
+    const int least = c > 1 ? 1 : 3, pad = D == 64 ? 4 : 3, ctas = D >= 128 && tokens == T ? 128 : kAttendCtas;
+    return {rows, tokens, least, pad, ctas};
 }
 
 cudaError_t launch_attend_bf16(const AttendArgs &a, cudaStream_t stream) {

@@ -307,7 +307,7 @@ static int block_rows(int T, int G) { return (long long)T * G <= 16 ? 16 : 64; }
 
 AttendBlock attend_f32_block(int T, int G) {
     const int rows = block_rows(T, G);
-    return {rows, rows / G < T ? rows / G : T, 1, 0};
+    return {rows, rows / G < T ? rows / G : T, 1, 0, kAttendCtas};
 }
 
 cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t stream) {

@@ -63,6 +63,7 @@ struct AttendBlock {
     int tokens;                       // that a block takes
     int least;                        // tiles a CTA takes at least
     int pad;                          // what a block costs beside its tiles, in tiles
+    int ctas;                         // of a launch, at most
 };
 AttendBlock attend_f32_block(int T, int G);
 AttendBlock attend_bf16_block(int T, int G, int D);

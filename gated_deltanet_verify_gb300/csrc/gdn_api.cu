@@ -971,7 +971,7 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     a.pad = block.pad;
     a.n_tb = (a.T + a.TB - 1) / a.TB;
     const int sms = dev_info().sms;
-    a.ctas = sms < gdn::kAttendCtas ? sms : gdn::kAttendCtas;
+    a.ctas = sms < block.ctas ? sms : block.ctas;
     a.partial = static_cast<float *>(workspace);
     a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(a.part_rows, a.D));
     const cudaError_t e = d.dtype == GDN_F32 ? gdn::launch_attend_f32(a, static_cast<cudaStream_t>(stream))
