@@ -18,14 +18,21 @@
 //     its own S, O and softmax warps, halve what the keys and values cost in shared memory, but ran slower: the chains
 //     of one tile's S, softmax and P V are what binds, and two of them took 4950 cycles where a single one takes 2200.)
 //   * Two threads do the softmax of a row (tensor memory's lane), half of the keys each, and exchange their maxima: S, softmax
-//     and P V of a tile follow one another, so its time counts (1400 cycles with one thread a row, XXX with two).  Where a slot
-//     has at most 32 rows they lie there four times instead, and each copy's warp takes a quarter of every tile's keys (its
-//     other weights are zeros); the four sums are added up at the end.
+//     and P V of a tile follow one another, so its time counts (a chunk of 4096 tokens with D = 128: 372 us, with one thread a
+//     row 396).  Where a slot has at most 32 rows they lie there four times instead, and each copy's warp takes a quarter of
+//     every tile's keys (its other weights are zeros); the four sums are added up at the end (64 slots of a window of 1024: 50
+//     us, with one warp for all the keys 67).
 //   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
 //     at the ends of its share are joined with its neighbours' parts by attend_join.cu.
 //
 // Positions that no row of the block sees are not loaded by whole pages, and their rows of V are cleared in shared memory
 // before the MMA (0 x NaN would be NaN); scores that a row may not see are replaced, whatever was there.
+//
+// What bounds it.  Few rows: the cache's bytes (4 single tokens behind 131000 positions, D = 128: 300 us, 7.15 TB/s; 32 slots of 16
+// tokens over up to 16384, D = 256: 184 us, 6.1 TB/s).  Many rows: shared memory, which a tile of D = 256 asks for 320 KB (the
+// loads write 128, S reads Q and K, 128, P V reads V, 64) in 3150 cycles where its MMAs take 2048 (4096 tokens over 8192 positions:
+// 526 us, 1180 TFLOP/s).  Few keys: latency -- a launch, dependent loads of lengths, page ids and pages, one tile's S, softmax and
+// P V, and instructions that come from L2 the first time.
 //
 // Every wait is bounded; one that gives up reports GDN_ERR_TIMEOUT and the CTA ends.
 #include "attn.cuh"
@@ -54,7 +61,7 @@ template <int D, int C> struct Shape {
     static constexpr int kRing = (224 * 1024 - kQBytes) / kStage < 12 ? (224 * 1024 - kQBytes) / kStage : 12;
     static constexpr int kBuffers = D == 256 ? 2 : 3;              // of S, in tensor memory beside O
     static constexpr int kOColumn = 128 * 2;                       // O, between the second S and the third
-    // a ring that reaches back to the tile before this S buffer's use, even if a block ends with each
+    // a ring that reaches back past the tile whose S buffer this one's is, even if a block ends with each
     static constexpr bool kLongRing = kRing >= kBuffers * (kKStages + kVStages + 2);
     static constexpr int kRows = kLanes / C;                       // of a block
     // Without copies two threads share a row, each with half of a tile's keys (and of O where it is moved).
