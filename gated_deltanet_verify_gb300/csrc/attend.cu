@@ -338,13 +338,13 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
         }
         if (lane < 3) {
             mbar_init(s_full(lane), 1);
-            mbar_init(p_full(lane), Sh::kSoftmax);
+            mbar_init(p_full(lane), Sh::kLoads);      // a warp's lanes arrive together
             mbar_init(o_done(lane), 1);
         }
         if (lane < 2) {
             mbar_init(q_full(lane), 1);
             mbar_init(q_empty(lane), 1);
-            if (lane) mbar_init(o_free, Sh::kSoftmax);
+            if (lane) mbar_init(o_free, Sh::kLoads);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane < 3) prefetch_map(lane == 0 ? &args.q_map : lane == 1 ? &args.k_map : &args.v_map);
@@ -548,7 +548,8 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                     if (q + 1 < n) r.next(Sh::kKStages);
                     r.next(Sh::kVStages);
                     fence_before();
-                    mbar_arrive(p_full(u.stage));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full(u.stage));
                     before = u;
                     any = true;
                     u.next();
@@ -626,7 +627,8 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                     }
                     if (at0 + kCols == D) {
                         fence_before();
-                        mbar_arrive(o_free);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(o_free);
                     }
                     softmax_sync<Sh::kSoftmax>();
 #pragma unroll 1
