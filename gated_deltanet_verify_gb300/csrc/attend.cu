@@ -9,7 +9,7 @@
 // so weights reach 2^8 and the rescale is rare; the rounding of P to bf16 (half a step, 2^-8, of each weight, and of the output as
 // a mean of them) is what the tensor cores take, and of the order of the output's own rounding.
 //
-//   * A warp streams keys and values through a ring of 16 or 32 KB stages: one TMA box a page, straight into the tensor
+//   * A warp (two for D = 64) streams keys and values through a ring of 16 or 32 KB stages: one TMA box a page, straight into the tensor
 //     cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
 //     side by side, so that boxes of any page size leave the same layout: group stride (D / 64) KB, chunk stride 1 KB.  It is
 //     K-major for K (8-row groups by the stride offset) and, read the other way, MN-major for V.
@@ -68,8 +68,12 @@ template <int D, int C> struct Shape {
     static constexpr int kShare = C == 1 ? 2 : 1;
     static constexpr int kKeys = kTile / (C * kShare);             // of a tile that a thread takes
     static constexpr int kSoftmax = kShare * kLanes;               // threads
-    static constexpr int kLoads = kSoftmax / 32, kMmas = kLoads + 1;   // warps: one of loads, two of MMAs
-    static constexpr int kThreads = kSoftmax + 96;
+    // Warps that load.  A tile of D = 64 is only 32 KB, and one warp takes 1200 cycles to send off its boxes of pages of 32 tokens:
+    // there one takes the keys and one the values (64 slots of 2 tokens in a window of 1024: 41.4 us against 43.1).  Larger
+    // heads' tiles take longer to come than to send for, and one warp does (8 trees of 64 tokens, D = 128: 42.5 us against 43.7).
+    static constexpr int kLoaders = D == 64 ? 2 : 1;
+    static constexpr int kLoads = kSoftmax / 32, kMmas = kLoads + kLoaders;   // the first warps of loads and MMAs
+    static constexpr int kThreads = kSoftmax + 32 * kLoaders + 64;
     // a row's sums on their way out: two stages are shared out among the softmax threads
     static constexpr int kOut = 2 * kStage / kLanes;
     static_assert(kRing >= 5, "a tile's V, the next one's K, and one more");
@@ -338,7 +342,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     } else if (wid == Sh::kLoads) {
         if (lane < Sh::kRing) {
-            mbar_init(full(lane), 1);
+            mbar_init(full(lane), Sh::kLoaders);
             mbar_init(empty(lane), 2);            // by both MMA warps
         }
         if (lane < 3) {
@@ -675,8 +679,9 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
             const bool some = c < share.ctas && w.begin(a, at, share.start(c + 1) - share.start(c));
             if (!some) {
                 // nothing to do: fewer tiles than CTAs
-            } else if (wid == Sh::kLoads) {
+            } else if (wid < Sh::kMmas) {
                 // ---- the loads
+                const int loader = wid - Sh::kLoads;
                 const int page_log2 = a.kv.page_log2, page = 1 << page_log2;
                 Ring<Sh::kRing> r;                // the next stage to fill
                 auto free_stage = [&] {
@@ -704,6 +709,11 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                             const uint32_t st = r.stage;
                             free_stage();
                             if (!ok) return;
+                            // (A stage is only full when both loaders have passed it, so that neither can fall a round behind.)
+                            if (Sh::kLoaders == 2 && value != (loader == 1)) {
+                                if (lane == 0) mbar_arrive(full(st));
+                                continue;
+                            }
                             const int from = tile0 + (value ? part * Sh::kVTokens : 0) + lane * box, to = from + box;
                             const bool on = lane < tokens / box && ((from < hi && to > lo) || from < sink);
                             int g = __shfl_sync(kWarp, id, ((from >> page_log2) - (tile0 >> page_log2)) & 31);
@@ -721,8 +731,8 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                     };
                     int id = page_id(w.j0), id1 = page_id(w.j0 + 1);
                     const int qb = blocks % Sh::kQBuffers, uses = blocks / Sh::kQBuffers;
-                    if (uses > 0) ok = ok && warp_wait(q_empty(qb), (uses - 1) & 1);
-                    if (ok) {
+                    if (loader == 0 && uses > 0) ok = ok && warp_wait(q_empty(qb), (uses - 1) & 1);
+                    if (loader == 0 && ok) {
                         const int q = lane / C;   // lane: chunk, copy
                         if (lane == 0) mbar_expect(q_full(qb), (uint32_t)(a.TB * a.G * 128 * (Sh::kChunks * C)));
                         __syncwarp();
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                 if (!ok)                          // the copies in flight land before the CTA ends
                     for (int i = 0; i < Sh::kRing; ++i) {
                         const uint32_t fills = r.round + (i < (int)r.stage);      // of stage i
-                        if (fills > 0) mbar_wait(full(i), (fills - 1) & 1);
+                        if (fills > 0 && !mbar_wait(full(i), (fills - 1) & 1)) break;     // (they have, in that time)
                     }
             } else {
                 // ---- the MMAs, from two warps: an MMA's end is known some 400 cycles after it, and what one warp waits for the
