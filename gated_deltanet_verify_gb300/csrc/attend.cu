@@ -160,6 +160,7 @@ __device__ __forceinline__ uint64_t make_desc(uint32_t saddr, uint32_t lead, uin
 __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
+constexpr uint32_t kNegateA = 1u << 13;   // takes -A: a maximum of scores stays one of S under a negative scale
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
@@ -383,8 +384,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
             // ---- the softmax: tensor memory's lane = row (of one of C copies), a thread or two for each
             const int tl = tid % kLanes, half = tid / kLanes, copy = tl / Sh::kRows, row = tl % Sh::kRows;
             const uint32_t lanes = tmem + ((uint32_t)(32 * (wid & 3)) << 16), o_at = lanes + Sh::kOColumn;
-            const bool negative = a.scale < 0.f;
-            // a scale of zero leaves all weights alike, and masked ones at none
+            // (a negative scale's sign is in S: see the MMAs)  A scale of zero leaves all weights alike, and masked ones at none
             const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
             Ring<Sh::kBuffers> u, before;         // this tile's S, and the tile's before it
             bool any = false;                     // was there one?
@@ -462,9 +462,6 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                                     tmem_st16(p_at + ((copy + e) & (C - 1)) * (Sh::kKeys / 2) + f, zero);
                         }
                         wait_ld();
-                        if (negative)
-#pragma unroll
-                            for (int e = 0; e < Sh::kKeys; ++e) x[e] ^= 0x80000000u;
                         // does every row see all of the keys?  (One answer for the warp: its lanes are of one copy.)
                         const bool all = mine0 + Sh::kKeys <= past + (a.parent ? 0 : first_t + 1) &&
                                          (!a.window || mine0 > past + last_t - a.window);
@@ -769,6 +766,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                 // not, and a stage is only filled again when both have: its barrier has two phases, so that who falls a
                 // round behind would wait for ever, and who runs ahead would take the last round's for this one's.
                 const int part = wid - Sh::kMmas;
+                const uint32_t qk_desc = idesc(kTile, false) | (a.scale < 0.f ? kNegateA : 0);
                 const bool leader = elect_one();  // one thread issues all of a warp's, so that its commits cover them
                 Ring<Sh::kRing> r;                // the next stage
                 Ring<Sh::kBuffers> x;             // this warp's next S
@@ -790,7 +788,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
 #pragma unroll
                             for (int k = 0; k < 4 * Sh::kKChunks; ++k)
                                 mma_ss(column(), qd + ((k / 4) * (kLanes * 128) + (k & 3) * 32) / 16, kd + ((k / 4) * 1024 + (k & 3) * 32) / 16,
-                                       idesc(kTile, false), p > 0 || k > 0);
+                                       qk_desc, p > 0 || k > 0);
                             mma_commit(empty(r.stage));
                             if (p + 1 == Sh::kKStages) mma_commit(s_full(x.stage));
                         }
