@@ -9,8 +9,8 @@
 // so weights reach 2^8 and the rescale is rare; the rounding of P to bf16 (half a step, 2^-8, of each weight, and of the output as
 // a mean of them) is what the tensor cores take, and of the order of the output's own rounding.
 //
-//   * A warp (two for D = 64) streams keys and values through a ring of 16 or 32 KB stages: one TMA box a page, straight into the tensor
-//     cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
+//   * A warp (two for D = 64) streams keys and values through a ring of 16 or 32 KB stages: one TMA box a page, straight into
+//     the tensor cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
 //     side by side, so that boxes of any page size leave the same layout: group stride (D / 64) KB, chunk stride 1 KB.  It is
 //     K-major for K (8-row groups by the stride offset) and, read the other way, MN-major for V.
 //   * Two warps issue the MMAs, one those of S and one those of P V; S has as many buffers as tensor memory holds beside O
@@ -28,10 +28,10 @@
 // Positions that no row of the block sees are not loaded by whole pages, and their rows of V are cleared in shared memory
 // before the MMA (0 x NaN would be NaN); scores that a row may not see are replaced, whatever was there.
 //
-// What bounds it.  Few rows: the cache's bytes (4 single tokens behind 131000 positions, D = 128: 300 us, 7.15 TB/s; 32 slots of 16
-// tokens over up to 16384, D = 256: 184 us, 6.1 TB/s).  Many rows: shared memory, which a tile of D = 256 asks for 320 KB (the
-// loads write 128, S reads Q and K, 128, P V reads V, 64) in 3150 cycles where its MMAs take 2048 (4096 tokens over 8192 positions:
-// 526 us, 1180 TFLOP/s).  Few keys: latency -- a launch, dependent loads of lengths, page ids and pages, one tile's S, softmax and
+// What bounds it.  Few rows: the cache's bytes (4 single tokens behind 131000 positions, D = 128: 298 us, 7.2 TB/s; 32 slots of 16
+// tokens over up to 16384, D = 256: 182 us, 6.1 TB/s).  Many rows: shared memory, which a tile of D = 256 asks for 320 KB (the
+// loads write 128, S reads Q and K, 128, P V reads V, 64), 2500 cycles at 128 bytes each, where its MMAs take 2048 (4096 tokens over
+// 8192 positions: 425 us, 1460 TFLOP/s).  Few keys: latency -- a launch, dependent loads of lengths, page ids and pages, one tile's S, softmax and
 // P V, and instructions that come from L2 the first time.
 //
 // Every wait is bounded; one that gives up reports GDN_ERR_TIMEOUT and the CTA ends.
@@ -129,8 +129,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     return false;
 }
 // The same by a whole warp, with one answer for all its lanes.  The first look stands by itself: mostly the phase is over by
-// then, and the warp goes on without having entered a loop that its lanes could leave one by one (434 us against 474 for a prompt of 4096
-// tokens with 24 heads of 256; as one loop of votes, 465).
+// then, and the warp goes on without having entered a loop that its lanes could leave one by one (434 us against 474 for a
+// prompt of 4096 tokens with 24 heads of 256; as one loop of votes, 465).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
