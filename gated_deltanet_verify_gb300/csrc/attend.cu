@@ -920,8 +920,9 @@ AttendBlock attend_bf16_block(int T, int G, int D) {
     const int c = copies(T, G), rows = kLanes / c, tokens = rows / G < T ? rows / G : T;
     // A part of many rows costs as much as a tile's keys and values.  A block's beginning and end take 3 to 5 us, a tile of 128
     // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).  Where a slot is one block the cache's bytes bind, and 128 CTAs take them a little
-    // faster than one on each of 152 SMs (8 slots of 20000 positions: 101.5 and 107.4 us for one token with D = 128, 111.2 and
-    // 115.0 for 16 with D = 256); with D = 64 (155 and 134 us) or several blocks (a prompt: 579 and 499) they do not.
+    // faster than one on each of 152 SMs (8 slots of 20000 positions: 98.9 and 103.5 us for one token with D = 128, 107.9 and
+    // 112.9 for 16 with D = 256); with D = 64 (58.5 and 58.3; 64 slots of a window 45.5 and 41.0) or several blocks (a prompt:
+    // 495 and 426) they do not.
     const int least = c > 1 ? 1 : 3, pad = D == 64 ? 4 : 3, ctas = D >= 128 && tokens == T ? 128 : kAttendCtas;
     return {rows, tokens, least, pad, ctas};
 }
