@@ -4,9 +4,12 @@
 // them.  out = sum_k 2^(x_k - m) v_k / sum_k 2^(x_k - m) with x = scale log2(e) q.k and the running maximum m: one pass
 // over the keys, a tile of 32 at a time, the sums rescaled when m grows.
 //
-// A CTA of 256 threads: the scores of BM rows x 32 keys (register tiles of rows x keys, operands from shared memory in
-// 16-byte reads whose rows are padded by four words), a warp's softmax for each row (a lane a key), then the
-// weighted sum of the values (a lane D / 32 columns of BM / 8 rows).  Tiles stream through two buffers of asynchronous
+// A CTA of 256 threads.  Many rows (64 a block): the scores of 64 rows x 32 keys (register tiles of rows x keys, operands from
+// shared memory in 16-byte reads whose rows are padded by four words), a warp's softmax for each row (a lane a key), then
+// the weighted sum of the values (a lane D / 32 columns of 8 rows).  Few rows (8 or 16): the bytes bind, so every key and value
+// leaves shared memory once for 8 rows.  The queries lie in registers, a lane D / 32 columns of 8 rows; a warp takes its share of the
+// keys, 4 at a time, whose 32 partial scores its lanes add up in 31 exchanges; for the values a warp takes its share of the
+// columns and its lanes the keys, their sums added up at the block's end.  Tiles stream through 2 to 6 buffers of asynchronous
 // copies.  Positions that no row may see are filled with zeros, and the scores of those that a row may not see are
 // replaced, so what lies there does not matter.
 #include "attn.cuh"
@@ -23,11 +26,43 @@ template <int N> __device__ __forceinline__ void store_row(float *to, const floa
 #pragma unroll
     for (int i = 0; i < N; ++i) to[i] = x[i];
 }
+// N floats (2 or 4) in one read
+template <int N> __device__ __forceinline__ void read_n(const float *p, float *x) {
+    if constexpr (N == 4) {
+        const float4 f = read4(p);
+        x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+    } else {
+        const float2 f = *reinterpret_cast<const float2 *>(p);
+        x[0] = f.x; x[1] = f.y;
+    }
+}
+// 32 values a lane -> of each the sum over the warp's lanes, the i-th in lane i: every step halves what is left
+__device__ __forceinline__ float sums_by_lane(float (&x)[32], int lane) {
+#pragma unroll
+    for (int n = 16; n; n >>= 1)
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const bool up = lane & n;
+            const float mine = up ? x[i + n] : x[i], other = up ? x[i] : x[i + n];
+            x[i] = mine + __shfl_xor_sync(kFull, other, n);
+        }
+    return x[0];
+}
+
+// Few rows: 8 or 16, the rest of the geometry being that of groups of 8 rows, each with its own kWarps warps.
+template <int D, int BM> struct Shape {
+    static constexpr bool kFew = BM <= 16;
+    static constexpr int kBuffers = !kFew ? 2 : D == 256 ? 3 : 6;
+    static constexpr int kGroups = kFew ? BM / 8 : 1, kWarps = 8 / kGroups;
+    [[maybe_unused]] static constexpr int kQ = D / 32, kQV = kQ < 4 ? kQ : 4;                // of a row, a lane's columns, and as it reads them
+    [[maybe_unused]] static constexpr int kLanes = D / (4 * kWarps), kParts = 32 / kLanes;   // lanes side by side, 4 columns each; parts of the keys
+    [[maybe_unused]] static constexpr int kKeys = kTile / kParts, kKeysV = kKeys < 4 ? kKeys : 4;
+};
 
 template <int D, int BM> struct Smem {
-    float q[BM][D + 4];
-    float k[2][kTile][D + 4];
-    float v[2][kTile][D];
+    float q[Shape<D, BM>::kFew ? 1 : BM][D + 4];
+    float k[Shape<D, BM>::kBuffers][kTile][D + 4];
+    float v[Shape<D, BM>::kBuffers][kTile][Shape<D, BM>::kFew ? D + 4 : D];
     float p[BM][kTile + 4];
     float m[BM], l[BM], scale[BM];
     unsigned long long line[BM];      // a tree's nodes that a row sees
@@ -58,7 +93,13 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
 
     constexpr int kCols = D / 32;                 // columns a lane holds of the sums
     constexpr int kRowsW = BM / 8;                // rows a warp holds
-    float o[kRowsW][kCols];
+    using Sh = Shape<D, BM>;
+    constexpr bool kFew = Sh::kFew;
+    constexpr int kBuffers = Sh::kBuffers;
+    // few rows: this warp's group of 8, its place among the group's, the lane's columns and its part of the keys
+    const int row0 = wid / Sh::kWarps * 8, wg = wid % Sh::kWarps, column = (wg * Sh::kLanes + lane % Sh::kLanes) * 4, kpart = lane / Sh::kLanes;
+    float qr[kFew ? 8 : 1][Sh::kQ];
+    float o[kFew ? 8 : kRowsW][kFew ? 4 : kCols];
 
     bool first_block = true;
     int pair = at.pair;
@@ -71,42 +112,65 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         const int32_t *table = a.kv.table + (size_t)s * a.kv.max_pages;
         const int sink = min(a.n_sink, span.lo);
 
-        // ---- a tile's copies
+        // ---- a tile's copies.  Lane r knows where the tile's row r lies, its page id having been read a tile ahead
+        auto page_id = [&](int jj) {
+            if (jj >= j1) return -1;
+            const int key = span.tile(jj) * kTile + lane;
+            return key < span.hi && (key >= span.lo || key < sink) ? table[key >> a.kv.page_log2] : -1;
+        };
+        int id = page_id(j0);
         auto fetch = [&](int jj, int buf) {
-            const int k0 = span.tile(jj) * kTile;
-            constexpr int kVecs = D / 4;
-            for (int i = tid; i < kTile * kVecs; i += kThreads) {
-                const int r = i / kVecs, x = (i % kVecs) * 4, key = k0 + r;
-                bool on = key < span.hi && (key >= span.lo || key < sink);
-                const int id = on ? table[key >> a.kv.page_log2] : 0;
-                if (on && (id < 0 || id >= a.kv.n_pages)) {
-                    report(a.d_status, GDN_ERR_PAGE);
-                    on = false;
+            if (jj < j1) {
+                const int key = span.tile(jj) * kTile + lane;
+                long long row = -1;
+                if (key < span.hi && (key >= span.lo || key < sink)) {
+                    if (id < 0 || id >= a.kv.n_pages) report(a.d_status, GDN_ERR_PAGE);
+                    else row = (long long)id * a.kv.page_stride + ((size_t)kvh * page + (key & (page - 1))) * D;
                 }
-                const long long off = (long long)(on ? id : 0) * a.kv.page_stride +
-                                      ((size_t)kvh * page + (key & (page - 1))) * D + x;
-                const float *kp = static_cast<const float *>(a.kv.k) + off, *vp = static_cast<const float *>(a.kv.v) + off;
-                float *ks = &sm.k[buf][r][x], *vs = &sm.v[buf][r][x];
-                const int bytes = on ? 16 : 0;                   // of the 16 written, those that are read
-                const void *kg = on ? (const void *)kp : a.kv.k, *vg = on ? (const void *)vp : a.kv.v;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                                 (uint32_t)__cvta_generic_to_shared(ks)), "l"(kg), "r"(bytes) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                                 (uint32_t)__cvta_generic_to_shared(vs)), "l"(vg), "r"(bytes) : "memory");
+                id = page_id(jj + 1);
+                constexpr int kVecs = D / 4;
+#pragma unroll
+                for (int n = 0; n < kTile * kVecs / kThreads; ++n) {
+                    const int i = tid + n * kThreads, r = i / kVecs, x = (i % kVecs) * 4;
+                    const long long from = __shfl_sync(kFull, row, r);
+                    const int bytes = from >= 0 ? 16 : 0;            // of the 16 written, those that are read
+                    const long long off = from >= 0 ? from + x : 0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                                     (uint32_t)__cvta_generic_to_shared(&sm.k[buf][r][x])), "l"(static_cast<const float *>(a.kv.k) + off),
+                                 "r"(bytes) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                                     (uint32_t)__cvta_generic_to_shared(&sm.v[buf][r][x])), "l"(static_cast<const float *>(a.kv.v) + off),
+                                 "r"(bytes) : "memory");
+                }
             }
             asm volatile("cp.async.commit_group;\n" ::: "memory");
         };
 
         __syncthreads();                          // the block before no longer reads shared memory
-        fetch(j0, 0);
-        // ---- the block's rows
-        for (int i = tid; i < BM * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), x = (i % (D / 4)) * 4;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < rows)
-                f = read4(static_cast<const float *>(a.q) +
-                             (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D + x);
-            *reinterpret_cast<float4 *>(&sm.q[r][x]) = f;
+#pragma unroll 1
+        for (int n = 0; n + 1 < kBuffers; ++n) fetch(j0 + n, n);
+        // ---- the block's rows: to registers where they are few, else to shared memory
+        auto query = [&](int r) {
+            return static_cast<const float *>(a.q) +
+                   (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D;
+        };
+        if constexpr (kFew) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool on = row0 + i < rows;
+                const float *from = query(on ? row0 + i : 0);
+#pragma unroll
+                for (int e = 0; e < Sh::kQ; e += Sh::kQV) {
+                    read_n<Sh::kQV>(from + e * 32 + lane * Sh::kQV, &qr[i][e]);
+#pragma unroll
+                    for (int f = 0; f < Sh::kQV; ++f) qr[i][e + f] = on ? qr[i][e + f] : 0.f;
+                }
+            }
+        } else {
+            for (int i = tid; i < BM * (D / 4); i += kThreads) {
+                const int r = i / (D / 4), x = (i % (D / 4)) * 4;
+                *reinterpret_cast<float4 *>(&sm.q[r][x]) = r < rows ? read4(query(r) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
         if (a.parent && tid < span.t1) {
             int p = a.parent[(size_t)s * a.T + tid];
@@ -135,18 +199,38 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
             sm.position[r] = span.past + (a.parent && t >= 0 ? sm.depth[t] : t);
         }
 #pragma unroll
-        for (int i = 0; i < kRowsW; ++i)
+        for (int i = 0; i < (int)(sizeof o / sizeof o[0]); ++i)
 #pragma unroll
-            for (int e = 0; e < kCols; ++e) o[i][e] = 0.f;
+            for (int e = 0; e < (int)(sizeof o[0] / sizeof o[0][0]); ++e) o[i][e] = 0.f;
 
-        for (int jj = j0; jj < j1; ++jj) {
-            const int buf = (jj - j0) & 1, k0 = span.tile(jj) * kTile;
-            if (jj + 1 < j1) fetch(jj + 1, buf ^ 1);
-            else asm volatile("cp.async.commit_group;\n" ::: "memory");
-            asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+        int buf = 0;
+        for (int jj = j0; jj < j1; ++jj, buf = buf + 1 == kBuffers ? 0 : buf + 1) {
+            const int k0 = span.tile(jj) * kTile;
+            fetch(jj + kBuffers - 1, buf == 0 ? kBuffers - 1 : buf - 1);      // where the tile before was
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(kBuffers - 1) : "memory");
             __syncthreads();
-            // ---- scores: rows rg + 16 i, keys kg + 16 n
-            {
+            if constexpr (kFew) {
+                // ---- scores: a warp 32 / kWarps keys for 8 rows, four keys at a time
+#pragma unroll
+                for (int n = 0; n < kTile / Sh::kWarps; n += 4) {
+                    const int key = wg * (kTile / Sh::kWarps) + n;
+                    float x[32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float kr[Sh::kQ];
+#pragma unroll
+                        for (int e = 0; e < Sh::kQ; e += Sh::kQV) read_n<Sh::kQV>(&sm.k[buf][key + k][e * 32 + lane * Sh::kQV], kr + e);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            x[k * 8 + i] = qr[i][0] * kr[0];
+#pragma unroll
+                            for (int e = 1; e < Sh::kQ; ++e) x[k * 8 + i] = fmaf(qr[i][e], kr[e], x[k * 8 + i]);
+                        }
+                    }
+                    sm.p[row0 + lane % 8][key + lane / 8] = sums_by_lane(x, lane) * scale2;
+                }
+            } else {
+                // ---- scores: rows rg + 16 i, keys kg + 16 n
                 constexpr int kR = BM / 16;
                 const int rg = tid >> 4, kg = tid & 15;
                 float x[kR][2];
@@ -197,37 +281,67 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
                     sm.m[r] = to;
                 }
             }
-            __syncwarp();
-            // ---- values: a warp's rows are its own (wid + 8 i), a lane's columns
-            constexpr int V = kCols < 4 ? kCols : 4;
+            if constexpr (kFew) {
+                __syncthreads();
+                // ---- values: a group's warps share out the columns, a warp's lanes the keys
+                bool moved = false;
+                float f[8];
 #pragma unroll
-            for (int i = 0; i < kRowsW; ++i) {
-                const float f = sm.scale[wid + 8 * i];
+                for (int i = 0; i < 8; ++i) moved |= (f[i] = sm.scale[row0 + i]) != 1.f;
+                if (moved)
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) o[i][e] *= f;
-            }
-#pragma unroll 2
-            for (int k = 0; k < kTile; k += 4) {
-                float v[4][kCols];
+                    for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                        for (int e = 0; e < 4; ++e) o[i][e] *= f[i];
 #pragma unroll
-                    for (int e = 0; e < kCols; e += V) {
-                        const float *from = &sm.v[buf][k + n][(e / V * 32 + lane) * V];
-                        if constexpr (V == 4) {
-                            const float4 f = *reinterpret_cast<const float4 *>(from);
-                            v[n][e] = f.x; v[n][e + 1] = f.y; v[n][e + 2] = f.z; v[n][e + 3] = f.w;
-                        } else {
-                            const float2 f = *reinterpret_cast<const float2 *>(from);
-                            v[n][e] = f.x; v[n][e + 1] = f.y;
-                        }
+                for (int k = 0; k < Sh::kKeys; k += Sh::kKeysV) {
+                    const int key = kpart * Sh::kKeys + k;
+                    float v[Sh::kKeysV][4];
+#pragma unroll
+                    for (int n = 0; n < Sh::kKeysV; ++n) read_n<4>(&sm.v[buf][key + n][column], v[n]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float w[Sh::kKeysV];
+                        read_n<Sh::kKeysV>(&sm.p[row0 + i][key], w);
+#pragma unroll
+                        for (int n = 0; n < Sh::kKeysV; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[i][e] = fmaf(w[n], v[n][e], o[i][e]);
                     }
+                }
+            } else {
+                __syncwarp();
+                // ---- values: a warp's rows are its own (wid + 8 i), a lane's columns
+                constexpr int V = kCols < 4 ? kCols : 4;
 #pragma unroll
                 for (int i = 0; i < kRowsW; ++i) {
-                    const float4 p = *reinterpret_cast<const float4 *>(&sm.p[wid + 8 * i][k]);
+                    const float f = sm.scale[wid + 8 * i];
 #pragma unroll
-                    for (int e = 0; e < kCols; ++e)
-                        o[i][e] = fmaf(p.x, v[0][e], fmaf(p.y, v[1][e], fmaf(p.z, v[2][e], fmaf(p.w, v[3][e], o[i][e]))));
+                    for (int e = 0; e < kCols; ++e) o[i][e] *= f;
+                }
+#pragma unroll 2
+                for (int k = 0; k < kTile; k += 4) {
+                    float v[4][kCols];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int e = 0; e < kCols; e += V) {
+                            const float *from = &sm.v[buf][k + n][(e / V * 32 + lane) * V];
+                            if constexpr (V == 4) {
+                                const float4 f = *reinterpret_cast<const float4 *>(from);
+                                v[n][e] = f.x; v[n][e + 1] = f.y; v[n][e + 2] = f.z; v[n][e + 3] = f.w;
+                            } else {
+                                const float2 f = *reinterpret_cast<const float2 *>(from);
+                                v[n][e] = f.x; v[n][e + 1] = f.y;
+                            }
+                        }
+#pragma unroll
+                    for (int i = 0; i < kRowsW; ++i) {
+                        const float4 p = *reinterpret_cast<const float4 *>(&sm.p[wid + 8 * i][k]);
+#pragma unroll
+                        for (int e = 0; e < kCols; ++e)
+                            o[i][e] = fmaf(p.x, v[0][e], fmaf(p.y, v[1][e], fmaf(p.z, v[2][e], fmaf(p.w, v[3][e], o[i][e]))));
+                    }
                 }
             }
             __syncthreads();                      // the tile's buffer may be filled again
@@ -235,25 +349,35 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant_
         // ---- the block's sums: its output, or a part of it
         const bool whole = j0 == 0 && j1 == span.n;
         const size_t part = size_t(2 * c + (first_block ? 0 : 1)) * a.part_rows;
-        constexpr int V = kCols < 4 ? kCols : 4;
+        float *out = static_cast<float *>(a.out) + (((size_t)s * a.T + span.t0) * a.H + (size_t)kvh * a.G) * D;
+        auto place = [&](int r) { return whole ? out + ((size_t)(r / a.G) * a.H + r % a.G) * D : a.partial + (part + r) * D; };
+        if constexpr (kFew) {
 #pragma unroll
-        for (int i = 0; i < kRowsW; ++i) {
-            const int r = wid + 8 * i;
-            if (r >= rows) continue;
-            const float l = sm.l[r];
-            if (whole) {
-                float *out = static_cast<float *>(a.out) +
-                         (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D;
-                const float inv = 1.f / l;
+            for (int d = Sh::kLanes; d < 32; d *= 2)
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) o[i][e] *= inv;
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int e = 0; e < kCols; e += V) store_row<V>(out + (e / V * 32 + lane) * V, &o[i][e]);
-            } else {
-                if (lane == 0) a.stats[part + r] = make_float2(sm.m[r], l);
-                float *to = a.partial + (part + r) * D;
+                    for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(kFull, o[i][e], d);
+            if (!whole && tid < rows) a.stats[part + tid] = make_float2(sm.m[tid], sm.l[tid]);
 #pragma unroll
-                for (int e = 0; e < kCols; e += V) store_row<V>(to + (e / V * 32 + lane) * V, &o[i][e]);
+            for (int i = 0; i < 8; ++i) {
+                const int r = row0 + i;
+                if (r >= rows || kpart != i % Sh::kParts) continue;
+                const float f = whole ? 1.f / sm.l[r] : 1.f;
+                *reinterpret_cast<float4 *>(place(r) + column) = make_float4(o[i][0] * f, o[i][1] * f, o[i][2] * f, o[i][3] * f);
+            }
+        } else {
+            constexpr int V = kCols < 4 ? kCols : 4;
+#pragma unroll
+            for (int i = 0; i < kRowsW; ++i) {
+                const int r = wid + 8 * i;
+                if (r >= rows) continue;
+                const float l = sm.l[r], f = whole ? 1.f / l : 1.f;
+                if (!whole && lane == 0) a.stats[part + r] = make_float2(sm.m[r], l);
+#pragma unroll
+                for (int e = 0; e < kCols; ++e) o[i][e] *= f;
+#pragma unroll
+                for (int e = 0; e < kCols; e += V) store_row<V>(place(r) + (e / V * 32 + lane) * V, &o[i][e]);
             }
         }
         // ---- the next block
@@ -302,8 +426,11 @@ template <int BM> cudaError_t launch_d(const AttendArgs &a, cudaStream_t stream)
 
 }  // namespace
 
-// rows of a block: 16 where a slot has no more (a wider block would spend its time on rows that are not there), else 64
-static int block_rows(int T, int G) { return (long long)T * G <= 16 ? 16 : 64; }
+// rows of a block: 8 or 16 where a slot has no more (a wider block would spend its time on rows that are not there), else 64
+static int block_rows(int T, int G) {
+    const long long rows = (long long)T * G;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : 64;
+}
 
 AttendBlock attend_f32_block(int T, int G) {
     const int rows = block_rows(T, G);
@@ -311,7 +438,8 @@ AttendBlock attend_f32_block(int T, int G) {
 }
 
 cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t stream) {
-    return block_rows(a.T, a.G) == 16 ? launch_d<16>(a, stream) : launch_d<64>(a, stream);
+    const int rows = block_rows(a.T, a.G);
+    return rows == 8 ? launch_d<8>(a, stream) : rows == 16 ? launch_d<16>(a, stream) : launch_d<64>(a, stream);
 }
 
 }  // namespace gdn
