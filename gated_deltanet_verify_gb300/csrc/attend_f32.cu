@@ -52,11 +52,13 @@ __device__ __forceinline__ float sums_by_lane(float (&x)[32], int lane) {
 // Few rows: 8 or 16, the rest of the geometry being that of groups of 8 rows, each with its own kWarps warps.
 template <int D, int BM> struct Shape {
     static constexpr bool kFew = BM <= 16;
-    static constexpr int kBuffers = !kFew ? 2 : D == 256 ? 3 : 6;
+    // CTAs an SM: what one does between its barriers (scores, softmax, values) the other's covers, where its tiles fit
+    static constexpr int kCtas = kFew && D <= 128 ? 2 : 1;
+    static constexpr int kBuffers = !kFew ? 2 : D == 64 ? 6 : 3;
     static constexpr int kGroups = kFew ? BM / 8 : 1, kWarps = 8 / kGroups;
-    [[maybe_unused]] static constexpr int kQ = D / 32, kQV = kQ < 4 ? kQ : 4;                // of a row, a lane's columns, and as it reads them
-    [[maybe_unused]] static constexpr int kLanes = D / (4 * kWarps), kParts = 32 / kLanes;   // lanes side by side, 4 columns each; parts of the keys
-    [[maybe_unused]] static constexpr int kKeys = kTile / kParts, kKeysV = kKeys < 4 ? kKeys : 4;
+    static constexpr int kQ = D / 32, kQV = kQ < 4 ? kQ : 4;                // of a row, a lane's columns, and as it reads them
+    static constexpr int kLanes = D / (4 * kWarps), kParts = 32 / kLanes;   // lanes side by side, 4 columns each; parts of the keys
+    static constexpr int kKeys = kTile / kParts, kKeysV = kKeys < 4 ? kKeys : 4;
 };
 
 template <int D, int BM> struct Smem {
@@ -73,7 +75,7 @@ template <int D, int BM> struct Smem {
 };
 
 template <int D, int BM>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel(const __grid_constant__ AttendArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
     Smem<D, BM> &sm = *reinterpret_cast<Smem<D, BM> *>(raw);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -432,9 +434,9 @@ static int block_rows(int T, int G) {
     return rows <= 8 ? 8 : rows <= 16 ? 16 : 64;
 }
 
-AttendBlock attend_f32_block(int T, int G) {
+AttendBlock attend_f32_block(int T, int G, int D) {
     const int rows = block_rows(T, G);
-    return {rows, rows / G < T ? rows / G : T, 1, 0, kAttendCtas};
+    return {rows, rows / G < T ? rows / G : T, 1, 0, (rows <= 16 && D <= 128 ? 2 : 1) * kAttendCtas};
 }
 
 cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t stream) {

@@ -14,7 +14,6 @@ namespace {
 
 constexpr int kJoinThreads = 128;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kPartWords = (kAttendCtas + 31) / 32;       // parts a lane looks after
 
 template <int N> __device__ __forceinline__ void store_row(float *to, const float *x) {
 #pragma unroll
@@ -31,6 +30,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     __shared__ int scratch[kJoinWarps + 2];
     constexpr int V = D / 32 < 4 ? D / 32 : 4;      // numbers a lane takes of a part
     constexpr int kWarpsRow = D / (32 * V);
+    constexpr int kPartWords = ((sizeof(E) == 4 ? 2 : 1) * kAttendCtas + 31) / 32;      // parts a lane looks after
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     // The lengths were there before the kernel whose sums are joined began, so this goes on beside its end.
     Share share;

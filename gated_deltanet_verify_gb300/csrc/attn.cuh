@@ -52,10 +52,7 @@ struct AttendArgs {
 
 constexpr int kTileF32 = 32, kTileBf16 = 128;   // keys a tile
 
-// What the workspace holds; rows: of a block, at most.
-constexpr int kAttendCtas = 152;      // CTAs of a launch, at most: one on every SM
-inline size_t attend_partial_bytes(int rows, int D) { return size_t(2) * kAttendCtas * rows * D * sizeof(float); }
-inline size_t attend_stats_bytes(int rows) { return size_t(2) * kAttendCtas * rows * sizeof(float2); }
+constexpr int kAttendCtas = 152;      // CTAs of a launch: one on every SM, or two (f32)
 
 // How the rows of a slot and a kv head are cut up.
 struct AttendBlock {
@@ -65,8 +62,11 @@ struct AttendBlock {
     int pad;                          // what a block costs beside its tiles, in tiles
     int ctas;                         // of a launch, at most
 };
-AttendBlock attend_f32_block(int T, int G);
+AttendBlock attend_f32_block(int T, int G, int D);
 AttendBlock attend_bf16_block(int T, int G, int D);
+// What the workspace holds.
+inline size_t attend_partial_bytes(const AttendBlock &b, int D) { return size_t(2) * b.ctas * b.rows * D * sizeof(float); }
+inline size_t attend_stats_bytes(const AttendBlock &b) { return size_t(2) * b.ctas * b.rows * sizeof(float2); }
 
 // Return a cudaError_t of the launch (cudaSuccess when enqueued).
 cudaError_t launch_append(const AppendArgs &a, gdn_dtype dtype, int sm_count, cudaStream_t stream);

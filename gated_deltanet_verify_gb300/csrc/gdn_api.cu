@@ -874,12 +874,12 @@ gdn::KvPages kv_pages(const gdn_attn_dims &d, const gdn_kv_cache &c) {
 
 gdn::AttendBlock attend_block(const gdn_attn_dims &d) {
     const int G = d.n_heads / d.n_kv_heads;
-    return d.dtype == GDN_F32 ? gdn::attend_f32_block(d.n_tokens, G) : gdn::attend_bf16_block(d.n_tokens, G, d.d_head);
+    return d.dtype == GDN_F32 ? gdn::attend_f32_block(d.n_tokens, G, d.d_head) : gdn::attend_bf16_block(d.n_tokens, G, d.d_head);
 }
 
 size_t attend_workspace(const gdn_attn_dims &d) {
-    const int rows = attend_block(d).rows;
-    return gdn::attend_partial_bytes(rows, d.d_head) + gdn::attend_stats_bytes(rows);
+    const gdn::AttendBlock block = attend_block(d);
+    return gdn::attend_partial_bytes(block, d.d_head) + gdn::attend_stats_bytes(block);
 }
 
 // key tiles of all blocks of rows, at most
@@ -971,9 +971,10 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     a.pad = block.pad;
     a.n_tb = (a.T + a.TB - 1) / a.TB;
     const int sms = dev_info().sms;
-    a.ctas = sms < block.ctas ? sms : block.ctas;
+    const int most = (block.ctas > gdn::kAttendCtas ? 2 : 1) * sms;
+    a.ctas = most < block.ctas ? most : block.ctas;
     a.partial = static_cast<float *>(workspace);
-    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(a.part_rows, a.D));
+    a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(block, a.D));
     const cudaError_t e = d.dtype == GDN_F32 ? gdn::launch_attend_f32(a, static_cast<cudaStream_t>(stream))
                                              : gdn::launch_attend_bf16(a, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail(GDN_ERR_LAUNCH, "attention launch failed: %s", cudaGetErrorString(e));
