@@ -6,12 +6,16 @@
 //
 // A CTA of 256 threads.  Many rows (64 a block): the scores of 64 rows x 32 keys (register tiles of rows x keys, operands from
 // shared memory in 16-byte reads whose rows are padded by four words), a warp's softmax for each row (a lane a key), then
-// the weighted sum of the values (a lane D / 32 columns of 8 rows).  Few rows (8 or 16): the bytes bind, so every key and value
+// the weighted sum of the values (a lane D / 32 columns of 8 rows).  Few rows (8, 16 or 32): the bytes bind, so every key and value
 // leaves shared memory once for 8 rows.  The queries lie in registers, a lane D / 32 columns of 8 rows; a warp takes its share of the
 // keys, 4 at a time, whose 32 partial scores its lanes add up in 31 exchanges; for the values a warp takes its share of the
 // columns and its lanes the keys, their sums added up at the block's end.  Tiles stream through 2 to 6 buffers of asynchronous
 // copies.  Positions that no row may see are filled with zeros, and the scores of those that a row may not see are
 // replaced, so what lies there does not matter.
+//
+// What bounds it.  Few rows: the copies' issue and the steps between barriers beside the cache's bytes (8 single tokens behind 20000
+// positions, 32 + 8 heads of 128: 309 us, 4.2 TB/s; 3 behind 57508, 24 + 4 of 256: 329 us, 4.3 TB/s).  Many rows: reads of
+// shared memory beside the products (1024 tokens over 2000 positions, 16 + 4 heads of 128: 709 us, 30 TFLOP/s).
 #include "attn.cuh"
 
 namespace gdn {
@@ -49,11 +53,12 @@ __device__ __forceinline__ float sums_by_lane(float (&x)[32], int lane) {
     return x[0];
 }
 
-// Few rows: 8 or 16, the rest of the geometry being that of groups of 8 rows, each with its own kWarps warps.
+// Few rows: 8, 16 or 32, in groups of 8, each with its own kWarps warps.
 template <int D, int BM> struct Shape {
-    static constexpr bool kFew = BM <= 16;
-    // CTAs an SM: what one does between its barriers (scores, softmax, values) the other's covers, where its tiles fit
-    static constexpr int kCtas = kFew && D <= 128 ? 2 : 1;
+    static constexpr bool kFew = BM <= 32;
+    // CTAs an SM: where their tiles fit, two, which cover each other's barriers (D = 128, 8 single tokens behind 20000 positions:
+    // 309 us, with one 425; 1024 tokens over 2000: 709 and 945)
+    static constexpr int kCtas = D <= 128 ? 2 : 1;
     static constexpr int kBuffers = !kFew ? 2 : D == 64 ? 6 : 3;
     static constexpr int kGroups = kFew ? BM / 8 : 1, kWarps = 8 / kGroups;
     static constexpr int kQ = D / 32, kQV = kQ < 4 ? kQ : 4;                // of a row, a lane's columns, and as it reads them
@@ -194,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
             sm.at[r] = t;
             sm.m[r] = -INFINITY;
             sm.l[r] = 0.f;
+            sm.scale[r] = 1.f;
             unsigned long long line = 0;
             if (a.parent)
                 for (int p = t; p >= 0; p = sm.parents[p]) line |= 1ull << p;
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
             }
             __syncthreads();
             // ---- softmax: a warp a row, a lane a key
-            for (int r = wid; r < BM; r += 8) {
+            for (int r = wid; r < (BM <= 16 ? BM : rows); r += 8) {
                 const int t = sm.at[r], key = k0 + lane, node = key - span.past;
                 bool sees = t >= 0 && node <= t;
                 int where = key;
@@ -428,20 +434,23 @@ template <int BM> cudaError_t launch_d(const AttendArgs &a, cudaStream_t stream)
 
 }  // namespace
 
-// rows of a block: 8 or 16 where a slot has no more (a wider block would spend its time on rows that are not there), else 64
+// Rows of a block: no more than a slot has, in steps of 2, up to 64: a wider block spends its time on rows that are not there (8
+// single tokens behind 20000 positions with G = 4, D = 128: 309 us with 8 rows, 494 with 16; 8 slots of 20 rows over 4000:
+// 97 us with 32, 128 with 64).
 static int block_rows(int T, int G) {
     const long long rows = (long long)T * G;
-    return rows <= 8 ? 8 : rows <= 16 ? 16 : 64;
+    return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 AttendBlock attend_f32_block(int T, int G, int D) {
     const int rows = block_rows(T, G);
-    return {rows, rows / G < T ? rows / G : T, 1, 0, (rows <= 16 && D <= 128 ? 2 : 1) * kAttendCtas};
+    return {rows, rows / G < T ? rows / G : T, 1, 0, (D <= 128 ? 2 : 1) * kAttendCtas};
 }
 
 cudaError_t launch_attend_f32(const AttendArgs &a, cudaStream_t stream) {
     const int rows = block_rows(a.T, a.G);
-    return rows == 8 ? launch_d<8>(a, stream) : rows == 16 ? launch_d<16>(a, stream) : launch_d<64>(a, stream);
+    return rows == 8 ? launch_d<8>(a, stream) : rows == 16 ? launch_d<16>(a, stream)
+           : rows == 32 ? launch_d<32>(a, stream) : launch_d<64>(a, stream);
 }
 
 }  // namespace gdn

@@ -120,6 +120,17 @@ def test_cases(name, dtype):
     r.check()
 
 
+# a slot's rows at and past each size of a block, its keys shared out among many CTAs and in one
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 31, 32, 33, 64, 65])
+def test_rows_of_a_block(rows, d, dtype):
+    T, G = next((rows // g, g) for g in (5, 4, 3, 2, 1) if rows % g == 0)
+    r = Run(Case(dtype=dtype, T=T, H=2 * G, Hk=2, D=d, page=16, past=[5000, 0, 61], length=[T, T, T - T // 2]))
+    r.call()
+    r.check()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_twice_the_same_bits(dtype):
     r = Run(Case(dtype=dtype, T=16, H=24, Hk=4, D=256, page=64, past=[3000, 3, 517]))
