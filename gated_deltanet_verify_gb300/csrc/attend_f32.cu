@@ -14,8 +14,8 @@
 // replaced, so what lies there does not matter.
 //
 // What bounds it.  Few rows: the copies' issue and the steps between barriers beside the cache's bytes (8 single tokens behind 20000
-// positions, 32 + 8 heads of 128: 309 us, 4.2 TB/s; 3 behind 57508, 24 + 4 of 256: 329 us, 4.3 TB/s).  Many rows: reads of
-// shared memory beside the products (1024 tokens over 2000 positions, 16 + 4 heads of 128: 709 us, 30 TFLOP/s).
+// positions, 32 + 8 heads of 128: 300 us, 4.4 TB/s; 3 behind 57508, 24 + 4 of 256: 321 us, 4.4 TB/s).  Many rows: reads of
+// shared memory beside the products (1024 tokens over 2000 positions, 16 + 4 heads of 128: 703 us, 30 TFLOP/s).
 #include "attn.cuh"
 
 namespace gdn {
@@ -214,8 +214,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
         int buf = 0;
         for (int jj = j0; jj < j1; ++jj, buf = buf + 1 == kBuffers ? 0 : buf + 1) {
             const int k0 = span.tile(jj) * kTile;
-            fetch(jj + kBuffers - 1, buf == 0 ? kBuffers - 1 : buf - 1);      // where the tile before was
-            asm volatile("cp.async.wait_group %0;\n" ::"n"(kBuffers - 1) : "memory");
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(kBuffers - 2) : "memory");
             __syncthreads();
             if constexpr (kFew) {
                 // ---- scores: a warp 32 / kWarps keys for 8 rows, four keys at a time
@@ -262,6 +261,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
                 }
             }
             __syncthreads();
+            // The next tile's copies, to where the tile before was, which all have read by now (sent off here, beside the softmax,
+            // and without a barrier at the loop's end: 300 us for 8 tokens behind 20000, before the scores 309).
+            fetch(jj + kBuffers - 1, buf == 0 ? kBuffers - 1 : buf - 1);
             // ---- softmax: a warp a row, a lane a key
             for (int r = wid; r < (BM <= 16 ? BM : rows); r += 8) {
                 const int t = sm.at[r], key = k0 + lane, node = key - span.past;
@@ -352,7 +354,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
                     }
                 }
             }
-            __syncthreads();                      // the tile's buffer may be filled again
         }
         // ---- the block's sums: its output, or a part of it
         const bool whole = j0 == 0 && j1 == span.n;
