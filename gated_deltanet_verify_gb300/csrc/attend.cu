@@ -453,7 +453,10 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                         uint32_t x[Sh::kKeys];
 #pragma unroll
                         for (int e = 0; e < Sh::kKeys; e += 32) tmem_ld32(s_at + e, x + e);
-                        if (C > 1) {              // the other copies' keys
+                        wait_ld();
+                        // The other copies' keys.  P takes the place of S, and a load and a store of tensor memory come in no order but
+                        // by a wait: not before the scores are here.
+                        if (C > 1) {
                             const uint32_t zero[16] = {};
 #pragma unroll
                             for (int e = 1; e < C; ++e)
@@ -461,7 +464,6 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                                 for (int f = 0; f < Sh::kKeys / 2; f += 16)
                                     tmem_st16(p_at + ((copy + e) & (C - 1)) * (Sh::kKeys / 2) + f, zero);
                         }
-                        wait_ld();
                         // does every row see all of the keys?  (One answer for the warp: its lanes are of one copy.)
                         const bool all = mine0 + Sh::kKeys <= past + (a.parent ? 0 : first_t + 1) &&
                                          (!a.window || mine0 > past + last_t - a.window);
