@@ -488,8 +488,11 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                             top[e / 2 & 3] = max3(top[e / 2 & 3], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
                         float to = max3(fmaxf(top[0], top[1]), top[2], top[3]);
                         if constexpr (Sh::kShare == 2) {
+                            // (the other thread's P goes over scores of this one's, so its store comes behind this load)
                             ctl.each[half][tl] = to;
+                            fence_before();
                             rows_sync(wid);
+                            fence_after();
                             to = fmaxf(to, ctl.each[half ^ 1][tl]);
                             rows_sync(wid);
                         }

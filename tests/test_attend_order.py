@@ -28,3 +28,14 @@ def test_no_store_between_a_load_and_its_wait(steps):
             pending = None
         elif name.startswith("tmem_st"):
             assert pending is None, f"a store {at - pending} lines behind a load that nothing has waited for"
+
+
+def test_the_other_threads_store_is_fenced(steps):
+    """Two threads share a row's scores, and the weights of one go over scores of the other: from a load's wait to the barrier
+    between the two there is a fence, and another one from the barrier to the store."""
+    names = [name for _, name in steps]
+    first = names.index("tmem_ld32")
+    between = names[first:names.index("rows_sync", first)]
+    assert "fence_before" in between[between.index("wait_ld"):]
+    behind = names[names.index("rows_sync", first):]
+    assert "fence_after" in behind[:behind.index("tmem_st32")]
