@@ -963,7 +963,9 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     a.B = d.n_slots; a.T = d.n_tokens; a.H = d.n_heads; a.Hk = d.n_kv_heads; a.D = d.d_head; a.G = d.n_heads / d.n_kv_heads;
     a.kv = kv_pages(d, *cache);
     a.q = q; a.out = out; a.length = d_length; a.parent = d_parent; a.scale = params->scale;
-    a.window = params->window; a.n_sink = params->window ? params->n_sink : 0; a.d_status = d_status;
+    // no position is further back than 2^30, so a wider window leaves the kernels' differences of positions within an int
+    a.window = params->window < 1 << 30 ? params->window : 1 << 30;
+    a.n_sink = params->window ? params->n_sink : 0; a.d_status = d_status;
     const gdn::AttendBlock block = attend_block(d);
     a.part_rows = block.rows;
     a.TB = block.tokens;
