@@ -384,8 +384,9 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
             // ---- the softmax: tensor memory's lane = row (of one of C copies), a thread or two for each
             const int tl = tid % kLanes, half = tid / kLanes, copy = tl / Sh::kRows, row = tl % Sh::kRows;
             const uint32_t lanes = tmem + ((uint32_t)(32 * (wid & 3)) << 16), o_at = lanes + Sh::kOColumn;
-            // (a negative scale's sign is in S: see the MMAs)  A scale of zero leaves all weights alike, and masked ones at none
-            const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+            // (a negative scale's sign is in S: see the MMAs)  A scale of zero leaves all weights alike, and masked ones at none: it is
+            // the smallest number, which brings no score to anything and leaves an infinity one
+            const float sc = fmaxf(fabsf(a.scale) * 1.4426950408889634f, __uint_as_float(1u));
             Ring<Sh::kBuffers> u, before;         // this tile's S, and the tile's before it
             bool any = false;                     // was there one?
             Ring<Sh::kRing> r;                    // the first stage of this tile
