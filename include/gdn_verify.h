@@ -573,8 +573,8 @@ size_t gdn_attend_workspace_bytes(const gdn_attn_dims *dims);
  * single tokens, verify batches, a prompt's chunk.
  *
  * Scores, maxima and sums are fp32.  In bf16 the weights w_p, scaled to at most
- * 2^8, are rounded to bf16 for the product with v (fp32 sums) and the output
- * once more.  What lies at positions that no token of the slot sees is never
+ * 2^8, are rounded to bf16, for the product with v as for their own sum (both
+ * fp32 sums), and the output once more.  What lies at positions that no token of the slot sees is never
  * used; k and v of the others must be finite.  q and out [B][T][n_heads][d_head]
  * do not overlap.  workspace: gdn_attend_workspace_bytes, 256-byte aligned; it
  * needs no initialisation, and calls that share it must be ordered.  The sums'
