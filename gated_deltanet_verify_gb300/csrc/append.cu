@@ -5,17 +5,19 @@
 // rope_dims numbers by the angle p * freq[i].  The new tokens' k' and v go to their slot's pages, q' to a dense matrix.
 //
 // Angles.  p * freq[i] in fp32 loses its turns at far positions (at p = 10^5 an error of 2^-8 radians).  Only the angle's
-// part of a full turn counts, so freq / 2 pi is held as a 64-bit fraction of a turn (rounded once, from fp64) and
-// multiplied by p in wrapping integers: exact but for that rounding, p * 2^-65 turns, and no fp64 in the loop (a CTA's SM
-// does two fp64 operations a cycle).  sincospif of the upper 32 bits follows.  A token's angles are computed once and
-// shared by its heads.
+// part of a full turn counts, so freq / 2 pi less its whole turns is held as a 64-bit fraction of a turn, off by 2^-63 at
+// most, and multiplied by p in wrapping integers; sincospif of the product's upper 32 bits follows.  The fraction comes from the
+// 24 bits of freq times the 128 bits of 1 / 2 pi that its exponent asks for (Payne and Hanek, Radian reduction for
+// trigonometric functions, 1983), for |freq| up to 2^40 and more.  No fp64: as one product of fp64 numbers it was off by |freq| 2^-56
+// of a turn, and a few such operations in every CTA cost the trees below 1.8 us (an SM does two a cycle).  A
+// token's angles are computed once and shared by its heads.
 //
 // Bytes bound it: every row is read once and written once.  A token is one CTA's (with few tokens several share its heads):
 // its threads take 8 numbers of a head each (16-byte accesses in bf16), so D / 8 lanes hold a head, its norm is a few
 // shuffles, and the other half of a rotated pair comes by a shuffle too (rope_dims / 2 is a multiple of 8).  Three heads a
 // thread are in flight, the first while the angles are computed.  8192 tokens of 32 + 8 + 8 heads of 128: 40 us, 5.0 TB/s of the
 // 6.7 that a copy has, with 62 % of the issue slots (46 us with the frequencies converted for every token and the
-// sines read where their threads met in a bank); one token 2.5 us, 32 x 16 in trees 8 us, in a captured graph.
+// sines read where their threads met in a bank); one token 2.6 us, 32 x 16 in trees 6.4 us, in a captured graph.
 #include "attn.cuh"
 
 #include <cuda_bf16.h>
@@ -61,6 +63,22 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// 1 / 2 pi, 64 bits a word behind the binary point, with zeros on both sides
+__constant__ const unsigned long long kTurn[6] = {0, 0, 0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull, 0};
+__device__ __forceinline__ unsigned long long turn_bits(int from) {
+    const int w = from >> 6, s = from & 63;
+    return s ? kTurn[w] << s | kTurn[w + 1] >> (64 - s) : kTurn[w];
+}
+// the part of a turn that f radians are, in 2^-64 of a turn: 24 bits of f times bits of 1 / 2 pi, of which those above the binary
+// point of the product do not count
+__device__ __forceinline__ unsigned long long turn_fraction(float f) {
+    const uint32_t u = __float_as_uint(f), e = u >> 23 & 255;
+    const unsigned long long m = (u & 0x7fffff) | (e ? 0x800000 : 0);
+    const int shift = min(max((int)e, 1) - 150 + 64, 128);     // (of larger numbers, infinities and NaN the angles are no one's)
+    const unsigned long long x = m * turn_bits(max(0, 64 + shift)) + __umul64hi(m, turn_bits(128 + shift));
+    return u >> 31 ? 0 - x : x;
+}
+
 template <typename E, int D, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kLanes = D / kPer;              // threads a head
@@ -81,12 +99,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     const bool low = sub < apart, turned = i0 < a.rope_dims;
     const int other = (low ? lane + apart : lane - apart) & 31;
     const bool norms = a.q_norm || a.k_norm;
-    // turns a position: the whole ones do not count, so the rest is a 64-bit fraction
-    unsigned long long part = 0;
-    if (tid < half) {
-        const double f = (double)a.freq[tid] * 0.15915494309189533577;
-        part = (unsigned long long)__double2ll_rn((f - rint(f)) * 18446744073709551616.0);
-    }
+    const unsigned long long part = tid < half ? turn_fraction(a.freq[tid]) : 0;      // of a turn, a position
     for (int row = blockIdx.x; row < a.B * a.T; row += gridDim.x) {
         const int s = row / a.T, t = row - s * a.T;
         int past;

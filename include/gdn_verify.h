@@ -537,7 +537,8 @@ typedef struct {
  * bytes), so they may be column blocks of one projection's output.  q_out
  * [B][T][n_heads][d_head] may be q itself if ld_q is n_heads * d_head; q NULL:
  * keys and values alone.  Sums, norms and rotations are fp32, the angles exact
- * to 2^-24 of a turn at any position; one rounding at the end.  v is copied.
+ * to 2^-24 of a turn at any position (|freq| up to 2^40); one rounding at the
+ * end.  v is copied.
  *
  * d_path (optional, DEVICE int32[B][T], with q and d_parent NULL): commits the
  * accepted path of a draft tree, as gdn_accept_tree's d_path gives it, from the
