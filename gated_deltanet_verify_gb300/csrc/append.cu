@@ -14,10 +14,10 @@
 //
 // Bytes bound it: every row is read once and written once.  A token is one CTA's (with few tokens several share its heads):
 // its threads take 8 numbers of a head each (16-byte accesses in bf16), so D / 8 lanes hold a head, its norm is a few
-// shuffles, and the other half of a rotated pair comes by a shuffle too (rope_dims / 2 is a multiple of 8).  Three heads a
-// thread are in flight, the first while the angles are computed.  8192 tokens of 32 + 8 + 8 heads of 128: 40 us, 5.0 TB/s of the
+// shuffles, and the other half of a rotated pair comes by a shuffle too (rope_dims / 2 is a multiple of 8).  Two or three
+// heads a thread are in flight, the first while the angles are computed.  8192 tokens of 32 + 8 + 8 heads of 128: 40 us, 5.0 TB/s of the
 // 6.7 that a copy has, with 62 % of the issue slots (46 us with the frequencies converted for every token and the
-// sines read where their threads met in a bank); one token 2.6 us, 32 x 16 in trees 6.4 us, in a captured graph.
+// sines read where their threads met in a bank); one token 2.4 us, 32 x 16 in trees 6.2 us, in a captured graph.
 #include "attn.cuh"
 
 #include <cuda_bf16.h>
@@ -27,7 +27,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 8;               // numbers a thread holds of a head
-constexpr int kBatch = 3;             // heads that a thread has in flight
 constexpr unsigned kFull = 0xffffffffu;
 
 template <typename E> struct Vec;
@@ -83,6 +82,10 @@ template <typename E, int D, bool ADJACENT>
 __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendArgs a) {
     constexpr int kLanes = D / kPer;              // threads a head
     constexpr int kHeads = kThreads / kLanes;     // heads at a time
+    // Heads that a thread has in flight.  Three of 32 bytes (f32) do not stay in 64 registers; in bf16 they nearly do, and were
+    // faster for heads of 128 alone (8192 tokens, us, three and two: f32 24 + 4 + 4 heads of 256 106 and 88, 40 + 8 + 8 of 64 58 and
+    // 47; bf16 72 and 69, 44 and 42; bf16 32 + 8 + 8 of 128 56 and 58, with neither norms nor shuffles 40 and 44).
+    constexpr int kBatch = sizeof(E) == 2 && D == 128 ? 3 : 2;
     // cos and sin of the token's angles; a thread's pairs are as far apart as there are threads, so that they do not meet in a bank
     __shared__ float2 turn[D / 2];
     constexpr int kPairs = ADJACENT ? kPer / 2 : kPer, kApart = D / 2 / kPairs;
@@ -214,7 +217,7 @@ cudaError_t launch(const AppendArgs &a, int sms, cudaStream_t stream) {
                              : (a.adjacent ? append_kernel<E, 256, true> : append_kernel<E, 256, false>);
     cudaLaunchConfig_t cfg = {};
     // As many CTAs as the SMs hold at once, which share out the tokens; with few tokens their heads too, twice as many then
-    // (32 x 16 tokens: 6.1 us, with one CTA a token 7.5).
+    // (32 x 16 tokens: in trees 6.2 us, with one CTA a token 6.5, in f32 6.8 and 8.4; in chains 7.2 and 6.5).
     const long long rows = (long long)a.B * a.T, most = 4LL * sms, spare = 2 * most / rows;
     const int groups = ((a.q ? a.H : 0) + 2 * a.Hk + kThreads * kPer / a.D - 1) / (kThreads * kPer / a.D);
     cfg.gridDim = dim3(unsigned(rows < most ? rows : most), unsigned(spare < 1 ? 1 : spare < groups ? spare : groups), 1);
