@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn_verify.so")
-# the checked variant: every global access of the verify-family and rollback kernels bounds-checked
+# the checked variant: every global access of the verify-family, rollback, append and attention kernels bounds-checked
 CHECKED_BUILD = os.path.join(PKG, "_build_checked")
 CHECKED_LIB = os.path.join(PKG, "libgdn_verify_checked.so")
 

@@ -102,15 +102,17 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
     const bool low = sub < apart, turned = i0 < a.rope_dims;
     const int other = (low ? lane + apart : lane - apart) & 31;
     const bool norms = a.q_norm || a.k_norm;
-    const unsigned long long part = tid < half ? turn_fraction(a.freq[tid]) : 0;      // of a turn, a position
+    auto chk = [&](const void *p, size_t bytes, const void *base, size_t extent) { return in_bounds(p, bytes, base, extent, a.d_status); };
+    const unsigned long long part = tid < half && chk(a.freq + tid, 4, a.freq, a.ext_freq) ? turn_fraction(a.freq[tid]) : 0;  // of a turn, a position
     for (int row = blockIdx.x; row < a.B * a.T; row += gridDim.x) {
         const int s = row / a.T, t = row - s * a.T;
         int past;
-        const int n = live_tokens(a.kv, a.length, a.T, s, past);
+        const int n = live_tokens(a.kv, a.length, a.T, s, past, a.d_status);
         if (n < 0 && t == 0 && tid == 0) report(a.d_status, GDN_ERR_LENGTH);
         if (t >= n) continue;
         int source = t, depth = t;
         if (a.path) {
+            if (!chk(a.path + row, 4, a.path, a.ext_nodes)) continue;
             source = a.path[row];
             if (source == -1) continue;
             if (source < 0 || source >= a.T) {
@@ -124,7 +126,11 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
         const E *from_k = static_cast<const E *>(a.k) + from * a.ld_k - (size_t)k_head * D + i0;
         const E *from_v = static_cast<const E *>(a.v) + from * a.ld_v - (size_t)v_head * D + i0;
         auto load = [&](int h) {
-            return *reinterpret_cast<const Vec<E> *>((h < k_head ? from_q : h < v_head ? from_k : from_v) + (size_t)h * D);
+            const E *from = (h < k_head ? from_q : h < v_head ? from_k : from_v) + (size_t)h * D;
+            if (!(h < k_head ? chk(from, sizeof(Vec<E>), a.q, a.ext_q) : h < v_head ? chk(from, sizeof(Vec<E>), a.k, a.ext_k)
+                                                                                   : chk(from, sizeof(Vec<E>), a.v, a.ext_v)))
+                return Vec<E>{};
+            return *reinterpret_cast<const Vec<E> *>(from);
         };
         // the first rows are on their way while the angles are computed
         Vec<E> v[kBatch];
@@ -132,19 +138,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
         for (int b = 0; b < kBatch; ++b)
             if (head0 + b * step < heads) v[b] = load(head0 + b * step);
         const int place = past + t;
-        const int id = a.kv.table[(size_t)s * a.kv.max_pages + (place >> a.kv.page_log2)];
+        const int id = page_at(a.kv, a.kv.table + (size_t)s * a.kv.max_pages + (place >> a.kv.page_log2), a.d_status);
         const bool held = id >= 0 && id < a.kv.n_pages;
         if (!held && tid == 0) report(a.d_status, GDN_ERR_PAGE);
         __syncthreads();                          // the last token's angles are no longer read
         if (a.parent) {
-            if (tid <= t) {
-                int p = a.parent[row - t + tid];
-                if (p < -1 || p >= tid) {         // as if it hung from the past
-                    if (tid == t) report(a.d_status, GDN_ERR_TREE);
-                    p = -1;
-                }
-                parents[tid] = p;
-            }
+            if (tid <= t) parents[tid] = parent_of(a.parent, a.T, s, tid, a.ext_nodes, a.d_status, tid == t);
             __syncthreads();
             depth = 0;
             for (int p = parents[t]; p >= 0; p = parents[p]) ++depth;
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
                         for (int i = 0; i < kPer; ++i) sum += x[i] * x[i];
 #pragma unroll
                         for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(kFull, sum, d);
-                        if (w) {
+                        if (w && chk(w + i0, 4 * kPer, w, a.ext_norm)) {
                             const float r = rsqrtf(sum / D + a.eps);
                             const float4 w0 = *reinterpret_cast<const float4 *>(w + i0), w1 = *reinterpret_cast<const float4 *>(w + i0 + 4);
                             const float ww[kPer] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -203,7 +202,9 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
                     if (h < v_head) v[b].set(y);
                 }
                 E *to = h < k_head ? to_q + (size_t)h * D : (h < v_head ? to_k : to_v) + (size_t)h * page * D;
-                if (h < heads && (h < k_head || held)) *reinterpret_cast<Vec<E> *>(to) = v[b];
+                if (h < heads && (h < k_head || held) &&
+                    (h < k_head ? chk(to, sizeof(Vec<E>), a.q_out, a.ext_out) : chk(to, sizeof(Vec<E>), h < v_head ? a.kv.k : a.kv.v, a.kv.ext_pool)))
+                    *reinterpret_cast<Vec<E> *>(to) = v[b];
             }
         }
     }

@@ -342,6 +342,8 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
     auto o_done = [&](int b) { return smem_u32(&ctl.o_done[b]); };
     const uint32_t o_free = smem_u32(&ctl.o_free);
 
+    auto chk = [&](const void *p, size_t bytes, const void *base, size_t extent) { return in_bounds(p, bytes, base, extent, a.d_status); };
+
     if (wid == Sh::kMmas) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&ctl.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
@@ -415,14 +417,8 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                     position = past + t;
                     if (a.parent) {
                         softmax_sync<Sh::kSoftmax>();
-                        if (half == 0 && tl < w.span.t1) {
-                            int p = a.parent[(size_t)s * a.T + tl];
-                            if (p < -1 || p >= tl) {              // it hangs from the past
-                                report(a.d_status, GDN_ERR_TREE);
-                                p = -1;
-                            }
-                            ctl.parents[tl] = p;
-                        }
+                        if (half == 0 && tl < w.span.t1)
+                            ctl.parents[tl] = parent_of(a.parent, a.T, s, tl, a.ext_nodes, a.d_status, true);
                         softmax_sync<Sh::kSoftmax>();
                         if (half == 0 && tl < w.span.t1) {
                             int d = 0;
@@ -601,7 +597,8 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                 }
                 if (w.whole) factor /= l;
                 const size_t part0 = size_t(2 * c + (w.first ? 0 : 1)) * a.part_rows;
-                if (!w.whole && on && copy == 0 && half == 0) a.stats[part0 + row] = make_float2(m * sc, l);
+                if (!w.whole && on && copy == 0 && half == 0 && chk(a.stats + part0 + row, 8, a.stats, a.ext_stats))
+                    a.stats[part0 + row] = make_float2(m * sc, l);
                 ok = ok && warp_wait(o_done(before.stage), before.round & 1);
                 fence_after();
                 // Rows go through the two stages, each turned by its number of 16 bytes (so that 32 lanes write 32 rows
@@ -665,10 +662,11 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                             if (rr >= rows) break;
                             if (w.whole) {
                                 const int tt = rr / a.G;
-                                *reinterpret_cast<uint2 *>(out0 + (((size_t)tt * a.H + rr - tt * a.G) * D + at0) * 2) =
-                                    make_uint2(pack_bf16(y[k].x, y[k].y), pack_bf16(y[k].z, y[k].w));
+                                uint2 *to = reinterpret_cast<uint2 *>(out0 + (((size_t)tt * a.H + rr - tt * a.G) * D + at0) * 2);
+                                if (chk(to, 8, a.out, a.ext_q)) *to = make_uint2(pack_bf16(y[k].x, y[k].y), pack_bf16(y[k].z, y[k].w));
                             } else {
-                                *reinterpret_cast<float4 *>(out0 + ((rr - row0) * D + at0) * 4) = y[k];
+                                float4 *to = reinterpret_cast<float4 *>(out0 + ((rr - row0) * D + at0) * 4);
+                                if (chk(to, 16, a.partial, a.ext_partial)) *to = y[k];
                             }
                         }
                     }
@@ -702,7 +700,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
                         if (j >= w.j1) return -1;
                         const int from = w.span.tile(j) * kTile + (lane << page_log2), to = from + min(page, kTile);
                         const bool on = lane < max(1, kTile >> page_log2) && ((from < hi && to > lo) || from < sink);
-                        return on ? table[from >> page_log2] : -1;
+                        return on ? page_at(a.kv, table + (from >> page_log2), a.d_status) : -1;
                     };
                     // a tile's K or V: of a stage kKChunks columns of all keys, or all columns of kVTokens keys
                     auto put = [&](int j, int id, bool value) {
@@ -858,7 +856,7 @@ __global__ void __launch_bounds__((Shape<D, C>::kThreads), 1) attend_tc_kernel(c
     if (c + 1 == a.ctas)
         for (int s = tid; s < a.B; s += kThreads) {
             int past;
-            if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
+            if (live_tokens(a.kv, a.length, a.T, s, past, a.d_status) < 0) report(a.d_status, GDN_ERR_LENGTH);
         }
     fence_before();
     __syncthreads();

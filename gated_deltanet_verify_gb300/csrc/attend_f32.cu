@@ -85,12 +85,13 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
     Smem<D, BM> &sm = *reinterpret_cast<Smem<D, BM> *>(raw);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, c = blockIdx.x;
+    auto chk = [&](const void *p, size_t bytes, const void *base, size_t extent) { return in_bounds(p, bytes, base, extent, a.d_status); };
     Share share;
     Place at = find_place<kTile, kThreads>(a, c, share, sm.scratch);
     if (c == 0)
         for (int s = tid; s < a.B; s += kThreads) {
             int past;
-            if (live_tokens(a.kv, a.length, a.T, s, past) < 0) report(a.d_status, GDN_ERR_LENGTH);
+            if (live_tokens(a.kv, a.length, a.T, s, past, a.d_status) < 0) report(a.d_status, GDN_ERR_LENGTH);
         }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (c >= share.ctas) return;
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
         auto page_id = [&](int jj) {
             if (jj >= j1) return -1;
             const int key = span.tile(jj) * kTile + lane;
-            return key < span.hi && (key >= span.lo || key < sink) ? table[key >> a.kv.page_log2] : -1;
+            return key < span.hi && (key >= span.lo || key < sink) ? page_at(a.kv, table + (key >> a.kv.page_log2), a.d_status) : -1;
         };
         int id = page_id(j0);
         auto fetch = [&](int jj, int buf) {
@@ -140,8 +141,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
                 for (int n = 0; n < kTile * kVecs / kThreads; ++n) {
                     const int i = tid + n * kThreads, r = i / kVecs, x = (i % kVecs) * 4;
                     const long long from = __shfl_sync(kFull, row, r);
-                    const int bytes = from >= 0 ? 16 : 0;            // of the 16 written, those that are read
-                    const long long off = from >= 0 ? from + x : 0;
+                    const bool there = from >= 0 && chk(static_cast<const float *>(a.kv.k) + from + x, 16, a.kv.k, a.kv.ext_pool) &&
+                                       chk(static_cast<const float *>(a.kv.v) + from + x, 16, a.kv.v, a.kv.ext_pool);
+                    const int bytes = there ? 16 : 0;                // of the 16 written, those that are read
+                    const long long off = there ? from + x : 0;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
                                      (uint32_t)__cvta_generic_to_shared(&sm.k[buf][r][x])), "l"(static_cast<const float *>(a.kv.k) + off),
                                  "r"(bytes) : "memory");
@@ -164,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
         if constexpr (kFew) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool on = row0 + i < rows;
-                const float *from = query(on ? row0 + i : 0);
+                const bool on = row0 + i < rows && chk(query(row0 + i), D * 4, a.q, a.ext_q);
+                const float *from = on || chk(query(0), D * 4, a.q, a.ext_q) ? query(on ? row0 + i : 0) : static_cast<const float *>(a.q);
 #pragma unroll
                 for (int e = 0; e < Sh::kQ; e += Sh::kQV) {
                     read_n<Sh::kQV>(from + e * 32 + lane * Sh::kQV, &qr[i][e]);
@@ -176,17 +179,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
         } else {
             for (int i = tid; i < BM * (D / 4); i += kThreads) {
                 const int r = i / (D / 4), x = (i % (D / 4)) * 4;
-                *reinterpret_cast<float4 *>(&sm.q[r][x]) = r < rows ? read4(query(r) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+                const bool on = r < rows && chk(query(r) + x, 16, a.q, a.ext_q);
+                *reinterpret_cast<float4 *>(&sm.q[r][x]) = on ? read4(query(r) + x) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
-        if (a.parent && tid < span.t1) {
-            int p = a.parent[(size_t)s * a.T + tid];
-            if (p < -1 || p >= tid) {
-                report(a.d_status, GDN_ERR_TREE);
-                p = -1;
-            }
-            sm.parents[tid] = p;
-        }
+        if (a.parent && tid < span.t1) sm.parents[tid] = parent_of(a.parent, a.T, s, tid, a.ext_nodes, a.d_status, true);
         __syncthreads();
         if (a.parent && tid < span.t1) {
             int d = 0;
@@ -360,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
         const size_t part = size_t(2 * c + (first_block ? 0 : 1)) * a.part_rows;
         float *out = static_cast<float *>(a.out) + (((size_t)s * a.T + span.t0) * a.H + (size_t)kvh * a.G) * D;
         auto place = [&](int r) { return whole ? out + ((size_t)(r / a.G) * a.H + r % a.G) * D : a.partial + (part + r) * D; };
+        auto put = [&](const float *to, size_t bytes) { return whole ? chk(to, bytes, a.out, a.ext_q) : chk(to, bytes, a.partial, a.ext_partial); };
         if constexpr (kFew) {
 #pragma unroll
             for (int d = Sh::kLanes; d < 32; d *= 2)
@@ -367,11 +365,11 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(kFull, o[i][e], d);
-            if (!whole && tid < rows) a.stats[part + tid] = make_float2(sm.m[tid], sm.l[tid]);
+            if (!whole && tid < rows && chk(a.stats + part + tid, 8, a.stats, a.ext_stats)) a.stats[part + tid] = make_float2(sm.m[tid], sm.l[tid]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = row0 + i;
-                if (r >= rows || kpart != i % Sh::kParts) continue;
+                if (r >= rows || kpart != i % Sh::kParts || !put(place(r) + column, 16)) continue;
                 const float f = whole ? 1.f / sm.l[r] : 1.f;
                 *reinterpret_cast<float4 *>(place(r) + column) = make_float4(o[i][0] * f, o[i][1] * f, o[i][2] * f, o[i][3] * f);
             }
@@ -382,11 +380,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<D, BM>::kCtas)) attend_kernel
                 const int r = wid + 8 * i;
                 if (r >= rows) continue;
                 const float l = sm.l[r], f = whole ? 1.f / l : 1.f;
-                if (!whole && lane == 0) a.stats[part + r] = make_float2(sm.m[r], l);
+                if (!whole && lane == 0 && chk(a.stats + part + r, 8, a.stats, a.ext_stats)) a.stats[part + r] = make_float2(sm.m[r], l);
 #pragma unroll
                 for (int e = 0; e < kCols; ++e) o[i][e] *= f;
 #pragma unroll
-                for (int e = 0; e < kCols; e += V) store_row<V>(place(r) + (e / V * 32 + lane) * V, &o[i][e]);
+                for (int e = 0; e < kCols; e += V)
+                    if (put(place(r) + (e / V * 32 + lane) * V, 4 * V)) store_row<V>(place(r) + (e / V * 32 + lane) * V, &o[i][e]);
             }
         }
         // ---- the next block

@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     constexpr int kWarpsRow = D / (32 * V);
     constexpr int kPartWords = ((sizeof(E) == 4 ? 2 : 1) * kAttendCtas + 31) / 32;      // parts a lane looks after
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    auto chk = [&](const void *p, size_t bytes, const void *base, size_t extent) { return in_bounds(p, bytes, base, extent, a.d_status); };
     // The lengths were there before the kernel whose sums are joined began, so this goes on beside its end.
     Share share;
     int c, s, kvh = 0, parts = 1;
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
         for (int k = 0; k < kPartWords; ++k) {
             const int i = 32 * k + lane;
-            st[k] = i < parts ? a.stats[part(i)] : make_float2(-INFINITY, 0.f);
+            st[k] = i < parts && chk(a.stats + part(i), 8, a.stats, a.ext_stats) ? a.stats[part(i)] : make_float2(-INFINITY, 0.f);
             m = fmaxf(m, st[k].x);
         }
 #pragma unroll
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 #pragma unroll
                 for (int q = 0; q < BATCH; ++q) {
                     const float *from = a.partial + part(i0 + q) * D + column;
-                    const bool there = i0 + q < parts;
+                    const bool there = i0 + q < parts && chk(from, 4 * V, a.partial, a.ext_partial);
                     if constexpr (V == 4) {
                         const float4 f = there ? *reinterpret_cast<const float4 *>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
                         x[q][0] = f.x; x[q][1] = f.y; x[q][2] = f.z; x[q][3] = f.w;
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const float inv = 1.f / sum;
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] *= inv;
-        store_row<V>(static_cast<E *>(a.out) + (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D + column, o);
+        E *to = static_cast<E *>(a.out) + (((size_t)s * a.T + span.t0 + r / a.G) * a.H + (size_t)kvh * a.G + r % a.G) * D + column;
+        if (chk(to, V * sizeof(E), a.out, a.ext_q)) store_row<V>(to, o);
     }
 }
 

@@ -2,6 +2,7 @@
 // what its kernels share: how a paged cache is addressed, what a new token may see, and how the work is dealt out.
 #pragma once
 
+#include "check.cuh"
 #include "internal.cuh"
 
 namespace gdn {
@@ -15,6 +16,7 @@ struct KvPages {
     long long page_stride;            // elements
     int n_pages, max_pages;
     int page_log2;                    // tokens a page: 2^page_log2
+    size_t ext_past, ext_table, ext_pool;     // bytes, for a checked build (as all ext_...): of past (and lengths), table, k and v
 };
 
 // Rotation and append of a batch's keys and values (append.cu).
@@ -29,6 +31,7 @@ struct AppendArgs {
     float eps;
     const int32_t *length, *parent, *path;
     int *d_status;
+    size_t ext_q, ext_k, ext_v, ext_out, ext_freq, ext_norm, ext_nodes;     // nodes: parent or path
 };
 
 // Attention of a batch over the cache (attend.cu, attend_f32.cu).
@@ -48,6 +51,7 @@ struct AttendArgs {
     float *partial;                   // [2 * ctas][part_rows][D]: unnormalised sums of split blocks
     float2 *stats;                    // [2 * ctas][part_rows]: their maxima (in powers of two) and sums
     int *d_status;
+    size_t ext_q, ext_nodes, ext_partial, ext_stats;      // q and out; parent; the workspace's two halves
 };
 
 constexpr int kTileF32 = 32, kTileBf16 = 128;   // keys a tile
@@ -82,12 +86,29 @@ __device__ __forceinline__ void report(int *d_status, gdn_status code) {
 }
 
 // The real tokens of slot s, or -1 where its past or its length cannot be.
-__device__ __forceinline__ int live_tokens(const KvPages &kv, const int32_t *length, int T, int s, int &past) {
+__device__ __forceinline__ int live_tokens(const KvPages &kv, const int32_t *length, int T, int s, int &past, int *d_status) {
+    past = 0;
+    if (!in_bounds(kv.past + s, 4, kv.past, kv.ext_past, d_status) ||
+        (length && !in_bounds(length + s, 4, length, kv.ext_past, d_status)))
+        return -1;
     past = kv.past[s];
     const int n = length ? length[s] : T;
     const long long room = (long long)kv.max_pages << kv.page_log2;
     if (n < 0 || n > T || past < 0 || (long long)past + n > room) return -1;
     return n;
+}
+
+// An entry of the page table.
+__device__ __forceinline__ int page_at(const KvPages &kv, const int32_t *at, int *d_status) {
+    return in_bounds(at, 4, kv.table, kv.ext_table, d_status) ? *at : -1;
+}
+// The parent of node t of slot s, of T nodes; one that cannot be (and a parent outside its buffer) hangs from the past.
+__device__ __forceinline__ int parent_of(const int32_t *parent, int T, int s, int t, size_t extent, int *d_status, bool report_it) {
+    const int32_t *at = parent + (size_t)s * T + t;
+    const int p = in_bounds(at, 4, parent, extent, d_status) ? *at : -1;
+    if (p >= -1 && p < t) return p;
+    if (report_it) report(d_status, GDN_ERR_TREE);
+    return -1;
 }
 
 // The key tiles (of TK positions) that a block of rows, tokens [t0, t1) of slot s, reads: those of the first positions that
@@ -102,7 +123,7 @@ struct Span {
 template <int TK>
 __device__ __forceinline__ Span block_span(const AttendArgs &a, int s, int tb) {
     Span p;
-    const int n = live_tokens(a.kv, a.length, a.T, s, p.past);
+    const int n = live_tokens(a.kv, a.length, a.T, s, p.past, a.d_status);
     p.t0 = tb * a.TB;
     p.t1 = min(n, p.t0 + a.TB);
     p.sink_tiles = p.first = p.n = p.lo = p.hi = 0;

@@ -1,7 +1,7 @@
 // check.cuh -- bounds checks of a checked build (nvcc -DGDN_CHECKED=1).
 //
-// A checked build tests every global access of the verify-family and rollback
-// kernels against the extent of its buffer before making it; an access that
+// A checked build tests every global access of the verify-family, rollback,
+// append and attention kernels (the attention's TMA boxes end with their tensor) against the extent of its buffer before making it; an access that
 // falls outside is skipped and the first such event writes GDN_ERR_BOUNDS to
 // the caller's status word (no trap, no assert).  The ordinary build compiles
 // every test away.  It stands in for a memory checker that cannot run here.

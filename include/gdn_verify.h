@@ -76,7 +76,8 @@ typedef enum {
     GDN_ERR_TIMEOUT = 8,     /* (device) a bounded wait gave up */
     GDN_ERR_WORKSPACE = 9,   /* workspace missing or smaller than the query returned */
     GDN_ERR_TREE = 10,       /* (device) a parent id is outside [-1, t-1]; that token ran from the root */
-    GDN_ERR_BOUNDS = 11,     /* (device, checked builds only) an access fell outside its buffer and was skipped */
+    GDN_ERR_BOUNDS = 11,     /* (device, checked builds only: the verifies, rollbacks, acceptance, append and attention) an
+                                access fell outside its buffer and was skipped */
     GDN_ERR_SAMPLE = 12,     /* (device) a row that cannot be sampled (see gdn_sample); its token is -1 */
     GDN_ERR_LENGTH = 13,     /* (device) a slot's length (or past) is out of range; nothing of it is accepted (or run) */
     GDN_ERR_ADAPTER = 14,    /* (device) an adapter id names none; the slot ran without one */
