@@ -492,8 +492,8 @@ int gdn_accept_tree(const gdn_dims *dims, const int32_t *d_parent, const int32_t
  * page_tokens at most 2^30; B*T at most 2^24; n_heads at most 65536; T * n_heads *
  * d_head below 2^38 (GDN_ERR_SHAPE).
  * Activations and cache are all f32 or all bf16.  d_length (optional, DEVICE
- * int32[B]): a slot's real tokens, 0 .. T; the rows behind them are neither read
- * nor written.  A length or a past outside [0, T] or [0, max_pages * page_tokens -
+ * int32[B]): a slot's real tokens, 0 .. T; the rows behind them are not written,
+ * and what q, k and v hold there does not matter (gdn_attend may read q's).  A length or a past outside [0, T] or [0, max_pages * page_tokens -
  * length] skips the slot and writes GDN_ERR_LENGTH to *d_status.  A page id
  * outside [0, n_pages) writes GDN_ERR_PAGE: its positions are not written, and
  * read as zeros (keys and values).  d_parent (optional, DEVICE int32[B][T], T <=
@@ -576,14 +576,20 @@ size_t gdn_attend_workspace_bytes(const gdn_attn_dims *dims);
  *
  * Scores, maxima and sums are fp32.  In bf16 the weights w_p, scaled to at most
  * 2^8, are rounded to bf16, for the product with v as for their own sum (both
- * fp32 sums), and the output once more.  What lies at positions that no token of the slot sees is never
- * used; k and v of the others must be finite.  q and out [B][T][n_heads][d_head]
- * do not overlap.  workspace: gdn_attend_workspace_bytes, 256-byte aligned; it
- * needs no initialisation, and calls that share it must be ordered.  The sums'
- * order, so the last bits of a row, depends on the lengths of the whole batch.
- * Limit: the slots' blocks of rows (a block: 128 rows of a kv head's queries at
- * the least, 16 in f32) times n_kv_heads times the key tiles of max_pages pages
- * (128 positions, 32 in f32) below 2^31 (GDN_ERR_SHAPE).
+ * fp32 sums), and the output once more.  What lies at positions that no token of
+ * the slot sees is never used; k and v of the others must be finite, with q . k
+ * (unscaled) below 2^126 and v below 2^88 in size, so that no sum overflows.
+ * q and out [B][T][n_heads][d_head] do not overlap.  workspace:
+ * gdn_attend_workspace_bytes, 256-byte aligned; it needs no initialisation, and
+ * calls that share it must be ordered.  The sums' order, so the last bits of a
+ * row, depends on the lengths of the whole batch.  A wait inside the kernel that
+ * gives up writes GDN_ERR_TIMEOUT; out is then undefined.
+ * Limit (GDN_ERR_SHAPE): n_slots * ceil(T / b) * n_kv_heads * tiles below 2^31,
+ * with b the tokens of a block of rows and tiles the key tiles of a full slot.
+ * With G = n_heads / n_kv_heads a block has r rows and b = min(T, r / G) tokens:
+ * in bf16 r = 32 if T * G <= 32, else 128; in f32 the smallest of 8, 16, 32 that
+ * T * G fits, else 64.  tiles = ceil(max_pages * page_tokens / 128) + 3 in bf16 (+ 4 if
+ * d_head is 64), ceil(max_pages * page_tokens / 32) in f32.
  */
 int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_attn_params *params,
                const void *q, void *out, const int32_t *d_length, const int32_t *d_parent,
