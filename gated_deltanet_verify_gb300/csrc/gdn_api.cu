@@ -967,7 +967,8 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     if (rc) return rc;
     if (!params) return fail(GDN_ERR_ARG, "params is NULL");
     const gdn_attn_dims &d = *dims;
-    if (!(params->scale > -INFINITY && params->scale < INFINITY)) return fail(GDN_ERR_ARG, "scale must be finite");
+    // (the kernels take it times log2 e, which has to be finite too)
+    if (!(params->scale > -0x1p126f && params->scale < 0x1p126f)) return fail(GDN_ERR_ARG, "scale must be below 2^126 in size");
     if (params->window < 0 || params->n_sink < 0)
         return fail(GDN_ERR_ARG, "window and n_sink must be >= 0 (got %d, %d)", params->window, params->n_sink);
     if (!q || !out) return fail(GDN_ERR_ARG, "q or out is NULL");

@@ -555,7 +555,7 @@ int gdn_kv_append(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gd
                   int *d_status, void *stream);
 
 typedef struct {
-    float scale;           /* of the scores (1/sqrt(d_head) is common); finite, and so the scaled scores in f32 */
+    float scale;           /* of the scores (1/sqrt(d_head) is common); it and the scaled scores below 2^126 in size */
     int window;            /* 0: none; else a token sees the last `window` positions, its own among them */
     int n_sink;            /* with a window: the first positions that stay visible */
 } gdn_attn_params;

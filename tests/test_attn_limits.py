@@ -1,4 +1,5 @@
-"""The largest work that a launch of gdn_attend counts, as its header states it (no GPU needed: asked of the workspace)."""
+"""Limits of gdn_attend as its header states them (no GPU needed): the largest work that a launch counts, asked of the
+workspace, and the largest scale."""
 import pytest
 
 import gated_deltanet_verify_gb300 as gdn
@@ -45,3 +46,13 @@ def test_padding_counts():
     kw = dict(n_tokens=1, n_heads=64, n_kv_heads=64, d_head=64, page_tokens=128, n_pages=1, max_pages=1, dtype=gdn.GDN_BF16)
     assert gdn.gdn_attend_workspace_bytes(gdn.make_attn_dims(n_slots=2 ** 24, **kw)) == 0
     assert gdn.gdn_attend_workspace_bytes(gdn.make_attn_dims(n_slots=2 ** 22, **kw)) > 0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 126, -(2.0 ** 126), 3.4e38])
+def test_scales_whose_powers_of_two_overflow_are_refused(scale):
+    """Scores are taken to powers of two: scale times log2 e has to be a number, or a score of 0 would become NaN."""
+    A = 0x10000
+    dims = gdn.make_attn_dims(2, 4, 8, 2, 64, 16, 10, 5)
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.gdn_attend(dims, gdn.kv_cache(A, A, A, A), gdn.attn_params(scale), A, A + 4096, A, 1 << 40, stream=0)
+    assert e.value.status == gdn.GDN_ERR_ARG
