@@ -48,3 +48,29 @@ FEW = {
 @pytest.mark.parametrize("name", FEW)
 def test_few_rows(name):
     replay(Run(Case(**FEW[name])))
+
+
+MANY = {
+    "window, sinks": dict(T=40, H=8, Hk=2, D=64, page=32, past=[2000, 130], window=300, n_sink=4),
+    "tree": dict(T=64, H=16, Hk=4, D=128, page=16, past=[700, 0, 127], tree=True),
+    "window over tree": dict(T=64, H=8, Hk=2, D=256, page=16, past=[900, 20], tree=True, window=40, n_sink=3),
+}
+
+
+@pytest.mark.parametrize("name", MANY)
+def test_many_rows(name):
+    replay(Run(Case(**MANY[name])))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("rows", [8, 16, 32, 64])
+def test_f32(rows, d):
+    """Each size of a block: a ring of 2 to 6 buffers, filled again beside the softmax."""
+    replay(Run(Case(dtype="f32", T=rows // 4, H=8, Hk=2, D=d, page=16, past=[3000, 5, 61])))
+
+
+@pytest.mark.parametrize("sizes", [dict(T=2, H=8, Hk=2, D=128, page=16, past=[2000, 30], window=300, n_sink=4),
+                                   dict(T=16, H=4, Hk=2, D=64, page=8, past=[1500, 30], tree=True),
+                                   dict(T=100, H=4, Hk=2, D=128, page=32, past=[500, 30])])
+def test_f32_forms(sizes):
+    replay(Run(Case(dtype="f32", **sizes)))
