@@ -15,8 +15,8 @@
 // Bytes bound it: every row is read once and written once.  A token is one CTA's (with few tokens several share its heads):
 // its threads take 8 numbers of a head each (16-byte accesses in bf16), so D / 8 lanes hold a head, its norm is a few
 // shuffles, and the other half of a rotated pair comes by a shuffle too (rope_dims / 2 is a multiple of 8).  Two or three
-// heads a thread are in flight, the first while the angles are computed.  8192 tokens of 32 + 8 + 8 heads of 128: 40 us, 5.0 TB/s of the
-// 6.7 that a copy has, with 62 % of the issue slots (46 us with the frequencies converted for every token and the
+// heads a thread are in flight, the first while the angles are computed.  8192 tokens of 32 + 8 + 8 heads of 128: 39 us, 5.2 TB/s of the
+// 6.7 that a copy has, with 70 % of the issue slots (46 us with the frequencies converted for every token and the
 // sines read where their threads met in a bank); one token 2.4 us, 32 x 16 in trees 6.2 us, in a captured graph.
 #include "attn.cuh"
 

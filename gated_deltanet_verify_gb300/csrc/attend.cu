@@ -10,7 +10,7 @@
 // rescale is rare.  The rounding of P to bf16 (half a step, 2^-8, of each weight) is what the tensor cores take, and of the
 // order of the output's own rounding.  The row sums, in fp32, are of the rounded weights: so an output is a mean of the values
 // that its row sees, and a row of equal values comes out as that value.  (A sum of the weights before their rounding left it off by
-// up to 2^-8; it saves an instruction a pair of weights: 428 us for the prompt below against 441, and 1 % elsewhere at most.)
+// up to 2^-8; it saves an instruction a pair of weights: 428 us for the prompt below against 442, and 1 % elsewhere at most.)
 //
 //   * A warp (two for D = 64) streams keys and values through a ring of 16 or 32 KB stages: one TMA box a page, straight into
 //     the tensor cores' 128-byte swizzle.  A page's tokens come in groups of 8 (a swizzle atom's rows), all 64-column chunks of a group
@@ -21,10 +21,10 @@
 //     its own S, O and softmax warps, halve what the keys and values cost in shared memory, but ran slower: the chains
 //     of one tile's S, softmax and P V are what binds, and two of them took 4950 cycles where a single one takes 2200.)
 //   * Two threads do the softmax of a row (tensor memory's lane), half of the keys each, and exchange their maxima: S, softmax
-//     and P V of a tile follow one another, so its time counts (a chunk of 4096 tokens with D = 128: 372 us, with one thread a
-//     row 396).  Where a slot has at most 32 rows they lie there four times instead, and each copy's warp takes a quarter of
-//     every tile's keys (its other weights are zeros); the four sums are added up at the end (64 slots of a window of 1024: 50
-//     us, with one warp for all the keys 67).
+//     and P V of a tile follow one another, so its time counts (4096 tokens of 32 + 8 heads of 128 over 8192 positions: 342 us, with
+//     one thread a row 356; 8 trees of 64: 42 and 46).  Where a slot has at most 32 rows they lie there four times instead, and each copy's warp takes a quarter of
+//     every tile's keys (its other weights are zeros); the four sums are added up at the end (64 slots of 2 tokens in a
+//     window of 1024: 41 us, with one copy of the rows 52; one token behind 1001 positions: 10.8 and 13.5).
 //   * The work is dealt out by tiles (attn.cuh): every CTA has the same number whatever the lengths, and the blocks of rows
 //     at the ends of its share are joined with its neighbours' parts by attend_join.cu.
 //
@@ -34,7 +34,7 @@
 // What bounds it.  Few rows: the cache's bytes (4 single tokens behind 131000 positions, D = 128: 298 us, 7.2 TB/s; 32 slots of 16
 // tokens over up to 16384, D = 256: 182 us, 6.1 TB/s).  Many rows: shared memory, which a tile of D = 256 asks for 320 KB (the
 // loads write 128, S reads Q and K, 128, P V reads V, 64), 2500 cycles at 128 bytes each, where its MMAs take 2048 (4096 tokens over
-// 8192 positions: 425 us, 1460 TFLOP/s).  Few keys: latency -- a launch, dependent loads of lengths, page ids and pages, one tile's S, softmax and
+// 8192 positions: 442 us in a captured graph, 1400 TFLOP/s).  Few keys: latency -- a launch, dependent loads of lengths, page ids and pages, one tile's S, softmax and
 // P V, and instructions that come from L2 the first time.
 //
 // Every wait is bounded; one that gives up reports GDN_ERR_TIMEOUT and the CTA ends.
@@ -927,9 +927,11 @@ AttendBlock attend_bf16_block(int T, int G, int D) {
     const int c = copies(T, G), rows = kLanes / c, tokens = rows / G < T ? rows / G : T;
     // A part of many rows costs as much as a tile's keys and values.  A block's beginning and end take 3 to 5 us, a tile of 128
     // keys 0.8 (D = 64), 1.5 (128) or 3 us (256).  Where a slot is one block the cache's bytes bind, and 128 CTAs take them a little
-    // faster than one on each of 152 SMs (8 slots of 20000 positions: 98.9 and 103.5 us for one token with D = 128, 107.9 and
-    // 112.9 for 16 with D = 256); with D = 64 (58.5 and 58.3; 64 slots of a window 45.5 and 41.0) or several blocks (a prompt:
-    // 495 and 426) they do not.
+    // faster than one on each of 152 SMs (8 slots of 20000 positions: 100.1 and 104.2 us for one token with D = 128, 108.8 and
+    // 113.7 for 16 with D = 256), or as fast where they come from L2 (8 of 1500: 17.8 and 17.9, 23.7 and 23.8; 64 single tokens of up
+    // to 300 with D = 256 lose, 26.0 and 24.3) or under a window of 1024 (D = 128, 16 and 64 single tokens: 21.5 and 23.0, 55.9
+    // and 55.8; D = 256, 32 slots of 16: 45.2 and 47.0).  With D = 64 (59.1 and 58.0; 64 slots of a window 44.7 and 41.0) or
+    // several blocks (a prompt: 509 and 442; trees of 64: 46.0 and 42.4) they are slower.
     const int least = c > 1 ? 1 : 3, pad = D == 64 ? 4 : 3, ctas = D >= 128 && tokens == T ? 128 : kAttendCtas;
     return {rows, tokens, least, pad, ctas};
 }

@@ -15,7 +15,7 @@
 //
 // What bounds it.  Few rows: the copies' issue and the steps between barriers beside the cache's bytes (8 single tokens behind 20000
 // positions, 32 + 8 heads of 128: 300 us, 4.4 TB/s; 3 behind 57508, 24 + 4 of 256: 321 us, 4.4 TB/s).  Many rows: reads of
-// shared memory beside the products (1024 tokens over 2000 positions, 16 + 4 heads of 128: 703 us, 30 TFLOP/s).
+// shared memory beside the products (1024 tokens behind 2000 positions, 16 + 4 heads of 128: 703 us, 30 TFLOP/s).
 #include "attn.cuh"
 
 namespace gdn {
@@ -57,7 +57,7 @@ __device__ __forceinline__ float sums_by_lane(float (&x)[32], int lane) {
 template <int D, int BM> struct Shape {
     static constexpr bool kFew = BM <= 32;
     // CTAs an SM: where their tiles fit, two, which cover each other's barriers (D = 128, 8 single tokens behind 20000 positions:
-    // 309 us, with one 425; 1024 tokens over 2000: 709 and 945)
+    // 309 us, with one 425; 1024 tokens behind 2000: 709 and 945)
     static constexpr int kCtas = D <= 128 ? 2 : 1;
     static constexpr int kBuffers = !kFew ? 2 : D == 64 ? 6 : 3;
     static constexpr int kGroups = kFew ? BM / 8 : 1, kWarps = 8 / kGroups;
