@@ -870,8 +870,8 @@ int check_kv_cache(const gdn_kv_cache *c) {
 
 // A buffer's bytes, for a checked build.  Test build only (the ordinary library never reads the environment):
 // GDN_TEST_SHORT=<name> has the checks take that buffer for half as long as it is, so that they refuse what is there.
-size_t extent(const char *name, long long elements, size_t size) {
-    const size_t bytes = size_t(elements) * size;
+size_t extent(const char *name, size_t elements, size_t size) {
+    const size_t bytes = elements * size;
 #if GDN_CHECKED
     const char *test = getenv("GDN_TEST_SHORT");
     if (test && !strcmp(test, name)) return bytes / 2;
@@ -884,9 +884,9 @@ size_t dtype_size(const gdn_attn_dims &d) { return d.dtype == GDN_F32 ? 4 : 2; }
 gdn::KvPages kv_pages(const gdn_attn_dims &d, const gdn_kv_cache &c) {
     int log2 = 0;
     while ((1 << log2) < d.page_tokens) ++log2;
-    const long long pool = (d.n_pages - 1) * d.page_stride + (long long)d.n_kv_heads * d.page_tokens * d.d_head;
+    const size_t pool = size_t(d.n_pages - 1) * size_t(d.page_stride) + size_t(d.n_kv_heads) * d.page_tokens * d.d_head;
     return {c.k, c.v, c.page_table, c.past, d.page_stride, d.n_pages, d.max_pages, log2,
-            extent("past", d.n_slots, 4), extent("table", (long long)d.n_slots * d.max_pages, 4), extent("pool", pool, dtype_size(d))};
+            extent("past", d.n_slots, 4), extent("table", size_t(d.n_slots) * d.max_pages, 4), extent("pool", pool, dtype_size(d))};
 }
 
 gdn::AttendBlock attend_block(const gdn_attn_dims &d) {
@@ -944,8 +944,8 @@ int gdn_kv_append(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gd
     a.rope_dims = p.rope_dims; a.adjacent = p.adjacent != 0; a.freq = p.freq;
     a.q_norm = p.q_norm; a.k_norm = p.k_norm; a.eps = p.norm_eps;
     a.length = d_length; a.parent = d_parent; a.path = d_path; a.d_status = d_status;
-    const long long rows = (long long)a.B * a.T;
-    a.ext_q = extent("q", (rows - 1) * ld_q + qw, dtype_size(d)); a.ext_k = extent("k", (rows - 1) * ld_k + kw, dtype_size(d));
+    const size_t rows = size_t(a.B) * a.T;
+    a.ext_q = q ? extent("q", (rows - 1) * ld_q + qw, dtype_size(d)) : 0; a.ext_k = extent("k", (rows - 1) * ld_k + kw, dtype_size(d));
     a.ext_v = extent("v", (rows - 1) * ld_v + kw, dtype_size(d)); a.ext_out = extent("out", rows * qw, dtype_size(d));
     a.ext_freq = extent("freq", a.rope_dims / 2, 4); a.ext_norm = extent("norm", a.D, 4); a.ext_nodes = extent("nodes", rows, 4);
     const cudaError_t e = gdn::launch_append(a, d.dtype, dev_info().sms, static_cast<cudaStream_t>(stream));
@@ -999,7 +999,7 @@ int gdn_attend(const gdn_attn_dims *dims, const gdn_kv_cache *cache, const gdn_a
     a.ctas = most < block.ctas ? most : block.ctas;
     a.partial = static_cast<float *>(workspace);
     a.stats = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + gdn::attend_partial_bytes(block, a.D));
-    const long long rows = (long long)a.B * a.T;
+    const size_t rows = size_t(a.B) * a.T;
     a.ext_q = extent("q", rows * a.H * a.D, dtype_size(d)); a.ext_nodes = extent("nodes", rows, 4);
     a.ext_partial = extent("partial", gdn::attend_partial_bytes(block, a.D), 1);
     a.ext_stats = extent("stats", gdn::attend_stats_bytes(block), 1);
